@@ -52,6 +52,83 @@ gs_status check_camera(const gs_camera* cam) {
     return GS_OK;
 }
 
+// Bytes of an element type, 0 for an unknown one.
+size_t type_bytes(int32_t dtype) {
+    return dtype == GS_F32 ? 4 : dtype == GS_BF16 || dtype == GS_F16 ? 2 : 0;
+}
+
+gs_status check_recurrence(const gs_recurrence* r, const char* who) {
+    constexpr int32_t kMost = 1 << 30;
+    if (!r) return fail(GS_ERR_INVALID, "%s: the description is NULL", who);
+    if (!type_bytes(r->dtype)) return fail(GS_ERR_INVALID, "%s: unknown dtype %d", who, r->dtype);
+    if (r->gating != GS_GATE_LINEAR && r->gating != GS_GATE_SIGMOID)
+        return fail(GS_ERR_INVALID, "%s: unknown gating %d", who, r->gating);
+    if (r->batch < 0 || r->steps < 0 || r->channels < 0 || r->batch > kMost || r->steps > kMost || r->channels > kMost)
+        return fail(GS_ERR_INVALID, "%s: batch %d, steps %d or channels %d outside [0, 2^30]", who, r->batch, r->steps,
+                    r->channels);
+    if (r->gate_batch < 0 || r->gate_step < 0 || r->x_batch < 0 || r->x_step < 0)
+        return fail(GS_ERR_INVALID, "%s: a stride is negative", who);
+    if (!gs::recurrence_fits(*r))
+        return fail(GS_ERR_INVALID, "%s: %d sequences of %d steps and %d channels are too many for one call", who,
+                    r->batch, r->steps, r->channels);
+    if ((uintptr_t)r->lengths & 3) return fail(GS_ERR_INVALID, "%s: lengths is not 4-byte aligned", who);
+    return GS_OK;
+}
+
+// Whether every pointer is aligned to `bytes` (a power of two).
+template <typename... P>
+bool aligned(size_t bytes, P... p) {
+    return !((0 | ... | (uintptr_t)p) & (bytes - 1));
+}
+
+gs::RecurrenceArgs recurrence_args(const gs_recurrence& r) {
+    gs::RecurrenceArgs a{};
+    a.gate_batch = r.gate_batch;
+    a.gate_step = r.gate_step;
+    a.x_batch = r.x_batch;
+    a.x_step = r.x_step;
+    a.lengths = r.lengths;
+    a.restart = r.restart;
+    a.batch = r.batch;
+    a.steps = r.steps;
+    a.channels = r.channels;
+    return a;
+}
+
+// Checks that the lists of gs_grad_norm, gs_clip_grads and gs_adam_step share.
+gs_status check_list(const void* tensors, int32_t n, const void* scratch, const char* who) {
+    if (n < 0 || n > GS_MAX_TENSORS)
+        return fail(GS_ERR_INVALID, "%s: n_tensors = %d outside [0, %d]", who, n, GS_MAX_TENSORS);
+    if (n && !tensors) return fail(GS_ERR_INVALID, "%s: tensors is NULL", who);
+    if (!scratch) return fail(GS_ERR_INVALID, "%s: scratch is NULL", who);
+    if (!aligned(8, scratch)) return fail(GS_ERR_INVALID, "%s: scratch is not 8-byte aligned", who);
+    return GS_OK;
+}
+
+gs_status check_count(int64_t count, int i, const char* who) {
+    if (count < 0 || count > GS_MAX_TENSOR_COUNT)
+        return fail(GS_ERR_INVALID, "%s: tensor %d has count %lld outside [0, 2^37]", who, i, (long long)count);
+    return GS_OK;
+}
+
+gs_status check_grads(const gs_grad_tensor* tensors, int32_t n, int32_t kind, const float* norm, const void* scratch,
+                      bool out, const char* who) {
+    if (gs_status s = check_list(tensors, n, scratch, who)) return s;
+    if (kind != GS_NORM_L2 && kind != GS_NORM_MAX) return fail(GS_ERR_INVALID, "%s: unknown kind %d", who, kind);
+    if (!norm || !aligned(4, norm)) return fail(GS_ERR_INVALID, "%s: norm is NULL or misaligned", who);
+    for (int i = 0; i < n; ++i) {
+        const gs_grad_tensor& t = tensors[i];
+        if (gs_status s = check_count(t.count, i, who)) return s;
+        if (!t.count) continue;
+        const size_t b = type_bytes(t.dtype);
+        if (!b) return fail(GS_ERR_INVALID, "%s: tensor %d has unknown dtype %d", who, i, t.dtype);
+        if (!t.grad || (out && !t.out)) return fail(GS_ERR_INVALID, "%s: tensor %d has a NULL pointer", who, i);
+        if (!aligned(b, t.grad, out ? t.out : nullptr))
+            return fail(GS_ERR_INVALID, "%s: tensor %d is not aligned to its type", who, i);
+    }
+    return GS_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -568,6 +645,120 @@ gs_status gs_composite_bwd_ex(const gs_camera* cam, int32_t n_views, int32_t n, 
                                               (float4*)grad_conic_op, (float4*)grad_rgb, nullptr, chunks,
                                               (uint32_t)capacity, (const float4*)ckpt, image, (hipStream_t)stream),
                      "composite bwd launch");
+}
+
+size_t gs_recurrence_scratch_bytes(const gs_recurrence* r) {
+    g_last_error.clear();
+    if (check_recurrence(r, "gs_recurrence_scratch_bytes")) return 0;
+    return gs::recurrence_scratch_bytes(*r);
+}
+
+gs_status gs_recurrence_fwd(const gs_recurrence* r, const void* gate, const void* x, const float* h0, void* h,
+                            float* h_last, float* ckpt, void* scratch, size_t scratch_bytes, void* stream) {
+    g_last_error.clear();
+    if (gs_status s = check_recurrence(r, "gs_recurrence_fwd")) return s;
+    if (r->batch == 0 || r->channels == 0) return GS_OK;
+    if (r->steps > 0 && (!gate || !x || !h)) return fail(GS_ERR_INVALID, "gs_recurrence_fwd: a required pointer is NULL");
+    if (!aligned(type_bytes(r->dtype), gate, x, h) || !aligned(4, h0, h_last, ckpt))
+        return fail(GS_ERR_INVALID, "gs_recurrence_fwd: a buffer is not aligned to its type");
+    const size_t need = gs::recurrence_scratch_bytes(*r);
+    if (need && (!scratch || scratch_bytes < need))
+        return fail(GS_ERR_INVALID, "gs_recurrence_fwd: scratch of %zu bytes is smaller than the required %zu",
+                    scratch ? scratch_bytes : (size_t)0, need);
+    if (need && !aligned(8, scratch)) return fail(GS_ERR_INVALID, "gs_recurrence_fwd: scratch is not 8-byte aligned");
+    gs::RecurrenceArgs a = recurrence_args(*r);
+    a.gate = gate;
+    a.x = x;
+    a.h0 = h0;
+    a.h = h;
+    a.h_last = h_last;
+    a.ckpt = ckpt;
+    return hip_check(gs::launch_recurrence_fwd(a, r->dtype, r->gating == GS_GATE_SIGMOID, scratch, (hipStream_t)stream),
+                     "gs_recurrence_fwd launch");
+}
+
+gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void* x, const float* h0,
+                            const float* ckpt, const void* grad_h, const float* grad_last, void* grad_gate,
+                            void* grad_x, float* grad_h0, void* scratch, size_t scratch_bytes, void* stream) {
+    g_last_error.clear();
+    if (gs_status s = check_recurrence(r, "gs_recurrence_bwd")) return s;
+    if (r->batch == 0 || r->channels == 0) return GS_OK;
+    if (r->steps > 0 && (!gate || !x || !grad_h || !grad_gate || !grad_x))
+        return fail(GS_ERR_INVALID, "gs_recurrence_bwd: a required pointer is NULL");
+    if (r->steps > GS_RECURRENCE_CHUNK && !ckpt)
+        return fail(GS_ERR_INVALID, "gs_recurrence_bwd: ckpt is NULL with more than %d steps", GS_RECURRENCE_CHUNK);
+    if (!aligned(type_bytes(r->dtype), gate, x, grad_h, grad_gate, grad_x) ||
+        !aligned(4, h0, ckpt, grad_last, grad_h0))
+        return fail(GS_ERR_INVALID, "gs_recurrence_bwd: a buffer is not aligned to its type");
+    const size_t need = gs::recurrence_scratch_bytes(*r);
+    if (need && (!scratch || scratch_bytes < need))
+        return fail(GS_ERR_INVALID, "gs_recurrence_bwd: scratch of %zu bytes is smaller than the required %zu",
+                    scratch ? scratch_bytes : (size_t)0, need);
+    if (need && !aligned(8, scratch)) return fail(GS_ERR_INVALID, "gs_recurrence_bwd: scratch is not 8-byte aligned");
+    gs::RecurrenceArgs a = recurrence_args(*r);
+    a.gate = gate;
+    a.x = x;
+    a.h0 = h0;
+    a.ckpt_in = ckpt;
+    a.grad_h = grad_h;
+    a.grad_last = grad_last;
+    a.grad_gate = grad_gate;
+    a.grad_x = grad_x;
+    a.grad_h0 = grad_h0;
+    return hip_check(gs::launch_recurrence_bwd(a, r->dtype, r->gating == GS_GATE_SIGMOID, scratch, (hipStream_t)stream),
+                     "gs_recurrence_bwd launch");
+}
+
+size_t gs_grad_scratch_bytes(void) { return gs::optim_scratch_bytes(); }
+
+gs_status gs_grad_norm(const gs_grad_tensor* tensors, int32_t n_tensors, int32_t kind, float* norm, void* scratch,
+                       void* stream) {
+    g_last_error.clear();
+    if (gs_status s = check_grads(tensors, n_tensors, kind, norm, scratch, false, "gs_grad_norm")) return s;
+    return hip_check(gs::launch_grad_norm(tensors, n_tensors, kind, norm, scratch, (hipStream_t)stream),
+                     "gs_grad_norm launch");
+}
+
+gs_status gs_clip_grads(const gs_grad_tensor* tensors, int32_t n_tensors, int32_t kind, float max_norm, float* norm,
+                        void* scratch, void* stream) {
+    g_last_error.clear();
+    if (gs_status s = check_grads(tensors, n_tensors, kind, norm, scratch, true, "gs_clip_grads")) return s;
+    if (!(max_norm > 0.0f) || !std::isfinite(max_norm))
+        return fail(GS_ERR_INVALID, "gs_clip_grads: max_norm %g is not positive and finite", max_norm);
+    return hip_check(gs::launch_clip_grads(tensors, n_tensors, kind, max_norm, norm, scratch, (hipStream_t)stream),
+                     "gs_clip_grads launch");
+}
+
+gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_t n_tensors, int64_t* step,
+                       float* norm, void* scratch, void* stream) {
+    g_last_error.clear();
+    if (!cfg) return fail(GS_ERR_INVALID, "gs_adam_step: cfg is NULL");
+    if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0))
+        return fail(GS_ERR_INVALID, "gs_adam_step: beta1 %g or beta2 %g outside [0, 1)", cfg->beta1, cfg->beta2);
+    if (!(cfg->eps > 0.0) || !std::isfinite(cfg->eps))
+        return fail(GS_ERR_INVALID, "gs_adam_step: eps %g is not positive and finite", cfg->eps);
+    if (!(cfg->max_norm >= 0.0f) || !std::isfinite(cfg->max_norm))
+        return fail(GS_ERR_INVALID, "gs_adam_step: max_norm %g is negative or not finite", cfg->max_norm);
+    if (cfg->flags & ~(uint32_t)GS_ADAM_SKIP_NONFINITE)
+        return fail(GS_ERR_INVALID, "gs_adam_step: unknown flags 0x%x", cfg->flags);
+    if (gs_status s = check_list(tensors, n_tensors, scratch, "gs_adam_step")) return s;
+    if (!step || !aligned(8, step)) return fail(GS_ERR_INVALID, "gs_adam_step: step is NULL or misaligned");
+    if (!aligned(4, norm)) return fail(GS_ERR_INVALID, "gs_adam_step: norm is misaligned");
+    for (int i = 0; i < n_tensors; ++i) {
+        const gs_adam_tensor& t = tensors[i];
+        if (gs_status s = check_count(t.count, i, "gs_adam_step")) return s;
+        if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
+            return fail(GS_ERR_INVALID, "gs_adam_step: tensor %d has a rate or decay that is not finite", i);
+        if (!t.count) continue;
+        const size_t pb = type_bytes(t.param_dtype), gb = type_bytes(t.grad_dtype);
+        if (!pb || !gb) return fail(GS_ERR_INVALID, "gs_adam_step: tensor %d has an unknown dtype", i);
+        if (!t.param || !t.grad || !t.m || !t.v)
+            return fail(GS_ERR_INVALID, "gs_adam_step: tensor %d has a NULL pointer", i);
+        if (!aligned(pb, t.param) || !aligned(gb, t.grad) || !aligned(4, t.m, t.v))
+            return fail(GS_ERR_INVALID, "gs_adam_step: tensor %d is not aligned to its type", i);
+    }
+    return hip_check(gs::launch_adam_step(*cfg, tensors, n_tensors, step, norm, scratch, (hipStream_t)stream),
+                     "gs_adam_step launch");
 }
 
 }  // extern "C"

@@ -216,4 +216,39 @@ hipError_t launch_appearance_bwd(const gs_camera& cam, int n, const float* means
                                  int H, const float* weights, const float* grad_rgb, float* grad_latent,
                                  float* grad_weights, float* partials, hipStream_t stream);
 
+// Gated linear recurrence: the arguments of one call, by value to its
+// kernels. Outputs (and the inputs of the other direction) that a call does
+// not have are NULL.
+struct RecurrenceArgs {
+    const void *gate, *x;
+    int64_t gate_batch, gate_step, x_batch, x_step;
+    const int32_t* lengths;
+    const uint8_t* restart;
+    int batch, steps, channels;
+    const float* h0;
+    void* h;         // forward: states
+    float* h_last;
+    float* ckpt;     // [batch][ceil(steps / 128) - 1][channels]
+    const float* ckpt_in;  // backward
+    const void* grad_h;
+    const float* grad_last;
+    void *grad_gate, *grad_x;
+    float* grad_h0;
+};
+// Whether the work items of one call (64 channels of 128 steps) can be counted in 31 bits.
+bool recurrence_fits(const gs_recurrence& r);
+size_t recurrence_scratch_bytes(const gs_recurrence& r);
+hipError_t launch_recurrence_fwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream);
+hipError_t launch_recurrence_bwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream);
+
+// Global gradient norm, clipping and the Adam update. The host arrays of
+// tensor descriptions are read during the call.
+size_t optim_scratch_bytes();
+hipError_t launch_grad_norm(const gs_grad_tensor* tensors, int n, int kind, float* norm, void* scratch,
+                            hipStream_t stream);
+hipError_t launch_clip_grads(const gs_grad_tensor* tensors, int n, int kind, float max_norm, float* norm,
+                             void* scratch, hipStream_t stream);
+hipError_t launch_adam_step(const gs_adam& cfg, const gs_adam_tensor* tensors, int n, int64_t* step, float* norm,
+                            void* scratch, hipStream_t stream);
+
 }  // namespace gs

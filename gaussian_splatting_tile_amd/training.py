@@ -1,0 +1,250 @@
+"""Binding of the sequence and training calls of libgs: the gated linear
+recurrence (gs_recurrence_fwd / gs_recurrence_bwd), the global gradient norm
+and clipping (gs_grad_norm, gs_clip_grads) and the Adam update with that
+clipping (gs_adam_step). As in rasterizer.py, torch supplies device memory
+and the current HIP stream; the work is libgs's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import GS_ADAM_SKIP_NONFINITE, GS_GATE_LINEAR, GS_GATE_SIGMOID, GS_NORM_L2, GS_NORM_MAX
+from .rasterizer import _ptr, _stream
+
+GATE_LINEAR, GATE_SIGMOID = GS_GATE_LINEAR, GS_GATE_SIGMOID
+NORM_L2, NORM_MAX = GS_NORM_L2, GS_NORM_MAX
+_TYPES = {torch.float32: _lib.GS_F32, torch.bfloat16: _lib.GS_BF16, torch.float16: _lib.GS_F16}
+
+
+def _dtype(t, name):
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return code
+
+
+def _shaped(t, shape, dtype, name):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    return _ptr(t, dtype, name)
+
+
+def _strided(t, name):
+    """Pointer and (batch, step) strides of a [B, T, D] tensor whose channels are contiguous."""
+    if t.device.type != "cuda":
+        raise TypeError(f"{name} must be a device tensor")
+    sb, st, sd = t.stride()
+    if sd != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have contiguous channels (last stride 1)")
+    return ctypes.c_void_p(t.data_ptr()), sb, st
+
+
+def _recurrence(gate, x, gating, lengths, restart):
+    """The C description of a call and the pointers of gate and x."""
+    if gate.dim() != 3 or gate.shape != x.shape or gate.dtype != x.dtype or gate.device != x.device:
+        raise ValueError("gate and x must be [B, T, D] of the same shape, type and device")
+    B, T, D = gate.shape
+    r = _lib.GsRecurrence()
+    r.dtype, r.gating = _dtype(gate, "gate"), int(gating)
+    r.batch, r.steps, r.channels = B, T, D
+    pg, r.gate_batch, r.gate_step = _strided(gate, "gate")
+    px, r.x_batch, r.x_step = _strided(x, "x")
+    r.lengths = _shaped(lengths, (B,), torch.int32, "lengths")
+    r.restart = _shaped(restart, (B, T), torch.uint8, "restart")
+    return r, pg, px
+
+
+def _scratch(lib, r, scratch, device):
+    if r.steps <= _lib.GS_RECURRENCE_CHUNK:
+        return None, 0
+    need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
+    if need == 0:
+        return None, 0
+    if scratch is None:
+        scratch = torch.empty((need,), dtype=torch.uint8, device=device)
+    return scratch, scratch.numel() * scratch.element_size()
+
+
+def recurrence_scratch_bytes(batch: int, steps: int, channels: int) -> int:
+    """Bytes of the workspace recurrence_fwd and recurrence_bwd take for this shape."""
+    r = _lib.GsRecurrence()
+    r.batch, r.steps, r.channels = int(batch), int(steps), int(channels)
+    return int(_lib.load().gs_recurrence_scratch_bytes(ctypes.byref(r)))
+
+
+def recurrence_ckpt_rows(steps: int) -> int:
+    """Checkpoint rows of a sequence: the states in front of steps 128, 256, ... below `steps`."""
+    return max(0, -(-int(steps) // _lib.GS_RECURRENCE_CHUNK) - 1)
+
+
+def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=None, checkpoints=False, out=None,
+                   scratch=None, stream=None):
+    """gs_recurrence_fwd: h_t = a_t h_{t-1} + u_t along dim 1 of gate and x ([B, T, D], float32,
+    bfloat16 or float16; any batch and step strides, contiguous channels). gating: GATE_LINEAR
+    (a = gate, u = x) or GATE_SIGMOID (a = sigmoid(gate), u = (1 - a) x). h0 float32 [B, D];
+    lengths int32 [B]; restart uint8 [B, T]. Returns dict h [B, T, D], h_last float32 [B, D] and
+    ckpt (float32 [B, recurrence_ckpt_rows(T), D] with checkpoints, for recurrence_bwd; else
+    None). `out` may give any of them; out["h_last"] may be h0 itself (one state buffer for
+    step-by-step serving, T = 1)."""
+    lib = _lib.load()
+    r, pg, px = _recurrence(gate, x, gating, lengths, restart)
+    B, T, D = gate.shape
+    dev, f32 = gate.device, torch.float32
+    given = out or {}
+    h, h_last, ckpt = given.get("h"), given.get("h_last"), given.get("ckpt")
+    if h is None:
+        h = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
+    if h_last is None:
+        h_last = torch.empty((B, D), dtype=f32, device=dev)
+    if ckpt is None and checkpoints:
+        ckpt = torch.empty((B, recurrence_ckpt_rows(T), D), dtype=f32, device=dev)
+    scratch, nbytes = _scratch(lib, r, scratch, dev)
+    _lib.check(lib.gs_recurrence_fwd(
+        ctypes.byref(r), pg, px, _shaped(h0, (B, D), f32, "h0"), _shaped(h, (B, T, D), gate.dtype, "h"),
+        _shaped(h_last, (B, D), f32, "h_last"), _shaped(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
+        _ptr(scratch), nbytes, _stream(stream)))
+    return dict(h=h, h_last=h_last, ckpt=ckpt)
+
+
+def recurrence_bwd(gate, x, grad_h, h0=None, ckpt=None, grad_last=None, gating=GATE_LINEAR, lengths=None,
+                   restart=None, out=None, scratch=None, stream=None):
+    """gs_recurrence_bwd: gradients of recurrence_fwd, which gave `ckpt` (needed when T > 128).
+    grad_h [B, T, D] of gate's type; grad_last float32 [B, D] or None. Returns dict grad_gate,
+    grad_x [B, T, D], grad_h0 float32 [B, D]."""
+    lib = _lib.load()
+    r, pg, px = _recurrence(gate, x, gating, lengths, restart)
+    B, T, D = gate.shape
+    dev, f32, t = gate.device, torch.float32, gate.dtype
+    if out is None:
+        out = dict(grad_gate=torch.empty((B, T, D), dtype=t, device=dev),
+                   grad_x=torch.empty((B, T, D), dtype=t, device=dev),
+                   grad_h0=torch.empty((B, D), dtype=f32, device=dev))
+    scratch, nbytes = _scratch(lib, r, scratch, dev)
+    _lib.check(lib.gs_recurrence_bwd(
+        ctypes.byref(r), pg, px, _shaped(h0, (B, D), f32, "h0"),
+        _shaped(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), _shaped(grad_h, (B, T, D), t, "grad_h"),
+        _shaped(grad_last, (B, D), f32, "grad_last"), _shaped(out["grad_gate"], (B, T, D), t, "grad_gate"),
+        _shaped(out["grad_x"], (B, T, D), t, "grad_x"), _shaped(out.get("grad_h0"), (B, D), f32, "grad_h0"),
+        _ptr(scratch), nbytes, _stream(stream)))
+    return out
+
+
+def _device_of(tensors, name):
+    if not tensors:
+        raise ValueError(f"{name}: the list is empty")
+    dev = tensors[0].device
+    if dev.type != "cuda" or any(t.device != dev for t in tensors):
+        raise TypeError(f"{name} must be tensors of one device")
+    return dev
+
+
+class GradList:
+    """A list of gradients (float32, bfloat16 or float16, each contiguous, types mixed as
+    wanted) whose global norm is taken and clipped. Holds the tensors, their description for
+    the C call and the workspace, so a step's call only launches. Clipping writes to `out`
+    (default: in place)."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        self.device = _device_of(self.grads, "grads")
+        if len(self.out) != len(self.grads):
+            raise ValueError("out must hold one tensor for each gradient")
+        self._n = len(self.grads)
+        self._list = (_lib.GsGradTensor * self._n)()
+        for d, g, o in zip(self._list, self.grads, self.out):
+            if o.shape != g.shape:
+                raise ValueError("out must have the shapes of grads")
+            d.grad, d.out = _ptr(g, None, "grad"), _ptr(o, g.dtype, "out")
+            d.count, d.dtype = g.numel(), _dtype(g, "grad")
+        self._lib = _lib.load()
+        self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=self.device)
+        self._pscratch = _ptr(self.scratch)
+
+    def norm(self, kind=NORM_L2, out=None, stream=None):
+        """gs_grad_norm: the global norm, a float32 tensor of no dimensions on the device."""
+        if out is None:
+            out = torch.empty((), dtype=torch.float32, device=self.device)
+        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), _shaped(out, (), torch.float32, "out"),
+                                          self._pscratch, _stream(stream)))
+        return out
+
+    def clip(self, max_norm, kind=NORM_L2, out=None, stream=None):
+        """gs_clip_grads: scales by min(1, max_norm / (norm + 1e-6)); returns the norm before."""
+        if out is None:
+            out = torch.empty((), dtype=torch.float32, device=self.device)
+        _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm),
+                                           _shaped(out, (), torch.float32, "out"), self._pscratch, _stream(stream)))
+        return out
+
+
+def grad_norm(grads, kind=NORM_L2, stream=None):
+    """The global norm of a list of gradients (GradList(grads).norm())."""
+    return GradList(grads).norm(kind, stream=stream)
+
+
+def clip_grads(grads, max_norm, kind=NORM_L2, out=None, stream=None):
+    """Clips a list of gradients by their global norm, in place or into `out`; returns the norm."""
+    return GradList(grads, out).clip(max_norm, kind, stream=stream)
+
+
+class Adam:
+    """gs_adam_step over a fixed list of parameters and gradient buffers: Adam with decoupled
+    weight decay, the gradients clipped on the way by their global norm (max_norm > 0). lr and
+    weight_decay are numbers or one number per tensor (`set_lr` changes them); the moments
+    (exp_avg, exp_avg_sq, float32) start at 0 and the device step counter at `step` unless
+    given. With skip_nonfinite a step whose gradients hold an infinity or a NaN changes
+    nothing."""
+
+    def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, max_norm=0.0,
+                 skip_nonfinite=False, exp_avg=None, exp_avg_sq=None, step=0):
+        self.params, self.grads = list(params), list(grads)
+        self.device = dev = _device_of(self.params + self.grads, "params and grads")
+        n = self._n = len(self.params)
+        if len(self.grads) != n:
+            raise ValueError("params and grads must be lists of one length")
+        f32 = torch.float32
+        zeros = lambda: [torch.zeros(p.shape, dtype=f32, device=dev) for p in self.params]
+        self.exp_avg = zeros() if exp_avg is None else list(exp_avg)
+        self.exp_avg_sq = zeros() if exp_avg_sq is None else list(exp_avg_sq)
+        if len(self.exp_avg) != n or len(self.exp_avg_sq) != n:
+            raise ValueError("exp_avg and exp_avg_sq must hold one tensor for each parameter")
+        self.steps = torch.full((1,), int(step), dtype=torch.int64, device=dev)
+        self.norm = torch.zeros((), dtype=f32, device=dev)
+        self._cfg = _lib.GsAdam(float(betas[0]), float(betas[1]), float(eps), float(max_norm),
+                                GS_ADAM_SKIP_NONFINITE if skip_nonfinite else 0)
+        self._want_norm = max_norm > 0 or skip_nonfinite
+        self._list = (_lib.GsAdamTensor * n)()
+        for d, p, g, m, v in zip(self._list, self.params, self.grads, self.exp_avg, self.exp_avg_sq):
+            if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
+                raise ValueError("a gradient or moment does not have its parameter's shape")
+            d.param, d.grad = _ptr(p, None, "param"), _ptr(g, None, "grad")
+            d.m, d.v = _ptr(m, f32, "exp_avg"), _ptr(v, f32, "exp_avg_sq")
+            d.count, d.param_dtype, d.grad_dtype = p.numel(), _dtype(p, "param"), _dtype(g, "grad")
+        self.set_lr(lr)
+        for d, wd in zip(self._list, self._each(weight_decay, "weight_decay")):
+            d.weight_decay = wd
+        self._lib = _lib.load()
+        self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=dev)
+        self._fixed = (ctypes.byref(self._cfg), self._list, n, _ptr(self.steps),
+                       _ptr(self.norm) if self._want_norm else None, _ptr(self.scratch))
+
+    def _each(self, v, name):
+        v = [float(v)] * self._n if isinstance(v, (int, float)) else [float(x) for x in v]
+        if len(v) != self._n:
+            raise ValueError(f"{name} must be a number or one number for each parameter")
+        return v
+
+    def set_lr(self, lr):
+        """The learning rate (or one for each tensor) of the steps that follow."""
+        for d, v in zip(self._list, self._each(lr, "lr")):
+            d.lr = v
+
+    def step(self, stream=None):
+        """One update. Returns the gradients' global norm before clipping (a device tensor that
+        the next step overwrites), or None when nothing asks for it."""
+        _lib.check(self._lib.gs_adam_step(*self._fixed, _stream(stream)))
+        return self.norm if self._want_norm else None

@@ -586,6 +586,173 @@ gs_status gs_appearance_bwd(const gs_camera* cam, int32_t n, const float* means,
                             float* grad_latent, float* grad_weights, void* scratch, size_t* scratch_bytes,
                             void* stream);
 
+/* Element types of the tensors of the sequence and training calls below.
+ * Sums, states, norms and moments are float32 or wider whatever the type. */
+#define GS_F32 0
+#define GS_BF16 1
+#define GS_F16 2
+
+/* ---------------------------------------------------------------------
+ * Gated linear recurrence over the steps of B independent sequences of D
+ * channels each, for states that live through the frames of a clip (an
+ * appearance latent per frame: the [L][n] latents of n Gaussians are the
+ * D = L n channels of one step) or the tokens of a text.
+ *
+ *   h_t = a_t h_{t-1} + u_t            t = 0 .. len_b - 1, h_{-1} = h0
+ *   GS_GATE_LINEAR   a_t = gate_t,             u_t = x_t
+ *   GS_GATE_SIGMOID  a_t = sigmoid(gate_t),    u_t = (1 - a_t) x_t
+ *
+ * At a step with restart set the previous state is dropped (h_t = u_t), as
+ * at the first token of the next document of a packed sequence. Steps at or
+ * behind len_b are padding: gate, x and the upstream gradient are not read
+ * there and h and the gradients are 0.
+ *
+ *   dtype       GS_F32, GS_BF16 or GS_F16: gate, x, h and their gradients
+ *   gating      GS_GATE_LINEAR or GS_GATE_SIGMOID
+ *   batch, steps, channels  B, T, D >= 0; each at most 2^30, and
+ *               B ceil(D / 64) ceil(T / 128) < 2^31
+ *   gate_batch, gate_step, x_batch, x_step  strides of gate and x in
+ *               elements, >= 0; channels are contiguous. 0 repeats a value
+ *               along that axis (its gradient is still written in full).
+ *   lengths     [B] int32, or NULL (every length is T); values outside
+ *               [0, T] are clamped to it
+ *   restart     [B][T] uint8, or NULL
+ * All other arrays are contiguous, [B][T][D] or [B][D]. Products of gates
+ * over GS_RECURRENCE_CHUNK steps are formed in float32; gates above 1 whose
+ * product overflows there give a state that is not finite.
+ * ------------------------------------------------------------------- */
+#define GS_GATE_LINEAR 0
+#define GS_GATE_SIGMOID 1
+#define GS_RECURRENCE_CHUNK 128
+typedef struct {
+    int32_t dtype, gating;
+    int32_t batch, steps, channels;
+    int64_t gate_batch, gate_step, x_batch, x_step;
+    const int32_t* lengths;
+    const uint8_t* restart;
+} gs_recurrence;
+
+/* gs_recurrence_scratch_bytes - workspace of gs_recurrence_fwd and
+ * gs_recurrence_bwd for this shape (8-byte aligned; 0 when none is needed,
+ * as for sequences of at most GS_RECURRENCE_CHUNK steps, and for invalid
+ * arguments). It needs no clearing. Calls that share one workspace must not
+ * overlap. */
+size_t gs_recurrence_scratch_bytes(const gs_recurrence* r);
+
+/* gs_recurrence_fwd - the states of every step.
+ *   gate, x     as described above
+ *   h0          [B][D] float32, or NULL (zero)
+ *   h           out [B][T][D], each state rounded once to dtype
+ *   h_last      out [B][D] float32, or NULL: the state behind the last step
+ *               (h0 for a sequence of length 0). May be h0 itself: a serving
+ *               loop calls this with T = 1 and keeps one state buffer.
+ *   ckpt        out [B][ceil(T / 128) - 1][D] float32, or NULL: row k is the
+ *               state in front of step 128 (k + 1), for gs_recurrence_bwd;
+ *               rows at or behind the length are not written. Not needed
+ *               (and may be NULL for both calls) when T <= 128.
+ *   scratch, scratch_bytes  workspace and its size
+ * Results do not depend on timing: two calls on the same inputs give the
+ * same bits. */
+gs_status gs_recurrence_fwd(const gs_recurrence* r, const void* gate, const void* x, const float* h0, void* h,
+                            float* h_last, float* ckpt, void* scratch, size_t scratch_bytes, void* stream);
+
+/* gs_recurrence_bwd - gradients of gs_recurrence_fwd. With d_t = dL/dh_t
+ * including what later steps pass back, d_t = grad_h_t + [t = len - 1]
+ * grad_last + a_{t+1} d_{t+1} (the last term 0 where step t + 1 restarts):
+ *   LINEAR   grad_gate = d_t h_{t-1}                     grad_x = d_t
+ *   SIGMOID  grad_gate = d_t (h_{t-1} - x_t) a_t (1 - a_t), grad_x = (1 - a_t) d_t
+ * with h_{t-1} = 0 at a restart; grad_h0 = a_0 d_0 (0 if step 0 restarts,
+ * grad_last for a sequence of length 0). The states are recomputed in
+ * float32 from the checkpoints: h is not read.
+ *   gate, x, h0, ckpt  as given to and written by gs_recurrence_fwd
+ *   grad_h      [B][T][D]
+ *   grad_last   [B][D] float32, or NULL (zero)
+ *   grad_gate, grad_x  out [B][T][D]
+ *   grad_h0     out [B][D] float32, or NULL
+ * Outputs must not overlap inputs. */
+gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void* x, const float* h0,
+                            const float* ckpt, const void* grad_h, const float* grad_last, void* grad_gate,
+                            void* grad_x, float* grad_h0, void* scratch, size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Global gradient norm over a list of tensors, and clipping by it.
+ *
+ *   norm = sqrt(sum over every element of every tensor of g^2)  GS_NORM_L2
+ *   norm = max |g|                                              GS_NORM_MAX
+ *   out  = min(1, max_norm / (norm + 1e-6)) g                   gs_clip_grads
+ *
+ * The squares are summed in float64, in an order that depends on the sizes
+ * only: no finite gradient overflows and two calls give the same bits.
+ * A NaN anywhere gives norm = NaN and, clipped, NaN everywhere; an infinity
+ * gives norm = inf and the factor 0.
+ *
+ *   tensors   (host) array of n_tensors descriptions, read during the call;
+ *             grad and out are device pointers aligned to their type, out may
+ *             be grad itself (and is not read by gs_grad_norm); tensors of
+ *             count 0 are allowed and their pointers not looked at; at most
+ *             GS_MAX_TENSORS of at most GS_MAX_TENSOR_COUNT elements
+ *   kind      GS_NORM_L2 or GS_NORM_MAX
+ *   max_norm  > 0 and finite
+ *   norm      out [1] float32 (device)
+ *   scratch   workspace of gs_grad_scratch_bytes() bytes, 8-byte aligned; no
+ *             clearing needed, not shared by overlapping calls
+ * ------------------------------------------------------------------- */
+#define GS_NORM_L2 0
+#define GS_NORM_MAX 1
+#define GS_MAX_TENSORS 16384
+#define GS_MAX_TENSOR_COUNT ((int64_t)1 << 37)
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t count;
+    int32_t dtype;
+} gs_grad_tensor;
+size_t gs_grad_scratch_bytes(void);
+gs_status gs_grad_norm(const gs_grad_tensor* tensors, int32_t n_tensors, int32_t kind, float* norm, void* scratch,
+                       void* stream);
+gs_status gs_clip_grads(const gs_grad_tensor* tensors, int32_t n_tensors, int32_t kind, float max_norm, float* norm,
+                        void* scratch, void* stream);
+
+/* ---------------------------------------------------------------------
+ * gs_adam_step - one Adam update of a list of tensors, with decoupled
+ * weight decay, the gradients clipped by their global L2 norm on the way
+ * (they are read, not changed). With t = *step + 1 and
+ * c = min(1, max_norm / (norm + 1e-6)), or 1 when max_norm is 0:
+ *   g = c grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   param = (1 - lr weight_decay) param
+ *           - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * computed in float32, param rounded once to its type.
+ *
+ *   cfg       (host) 0 <= beta1, beta2 < 1; eps > 0; max_norm >= 0, finite;
+ *             flags: GS_ADAM_SKIP_NONFINITE leaves params, moments and step
+ *             as they are when the norm of the gradients is not finite
+ *   tensors   (host) array of n_tensors descriptions, read during the call:
+ *             param (param_dtype) and grad (grad_dtype), each GS_F32, GS_BF16
+ *             or GS_F16; m, v float32; lr and weight_decay of this tensor
+ *   step      device int64: the updates taken so far; the call adds 1 (it is
+ *             on the device so that a recorded graph counts its replays)
+ *   norm      out [1] float32 (device): the global norm before clipping, or
+ *             NULL. It is formed only if norm, max_norm or the flag asks.
+ *   scratch   as for gs_clip_grads
+ * ------------------------------------------------------------------- */
+#define GS_ADAM_SKIP_NONFINITE 1u
+typedef struct {
+    double beta1, beta2, eps;
+    float max_norm;
+    uint32_t flags;
+} gs_adam;
+typedef struct {
+    void* param;
+    const void* grad;
+    float* m;
+    float* v;
+    int64_t count;
+    int32_t param_dtype, grad_dtype;
+    float lr, weight_decay;
+} gs_adam_tensor;
+gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_t n_tensors, int64_t* step,
+                       float* norm, void* scratch, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
