@@ -372,3 +372,5 @@ def test_recurrence_refuses():
         gs.recurrence_fwd(x, x, gating=2)
     with pytest.raises(gs.GsError):
         gs.recurrence_bwd(x, x, x)  # 200 steps need the checkpoints
+    with pytest.raises(gs.GsError):  # 200 steps need a workspace of some size
+        gs.recurrence_fwd(x, x, scratch=torch.empty((8,), dtype=torch.uint8, device="cuda"))

@@ -60,6 +60,18 @@ def test_recurrence_scratch_size(gs):
     assert size(steps=128) == 0 and size(steps=0) == 0 and size(batch=0, steps=1000) == 0
     assert size(dtype=9, steps=1000) == 0 and size(steps=-1) == 0
     assert gs.gs_recurrence_scratch_bytes(None) == 0
+    # a word per chunk and channel, a state per 16 chunks and channel, a counter per 64 channels
+    assert size(batch=3, steps=129, channels=65) == 3 * (2 * 65 * 8 + 65 * 4 + 2 * 4)
+    assert size(batch=1, steps=128 * 17, channels=64) == 17 * 64 * 8 + 2 * 64 * 4 + 4
+    from gaussian_splatting_tile_amd import _lib
+    r = _rec(steps=129, gate_batch=0, x_batch=0)
+    need = gs.gs_recurrence_scratch_bytes(ctypes.byref(r))
+    for scratch, n, word in ((None, need, b"smaller"), (D, need - 1, b"smaller"), (P(260), need, b"aligned")):
+        assert gs.gs_recurrence_fwd(ctypes.byref(r), D, D, None, D, None, None, scratch, n, None) == _lib.GS_ERR_INVALID
+        assert word in gs.gs_last_error()
+        assert gs.gs_recurrence_bwd(ctypes.byref(r), D, D, None, D, D, None, D, D, None, scratch, n,
+                                    None) == _lib.GS_ERR_INVALID
+        assert word in gs.gs_last_error()
 
 
 def test_recurrence_checkpoint_rows():
