@@ -107,7 +107,7 @@ gs_status check_list(const void* tensors, int32_t n, const void* scratch, const 
 
 gs_status check_count(int64_t count, int i, const char* who) {
     if (count < 0 || count > GS_MAX_TENSOR_COUNT)
-        return fail(GS_ERR_INVALID, "%s: tensor %d has count %lld outside [0, 2^36]", who, i, (long long)count);
+        return fail(GS_ERR_INVALID, "%s: tensor %d has count %lld outside [0, 2^35]", who, i, (long long)count);
     return GS_OK;
 }
 

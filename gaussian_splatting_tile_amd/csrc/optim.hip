@@ -25,11 +25,16 @@ namespace gs {
 namespace {
 
 constexpr int kOptThreads = 256;     // threads that share a tile
-constexpr int kOptTile = 16384;      // bytes (of the float32 moments in an update)
+constexpr int kNormTile = 16384;     // bytes
+constexpr int kClipTile = 16384;
+constexpr int kAdamTile = 8192;      // bytes of the float32 moments
 constexpr int kNormThreads = 1024;   // first pass: four tiles at once, one partial
 constexpr int kNormBlocks = 512;     // of a launch: two to a compute unit
 constexpr int kOptSlots = 2048;      // partial sums of all launches of a call
-constexpr int kOptBlocks = 2048;     // workgroups of a second-pass launch
+// Workgroups of a second-pass launch: one for each tile up to a bound that
+// only keeps the grid within limits. Fewer that take several tiles each were
+// slower (an update of 59M float32 parameters: 320 us with 2048, 298 us).
+constexpr int kOptBlocks = 1 << 22;
 constexpr int kSmallThreads = 1024;  // small lists: a wave shares a tile
 constexpr int kSmallTile = 2048;
 constexpr int64_t kSmall = 32768;
@@ -56,48 +61,48 @@ struct OptTable {
 // is not used again soon and is kept from pushing the gradients out of the
 // cache between the two passes (an update of 59M float32 parameters: 373 us
 // without, 353 us with; on the gradients themselves it costs 13%).
+template <typename T, int U>
+struct Access {
+    typedef T Vec __attribute__((ext_vector_type(U), aligned(sizeof(T))));
+};
 template <bool WHOLE, bool STREAM, typename T, int U>
 __device__ __forceinline__ void load_n(const T* p, int64_t e, int64_t count, float (&v)[U]) {
-    if (WHOLE) {
-        typedef T Vec __attribute__((ext_vector_type(U), aligned(sizeof(T))));
+    using Vec = typename Access<T, U>::Vec;
+    Vec r = {};
+    if (WHOLE || (e >= 0 && e + U <= count)) {
         const Vec* const at = (const Vec*)(p + e);
-        const Vec r = STREAM ? __builtin_nontemporal_load(at) : *at;
+        r = STREAM ? __builtin_nontemporal_load(at) : *at;
+    } else if (e + U > 0 && e < count) {  // one lane at either end of a tensor
 #pragma unroll
-        for (int j = 0; j < U; ++j) v[j] = (float)r[j];
-    } else {  // no branches: all loads of a thread are in flight at once
-        float r[U];
-#pragma unroll
-        for (int j = 0; j < U; ++j) r[j] = (float)p[max((int64_t)0, min(e + j, count - 1))];
-#pragma unroll
-        for (int j = 0; j < U; ++j) v[j] = e + j >= 0 && e + j < count ? r[j] : 0.0f;
+        for (int j = 0; j < U; ++j)
+            if (e + j >= 0 && e + j < count) r[j] = p[e + j];
     }
+#pragma unroll
+    for (int j = 0; j < U; ++j) v[j] = (float)r[j];
 }
 template <bool WHOLE, typename T, int U>
 __device__ __forceinline__ void store_n(T* p, int64_t e, int64_t count, const float (&v)[U]) {
-    if (WHOLE) {
-        typedef T Vec __attribute__((ext_vector_type(U), aligned(sizeof(T))));
+    using Vec = typename Access<T, U>::Vec;
+    if (WHOLE || (e >= 0 && e + U <= count)) {
         Vec r;
 #pragma unroll
         for (int j = 0; j < U; ++j) r[j] = (T)v[j];
         __builtin_nontemporal_store(r, (Vec*)(p + e));
-    } else {
+    } else if (e + U > 0 && e < count) {
 #pragma unroll
         for (int j = 0; j < U; ++j)
             if (e + j >= 0 && e + j < count) p[e + j] = (T)v[j];
     }
 }
 
-// Calls f(whole, N) for a tile of `count` elements of a tensor, N accesses a
-// thread: all at once (all loads of the thread in flight together) if the
-// tile lies inside the tensor, else one after another (few tiles do not).
-template <int N, typename F>
+// Calls f(whole): whether `elements` from e0 on lie inside their tensor. The
+// common case then has no branch between the loads of a thread.
+template <typename F>
 __device__ __forceinline__ void by_extent(int64_t e0, int elements, int64_t count, F f) {
-    if (e0 >= 0 && e0 + elements <= count) {
-        f(std::true_type(), std::integral_constant<int, N>(), 0);
-    } else {
-#pragma unroll 1
-        for (int k = 0; k < N; ++k) f(std::false_type(), std::integral_constant<int, 1>(), k);
-    }
+    if (e0 >= 0 && e0 + elements <= count)
+        f(std::true_type());
+    else
+        f(std::false_type());
 }
 
 // Calls f with a value of the element type.
@@ -223,14 +228,13 @@ __device__ __forceinline__ int type2_of(const D& d) {
 // start and may be negative), by THREADS threads of which this is number i.
 template <int THREADS, int TILE, typename T>
 __device__ __forceinline__ double norm_tile(const T* g, int64_t e0, int64_t count, int kind, int i, double v) {
-    constexpr int U = kUnit<T>;
-    by_extent<TILE / (THREADS * 16)>(e0, TILE / (int)sizeof(T), count, [&](auto whole, auto n, int from) {
-        float x[n.value][U];
+    constexpr int U = kUnit<T>, N = TILE / (THREADS * 16);
+    by_extent(e0, TILE / (int)sizeof(T), count, [&](auto whole) {
+        float x[N][U];
 #pragma unroll
-        for (int k = 0; k < n.value; ++k)
-            load_n<whole.value, false>(g, e0 + ((from + k) * THREADS + i) * U, count, x[k]);
+        for (int k = 0; k < N; ++k) load_n<whole.value, false>(g, e0 + (k * THREADS + i) * U, count, x[k]);
 #pragma unroll
-        for (int k = 0; k < n.value; ++k)
+        for (int k = 0; k < N; ++k)
 #pragma unroll
             for (int j = 0; j < U; ++j) v = take(v, x[k][j], kind);
     });
@@ -239,17 +243,16 @@ __device__ __forceinline__ double norm_tile(const T* g, int64_t e0, int64_t coun
 
 template <int THREADS, int TILE, typename T>
 __device__ __forceinline__ void clip_tile(const T* g, T* out, int64_t e0, int64_t count, float c, int i) {
-    constexpr int U = kUnit<T>;
-    by_extent<TILE / (THREADS * 16)>(e0, TILE / (int)sizeof(T), count, [&](auto whole, auto n, int from) {
-        float x[n.value][U];
+    constexpr int U = kUnit<T>, N = TILE / (THREADS * 16);
+    by_extent(e0, TILE / (int)sizeof(T), count, [&](auto whole) {
+        float x[N][U];
 #pragma unroll
-        for (int k = 0; k < n.value; ++k)
-            load_n<whole.value, false>(g, e0 + ((from + k) * THREADS + i) * U, count, x[k]);
+        for (int k = 0; k < N; ++k) load_n<whole.value, false>(g, e0 + (k * THREADS + i) * U, count, x[k]);
 #pragma unroll
-        for (int k = 0; k < n.value; ++k) {
+        for (int k = 0; k < N; ++k) {
 #pragma unroll
             for (int j = 0; j < U; ++j) x[k][j] *= c;
-            store_n<whole.value>(out, e0 + ((from + k) * THREADS + i) * U, count, x[k]);
+            store_n<whole.value>(out, e0 + (k * THREADS + i) * U, count, x[k]);
         }
     });
 }
@@ -347,16 +350,22 @@ __host__ __device__ inline uint32_t tiles_in(const OptTable<D>& t) {
 
 // Calls f(tensor, first byte from its aligned front) for every `stride`th
 // tile of a table from `begin` on, in ascending order or (BACK) descending.
+// A wave holds the table's ends, one a lane, and finds a tile's tensor by
+// counting those at or below the tile: walking the ends in scalar loads cost
+// more than the tiles for lists of a hundred tensors.
 template <int TILE, bool BACK, typename D, typename F>
 __device__ __forceinline__ void for_tiles(const OptTable<D>& t, uint32_t begin, uint32_t stride, F f) {
+    constexpr int kLoads = (OptTable<D>::kMost + 63) / 64;
+    const int lane = threadIdx.x & 63;
+    uint32_t ends[kLoads];
+#pragma unroll
+    for (int m = 0; m < kLoads; ++m) ends[m] = m * 64 + lane < t.n ? t.ends[m * 64 + lane] : ~0u;
     const uint32_t tiles = tiles_in(t);
-    int k = BACK ? t.n - 1 : 0;
     for (uint32_t i = begin; i < tiles; i += stride) {
         const uint32_t tile = BACK ? tiles - 1 - i : i;
-        if (BACK)
-            while (k && tile < t.ends[k - 1]) --k;
-        else
-            while (tile >= t.ends[k]) ++k;
+        int k = 0;
+#pragma unroll
+        for (int m = 0; m < kLoads; ++m) k += __popcll(__ballot(ends[m] <= tile));
         f(t.tensor[k], (int64_t)(tile - (k ? t.ends[k - 1] : 0)) * TILE);
     }
 }
@@ -370,8 +379,8 @@ __global__ __launch_bounds__(kNormThreads) void k_norm_partial(OptTable<NormTens
     constexpr int kTeams = kNormThreads / kOptThreads;
     const int team = wave_id() / (kOptThreads / 64), i = threadIdx.x % kOptThreads;
     double v = 0.0;
-    for_tiles<kOptTile, false>(t, blockIdx.x * kTeams + team, gridDim.x * kTeams, [&](const NormTensor& d, int64_t at) {
-        v = norm_tile_of<kOptThreads, kOptTile>(d, at, kind, i, v);
+    for_tiles<kNormTile, false>(t, blockIdx.x * kTeams + team, gridDim.x * kTeams, [&](const NormTensor& d, int64_t at) {
+        v = norm_tile_of<kOptThreads, kNormTile>(d, at, kind, i, v);
     });
     v = block_combine<kNormThreads>(v, kind);
     if (threadIdx.x == 0) s->partial[slot0 + blockIdx.x] = v;
@@ -387,8 +396,8 @@ __global__ __launch_bounds__(kOptThreads) void k_clip(OptTable<ClipTensor> t, co
     const double n = total_norm(s, slots, kind);
     if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
     const float c = clip_factor(n, max_norm);
-    for_tiles<kOptTile, true>(t, blockIdx.x, gridDim.x, [&](const ClipTensor& d, int64_t at) {
-        clip_tile_of<kOptThreads, kOptTile>(d, at, c, threadIdx.x);
+    for_tiles<kClipTile, true>(t, blockIdx.x, gridDim.x, [&](const ClipTensor& d, int64_t at) {
+        clip_tile_of<kOptThreads, kClipTile>(d, at, c, threadIdx.x);
     });
 }
 
@@ -403,17 +412,14 @@ __global__ __launch_bounds__(kOptThreads) void k_adam(OptTable<AdamTensor> t, co
     }
     if (last && blockIdx.x == 0 && threadIdx.x == 0) *step = s->step;
     const AdamConsts consts(cfg, s->inv_bc1, s->inv_bc2, c);
-    for_tiles<kOptTile, true>(t, blockIdx.x, gridDim.x, [&](const AdamTensor& d, int64_t at) {
-        constexpr int kElements = kOptTile / (int)sizeof(float), N = 2, kPart = N * kOptThreads * kAdamUnit;
-#pragma unroll 1
-        for (int part = 0; part < kElements; part += kPart) {
-            const int64_t e0 = adam_first(d, at) + part;
-            by_extent<N>(e0, kPart, count_of(d), [&](auto whole, auto n, int from) {
-                AdamRegs<n.value> x;
-                adam_load<whole.value, kOptThreads>(x, d, e0 + from * (kOptThreads * kAdamUnit), threadIdx.x);
-                adam_update<whole.value, kOptThreads>(x, d, e0 + from * (kOptThreads * kAdamUnit), threadIdx.x, consts);
-            });
-        }
+    for_tiles<kAdamTile, true>(t, blockIdx.x, gridDim.x, [&](const AdamTensor& d, int64_t at) {
+        constexpr int kElements = kAdamTile / (int)sizeof(float), N = kElements / (kOptThreads * kAdamUnit);
+        const int64_t e0 = adam_first(d, at);
+        by_extent(e0, kElements, count_of(d), [&](auto whole) {
+            AdamRegs<N> x;
+            adam_load<whole.value, kOptThreads>(x, d, e0, threadIdx.x);
+            adam_update<whole.value, kOptThreads>(x, d, e0, threadIdx.x, consts);
+        });
     });
 }
 
@@ -436,7 +442,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_clip_small(OptTable<ClipTenso
 
 // The wave's first tile is loaded at the start and stays in registers: lists
 // of up to kSmallThreads / 64 tiles wait for memory once. Most tiles here
-// have an end of their tensor in them: all go element by element.
+// have an end of their tensor in them.
 __global__ __launch_bounds__(kSmallThreads) void k_adam_small(OptTable<AdamTensor> t, gs_adam cfg, bool want,
                                                               int64_t* step, float* norm) {
     constexpr int kElements = kSmallTile / (int)sizeof(float), N = kElements / (64 * kAdamUnit);
@@ -533,7 +539,7 @@ hipError_t launch_partials(const S* tensors, int n, OptScratch* s, int kind, con
     const uint64_t share = std::min(kNormBlocks, kOptSlots / launches);
     for (int i = 0; i < n;) {
         OptTable<NormTensor> t;
-        i = fill_table(t, tensors, i, n, kOptTile, make);
+        i = fill_table(t, tensors, i, n, kNormTile, make);
         const uint64_t tiles = tiles_in(t);
         if (!tiles) continue;
         const uint64_t needed = (tiles * kOptThreads + kNormThreads - 1) / kNormThreads;
@@ -569,7 +575,11 @@ int launch_starts(const S* tensors, int n, int* starts) {
 template <typename D>
 constexpr int kMostLaunches = (GS_MAX_TENSORS + OptTable<D>::kMost - 1) / OptTable<D>::kMost;
 // A launch's tiles, and one stride past them, are counted in 32 bits.
-static_assert((GS_MAX_TENSOR_COUNT * 4 / kOptTile + 1) * OptTable<NormTensor>::kMost + 65536 < (int64_t)1 << 32,
+template <typename D>
+constexpr bool tiles_fit(int tile) {
+    return (GS_MAX_TENSOR_COUNT * 4 / tile + 1) * OptTable<D>::kMost + kOptBlocks < (int64_t)1 << 32;
+}
+static_assert(tiles_fit<NormTensor>(kNormTile) && tiles_fit<ClipTensor>(kClipTile) && tiles_fit<AdamTensor>(kAdamTile),
               "tile counts");
 static_assert(kMostLaunches<NormTensor> < kOptSlots, "every launch of the first pass has a partial");
 
@@ -603,7 +613,7 @@ hipError_t launch_clip_grads(const gs_grad_tensor* tensors, int n, int kind, flo
     }
     int starts[kMostLaunches<ClipTensor>];
     for (int l = launch_starts<ClipTensor>(tensors, n, starts); l--;) {
-        fill_table(t, tensors, starts[l], n, kOptTile, clip_of);
+        fill_table(t, tensors, starts[l], n, kClipTile, clip_of);
         k_clip<<<std::min<uint32_t>(tiles_in(t), kOptBlocks), kOptThreads, 0, stream>>>(t, s, slots, kind, max_norm,
                                                                                         norm);
         if (hipError_t e = hipGetLastError()) return e;
@@ -635,7 +645,7 @@ hipError_t launch_adam_step(const gs_adam& cfg, const gs_adam_tensor* tensors, i
     // the last launch takes the new step count; one without tensors if the list has none
     int starts[kMostLaunches<AdamTensor> + 1] = {};
     for (int l = std::max(1, launch_starts<AdamTensor>(tensors, n, starts)); l--;) {
-        fill_table(t, tensors, starts[l], n, kOptTile, adam_of);
+        fill_table(t, tensors, starts[l], n, kAdamTile, adam_of);
         k_adam<<<std::max(1u, std::min<uint32_t>(tiles_in(t), kOptBlocks)), kOptThreads, 0, stream>>>(
             t, s, slots, cfg, step, norm, l == 0);
         if (hipError_t e = hipGetLastError()) return e;

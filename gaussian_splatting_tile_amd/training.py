@@ -12,11 +12,36 @@ import torch
 
 from . import _lib
 from ._lib import GS_ADAM_SKIP_NONFINITE, GS_GATE_LINEAR, GS_GATE_SIGMOID, GS_NORM_L2, GS_NORM_MAX
-from .rasterizer import _ptr, _stream
 
 GATE_LINEAR, GATE_SIGMOID = GS_GATE_LINEAR, GS_GATE_SIGMOID
 NORM_L2, NORM_MAX = GS_NORM_L2, GS_NORM_MAX
 _TYPES = {torch.float32: _lib.GS_F32, torch.bfloat16: _lib.GS_BF16, torch.float16: _lib.GS_F16}
+
+
+# A call's own time on the host counts where a step is a few microseconds of
+# GPU work: pointers are passed as plain integers and checked with the
+# cheapest tensor attributes that say what is needed.
+
+def _stream(stream, device):
+    """The raw handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _ptr(t, shape, dtype, name):
+    """The address of a contiguous device tensor of this shape (None: any) and type (None: any)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _dtype(t, name):
@@ -26,46 +51,32 @@ def _dtype(t, name):
     return code
 
 
-def _shaped(t, shape, dtype, name):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    return _ptr(t, dtype, name)
-
-
-def _strided(t, name):
-    """Pointer and (batch, step) strides of a [B, T, D] tensor whose channels are contiguous."""
-    if t.device.type != "cuda":
-        raise TypeError(f"{name} must be a device tensor")
-    sb, st, sd = t.stride()
-    if sd != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name} must have contiguous channels (last stride 1)")
-    return ctypes.c_void_p(t.data_ptr()), sb, st
-
-
 def _recurrence(gate, x, gating, lengths, restart):
-    """The C description of a call and the pointers of gate and x."""
-    if gate.dim() != 3 or gate.shape != x.shape or gate.dtype != x.dtype or gate.device != x.device:
+    """The C description of a call, and its sizes."""
+    shape = gate.shape
+    if len(shape) != 3 or x.shape != shape or x.dtype != gate.dtype or x.device != gate.device:
         raise ValueError("gate and x must be [B, T, D] of the same shape, type and device")
-    B, T, D = gate.shape
-    r = _lib.GsRecurrence()
-    r.dtype, r.gating = _dtype(gate, "gate"), int(gating)
-    r.batch, r.steps, r.channels = B, T, D
-    pg, r.gate_batch, r.gate_step = _strided(gate, "gate")
-    px, r.x_batch, r.x_step = _strided(x, "x")
-    r.lengths = _shaped(lengths, (B,), torch.int32, "lengths")
-    r.restart = _shaped(restart, (B, T), torch.uint8, "restart")
-    return r, pg, px
+    if not gate.is_cuda:
+        raise TypeError("gate and x must be device tensors")
+    B, T, D = shape
+    gb, gt, gd = gate.stride()
+    xb, xt, xd = x.stride()
+    if D > 1 and (gd != 1 or xd != 1):
+        raise ValueError("gate and x must have contiguous channels (last stride 1)")
+    r = _lib.GsRecurrence(_dtype(gate, "gate and x"), int(gating), B, T, D, gb, gt, xb, xt,
+                          _ptr(lengths, (B,), torch.int32, "lengths"),
+                          _ptr(restart, (B, T), torch.uint8, "restart"))
+    return r, B, T, D
 
 
 def _scratch(lib, r, scratch, device):
+    """The workspace's tensor (kept until the call is enqueued), address and size."""
     if r.steps <= _lib.GS_RECURRENCE_CHUNK:
-        return None, 0
-    need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
-    if need == 0:
-        return None, 0
+        return None, None, 0
     if scratch is None:
+        need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
         scratch = torch.empty((need,), dtype=torch.uint8, device=device)
-    return scratch, scratch.numel() * scratch.element_size()
+    return scratch, _ptr(scratch, None, None, "scratch"), scratch.numel() * scratch.element_size()
 
 
 def recurrence_scratch_bytes(batch: int, steps: int, channels: int) -> int:
@@ -90,22 +101,23 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
     None). `out` may give any of them; out["h_last"] may be h0 itself (one state buffer for
     step-by-step serving, T = 1)."""
     lib = _lib.load()
-    r, pg, px = _recurrence(gate, x, gating, lengths, restart)
-    B, T, D = gate.shape
-    dev, f32 = gate.device, torch.float32
-    given = out or {}
-    h, h_last, ckpt = given.get("h"), given.get("h_last"), given.get("ckpt")
+    r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
+    dev, f32, whole, state = gate.device, torch.float32, (B, T, D), (B, D)
+    h = h_last = ckpt = None
+    if out is not None:
+        h, h_last, ckpt = out.get("h"), out.get("h_last"), out.get("ckpt")
     if h is None:
-        h = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
+        h = gate.new_empty(whole)
     if h_last is None:
-        h_last = torch.empty((B, D), dtype=f32, device=dev)
+        h_last = gate.new_empty(state, dtype=f32)
     if ckpt is None and checkpoints:
-        ckpt = torch.empty((B, recurrence_ckpt_rows(T), D), dtype=f32, device=dev)
-    scratch, nbytes = _scratch(lib, r, scratch, dev)
+        ckpt = gate.new_empty((B, recurrence_ckpt_rows(T), D), dtype=f32)
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
     _lib.check(lib.gs_recurrence_fwd(
-        ctypes.byref(r), pg, px, _shaped(h0, (B, D), f32, "h0"), _shaped(h, (B, T, D), gate.dtype, "h"),
-        _shaped(h_last, (B, D), f32, "h_last"), _shaped(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
-        _ptr(scratch), nbytes, _stream(stream)))
+        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), _ptr(h, whole, gate.dtype, "h"),
+        _ptr(h_last, state, f32, "h_last"),
+        None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), ps, nbytes,
+        _stream(stream, dev)))
     return dict(h=h, h_last=h_last, ckpt=ckpt)
 
 
@@ -115,20 +127,18 @@ def recurrence_bwd(gate, x, grad_h, h0=None, ckpt=None, grad_last=None, gating=G
     grad_h [B, T, D] of gate's type; grad_last float32 [B, D] or None. Returns dict grad_gate,
     grad_x [B, T, D], grad_h0 float32 [B, D]."""
     lib = _lib.load()
-    r, pg, px = _recurrence(gate, x, gating, lengths, restart)
-    B, T, D = gate.shape
-    dev, f32, t = gate.device, torch.float32, gate.dtype
+    r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
+    dev, f32, t, whole, state = gate.device, torch.float32, gate.dtype, (B, T, D), (B, D)
     if out is None:
-        out = dict(grad_gate=torch.empty((B, T, D), dtype=t, device=dev),
-                   grad_x=torch.empty((B, T, D), dtype=t, device=dev),
-                   grad_h0=torch.empty((B, D), dtype=f32, device=dev))
-    scratch, nbytes = _scratch(lib, r, scratch, dev)
+        out = dict(grad_gate=gate.new_empty(whole), grad_x=gate.new_empty(whole),
+                   grad_h0=gate.new_empty(state, dtype=f32))
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
     _lib.check(lib.gs_recurrence_bwd(
-        ctypes.byref(r), pg, px, _shaped(h0, (B, D), f32, "h0"),
-        _shaped(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), _shaped(grad_h, (B, T, D), t, "grad_h"),
-        _shaped(grad_last, (B, D), f32, "grad_last"), _shaped(out["grad_gate"], (B, T, D), t, "grad_gate"),
-        _shaped(out["grad_x"], (B, T, D), t, "grad_x"), _shaped(out.get("grad_h0"), (B, D), f32, "grad_h0"),
-        _ptr(scratch), nbytes, _stream(stream)))
+        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"),
+        None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
+        _ptr(grad_h, whole, t, "grad_h"), _ptr(grad_last, state, f32, "grad_last"),
+        _ptr(out["grad_gate"], whole, t, "grad_gate"), _ptr(out["grad_x"], whole, t, "grad_x"),
+        _ptr(out.get("grad_h0"), state, f32, "grad_h0"), ps, nbytes, _stream(stream, dev)))
     return out
 
 
@@ -158,18 +168,18 @@ class GradList:
         for d, g, o in zip(self._list, self.grads, self.out):
             if o.shape != g.shape:
                 raise ValueError("out must have the shapes of grads")
-            d.grad, d.out = _ptr(g, None, "grad"), _ptr(o, g.dtype, "out")
+            d.grad, d.out = _ptr(g, None, None, "grad"), _ptr(o, None, g.dtype, "out")
             d.count, d.dtype = g.numel(), _dtype(g, "grad")
         self._lib = _lib.load()
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=self.device)
-        self._pscratch = _ptr(self.scratch)
+        self._pscratch = self.scratch.data_ptr()
 
     def norm(self, kind=NORM_L2, out=None, stream=None):
         """gs_grad_norm: the global norm, a float32 tensor of no dimensions on the device."""
         if out is None:
             out = torch.empty((), dtype=torch.float32, device=self.device)
-        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), _shaped(out, (), torch.float32, "out"),
-                                          self._pscratch, _stream(stream)))
+        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), _ptr(out, (), torch.float32, "out"),
+                                          self._pscratch, _stream(stream, self.device)))
         return out
 
     def clip(self, max_norm, kind=NORM_L2, out=None, stream=None):
@@ -177,7 +187,8 @@ class GradList:
         if out is None:
             out = torch.empty((), dtype=torch.float32, device=self.device)
         _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm),
-                                           _shaped(out, (), torch.float32, "out"), self._pscratch, _stream(stream)))
+                                           _ptr(out, (), torch.float32, "out"), self._pscratch,
+                                           _stream(stream, self.device)))
         return out
 
 
@@ -221,16 +232,16 @@ class Adam:
         for d, p, g, m, v in zip(self._list, self.params, self.grads, self.exp_avg, self.exp_avg_sq):
             if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
                 raise ValueError("a gradient or moment does not have its parameter's shape")
-            d.param, d.grad = _ptr(p, None, "param"), _ptr(g, None, "grad")
-            d.m, d.v = _ptr(m, f32, "exp_avg"), _ptr(v, f32, "exp_avg_sq")
+            d.param, d.grad = _ptr(p, None, None, "param"), _ptr(g, None, None, "grad")
+            d.m, d.v = _ptr(m, None, f32, "exp_avg"), _ptr(v, None, f32, "exp_avg_sq")
             d.count, d.param_dtype, d.grad_dtype = p.numel(), _dtype(p, "param"), _dtype(g, "grad")
         self.set_lr(lr)
         for d, wd in zip(self._list, self._each(weight_decay, "weight_decay")):
             d.weight_decay = wd
         self._lib = _lib.load()
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=dev)
-        self._fixed = (ctypes.byref(self._cfg), self._list, n, _ptr(self.steps),
-                       _ptr(self.norm) if self._want_norm else None, _ptr(self.scratch))
+        self._fixed = (ctypes.byref(self._cfg), self._list, n, self.steps.data_ptr(),
+                       self.norm.data_ptr() if self._want_norm else None, self.scratch.data_ptr())
 
     def _each(self, v, name):
         v = [float(v)] * self._n if isinstance(v, (int, float)) else [float(x) for x in v]
@@ -246,5 +257,5 @@ class Adam:
     def step(self, stream=None):
         """One update. Returns the gradients' global norm before clipping (a device tensor that
         the next step overwrites), or None when nothing asks for it."""
-        _lib.check(self._lib.gs_adam_step(*self._fixed, _stream(stream)))
+        _lib.check(self._lib.gs_adam_step(*self._fixed, _stream(stream, self.device)))
         return self.norm if self._want_norm else None

@@ -700,7 +700,7 @@ gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void
 #define GS_NORM_L2 0
 #define GS_NORM_MAX 1
 #define GS_MAX_TENSORS 16384
-#define GS_MAX_TENSOR_COUNT ((int64_t)1 << 36)
+#define GS_MAX_TENSOR_COUNT ((int64_t)1 << 35)
 typedef struct {
     const void* grad;
     void* out;
