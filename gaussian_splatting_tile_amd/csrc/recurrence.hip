@@ -9,18 +9,21 @@
 //    64 V channels, so every load and store is a contiguous 256-byte row.
 //    Every input is read once, all loads of a thread are issued together.
 //  * The waves of a workgroup cover up to kWaves * 16 = 128 steps of the
-//    same channels and exchange (A, H) through LDS; a thread then walks its
-//    16 steps from its true state. With few steps the waves lie side by side
-//    over the channels instead.
+//    same channels and exchange (A, H) through LDS; one of them hands each
+//    wave the state in front of its steps, and every thread walks its 16
+//    steps from there. With few steps the waves lie side by side over the
+//    channels instead.
 //  * Longer sequences are chunks of 128 steps, one workgroup each, in one
-//    pass: a chunk publishes (A, H) per channel as one 64-bit word and takes
-//    the state in front of it from the words of the chunks before it in its
-//    group of kGroup and the state behind the group before. All words of a
-//    group are published without waiting for anything, so the chain that
-//    has to be waited for has one link per group, and the formula does not
-//    depend on which word came first: results are the same bits every time.
-//    A word carries its own validity (all ones: not there yet; a NaN of that
-//    pattern is stored as another one), so no fence is needed.
+//    pass: a chunk publishes (A, H) per channel as one 64-bit word, the last
+//    of kGroup chunks the run of its group, and the last of kGroup groups the
+//    state behind it. A chunk takes the state in front of it from the words
+//    of the chunks before it in its group, of the groups before that in
+//    theirs, and the state behind the super-group before: a sequence of 65536
+//    steps has a chain of 8 links to wait for, where one that passes the
+//    state from chunk to chunk would have 512. The formula does not depend on
+//    which word came first, so results are the same bits every time. A word
+//    carries its own validity (all ones: not there yet; a NaN of that pattern
+//    is stored as another one), so no fence is needed.
 //  * Chunks are handed out per chain (a sequence's group of channels) by a
 //    counter, in order: a workgroup waits only for chunks whose workgroups
 //    have started and themselves wait only for earlier ones, so every wait
@@ -30,6 +33,7 @@
 //    states it needs are recomputed from the forward's checkpoints (one
 //    float32 row per 128 steps), in LDS and registers as in the forward.
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_internal.h"
 
@@ -40,20 +44,22 @@ constexpr int kRecChunk = GS_RECURRENCE_CHUNK;
 constexpr int kSub = 16;
 constexpr int kWaves = 8;
 constexpr int kRecThreads = 64 * kWaves;
-constexpr int kGroup = 2 * kWaves;  // chunks per group: each wave fetches two words
+constexpr int kGroup = kWaves;  // a wave fetches one word of either level, the last one the state
 static_assert(kRecChunk == kSub * kWaves, "a chunk is one workgroup's steps");
 
 constexpr uint32_t kDropped = 0x80000000u;  // A of a run in which the state is dropped (a restart)
 
 // Geometry of a launch and its workspace.
 struct RecShape {
-    int chunks;     // K
-    int groups;     // of kGroup chunks
-    int columns;    // groups of 64 V channels
-    int steps_log2; // waves of a workgroup along the steps (1 << steps_log2)
+    int chunks;      // K
+    int groups;      // of kGroup chunks
+    int supers;      // of kGroup groups
+    int columns;     // groups of 64 V channels
+    int steps_log2;  // waves of a workgroup along the steps (1 << steps_log2)
+    uint64_t* word;    // [batch][chunks][channels] (A, H) or (A, C) of a chunk
+    uint64_t* group;   // [batch][groups][channels] of a group
+    uint32_t* state;   // [batch][supers][channels] state behind a super-group
     uint32_t* ticket;  // [batch * columns], all ones: none taken
-    uint64_t* word;    // [batch][K][channels] (A, H) or (A, C) of a chunk
-    uint32_t* state;   // [batch][groups][channels] state behind a group
 };
 
 template <typename T, int V>
@@ -88,11 +94,14 @@ struct Lanes<T, 2> {
 // kept below the largest float they are 1 / (1 + e) and e / (1 + e). The
 // hardware's exponential and reciprocal are within an ulp; the product
 // z log2(e) adds a relative |z| 2^-24.
-__device__ __forceinline__ void sigmoids(float z, float& a, float& rest) {
-    const float e = fminf(__builtin_amdgcn_exp2f(z * -1.44269504f), 1e38f);
+__device__ __forceinline__ float exp_minus(float z) {
+    return fminf(__builtin_amdgcn_exp2f(z * -1.44269504f), 1e38f);
+}
+__device__ __forceinline__ void of_exp_minus(float e, float& a, float& rest) {
     a = __builtin_amdgcn_rcpf(1.0f + e);
     rest = e * a;
 }
+__device__ __forceinline__ void sigmoids(float z, float& a, float& rest) { of_exp_minus(exp_minus(z), a, rest); }
 
 template <bool SIGMOID>
 __device__ __forceinline__ void step_terms(float gate, float x, float& a, float& u, float& rest) {
@@ -107,8 +116,8 @@ __device__ __forceinline__ void step_terms(float gate, float x, float& a, float&
 }
 
 // The terms of row i; one that is not there leaves the state as it is.
-template <typename T, int V, bool SIGMOID, bool FULL>
-__device__ __forceinline__ void row_terms(const uint32_t (&gate)[kSub], const uint32_t (&x)[kSub], int i, int v,
+template <typename T, int V, bool SIGMOID, bool FULL, int SUB>
+__device__ __forceinline__ void row_terms(const uint32_t (&gate)[SUB], const uint32_t (&x)[SUB], int i, int v,
                                           int rows, float& a, float& u, float& rest) {
     step_terms<SIGMOID>(Lanes<T, V>::get(gate[i], v), Lanes<T, V>::get(x[i], v), a, u, rest);
     if (!FULL && i >= rows) {
@@ -117,8 +126,8 @@ __device__ __forceinline__ void row_terms(const uint32_t (&gate)[kSub], const ui
     }
 }
 
-template <typename T, int V, bool FULL>
-__device__ __forceinline__ float row_grad(const uint32_t (&g)[kSub], int i, int v, int rows) {
+template <typename T, int V, bool FULL, int SUB>
+__device__ __forceinline__ float row_grad(const uint32_t (&g)[SUB], int i, int v, int rows) {
     return FULL || i < rows ? Lanes<T, V>::get(g[i], v) : 0.0f;
 }
 
@@ -139,31 +148,40 @@ __device__ __forceinline__ Run then(const Run& f, const Run& g) {
 constexpr uint32_t kNaN = 0x7fc00000u;
 constexpr int kMostPolls = 1 << 22;  // seconds; see above: no wait is expected to reach it
 
+// A word of all ones is not there yet.
+template <typename W>
+__device__ __forceinline__ void publish_word(W* p, W w, W nan) {
+    __hip_atomic_store(p, w == (W)~(W)0 ? nan : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename W>
+__device__ __forceinline__ W word_at(const W* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// The wave's words at p (one a lane). One lane watches its own until it is
+// there; then all read theirs, which were stored together, and only lanes
+// that came too early go on. (All lanes watching took bandwidth from the rows.)
+template <typename W>
+__device__ __forceinline__ W await_word(const W* p) {
+    int polls = 0;
+    if ((threadIdx.x & 63) == 0) {
+        while (word_at(p) == (W)~(W)0 && ++polls < kMostPolls) __builtin_amdgcn_s_sleep(4);
+    }
+    W w = word_at(p);
+    while (w == (W)~(W)0 && ++polls < kMostPolls) {
+        __builtin_amdgcn_s_sleep(1);
+        w = word_at(p);
+    }
+    return w;
+}
 __device__ __forceinline__ void publish(uint64_t* p, const Run& f) {
-    uint64_t w = (uint64_t)__float_as_uint(f.H) << 32 | __float_as_uint(f.A);
-    if (w == ~0ull) w = (uint64_t)kNaN << 32 | kNaN;
-    __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    publish_word(p, (uint64_t)__float_as_uint(f.H) << 32 | __float_as_uint(f.A), (uint64_t)kNaN << 32 | kNaN);
 }
 __device__ __forceinline__ Run await(const uint64_t* p) {
-    uint64_t w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int polls = 0; w == ~0ull && polls < kMostPolls; ++polls) {
-        __builtin_amdgcn_s_sleep(1);
-        w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+    const uint64_t w = await_word(p);
     return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
 }
-__device__ __forceinline__ void publish(uint32_t* p, float h) {
-    const uint32_t w = __float_as_uint(h);
-    __hip_atomic_store(p, w == ~0u ? kNaN : w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float await(const uint32_t* p) {
-    uint32_t w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int polls = 0; w == ~0u && polls < kMostPolls; ++polls) {
-        __builtin_amdgcn_s_sleep(1);
-        w = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    return __uint_as_float(w);
-}
+__device__ __forceinline__ void publish(uint32_t* p, float h) { publish_word(p, __float_as_uint(h), kNaN); }
+__device__ __forceinline__ float await(const uint32_t* p) { return __uint_as_float(await_word(p)); }
 
 // Where a wave works. All but `at` are the same in every lane.
 template <int V>
@@ -208,219 +226,244 @@ struct Place {
     }
 };
 
-// Bits of the steps row0 .. row0 + 15 below len that restart.
+// Bits of the steps row0 .. row0 + SUB - 1 below len that restart.
+template <int SUB>
 __device__ __forceinline__ uint32_t restarts(const RecurrenceArgs& r, int b, int row0, int len) {
-    if (!r.restart) return 0u;
     const int i = threadIdx.x & 63;
-    const bool set = i < kSub && row0 + i < len && r.restart[(int64_t)b * r.steps + row0 + i];
+    const bool set = i < SUB && row0 + i < len && r.restart[(int64_t)b * r.steps + row0 + i];
     return (uint32_t)__ballot(set);
 }
 
 // Lets the compiler believe that the packed rows changed, so that it computes
 // their terms again where they are used rather than keep them in registers.
-__device__ __forceinline__ void forget(uint32_t (&rows)[kSub]) {
+template <int SUB>
+__device__ __forceinline__ void forget(uint32_t (&rows)[SUB]) {
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) asm volatile("" : "+v"(rows[i]));
+    for (int i = 0; i < SUB; ++i) asm volatile("" : "+v"(rows[i]));
 }
 
 // v, or +0 if step i restarts (whatever v was); ... if any step up to i does.
+// Without CUT none does.
+template <bool CUT>
 __device__ __forceinline__ float unless_at(float v, uint32_t cut, int i) {
-    return __uint_as_float(__float_as_uint(v) & ~(uint32_t)((int32_t)(cut << (31 - i)) >> 31));
+    return CUT ? __uint_as_float(__float_as_uint(v) & ~(uint32_t)((int32_t)(cut << (31 - i)) >> 31)) : v;
 }
+template <bool CUT>
 __device__ __forceinline__ float unless_before(float v, uint32_t cut, int i) {
-    return __uint_as_float(__float_as_uint(v) & (cut & ((2u << i) - 1) ? 0u : ~0u));
+    return CUT ? __uint_as_float(__float_as_uint(v) & (cut & ((2u << i) - 1) ? 0u : ~0u)) : v;
 }
-
-template <typename T>
-__device__ __forceinline__ const void* step_ptr(const void* p, int64_t offset) {
-    return (const T*)p + offset;
+// Keeps the compiler from moving work across every kBlock rows: taken all
+// together, the rows' terms fill the registers.
+constexpr int kBlock = 4;
+__device__ __forceinline__ void end_of_row(int i) {
+    if (i % kBlock == kBlock - 1) __builtin_amdgcn_sched_barrier(0);
 }
-template <typename T>
-__device__ __forceinline__ void* step_ptr(void* p, int64_t offset) {
-    return (T*)p + offset;
-}
-
 // Loads the wave's rows of one tensor of a sequence whose first element is
 // at `base`. Rows that are not there (unless FULL) repeat the last step that
 // is, or step 0 of an empty sequence: no branch, and nothing out of bounds.
-template <typename T, int V, bool FULL>
-__device__ __forceinline__ void load_rows(uint32_t (&out)[kSub], const void* p, int64_t base, int64_t step, int row0,
+template <typename T, int V, bool FULL, int SUB>
+__device__ __forceinline__ void load_rows(uint32_t (&out)[SUB], const void* p, int64_t base, int64_t step, int row0,
                                           int len, uint32_t at) {
+    const T* q = (const T*)p + base + (FULL ? row0 : max(0, min(row0, len - 1))) * step;
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-        const int t = FULL ? row0 + i : max(0, min(row0 + i, len - 1));
-        out[i] = Lanes<T, V>::load(step_ptr<T>(p, base + t * step), at);
+    for (int i = 0; i < SUB; ++i) {
+        out[i] = Lanes<T, V>::load(q, at);
+        if (FULL || row0 + i + 1 < len) q += step;
     }
+}
+// A row of a [T][channels] output of a sequence.
+template <typename T, int V>
+__device__ __forceinline__ T* row_of(void* p, int64_t base, int64_t channels, int row) {
+    return (T*)p + base + row * channels;
 }
 
 // Zeroes rows [from, to) of a [T][channels] output of a sequence.
 template <typename T, int V>
 __device__ __forceinline__ void zero_rows(void* p, int64_t base, int64_t channels, int from, int to, uint32_t at) {
     const float zero[V] = {};
-    for (int t = from; t < to; ++t) Lanes<T, V>::store(step_ptr<T>(p, base + t * channels), at, zero);
+    T* q = row_of<T, V>(p, base, channels, from);
+    for (int t = from; t < to; ++t, q += channels) Lanes<T, V>::store(q, at, zero);
 }
 
-// LDS of a workgroup: one run per wave and channel, the runs of pairs of
-// earlier chunks, and the state (or gradient) that enters the group.
+// LDS of a workgroup: one run per wave and channel, the runs of the groups
+// and chunks in front, what enters the super-group, and what enters each
+// wave's steps.
 template <int V>
 struct RecLds {
     Run wave[kWaves][64 * V];
-    Run pair[kWaves][64 * V];
+    Run group[kGroup - 1][64 * V];
+    Run chunk[kGroup - 1][64 * V];
     float enter[64 * V];
+    float start[kWaves][64 * V];
     int pos;
 };
 
-// Fetches what enters the chunk at p.pos: leaves the pairs of words before it
-// in the group, and the state behind the group before, in LDS. Ends with a
-// barrier; returns the number of pairs.
+// Hands the chunk's run f on to the chunks behind (wave 0; followed: there
+// are some) and fetches what the chunk's place in the chain needs. With
+// pos > 0 it ends with a barrier, after which entering() can be called.
 template <int V>
-__device__ __forceinline__ int gather(RecLds<V>& lds, const RecurrenceArgs& r, const RecShape& s, const Place<V>& p) {
-    const int lane = threadIdx.x & 63, g = p.pos / kGroup, j = p.pos % kGroup;
+__device__ __forceinline__ void exchange(RecLds<V>& lds, const RecurrenceArgs& r, const RecShape& s, const Place<V>& p,
+                                         bool followed, const Run (&f)[V]) {
+    const int lane = threadIdx.x & 63;
     const int64_t D = r.channels, c = p.c0 + p.at;
-    const int k = 2 * p.wave;
-    if (k < j) {
-        const uint64_t* w = s.word + ((int64_t)p.b * s.chunks + (g * kGroup + k)) * D + c;
+    const int g = p.pos / kGroup, j = p.pos % kGroup, sg = g / kGroup, gj = g % kGroup;
+    uint64_t* const word = s.word + ((int64_t)p.b * s.chunks + g * kGroup) * D + c;
+    uint64_t* const group = s.group + ((int64_t)p.b * s.groups + sg * kGroup) * D + c;
+    const bool tells = followed && p.wave == 0 && p.mine;
+    if (tells) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            Run f = await(w + v);
-            if (k + 1 < j) f = then(f, await(w + D + v));
-            lds.pair[p.wave][lane * V + v] = f;
+        for (int v = 0; v < V; ++v) publish(word + j * D + v, f[v]);
+    }
+    if (!p.pos) return;
+    if (p.wave < j) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) lds.chunk[p.wave][lane * V + v] = await(word + p.wave * D + v);
+    }
+    if (j == kGroup - 1) {  // the group's run, before anything of earlier groups is waited for
+        __syncthreads();
+        if (tells) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int i = lane * V + v;
+                Run all = lds.chunk[0][i];
+                for (int w = 1; w < kGroup - 1; ++w) all = then(all, lds.chunk[w][i]);
+                publish(group + gj * D + v, then(all, f[v]));
+            }
         }
     }
-    if (p.wave == kWaves - 1) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            lds.enter[lane * V + v] = g ? await(s.state + ((int64_t)p.b * s.groups + g - 1) * D + c + v) : 0.0f;
+    for (int v = 0; v < V; ++v) {
+        const int i = lane * V + v;
+        if (p.wave < gj) lds.group[p.wave][i] = await(group + p.wave * D + v);
+        if (p.wave == kWaves - 1)
+            lds.enter[i] = sg ? await(s.state + ((int64_t)p.b * s.supers + sg - 1) * D + c + v) : 0.0f;
     }
     __syncthreads();
-    return (j + 1) / 2;
 }
 
-// The state that enters the chunk.
+// What enters the chunk at channel i of the workgroup (pos > 0).
 template <int V>
-__device__ __forceinline__ float entering(const RecLds<V>& lds, int pairs, int i) {
+__device__ __forceinline__ float entering(const RecLds<V>& lds, const Place<V>& p, int i) {
+    const int j = p.pos % kGroup, gj = p.pos / kGroup % kGroup;
     float h = lds.enter[i];
-    for (int w = 0; w < pairs; ++w) h = apply(lds.pair[w][i], h);
+    for (int w = 0; w < gj; ++w) h = apply(lds.group[w][i], h);
+    for (int w = 0; w < j; ++w) h = apply(lds.chunk[w][i], h);
     return h;
 }
 
-// Wave 0 publishes the chunk's own run f as its word.
+// ... and, behind the last chunk of a super-group, what leaves it.
 template <int V>
-__device__ __forceinline__ void publish_chunk(const RecurrenceArgs& r, const RecShape& s, const Place<V>& p,
-                                              const Run (&f)[V]) {
-    uint64_t* w = s.word + ((int64_t)p.b * s.chunks + p.pos) * r.channels + p.c0 + p.at;
-#pragma unroll
-    for (int v = 0; v < V; ++v) publish(w + v, f[v]);
-}
-// ... and, for the last chunk of a group, the state behind it.
-template <int V>
-__device__ __forceinline__ void publish_group(const RecurrenceArgs& r, const RecShape& s, const Place<V>& p,
-                                              const Run (&f)[V], const float (&h)[V]) {
-    uint32_t* w = s.state + ((int64_t)p.b * s.groups + p.pos / kGroup) * r.channels + p.c0 + p.at;
-#pragma unroll
-    for (int v = 0; v < V; ++v) publish(w + v, apply(f[v], h[v]));
+__device__ __forceinline__ void tell_state(const RecurrenceArgs& r, const RecShape& s, const Place<V>& p, bool followed,
+                                           int v, float h) {
+    if (followed && p.mine && p.pos % (kGroup * kGroup) == kGroup * kGroup - 1)
+        publish(s.state + ((int64_t)p.b * s.supers + p.pos / (kGroup * kGroup)) * r.channels + p.c0 + p.at + v, h);
 }
 
-template <typename T, int V, bool SIGMOID, bool FULL>
+template <typename T, int V, bool SIGMOID, bool CUT, bool FULL, int SUB>
 __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape& s, RecLds<V>& lds, const Place<V>& p) {
     const int lane = threadIdx.x & 63;
     const int64_t D = r.channels;
-    const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * kSub;
+    const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * SUB;
     const int64_t out0 = (int64_t)p.b * r.steps * D + p.c0, state0 = (int64_t)p.b * D + p.c0 + p.at;
-    const int rows = FULL ? kSub : max(0, min(p.len - row0, kSub));
-    const bool starts = p.pos == 0 && p.row == 0;
-    float a[kSub][V], u[kSub][V], h0[V];
-    uint32_t cut;
-    {
-        uint32_t gate[kSub], x[kSub];
-        load_rows<T, V, FULL>(gate, r.gate, p.b * r.gate_batch + p.c0, r.gate_step, row0, p.len, p.at);
-        load_rows<T, V, FULL>(x, r.x, p.b * r.x_batch + p.c0, r.x_step, row0, p.len, p.at);
+    const int rows = FULL ? SUB : max(0, min(p.len - row0, SUB));
+    uint32_t gate[SUB], x[SUB];
+    load_rows<T, V, FULL>(gate, r.gate, p.b * r.gate_batch + p.c0, r.gate_step, row0, p.len, p.at);
+    load_rows<T, V, FULL>(x, r.x, p.b * r.x_batch + p.c0, r.x_step, row0, p.len, p.at);
+    float h[V];  // the state in front of the sequence, then of the wave's steps
 #pragma unroll
-        for (int v = 0; v < V; ++v) h0[v] = starts && r.h0 ? r.h0[state0 + v] : 0.0f;
-        cut = restarts(r, p.b, row0, p.len);
+    for (int v = 0; v < V; ++v) h[v] = p.pos == 0 && p.row == 0 && r.h0 ? r.h0[state0 + v] : 0.0f;
+    const uint32_t cut = CUT ? restarts<SUB>(r, p.b, row0, p.len) : 0u;
+    if (p.waves > 1) {
+        Run own[V];
 #pragma unroll
-        for (int i = 0; i < kSub; ++i)
+        for (int v = 0; v < V; ++v) own[v] = {1.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float rest;
-                row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a[i][v], u[i][v], rest);
-                a[i][v] = unless_at(a[i][v], cut, i);
+                float a, u, rest;
+                row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
+                own[v].A *= a;
+                own[v].H = fmaf(unless_at<CUT>(a, cut, i), unless_at<CUT>(own[v].H, cut, i), u);
             }
-    }
-    Run own[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        own[v] = {1.0f, h0[v]};
-#pragma unroll
-        for (int i = 0; i < kSub; ++i) {
-            own[v].A *= a[i][v];
-            own[v].H = fmaf(a[i][v], unless_at(own[v].H, cut, i), u[i][v]);
+            end_of_row(i);
         }
-        own[v].A = cut ? __uint_as_float(kDropped) : own[v].A + 0.0f;
-        lds.wave[p.wave][lane * V + v] = own[v];
-    }
-    __syncthreads();
-    Run chunk[V];
-    const bool followed = t0 + kRecChunk < p.len;
-    if (followed && p.wave == 0) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            chunk[v] = own[v];
-            for (int w = 1; w < kWaves; ++w) chunk[v] = then(chunk[v], lds.wave[w][lane * V + v]);
+            own[v].A = cut ? __uint_as_float(kDropped) : own[v].A + 0.0f;
+            lds.wave[p.wave][lane * V + v] = own[v];
         }
-        if (p.mine) publish_chunk<V>(r, s, p, chunk);
-    }
-    float h[V];
+        __syncthreads();
+        const bool followed = t0 + kRecChunk < p.len;
+        if (s.chunks > 1) {
+            if (followed && p.wave == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = 0.0f;
-    if (p.pos) {
-        const int pairs = gather<V>(lds, r, s, p);
-#pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = entering<V>(lds, pairs, lane * V + v);
-        if (p.wave == 0 && p.mine && r.ckpt) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                r.ckpt[((int64_t)p.b * (s.chunks - 1) + p.pos - 1) * D + p.c0 + p.at + v] = h[v];
+                for (int v = 0; v < V; ++v) {
+                    for (int w = 1; w < kWaves; ++w) own[v] = then(own[v], lds.wave[w][lane * V + v]);
+                    if (p.pos == 0) own[v].H = apply(own[v], h[v]);
+                }
+            }
+            exchange<V>(lds, r, s, p, followed, own);
         }
-    }
-    if (followed && p.wave == 0 && p.mine && p.pos % kGroup == kGroup - 1) publish_group<V>(r, s, p, chunk, h);
+        if (p.row == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (starts) h[v] = h0[v];
-        for (int w = p.first; w < p.wave; ++w) h[v] = apply(lds.wave[w][lane * V + v], h[v]);
+            for (int v = 0; v < V; ++v) {
+                const int i = lane * V + v;
+                float e = p.pos ? entering<V>(lds, p, i) : h[v];
+                if (p.pos && p.mine && r.ckpt)
+                    r.ckpt[((int64_t)p.b * (s.chunks - 1) + p.pos - 1) * D + p.c0 + p.at + v] = e;
+                for (int w = p.first; w < p.first + p.waves; ++w) {
+                    lds.start[w][i] = e;
+                    e = apply(lds.wave[w][i], e);
+                }
+                tell_state<V>(r, s, p, followed, v, e);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = lds.start[p.wave][lane * V + v];
+        forget(gate);
+        forget(x);
     }
     if (!p.mine) return;
+    T* out = row_of<T, V>(r.h, out0, D, row0);
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
+    for (int i = 0; i < SUB; ++i, out += D) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], unless_at(h[v], cut, i), u[i][v]);
-        if (FULL || i < rows) Lanes<T, V>::store(step_ptr<T>(r.h, out0 + (row0 + i) * D), p.at, h);
+        for (int v = 0; v < V; ++v) {
+            float a, u, rest;
+            row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
+            h[v] = fmaf(unless_at<CUT>(a, cut, i), unless_at<CUT>(h[v], cut, i), u);
+        }
+        if (FULL || i < rows) Lanes<T, V>::store(out, p.at, h);
+        end_of_row(i);
     }
-    if (!FULL) zero_rows<T, V>(r.h, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at);
+    if (!FULL) zero_rows<T, V>(r.h, out0, D, row0 + rows, min(row0 + SUB, r.steps), p.at);
     // the wave with the last step, or the first one of an empty sequence
-    if (r.h_last && (rows ? row0 + rows == p.len : starts && p.len == 0)) {
+    if (r.h_last && (rows ? row0 + rows == p.len : p.row == 0 && p.len == 0)) {
 #pragma unroll
         for (int v = 0; v < V; ++v) r.h_last[state0 + v] = h[v];
     }
 }
 
-template <typename T, int V, bool SIGMOID>
-__global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
+template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
+__global__ __launch_bounds__(kRecThreads, 8) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
     __shared__ RecLds<V> lds;
     const Place<V> p(r, s, &lds.pos);
-    const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * kSub;
-    if (t0 + p.waves * kSub <= p.len)
-        forward<T, V, SIGMOID, true>(r, s, lds, p);
+    const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * SUB;
+    if (t0 + p.waves * SUB <= p.len)
+        forward<T, V, SIGMOID, CUT, true, SUB>(r, s, lds, p);
     else if (t0 < p.len || p.pos == 0)
-        forward<T, V, SIGMOID, false>(r, s, lds, p);
+        forward<T, V, SIGMOID, CUT, false, SUB>(r, s, lds, p);
     else if (p.mine)  // padding
-        zero_rows<T, V>(r.h, (int64_t)p.b * r.steps * r.channels + p.c0, r.channels, row0, min(row0 + kSub, r.steps),
+        zero_rows<T, V>(r.h, (int64_t)p.b * r.steps * r.channels + p.c0, r.channels, row0, min(row0 + SUB, r.steps),
                         p.at);
 }
 
-template <typename T, int V, bool SIGMOID, bool FULL>
+template <typename T, int V, bool SIGMOID, bool CUT, bool FULL>
 __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape& s, RecLds<V>& lds,
-                                         float (&wave_c)[kWaves][64 * V], const Place<V>& p, int k) {
+                                         float (&wave_c)[kWaves][64 * V], float (&start_h)[kWaves][64 * V],
+                                         const Place<V>& p, int k) {
     const int lane = threadIdx.x & 63;
     const int64_t D = r.channels;
     const int t0 = k * kRecChunk, row0 = t0 + p.row * kSub;
@@ -432,107 +475,137 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     load_rows<T, V, FULL>(x, r.x, p.b * r.x_batch + p.c0, r.x_step, row0, p.len, p.at);
     load_rows<T, V, FULL>(g, r.grad_h, out0, D, row0, p.len, p.at);
     const bool ends = rows ? row0 + rows == p.len : starts && p.len == 0;  // has the last step
+    const bool leads = p.row == p.waves - 1;  // hands the waves of these channels their states
     float h[V], last[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        h[v] = k ? r.ckpt_in[((int64_t)p.b * (s.chunks - 1) + k - 1) * D + p.c0 + p.at + v]
-                 : r.h0 ? r.h0[state0 + v] : 0.0f;
+        h[v] = !leads ? 0.0f
+               : k    ? r.ckpt_in[((int64_t)p.b * (s.chunks - 1) + k - 1) * D + p.c0 + p.at + v]
+               : r.h0 ? r.h0[state0 + v]
+                      : 0.0f;
         last[v] = ends && r.grad_last ? r.grad_last[state0 + v] : 0.0f;
     }
-    const uint32_t cut = restarts(r, p.b, row0, p.len);
-
-    // the wave's run of the states, (A, H), and of what it passes back, (A, C)
-    Run own[V];
-    float C[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        own[v] = {1.0f, 0.0f};
-        C[v] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float a, u, rest;
-            row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
-            own[v].H = fmaf(unless_at(a, cut, i), unless_at(own[v].H, cut, i), u);
-            // steps from a restart on pass nothing back in front of it
-            own[v].A = unless_before(own[v].A * a, cut, i);
-            C[v] = fmaf(own[v].A, unless_before(row_grad<T, V, FULL>(g, i, v, rows), cut, i), C[v]);
-        }
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        if (!cut) C[v] = fmaf(own[v].A, last[v], C[v]);
-        own[v].A = cut ? __uint_as_float(kDropped) : own[v].A + 0.0f;
-        lds.wave[p.wave][lane * V + v] = own[v];
-        wave_c[p.wave][lane * V + v] = C[v];
-    }
-    __syncthreads();
-
-    Run chunk[V];
+    const uint32_t cut = CUT ? restarts<kSub>(r, p.b, row0, p.len) : 0u;
     const bool followed = k > 0;
-    if (followed && p.wave == 0) {
+    if (p.waves > 1) {
+        // the wave's run of the states, (A, H), and of what it passes back, (A, C)
+        Run own[V];
+        float C[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int i = lane * V + v;
-            chunk[v] = {lds.wave[kWaves - 1][i].A, wave_c[kWaves - 1][i]};
-            for (int w = kWaves - 2; w >= 0; --w) chunk[v] = then(chunk[v], Run{lds.wave[w][i].A, wave_c[w][i]});
+            own[v] = {1.0f, 0.0f};
+            C[v] = 0.0f;
         }
-        if (p.mine) publish_chunk<V>(r, s, p, chunk);
-    }
-    // the states in front of the wave's steps
-    forget(gate);
-    forget(x);
-    float prev[kSub][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        for (int w = p.first; w < p.wave; ++w) h[v] = apply(lds.wave[w][lane * V + v], h[v]);
+        for (int i = 0; i < kSub; ++i) {
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
+            for (int v = 0; v < V; ++v) {
+                float a, u, rest;
+                row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
+                own[v].H = fmaf(unless_at<CUT>(a, cut, i), unless_at<CUT>(own[v].H, cut, i), u);
+                // steps from a restart on pass nothing back in front of it
+                own[v].A = unless_before<CUT>(own[v].A * a, cut, i);
+                C[v] = fmaf(own[v].A,
+                            unless_before<CUT>(row_grad<T, V, FULL>(g, i, v, rows), cut, i), C[v]);
+            }
+            end_of_row(i);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, u, rest;
-            row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
-            prev[i][v] = unless_at(h[v], cut, i);
-            h[v] = fmaf(unless_at(a, cut, i), prev[i][v], u);
+            if (!cut) C[v] = fmaf(own[v].A, last[v], C[v]);
+            own[v].A = cut ? __uint_as_float(kDropped) : own[v].A + 0.0f;
+            lds.wave[p.wave][lane * V + v] = own[v];
+            wave_c[p.wave][lane * V + v] = C[v];
         }
-    }
-    forget(gate);
-    forget(x);
-    // what the steps behind the wave's pass back
-    float c[V];
+        __syncthreads();
+        if (leads) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = 0.0f;
-    if (p.pos) {
-        const int pairs = gather<V>(lds, r, s, p);
+            for (int v = 0; v < V; ++v) {
+                float e = h[v];
+                for (int w = p.first; w <= p.wave; ++w) {
+                    start_h[w][lane * V + v] = e;
+                    e = apply(lds.wave[w][lane * V + v], e);
+                }
+            }
+        }
+        if (s.chunks > 1) {
+            if (followed && p.wave == 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) c[v] = entering<V>(lds, pairs, lane * V + v);
-    }
-    if (followed && p.wave == 0 && p.mine && p.pos % kGroup == kGroup - 1) publish_group<V>(r, s, p, chunk, c);
+                for (int v = 0; v < V; ++v) {
+                    const int i = lane * V + v;
+                    own[v] = {lds.wave[kWaves - 1][i].A, wave_c[kWaves - 1][i]};
+                    for (int w = kWaves - 2; w >= 0; --w) own[v] = then(own[v], Run{lds.wave[w][i].A, wave_c[w][i]});
+                }
+            }
+            exchange<V>(lds, r, s, p, followed, own);
+        }
+        if (p.row == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int i = lane * V + v;
-        for (int w = p.first + p.waves - 1; w > p.wave; --w) c[v] = apply(Run{lds.wave[w][i].A, wave_c[w][i]}, c[v]);
-        c[v] += last[v];
+            for (int v = 0; v < V; ++v) {
+                const int i = lane * V + v;
+                float e = p.pos ? entering<V>(lds, p, i) : 0.0f;
+                for (int w = p.first + p.waves - 1; w >= p.first; --w) {
+                    lds.start[w][i] = e;
+                    e = apply(Run{lds.wave[w][i].A, wave_c[w][i]}, e);
+                }
+                tell_state<V>(r, s, p, followed, v, e);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = start_h[p.wave][lane * V + v];
+        forget(gate);
+        forget(x);
+        forget(g);
     }
     if (!p.mine) return;
+    // Walk the states, keeping what step i's gradients take: weight, by which
+    // d_i is grad_gate_i, and (SIGMOID) e = exp(-gate), of which a and 1 - a
+    // are cheap; then walk back.
+    float weight[kSub][V], e[kSub][V];
 #pragma unroll
-    for (int i = kSub - 1; i >= 0; --i) {
-        float dg[V], dx[V];
+    for (int i = 0; i < kSub; ++i) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float a, u, rest;
-            row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
-            const float d = row_grad<T, V, FULL>(g, i, v, rows) + c[v], xi = Lanes<T, V>::get(x[i], v);
-            dg[v] = SIGMOID ? d * (prev[i][v] - xi) * (a * rest) : d * prev[i][v];
-            dx[v] = SIGMOID ? d * rest : d;
-            c[v] = unless_at(a * d, cut, i);
+            float a = Lanes<T, V>::get(gate[i], v), u = Lanes<T, V>::get(x[i], v);
+            const float prev = unless_at<CUT>(h[v], cut, i);
+            weight[i][v] = prev;
+            if (SIGMOID) {
+                float rest;
+                e[i][v] = exp_minus(a);
+                of_exp_minus(e[i][v], a, rest);
+                weight[i][v] = (prev - u) * (a * rest);
+                u *= rest;
+            }
+            h[v] = FULL || i < rows ? fmaf(unless_at<CUT>(a, cut, i), prev, u) : h[v];
+        }
+        end_of_row(i);
+    }
+    float c[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) c[v] = (p.waves > 1 ? lds.start[p.wave][lane * V + v] : 0.0f) + last[v];
+    T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + kSub - 1);
+    T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + kSub - 1);
+#pragma unroll
+    for (int i = kSub - 1; i >= 0; --i, dg -= D, dx -= D) {
+        float vg[V], vx[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float a, rest = 1.0f;
+            if (SIGMOID)
+                of_exp_minus(e[i][v], a, rest);
+            else
+                a = Lanes<T, V>::get(gate[i], v);
+            const float d = row_grad<T, V, FULL>(g, i, v, rows) + c[v];
+            vg[v] = d * weight[i][v];
+            vx[v] = SIGMOID ? d * rest : d;
+            if (FULL || i < rows) c[v] = unless_at<CUT>(a * d, cut, i);
         }
         if (FULL || i < rows) {
-            Lanes<T, V>::store(step_ptr<T>(r.grad_gate, out0 + (row0 + i) * D), p.at, dg);
-            Lanes<T, V>::store(step_ptr<T>(r.grad_x, out0 + (row0 + i) * D), p.at, dx);
+            Lanes<T, V>::store(dg, p.at, vg);
+            Lanes<T, V>::store(dx, p.at, vx);
         }
+        end_of_row(kSub - 1 - i);
     }
     if (!FULL) {
         zero_rows<T, V>(r.grad_gate, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at);
@@ -544,18 +617,18 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     }
 }
 
-template <typename T, int V, bool SIGMOID>
+template <typename T, int V, bool SIGMOID, bool CUT>
 __global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_bwd(RecurrenceArgs r, RecShape s) {
     __shared__ RecLds<V> lds;
-    __shared__ float wave_c[kWaves][64 * V];
+    __shared__ float wave_c[kWaves][64 * V], start_h[kWaves][64 * V];
     const Place<V> p(r, s, &lds.pos);
     const int used = (p.len + kRecChunk - 1) / kRecChunk;  // chunks with steps: taken from the last on
     const int k = p.pos < used ? used - 1 - p.pos : p.pos;
     const int t0 = k * kRecChunk, row0 = t0 + p.row * kSub;
     if (t0 + p.waves * kSub <= p.len) {
-        backward<T, V, SIGMOID, true>(r, s, lds, wave_c, p, k);
+        backward<T, V, SIGMOID, CUT, true>(r, s, lds, wave_c, start_h, p, k);
     } else if (t0 < p.len || k == 0) {
-        backward<T, V, SIGMOID, false>(r, s, lds, wave_c, p, k);
+        backward<T, V, SIGMOID, CUT, false>(r, s, lds, wave_c, start_h, p, k);
     } else if (p.mine) {  // padding
         const int64_t out0 = (int64_t)p.b * r.steps * r.channels + p.c0;
         zero_rows<T, V>(r.grad_gate, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at);
@@ -574,21 +647,32 @@ int chunks_of(int steps) { return std::max(1, (int)(((int64_t)steps + kRecChunk 
 size_t layout(int batch, int steps, int channels, int columns, RecShape* s, void* base) {
     s->chunks = chunks_of(steps);
     s->groups = (s->chunks + kGroup - 1) / kGroup;
+    s->supers = (s->groups + kGroup - 1) / kGroup;
     s->columns = columns;
     s->steps_log2 = 0;
     while ((kSub << s->steps_log2) < std::min(steps, kRecChunk)) ++s->steps_log2;
-    s->ticket = nullptr;
-    s->word = nullptr;
-    s->state = nullptr;
+    s->word = s->group = nullptr;
+    s->state = s->ticket = nullptr;
     if (s->chunks == 1) return 0;
-    const size_t words = (size_t)batch * s->chunks * channels, states = (size_t)batch * s->groups * channels;
+    const size_t row = (size_t)batch * channels, words = row * (s->chunks + s->groups), states = row * s->supers;
     s->word = (uint64_t*)base;
+    s->group = s->word + row * s->chunks;
     s->state = (uint32_t*)(s->word + words);
     s->ticket = s->state + states;
     return words * 8 + (states + (size_t)batch * columns) * 4;
 }
 
-template <typename T, int V, bool SIGMOID>
+// Fills the workspace with ones, 16 bytes a thread.
+__global__ void k_recurrence_clear(uint32_t* p, size_t words) {
+    const size_t i = ((size_t)blockIdx.x * kRecThreads + threadIdx.x) * 4;
+    if (i + 4 <= words) {
+        *(uint4*)(p + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
+    } else {
+        for (size_t j = i; j < words; ++j) p[j] = ~0u;
+    }
+}
+
+template <typename T, int V, bool SIGMOID, bool CUT>
 hipError_t launch_of(const RecurrenceArgs& r, bool backward, void* scratch, hipStream_t stream) {
     RecShape s;
     const size_t bytes = layout(r.batch, r.steps, r.channels, (r.channels + 64 * V - 1) / (64 * V), &s, scratch);
@@ -596,20 +680,28 @@ hipError_t launch_of(const RecurrenceArgs& r, bool backward, void* scratch, hipS
     if (s.chunks == 1) {
         const int across = kWaves >> s.steps_log2;
         blocks = (int64_t)r.batch * ((s.columns + across - 1) / across);
-    } else if (hipError_t e = launch_fill_u32((uint32_t*)scratch, bytes / 4, ~0u, stream)) {
-        return e;
+    } else {
+        const size_t threads = (bytes + 15) / 16;
+        k_recurrence_clear<<<(unsigned)((threads + kRecThreads - 1) / kRecThreads), kRecThreads, 0, stream>>>(
+            (uint32_t*)scratch, bytes / 4);
+        if (hipError_t e = hipGetLastError()) return e;
     }
     if (backward)
-        k_recurrence_bwd<T, V, SIGMOID><<<(unsigned)blocks, kRecThreads, 0, stream>>>(r, s);
+        k_recurrence_bwd<T, V, SIGMOID, CUT><<<(unsigned)blocks, kRecThreads, 0, stream>>>(r, s);
+    else if (r.steps == 1)  // serving: no row but the one
+        k_recurrence_fwd<T, V, SIGMOID, CUT, 1><<<(unsigned)blocks, kRecThreads, 0, stream>>>(r, s);
     else
-        k_recurrence_fwd<T, V, SIGMOID><<<(unsigned)blocks, kRecThreads, 0, stream>>>(r, s);
+        k_recurrence_fwd<T, V, SIGMOID, CUT, kSub><<<(unsigned)blocks, kRecThreads, 0, stream>>>(r, s);
     return hipGetLastError();
 }
 
 template <typename T, int V>
 hipError_t launch_of(const RecurrenceArgs& r, bool sigmoid, bool backward, void* scratch, hipStream_t stream) {
-    return sigmoid ? launch_of<T, V, true>(r, backward, scratch, stream)
-                   : launch_of<T, V, false>(r, backward, scratch, stream);
+    if (sigmoid)
+        return r.restart ? launch_of<T, V, true, true>(r, backward, scratch, stream)
+                         : launch_of<T, V, true, false>(r, backward, scratch, stream);
+    return r.restart ? launch_of<T, V, false, true>(r, backward, scratch, stream)
+                     : launch_of<T, V, false, false>(r, backward, scratch, stream);
 }
 
 // Two 16-bit channels a lane need every row of every tensor on a 4-byte boundary.
