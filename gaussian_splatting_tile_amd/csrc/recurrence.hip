@@ -62,31 +62,43 @@ struct RecShape {
     uint32_t* ticket;  // [batch * columns], all ones: none taken
 };
 
+// A lane's V channels of one row, packed in 32 bits. Rows go past the caches
+// (NT): nothing is read twice, and without it the pure copy of a sequence's
+// rows reaches 3.7 TB/s, with it 5.6 (65536 x 1024 bf16, two in, one out).
 template <typename T, int V>
 struct Lanes;
 template <>
 struct Lanes<float, 1> {
-    static __device__ __forceinline__ uint32_t load(const void* p, uint32_t i) { return ((const uint32_t*)p)[i]; }
+    static __device__ __forceinline__ uint32_t load(const float* p, uint32_t i) {
+        return __builtin_nontemporal_load((const uint32_t*)p + i);
+    }
     static __device__ __forceinline__ float get(uint32_t r, int) { return __uint_as_float(r); }
-    static __device__ __forceinline__ void store(void* p, uint32_t i, const float (&v)[1]) { ((float*)p)[i] = v[0]; }
+    static __device__ __forceinline__ void store(float* p, uint32_t i, const float (&v)[1]) {
+        __builtin_nontemporal_store(v[0], p + i);
+    }
 };
 template <typename T>
 struct Lanes<T, 1> {
-    static __device__ __forceinline__ uint32_t load(const void* p, uint32_t i) { return ((const uint16_t*)p)[i]; }
+    static __device__ __forceinline__ uint32_t load(const T* p, uint32_t i) {
+        return __builtin_nontemporal_load((const uint16_t*)p + i);
+    }
     static __device__ __forceinline__ float get(uint32_t r, int) { return (float)__builtin_bit_cast(T, (uint16_t)r); }
-    static __device__ __forceinline__ void store(void* p, uint32_t i, const float (&v)[1]) { ((T*)p)[i] = (T)v[0]; }
+    static __device__ __forceinline__ void store(T* p, uint32_t i, const float (&v)[1]) {
+        __builtin_nontemporal_store((T)v[0], p + i);
+    }
 };
 template <typename T>
 struct Lanes<T, 2> {
-    static __device__ __forceinline__ uint32_t load(const void* p, uint32_t i) {
-        return *(const uint32_t*)((const uint16_t*)p + i);
+    static __device__ __forceinline__ uint32_t load(const T* p, uint32_t i) {
+        return __builtin_nontemporal_load((const uint32_t*)(p + i));
     }
     static __device__ __forceinline__ float get(uint32_t r, int j) {
         return (float)__builtin_bit_cast(T, (uint16_t)(j ? r >> 16 : r));
     }
-    static __device__ __forceinline__ void store(void* p, uint32_t i, const float (&v)[2]) {
+    static __device__ __forceinline__ void store(T* p, uint32_t i, const float (&v)[2]) {
         typedef T Pair __attribute__((ext_vector_type(2)));
-        *(Pair*)((T*)p + i) = Pair{(T)v[0], (T)v[1]};
+        const Pair r = {(T)v[0], (T)v[1]};
+        __builtin_nontemporal_store(r, (Pair*)(p + i));
     }
 };
 
@@ -447,7 +459,7 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
-__global__ __launch_bounds__(kRecThreads, 8) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
+__global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
     __shared__ RecLds<V> lds;
     const Place<V> p(r, s, &lds.pos);
     const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * SUB;
