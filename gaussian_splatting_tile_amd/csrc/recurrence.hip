@@ -27,7 +27,10 @@
 //  * Chunks are handed out per chain (a sequence's group of channels) by a
 //    counter, in order: a workgroup waits only for chunks whose workgroups
 //    have started and themselves wait only for earlier ones, so every wait
-//    ends whatever the dispatch order. It is bounded all the same.
+//    ends whatever the dispatch order. It is bounded all the same. (One
+//    counter for all chains, with workgroups that stay and fetch their next
+//    number ahead, was slower: 8 x 2048 x 2048 bf16 forward and backward 160
+//    us instead of 100, the fetches queue at one address.)
 //  * The backward passes back c_t = a_t (g_t + c_{t+1}), the same kind of map
 //    from the other end, C = sum over t of g_t times the gates up to t. The
 //    states it needs are recomputed from the forward's checkpoints (one
@@ -56,9 +59,10 @@ struct RecShape {
     int supers;      // of kGroup groups
     int columns;     // groups of 64 V channels
     int steps_log2;  // waves of a workgroup along the steps (1 << steps_log2)
-    uint64_t* word;    // [batch][chunks][channels] (A, H) or (A, C) of a chunk
-    uint64_t* group;   // [batch][groups][channels] of a group
-    uint32_t* state;   // [batch][supers][channels] state behind a super-group
+    // rows of columns * 64 V, see exchange()
+    uint64_t* word;    // [batch][chunks][row] (A, H) or (A, C) of a chunk
+    uint64_t* group;   // [batch][groups][row] of a group
+    uint32_t* state;   // [batch][supers][row] state behind a super-group
     uint32_t* ticket;  // [batch * columns], all ones: none taken
 };
 
@@ -169,16 +173,18 @@ template <typename W>
 __device__ __forceinline__ W word_at(const W* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// The wave's words at p (one a lane). One lane watches its own until it is
-// there; then all read theirs, which were stored together, and only lanes
-// that came too early go on. (All lanes watching took bandwidth from the rows.)
+// w, read from p (one word a lane), if all lanes' are there; else waits. One
+// lane watches its own until it is there; then all read theirs, which were
+// stored together, and only lanes that came too early go on. (All lanes
+// watching took bandwidth from the rows.)
 template <typename W>
-__device__ __forceinline__ W await_word(const W* p) {
+__device__ __forceinline__ W settle_word(const W* p, W w) {
+    if (!__any(w == (W)~(W)0)) return w;
     int polls = 0;
     if ((threadIdx.x & 63) == 0) {
         while (word_at(p) == (W)~(W)0 && ++polls < kMostPolls) __builtin_amdgcn_s_sleep(4);
     }
-    W w = word_at(p);
+    w = word_at(p);
     while (w == (W)~(W)0 && ++polls < kMostPolls) {
         __builtin_amdgcn_s_sleep(1);
         w = word_at(p);
@@ -188,12 +194,12 @@ __device__ __forceinline__ W await_word(const W* p) {
 __device__ __forceinline__ void publish(uint64_t* p, const Run& f) {
     publish_word(p, (uint64_t)__float_as_uint(f.H) << 32 | __float_as_uint(f.A), (uint64_t)kNaN << 32 | kNaN);
 }
-__device__ __forceinline__ Run await(const uint64_t* p) {
-    const uint64_t w = await_word(p);
+__device__ __forceinline__ Run settle(const uint64_t* p, uint64_t w) {
+    w = settle_word(p, w);
     return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
 }
 __device__ __forceinline__ void publish(uint32_t* p, float h) { publish_word(p, __float_as_uint(h), kNaN); }
-__device__ __forceinline__ float await(const uint32_t* p) { return __uint_as_float(await_word(p)); }
+__device__ __forceinline__ float settle(const uint32_t* p, uint32_t w) { return __uint_as_float(settle_word(p, w)); }
 
 // Where a wave works. All but `at` are the same in every lane.
 template <int V>
@@ -264,6 +270,10 @@ template <bool CUT>
 __device__ __forceinline__ float unless_before(float v, uint32_t cut, int i) {
     return CUT ? __uint_as_float(__float_as_uint(v) & (cut & ((2u << i) - 1) ? 0u : ~0u)) : v;
 }
+// Keeps the compiler from holding every row's distance: sixteen 64-bit values a
+// tensor are more than there are scalar registers. From row to row it is one
+// addition.
+__device__ __forceinline__ void hide(int64_t& step) { asm volatile("" : "+s"(step)); }
 // Keeps the compiler from moving work across every kBlock rows: taken all
 // together, the rows' terms fill the registers.
 constexpr int kBlock = 4;
@@ -277,6 +287,7 @@ template <typename T, int V, bool FULL, int SUB>
 __device__ __forceinline__ void load_rows(uint32_t (&out)[SUB], const void* p, int64_t base, int64_t step, int row0,
                                           int len, uint32_t at) {
     const T* q = (const T*)p + base + (FULL ? row0 : max(0, min(row0, len - 1))) * step;
+    hide(step);
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
         out[i] = Lanes<T, V>::load(q, at);
@@ -317,19 +328,30 @@ template <int V>
 __device__ __forceinline__ void exchange(RecLds<V>& lds, const RecurrenceArgs& r, const RecShape& s, const Place<V>& p,
                                          bool followed, const Run (&f)[V]) {
     const int lane = threadIdx.x & 63;
-    const int64_t D = r.channels, c = p.c0 + p.at;
+    // words lie by channel group, one row of 64 for each of a lane's V channels
+    const int64_t D = (int64_t)s.columns * (64 * V), c = p.c0 + lane;
     const int g = p.pos / kGroup, j = p.pos % kGroup, sg = g / kGroup, gj = g % kGroup;
     uint64_t* const word = s.word + ((int64_t)p.b * s.chunks + g * kGroup) * D + c;
     uint64_t* const group = s.group + ((int64_t)p.b * s.groups + sg * kGroup) * D + c;
-    const bool tells = followed && p.wave == 0 && p.mine;
+    const bool tells = followed && p.wave == 0;
     if (tells) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) publish(word + j * D + v, f[v]);
+        for (int v = 0; v < V; ++v) publish(word + j * D + v * 64, f[v]);
     }
     if (!p.pos) return;
+    // all words at once: as a rule they are there
+    const uint32_t* const state = s.state + ((int64_t)p.b * s.supers + sg - 1) * D + c;
+    uint64_t near[V], far[V];
+    uint32_t before[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        near[v] = p.wave < j ? word_at(word + p.wave * D + v * 64) : 0u;
+        far[v] = p.wave < gj ? word_at(group + p.wave * D + v * 64) : 0u;
+        before[v] = p.wave == kWaves - 1 && sg ? word_at(state + v * 64) : 0u;
+    }
     if (p.wave < j) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) lds.chunk[p.wave][lane * V + v] = await(word + p.wave * D + v);
+        for (int v = 0; v < V; ++v) lds.chunk[p.wave][lane * V + v] = settle(word + p.wave * D + v * 64, near[v]);
     }
     if (j == kGroup - 1) {  // the group's run, before anything of earlier groups is waited for
         __syncthreads();
@@ -339,16 +361,15 @@ __device__ __forceinline__ void exchange(RecLds<V>& lds, const RecurrenceArgs& r
                 const int i = lane * V + v;
                 Run all = lds.chunk[0][i];
                 for (int w = 1; w < kGroup - 1; ++w) all = then(all, lds.chunk[w][i]);
-                publish(group + gj * D + v, then(all, f[v]));
+                publish(group + gj * D + v * 64, then(all, f[v]));
             }
         }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int i = lane * V + v;
-        if (p.wave < gj) lds.group[p.wave][i] = await(group + p.wave * D + v);
-        if (p.wave == kWaves - 1)
-            lds.enter[i] = sg ? await(s.state + ((int64_t)p.b * s.supers + sg - 1) * D + c + v) : 0.0f;
+        if (p.wave < gj) lds.group[p.wave][i] = settle(group + p.wave * D + v * 64, far[v]);
+        if (p.wave == kWaves - 1) lds.enter[i] = sg ? settle(state + v * 64, before[v]) : 0.0f;
     }
     __syncthreads();
 }
@@ -367,8 +388,10 @@ __device__ __forceinline__ float entering(const RecLds<V>& lds, const Place<V>& 
 template <int V>
 __device__ __forceinline__ void tell_state(const RecurrenceArgs& r, const RecShape& s, const Place<V>& p, bool followed,
                                            int v, float h) {
-    if (followed && p.mine && p.pos % (kGroup * kGroup) == kGroup * kGroup - 1)
-        publish(s.state + ((int64_t)p.b * s.supers + p.pos / (kGroup * kGroup)) * r.channels + p.c0 + p.at + v, h);
+    if (followed && p.pos % (kGroup * kGroup) == kGroup * kGroup - 1)
+        publish(s.state + ((int64_t)p.b * s.supers + p.pos / (kGroup * kGroup)) * s.columns * (64 * V) + p.c0 + v * 64 +
+                    (threadIdx.x & 63),
+                h);
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT, bool FULL, int SUB>
@@ -439,8 +462,10 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
     }
     if (!p.mine) return;
     T* out = row_of<T, V>(r.h, out0, D, row0);
+    int64_t next = D;
+    hide(next);
 #pragma unroll
-    for (int i = 0; i < SUB; ++i, out += D) {
+    for (int i = 0; i < SUB; ++i, out += next) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float a, u, rest;
@@ -459,7 +484,7 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
-__global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
+__global__ __launch_bounds__(kRecThreads, 6) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
     __shared__ RecLds<V> lds;
     const Place<V> p(r, s, &lds.pos);
     const int t0 = p.pos * kRecChunk, row0 = t0 + p.row * SUB;
@@ -468,8 +493,8 @@ __global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_fwd(RecurrenceArg
     else if (t0 < p.len || p.pos == 0)
         forward<T, V, SIGMOID, CUT, false, SUB>(r, s, lds, p);
     else if (p.mine)  // padding
-        zero_rows<T, V>(r.h, (int64_t)p.b * r.steps * r.channels + p.c0, r.channels, row0, min(row0 + SUB, r.steps),
-                        p.at);
+        zero_rows<T, V>(r.h, (int64_t)p.b * r.steps * r.channels + p.c0, r.channels, row0,
+                        min(row0 + SUB, r.steps), p.at);
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT, bool FULL>
@@ -598,8 +623,10 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     for (int v = 0; v < V; ++v) c[v] = (p.waves > 1 ? lds.start[p.wave][lane * V + v] : 0.0f) + last[v];
     T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + kSub - 1);
     T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + kSub - 1);
+    int64_t next = D;
+    hide(next);
 #pragma unroll
-    for (int i = kSub - 1; i >= 0; --i, dg -= D, dx -= D) {
+    for (int i = kSub - 1; i >= 0; --i, dg -= next, dx -= next) {
         float vg[V], vx[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -666,7 +693,7 @@ size_t layout(int batch, int steps, int channels, int columns, RecShape* s, void
     s->word = s->group = nullptr;
     s->state = s->ticket = nullptr;
     if (s->chunks == 1) return 0;
-    const size_t row = (size_t)batch * channels, words = row * (s->chunks + s->groups), states = row * s->supers;
+    const size_t row = (size_t)batch * (((size_t)channels + 127) / 128 * 128), words = row * (s->chunks + s->groups), states = row * s->supers;
     s->word = (uint64_t*)base;
     s->group = s->word + row * s->chunks;
     s->state = (uint32_t*)(s->word + words);
