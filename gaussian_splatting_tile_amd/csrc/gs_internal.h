@@ -235,7 +235,7 @@ struct RecurrenceArgs {
     void *grad_gate, *grad_x;
     float* grad_h0;
 };
-// Whether the work items of one call (64 channels of 128 steps) can be counted in 31 bits.
+// Whether the work items of one call (64 channels of 128 steps) fit one launch.
 bool recurrence_fits(const gs_recurrence& r);
 size_t recurrence_scratch_bytes(const gs_recurrence& r);
 hipError_t launch_recurrence_fwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream);

@@ -69,13 +69,15 @@ def _recurrence(gate, x, gating, lengths, restart):
     return r, B, T, D
 
 
-def _scratch(lib, r, scratch, device):
+def _scratch(lib, r, scratch, device, stream):
     """The workspace's tensor (kept until the call is enqueued), address and size."""
     if r.steps <= _lib.GS_RECURRENCE_CHUNK:
         return None, None, 0
     if scratch is None:
         need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
         scratch = torch.empty((need,), dtype=torch.uint8, device=device)
+        if stream is not None:  # freed by this function's caller, in the order of the current stream
+            scratch.record_stream(stream)
     return scratch, _ptr(scratch, None, None, "scratch"), scratch.numel() * scratch.element_size()
 
 
@@ -112,7 +114,7 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
         h_last = gate.new_empty(state, dtype=f32)
     if ckpt is None and checkpoints:
         ckpt = gate.new_empty((B, recurrence_ckpt_rows(T), D), dtype=f32)
-    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev, stream)
     _lib.check(lib.gs_recurrence_fwd(
         ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), _ptr(h, whole, gate.dtype, "h"),
         _ptr(h_last, state, f32, "h_last"),
@@ -132,7 +134,7 @@ def recurrence_bwd(gate, x, grad_h, h0=None, ckpt=None, grad_last=None, gating=G
     if out is None:
         out = dict(grad_gate=gate.new_empty(whole), grad_x=gate.new_empty(whole),
                    grad_h0=gate.new_empty(state, dtype=f32))
-    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev, stream)
     _lib.check(lib.gs_recurrence_bwd(
         ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"),
         None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
@@ -192,14 +194,22 @@ class GradList:
         return out
 
 
+def _once(grads, out, stream):
+    """A list for one call, whose workspace outlives the call on its stream."""
+    lst = GradList(grads, out)
+    if stream is not None:
+        lst.scratch.record_stream(stream)
+    return lst
+
+
 def grad_norm(grads, kind=NORM_L2, stream=None):
     """The global norm of a list of gradients (GradList(grads).norm())."""
-    return GradList(grads).norm(kind, stream=stream)
+    return _once(grads, None, stream).norm(kind, stream=stream)
 
 
 def clip_grads(grads, max_norm, kind=NORM_L2, out=None, stream=None):
     """Clips a list of gradients by their global norm, in place or into `out`; returns the norm."""
-    return GradList(grads, out).clip(max_norm, kind, stream=stream)
+    return _once(grads, out, stream).clip(max_norm, kind, stream=stream)
 
 
 class Adam:
@@ -223,6 +233,8 @@ class Adam:
         self.exp_avg_sq = zeros() if exp_avg_sq is None else list(exp_avg_sq)
         if len(self.exp_avg) != n or len(self.exp_avg_sq) != n:
             raise ValueError("exp_avg and exp_avg_sq must hold one tensor for each parameter")
+        if step < 0:
+            raise ValueError("step counts the updates taken before: it is not negative")
         self.steps = torch.full((1,), int(step), dtype=torch.int64, device=dev)
         self.norm = torch.zeros((), dtype=f32, device=dev)
         self._cfg = _lib.GsAdam(float(betas[0]), float(betas[1]), float(eps), float(max_norm),

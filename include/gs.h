@@ -610,7 +610,7 @@ gs_status gs_appearance_bwd(const gs_camera* cam, int32_t n, const float* means,
  *   dtype       GS_F32, GS_BF16 or GS_F16: gate, x, h and their gradients
  *   gating      GS_GATE_LINEAR or GS_GATE_SIGMOID
  *   batch, steps, channels  B, T, D >= 0; each at most 2^30, and
- *               B ceil(D / 64) ceil(T / 128) < 2^31
+ *               B ceil(D / 64) ceil(T / 128) < 2^23 - 1
  *   gate_batch, gate_step, x_batch, x_step  strides of gate and x in
  *               elements, >= 0; channels are contiguous. 0 repeats a value
  *               along that axis (its gradient is still written in full).
@@ -729,7 +729,7 @@ gs_status gs_clip_grads(const gs_grad_tensor* tensors, int32_t n_tensors, int32_
  *   tensors   (host) array of n_tensors descriptions, read during the call:
  *             param (param_dtype) and grad (grad_dtype), each GS_F32, GS_BF16
  *             or GS_F16; m, v float32; lr and weight_decay of this tensor
- *   step      device int64: the updates taken so far; the call adds 1 (it is
+ *   step      device int64 >= 0: the updates taken so far; the call adds 1 (it is
  *             on the device so that a recorded graph counts its replays)
  *   norm      out [1] float32 (device): the global norm before clipping, or
  *             NULL. It is formed only if norm, max_norm or the flag asks.

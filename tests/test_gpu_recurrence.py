@@ -257,6 +257,22 @@ def test_recurrence_is_deterministic_and_uses_its_stream():
             assert torch.equal(first["ckpt"][b, :rows], again["ckpt"][b, :rows])
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 70), ("bf16", 130), ("f16", 33)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("T", [300, 128 * 67 + 5])
+def test_recurrence_without_waiting_gives_the_same_bits(monkeypatch, dtype, D, sigmoid, T):
+    """A chunk that finds nothing of what the chunks before it publish computes it from the
+    inputs: forced for every chunk, over more than one group of groups, it changes no bit."""
+    say(f"[recurrence alone {dtype} D={D} T={T} sigmoid={sigmoid}]")
+    host, dev = _inputs(T + D, 2, T, D, dtype, sigmoid, ragged=False, restarts=T == 300, remember=4.0)
+    keys = ("h", "h_last", "grad_gate", "grad_x", "grad_h0", "ckpt")
+    want = _run(dev, sigmoid)
+    monkeypatch.setenv("GS_RECURRENCE_PATIENCE", "0")
+    got = _run(dev, sigmoid)
+    for k in keys:
+        assert (want[k] == got[k]).all(), k
+
+
 def test_recurrence_in_a_graph():
     """Recorded once and replayed on changing inputs, with eager work between the replays."""
     import torch

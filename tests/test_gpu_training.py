@@ -247,6 +247,24 @@ def test_training_calls_are_deterministic_and_use_their_stream():
         assert all(torch.equal(a, b) for a, b in zip(first[1] + first[2], outs + P))
 
 
+def test_training_calls_on_a_given_stream():
+    """A stream argument that is not the current stream, workspaces that the call allocates."""
+    import torch
+    import gaussian_splatting_tile_amd as gs
+    say("[training other stream]")
+    side = torch.cuda.Stream()
+    g = [torch.randn(100_000, device="cuda"), torch.randn(77, device="cuda")]
+    x = torch.randn((1, 400, 70), device="cuda")
+    want_n, want_h = gs.grad_norm(g), gs.recurrence_fwd(x, x, gating=gs.GATE_SIGMOID)["h"]
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        n = gs.grad_norm(g, stream=side)
+        h = gs.recurrence_fwd(x, x, gating=gs.GATE_SIGMOID, stream=side)["h"]
+        torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda")  # what the current stream allocates next
+        side.synchronize()
+        assert torch.equal(n, want_n) and torch.equal(h, want_h)
+
+
 def test_training_calls_in_a_graph():
     """A recorded step counts its replays and follows its buffers."""
     import torch
@@ -331,6 +349,8 @@ def test_training_calls_refuse():
             gs.Adam([g.clone()], [g], **kw).step()
     with pytest.raises(ValueError):
         gs.Adam([g], [torch.zeros((9,), device="cuda")])
+    with pytest.raises(ValueError):
+        gs.Adam([g], [g], step=-1)
     with pytest.raises(ValueError):
         gs.Adam([g], [g], lr=[1.0, 2.0])
     with pytest.raises(TypeError):

@@ -61,9 +61,9 @@ def test_recurrence_scratch_size(gs):
     assert size(dtype=9, steps=1000) == 0 and size(steps=-1) == 0
     assert gs.gs_recurrence_scratch_bytes(None) == 0
     # a word per channel of each chunk and of each 8 chunks, a state per 64 chunks (channels in
-    # rows of 128), and a counter per 64 channels
-    assert size(batch=3, steps=129, channels=65) == 3 * (2 * 128 * 8 + 128 * 8 + 128 * 4 + 2 * 4)
-    assert size(batch=1, steps=128 * 65, channels=64) == 65 * 128 * 8 + 9 * 128 * 8 + 2 * 128 * 4 + 4
+    # rows of 128)
+    assert size(batch=3, steps=129, channels=65) == 3 * (2 * 128 * 8 + 128 * 8 + 128 * 4)
+    assert size(batch=1, steps=128 * 65, channels=64) == 65 * 128 * 8 + 9 * 128 * 8 + 2 * 128 * 4
     from gaussian_splatting_tile_amd import _lib
     r = _rec(steps=129, gate_batch=0, x_batch=0)
     need = gs.gs_recurrence_scratch_bytes(ctypes.byref(r))
