@@ -60,6 +60,7 @@ struct RecShape {
     int supers;      // of kGroup groups
     int columns;     // groups of 64 V channels
     int steps_log2;  // waves of a workgroup along the steps (1 << steps_log2)
+    bool lines;      // every row of every tensor is whole 128-byte lines
     // rows of columns * 64 V, see exchange()
     uint64_t* word;    // [batch][chunks][row] (A, H) or (A, C) of a chunk
     uint64_t* group;   // [batch][groups][row] of a group
@@ -67,39 +68,56 @@ struct RecShape {
     int patience;      // polls; 0: waits for nothing and computes every word itself
 };
 
-// A lane's V channels of one row, packed in 32 bits. Rows go past the caches
-// (NT): nothing is read twice, and without it the pure copy of a sequence's
-// rows reaches 3.7 TB/s, with it 5.6 (65536 x 1024 bf16, two in, one out).
+// A lane's V channels of one row, packed in 32 bits. Rows can go past the
+// caches (PAST): nothing is read twice, and the pure copy of a sequence's rows
+// reaches 3.7 TB/s without it and 5.6 with it (65536 x 1024 bf16, two in, one
+// out). That holds for rows that are whole 128-byte lines: others share lines
+// with their neighbours, and are read the common way (8 x 2048 x 2047 float32
+// forward 145 us past the caches, 92 through them). A wave's rows of single
+// 16-bit channels are one line, read the common way always (16 x 2048 x 1024
+// bf16 backward 74 us past the caches, 54 through them) and written past them
+// if they are whole lines (54 and 66 us; 16 x 2049 x 1025: 115 and 98).
 template <typename T, int V>
 struct Lanes;
 template <>
 struct Lanes<float, 1> {
+    template <bool PAST>
     static __device__ __forceinline__ uint32_t load(const float* p, uint32_t i) {
-        return __builtin_nontemporal_load((const uint32_t*)p + i);
+        const uint32_t* const q = (const uint32_t*)p + i;
+        return PAST ? __builtin_nontemporal_load(q) : *q;
     }
     static __device__ __forceinline__ float get(uint32_t r, int) { return __uint_as_float(r); }
+    template <bool PAST>
     static __device__ __forceinline__ void store(float* p, uint32_t i, const float (&v)[1]) {
         __builtin_nontemporal_store(v[0], p + i);
     }
 };
 template <typename T>
 struct Lanes<T, 1> {
+    template <bool PAST>
     static __device__ __forceinline__ uint32_t load(const T* p, uint32_t i) {
-        return __builtin_nontemporal_load((const uint16_t*)p + i);
+        return ((const uint16_t*)p)[i];
     }
     static __device__ __forceinline__ float get(uint32_t r, int) { return (float)__builtin_bit_cast(T, (uint16_t)r); }
+    template <bool PAST>
     static __device__ __forceinline__ void store(T* p, uint32_t i, const float (&v)[1]) {
-        __builtin_nontemporal_store((T)v[0], p + i);
+        if (PAST)
+            __builtin_nontemporal_store((T)v[0], p + i);
+        else
+            p[i] = (T)v[0];
     }
 };
 template <typename T>
 struct Lanes<T, 2> {
+    template <bool PAST>
     static __device__ __forceinline__ uint32_t load(const T* p, uint32_t i) {
-        return __builtin_nontemporal_load((const uint32_t*)(p + i));
+        const uint32_t* const q = (const uint32_t*)(p + i);
+        return PAST ? __builtin_nontemporal_load(q) : *q;
     }
     static __device__ __forceinline__ float get(uint32_t r, int j) {
         return (float)__builtin_bit_cast(T, (uint16_t)(j ? r >> 16 : r));
     }
+    template <bool PAST>
     static __device__ __forceinline__ void store(T* p, uint32_t i, const float (&v)[2]) {
         typedef T Pair __attribute__((ext_vector_type(2)));
         const Pair r = {(T)v[0], (T)v[1]};
@@ -287,29 +305,44 @@ __device__ __forceinline__ void end_of_row(int i) {
 // Loads the wave's rows of one tensor of a sequence whose first element is
 // at `base`. Rows that are not there (unless FULL) repeat the last step that
 // is, or step 0 of an empty sequence: no branch, and nothing out of bounds.
-template <typename T, int V, bool FULL, int SUB>
+template <typename T, int V, bool FULL, bool PAST, int SUB>
 __device__ __forceinline__ void load_rows(uint32_t (&out)[SUB], const void* p, int64_t base, int64_t step, int row0,
                                           int len, uint32_t at) {
     const T* q = (const T*)p + base + (FULL ? row0 : max(0, min(row0, len - 1))) * step;
     hide(step);
 #pragma unroll
     for (int i = 0; i < SUB; ++i) {
-        out[i] = Lanes<T, V>::load(q, at);
+        out[i] = Lanes<T, V>::template load<PAST>(q, at);
         if (FULL || row0 + i + 1 < len) q += step;
     }
 }
+
 // A row of a [T][channels] output of a sequence.
 template <typename T, int V>
 __device__ __forceinline__ T* row_of(void* p, int64_t base, int64_t channels, int row) {
     return (T*)p + base + row * channels;
 }
 
+// Calls f(PAST) by how rows of this kind are written (see Lanes).
+template <typename T, int V, typename F>
+__device__ __forceinline__ void by_lines(bool lines, F f) {
+    if (sizeof(T) == 2 && V == 1 && !lines) {
+        f(std::false_type());
+    } else {
+        asm volatile("");  // else the compiler makes one way of the two, through the caches
+        f(std::true_type());
+    }
+}
+
 // Zeroes rows [from, to) of a [T][channels] output of a sequence.
 template <typename T, int V>
-__device__ __forceinline__ void zero_rows(void* p, int64_t base, int64_t channels, int from, int to, uint32_t at) {
+__device__ __forceinline__ void zero_rows(void* p, int64_t base, int64_t channels, int from, int to, uint32_t at,
+                                          bool lines) {
     const float zero[V] = {};
-    T* q = row_of<T, V>(p, base, channels, from);
-    for (int t = from; t < to; ++t, q += channels) Lanes<T, V>::store(q, at, zero);
+    by_lines<T, V>(lines, [&](auto past) {
+        T* q = row_of<T, V>(p, base, channels, from);
+        for (int t = from; t < to; ++t, q += channels) Lanes<T, V>::template store<past.value>(q, at, zero);
+    });
 }
 
 // LDS of a workgroup: one run per wave and channel, the runs of the groups
@@ -491,8 +524,14 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
     const int64_t out0 = (int64_t)p.b * r.steps * D + p.c0, state0 = (int64_t)p.b * D + p.c0 + p.at;
     const int rows = FULL ? SUB : max(0, min(p.len - row0, SUB));
     uint32_t gate[SUB], x[SUB];
-    load_rows<T, V, FULL>(gate, r.gate, p.b * r.gate_batch + p.c0, r.gate_step, row0, p.len, p.at);
-    load_rows<T, V, FULL>(x, r.x, p.b * r.x_batch + p.c0, r.x_step, row0, p.len, p.at);
+    const int64_t gate0 = p.b * r.gate_batch + p.c0, x0 = p.b * r.x_batch + p.c0;
+    if (s.lines) {
+        load_rows<T, V, FULL, true>(gate, r.gate, gate0, r.gate_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, true>(x, r.x, x0, r.x_step, row0, p.len, p.at);
+    } else {
+        load_rows<T, V, FULL, false>(gate, r.gate, gate0, r.gate_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, false>(x, r.x, x0, r.x_step, row0, p.len, p.at);
+    }
     float h[V];  // the state in front of the sequence, then of the wave's steps
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = p.pos == 0 && p.row == 0 && r.h0 ? r.h0[state0 + v] : 0.0f;
@@ -561,10 +600,10 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
             row_terms<T, V, SIGMOID, FULL>(gate, x, i, v, rows, a, u, rest);
             h[v] = fmaf(unless_at<CUT>(a, cut, i), unless_at<CUT>(h[v], cut, i), u);
         }
-        if (FULL || i < rows) Lanes<T, V>::store(out, p.at, h);
+        if (FULL || i < rows) Lanes<T, V>::template store<(V > 1 || sizeof(T) > 2)>(out, p.at, h);
         end_of_row(i);
     }
-    if (!FULL) zero_rows<T, V>(r.h, out0, D, row0 + rows, min(row0 + SUB, r.steps), p.at);
+    if (!FULL) zero_rows<T, V>(r.h, out0, D, row0 + rows, min(row0 + SUB, r.steps), p.at, s.lines);
     // the wave with the last step, or the first one of an empty sequence
     if (r.h_last && (rows ? row0 + rows == p.len : p.row == 0 && p.len == 0)) {
 #pragma unroll
@@ -583,7 +622,7 @@ __global__ __launch_bounds__(kRecThreads, 6) void k_recurrence_fwd(RecurrenceArg
         forward<T, V, SIGMOID, CUT, false, SUB>(r, s, lds, p);
     else if (p.mine)  // padding
         zero_rows<T, V>(r.h, (int64_t)p.b * r.steps * r.channels + p.c0, r.channels, row0,
-                        min(row0 + SUB, r.steps), p.at);
+                        min(row0 + SUB, r.steps), p.at, s.lines);
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT, bool FULL>
@@ -597,9 +636,16 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     const bool starts = k == 0 && p.row == 0;
     const int rows = FULL ? kSub : max(0, min(p.len - row0, kSub));
     uint32_t gate[kSub], x[kSub], g[kSub];
-    load_rows<T, V, FULL>(gate, r.gate, p.b * r.gate_batch + p.c0, r.gate_step, row0, p.len, p.at);
-    load_rows<T, V, FULL>(x, r.x, p.b * r.x_batch + p.c0, r.x_step, row0, p.len, p.at);
-    load_rows<T, V, FULL>(g, r.grad_h, out0, D, row0, p.len, p.at);
+    const int64_t gate0 = p.b * r.gate_batch + p.c0, x0 = p.b * r.x_batch + p.c0;
+    if (s.lines) {
+        load_rows<T, V, FULL, true>(gate, r.gate, gate0, r.gate_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, true>(x, r.x, x0, r.x_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, true>(g, r.grad_h, out0, D, row0, p.len, p.at);
+    } else {
+        load_rows<T, V, FULL, false>(gate, r.gate, gate0, r.gate_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, false>(x, r.x, x0, r.x_step, row0, p.len, p.at);
+        load_rows<T, V, FULL, false>(g, r.grad_h, out0, D, row0, p.len, p.at);
+    }
     const bool ends = rows ? row0 + rows == p.len : starts && p.len == 0;  // has the last step
     const bool leads = p.row == p.waves - 1;  // hands the waves of these channels their states
     float h[V], last[V];
@@ -710,34 +756,36 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     float c[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) c[v] = (p.waves > 1 ? lds.start[p.wave][lane * V + v] : 0.0f) + last[v];
-    T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + kSub - 1);
-    T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + kSub - 1);
-    int64_t next = D;
-    hide(next);
+    by_lines<T, V>(s.lines, [&](auto past) {
+        T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + kSub - 1);
+        T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + kSub - 1);
+        int64_t next = D;
+        hide(next);
 #pragma unroll
-    for (int i = kSub - 1; i >= 0; --i, dg -= next, dx -= next) {
-        float vg[V], vx[V];
+        for (int i = kSub - 1; i >= 0; --i, dg -= next, dx -= next) {
+            float vg[V], vx[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float a, rest = 1.0f;
-            if (SIGMOID)
-                of_exp_minus(e[i][v], a, rest);
-            else
-                a = Lanes<T, V>::get(gate[i], v);
-            const float d = row_grad<T, V, FULL>(g, i, v, rows) + c[v];
-            vg[v] = d * weight[i][v];
-            vx[v] = SIGMOID ? d * rest : d;
-            if (FULL || i < rows) c[v] = unless_at<CUT>(a * d, cut, i);
+            for (int v = 0; v < V; ++v) {
+                float a, rest = 1.0f;
+                if (SIGMOID)
+                    of_exp_minus(e[i][v], a, rest);
+                else
+                    a = Lanes<T, V>::get(gate[i], v);
+                const float d = row_grad<T, V, FULL>(g, i, v, rows) + c[v];
+                vg[v] = d * weight[i][v];
+                vx[v] = SIGMOID ? d * rest : d;
+                if (FULL || i < rows) c[v] = unless_at<CUT>(a * d, cut, i);
+            }
+            if (FULL || i < rows) {
+                Lanes<T, V>::template store<past.value>(dg, p.at, vg);
+                Lanes<T, V>::template store<past.value>(dx, p.at, vx);
+            }
+            end_of_row(kSub - 1 - i);
         }
-        if (FULL || i < rows) {
-            Lanes<T, V>::store(dg, p.at, vg);
-            Lanes<T, V>::store(dx, p.at, vx);
-        }
-        end_of_row(kSub - 1 - i);
-    }
+    });
     if (!FULL) {
-        zero_rows<T, V>(r.grad_gate, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at);
-        zero_rows<T, V>(r.grad_x, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at);
+        zero_rows<T, V>(r.grad_gate, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_x, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at, s.lines);
     }
     if (r.grad_h0 && starts) {
 #pragma unroll
@@ -759,8 +807,8 @@ __global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_bwd(RecurrenceArg
         backward<T, V, SIGMOID, CUT, false>(r, s, lds, wave_c, start_h, p, k);
     } else if (p.mine) {  // padding
         const int64_t out0 = (int64_t)p.b * r.steps * r.channels + p.c0;
-        zero_rows<T, V>(r.grad_gate, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at);
-        zero_rows<T, V>(r.grad_x, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at);
+        zero_rows<T, V>(r.grad_gate, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_x, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at, s.lines);
     }
 }
 
@@ -800,10 +848,22 @@ __global__ void k_recurrence_clear(uint32_t* p, size_t words) {
     }
 }
 
+// The low bits of where the rows of any tensor start: of the tensors' addresses
+// and (in elements) of the distances between rows.
+uint64_t starts_of(const RecurrenceArgs& r) {
+    return (uint64_t)r.gate | (uint64_t)r.x | (uint64_t)r.h | (uint64_t)r.grad_h | (uint64_t)r.grad_gate |
+           (uint64_t)r.grad_x;
+}
+uint64_t strides_of(const RecurrenceArgs& r) {
+    return (uint64_t)r.channels | (uint64_t)(r.gate_batch | r.gate_step | r.x_batch | r.x_step);
+}
+
 // Lays out the launch (and clears its workspace); gives its workgroups.
 template <int V>
-hipError_t prepare(const RecurrenceArgs& r, void* scratch, RecShape* s, unsigned* blocks, hipStream_t stream) {
+hipError_t prepare(const RecurrenceArgs& r, int bytes_each, void* scratch, RecShape* s, unsigned* blocks,
+                   hipStream_t stream) {
     const size_t bytes = layout(r.batch, r.steps, r.channels, (r.channels + 64 * V - 1) / (64 * V), s, scratch);
+    s->lines = !((starts_of(r) | (strides_of(r) * bytes_each)) & 127);
     if (s->chunks == 1) {
         const int across = kWaves >> s->steps_log2;
         *blocks = (unsigned)r.batch * ((s->columns + across - 1) / across);
@@ -821,7 +881,7 @@ struct Forward {
     static hipError_t launch(const RecurrenceArgs& r, void* scratch, hipStream_t stream) {
         RecShape s;
         unsigned blocks;
-        if (hipError_t e = prepare<V>(r, scratch, &s, &blocks, stream)) return e;
+        if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
         if (r.steps == 1)  // serving: no row but the one
             k_recurrence_fwd<T, V, SIGMOID, CUT, 1><<<blocks, kRecThreads, 0, stream>>>(r, s);
         else
@@ -834,7 +894,7 @@ struct Backward {
     static hipError_t launch(const RecurrenceArgs& r, void* scratch, hipStream_t stream) {
         RecShape s;
         unsigned blocks;
-        if (hipError_t e = prepare<V>(r, scratch, &s, &blocks, stream)) return e;
+        if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
         k_recurrence_bwd<T, V, SIGMOID, CUT><<<blocks, kRecThreads, 0, stream>>>(r, s);
         return hipGetLastError();
     }
@@ -850,11 +910,7 @@ hipError_t launch_of(const RecurrenceArgs& r, bool sigmoid, void* scratch, hipSt
 }
 
 // Two 16-bit channels a lane need every row of every tensor on a 4-byte boundary.
-bool pairs_fit(const RecurrenceArgs& r) {
-    const uintptr_t p = (uintptr_t)r.gate | (uintptr_t)r.x | (uintptr_t)r.h;
-    const int64_t n = r.channels | r.gate_batch | r.gate_step | r.x_batch | r.x_step;
-    return !(p & 3) && !(n & 1);
-}
+bool pairs_fit(const RecurrenceArgs& r) { return !((starts_of(r) | (strides_of(r) * 2)) & 3); }
 
 // No steps at all: the state, or its gradient, passes through.
 hipError_t pass_through(const RecurrenceArgs& r, const float* from, float* to, hipStream_t stream) {

@@ -110,14 +110,19 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
         h, h_last, ckpt = out.get("h"), out.get("h_last"), out.get("ckpt")
     if h is None:
         h = gate.new_empty(whole)
+        ph = h.data_ptr()
+    else:
+        ph = _ptr(h, whole, gate.dtype, "h")
     if h_last is None:
         h_last = gate.new_empty(state, dtype=f32)
+        pl = h_last.data_ptr()
+    else:
+        pl = _ptr(h_last, state, f32, "h_last")
     if ckpt is None and checkpoints:
         ckpt = gate.new_empty((B, recurrence_ckpt_rows(T), D), dtype=f32)
     scratch, ps, nbytes = _scratch(lib, r, scratch, dev, stream)
     _lib.check(lib.gs_recurrence_fwd(
-        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), _ptr(h, whole, gate.dtype, "h"),
-        _ptr(h_last, state, f32, "h_last"),
+        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), ph, pl,
         None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), ps, nbytes,
         _stream(stream, dev)))
     return dict(h=h, h_last=h_last, ckpt=ckpt)
@@ -176,20 +181,23 @@ class GradList:
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=self.device)
         self._pscratch = self.scratch.data_ptr()
 
+    def _norm(self, out):
+        if out is not None:
+            return out, _ptr(out, (), torch.float32, "out")
+        out = torch.empty((), dtype=torch.float32, device=self.device)
+        return out, out.data_ptr()
+
     def norm(self, kind=NORM_L2, out=None, stream=None):
         """gs_grad_norm: the global norm, a float32 tensor of no dimensions on the device."""
-        if out is None:
-            out = torch.empty((), dtype=torch.float32, device=self.device)
-        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), _ptr(out, (), torch.float32, "out"),
-                                          self._pscratch, _stream(stream, self.device)))
+        out, po = self._norm(out)
+        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), po, self._pscratch,
+                                          _stream(stream, self.device)))
         return out
 
     def clip(self, max_norm, kind=NORM_L2, out=None, stream=None):
         """gs_clip_grads: scales by min(1, max_norm / (norm + 1e-6)); returns the norm before."""
-        if out is None:
-            out = torch.empty((), dtype=torch.float32, device=self.device)
-        _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm),
-                                           _ptr(out, (), torch.float32, "out"), self._pscratch,
+        out, po = self._norm(out)
+        _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm), po, self._pscratch,
                                            _stream(stream, self.device)))
         return out
 
