@@ -46,6 +46,9 @@ namespace {
 
 constexpr int kRecChunk = GS_RECURRENCE_CHUNK;
 constexpr int kSub = 16;
+// Rows a thread holds where a sequence has no more (and 1 forward for T = 1):
+// the rows up to kSub would be loads and steps for nothing.
+constexpr int kFew = 4;
 constexpr int kWaves = 8;
 constexpr int kRecThreads = 64 * kWaves;
 constexpr int kGroup = kWaves;  // a wave fetches one word of either level, the last one the state
@@ -536,7 +539,7 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v] = p.pos == 0 && p.row == 0 && r.h0 ? r.h0[state0 + v] : 0.0f;
     const uint32_t cut = CUT ? restarts<SUB>(r, p.b, row0, p.len) : 0u;
-    if (p.waves > 1) {
+    if (SUB == kSub && p.waves > 1) {  // fewer rows a thread: fewer steps than a wave holds
         Run own[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) own[v] = {1.0f, 0.0f};
@@ -625,17 +628,17 @@ __global__ __launch_bounds__(kRecThreads, 6) void k_recurrence_fwd(RecurrenceArg
                         min(row0 + SUB, r.steps), p.at, s.lines);
 }
 
-template <typename T, int V, bool SIGMOID, bool CUT, bool FULL>
+template <typename T, int V, bool SIGMOID, bool CUT, bool FULL, int SUB>
 __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape& s, RecLds<V>& lds,
                                          float (&wave_c)[kWaves][64 * V], float (&start_h)[kWaves][64 * V],
                                          const Place<V>& p, int k) {
     const int lane = threadIdx.x & 63;
     const int64_t D = r.channels;
-    const int t0 = k * kRecChunk, row0 = t0 + p.row * kSub;
+    const int t0 = k * kRecChunk, row0 = t0 + p.row * SUB;
     const int64_t out0 = (int64_t)p.b * r.steps * D + p.c0, state0 = (int64_t)p.b * D + p.c0 + p.at;
     const bool starts = k == 0 && p.row == 0;
-    const int rows = FULL ? kSub : max(0, min(p.len - row0, kSub));
-    uint32_t gate[kSub], x[kSub], g[kSub];
+    const int rows = FULL ? SUB : max(0, min(p.len - row0, SUB));
+    uint32_t gate[SUB], x[SUB], g[SUB];
     const int64_t gate0 = p.b * r.gate_batch + p.c0, x0 = p.b * r.x_batch + p.c0;
     if (s.lines) {
         load_rows<T, V, FULL, true>(gate, r.gate, gate0, r.gate_step, row0, p.len, p.at);
@@ -657,9 +660,9 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
                       : 0.0f;
         last[v] = ends && r.grad_last ? r.grad_last[state0 + v] : 0.0f;
     }
-    const uint32_t cut = CUT ? restarts<kSub>(r, p.b, row0, p.len) : 0u;
+    const uint32_t cut = CUT ? restarts<SUB>(r, p.b, row0, p.len) : 0u;
     const bool followed = k > 0;
-    if (p.waves > 1) {
+    if (SUB == kSub && p.waves > 1) {
         // the wave's run of the states, (A, H), and of what it passes back, (A, C)
         Run own[V];
         float C[V];
@@ -669,7 +672,7 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
             C[v] = 0.0f;
         }
 #pragma unroll
-        for (int i = 0; i < kSub; ++i) {
+        for (int i = 0; i < SUB; ++i) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 float a, u, rest;
@@ -734,9 +737,9 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     // Walk the states, keeping what step i's gradients take: weight, by which
     // d_i is grad_gate_i, and (SIGMOID) e = exp(-gate), of which a and 1 - a
     // are cheap; then walk back.
-    float weight[kSub][V], e[kSub][V];
+    float weight[SUB][V], e[SUB][V];
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
+    for (int i = 0; i < SUB; ++i) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float a = Lanes<T, V>::get(gate[i], v), u = Lanes<T, V>::get(x[i], v);
@@ -755,14 +758,14 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     }
     float c[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) c[v] = (p.waves > 1 ? lds.start[p.wave][lane * V + v] : 0.0f) + last[v];
+    for (int v = 0; v < V; ++v) c[v] = (SUB == kSub && p.waves > 1 ? lds.start[p.wave][lane * V + v] : 0.0f) + last[v];
     by_lines<T, V>(s.lines, [&](auto past) {
-        T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + kSub - 1);
-        T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + kSub - 1);
+        T* dg = row_of<T, V>(r.grad_gate, out0, D, row0 + SUB - 1);
+        T* dx = row_of<T, V>(r.grad_x, out0, D, row0 + SUB - 1);
         int64_t next = D;
         hide(next);
 #pragma unroll
-        for (int i = kSub - 1; i >= 0; --i, dg -= next, dx -= next) {
+        for (int i = SUB - 1; i >= 0; --i, dg -= next, dx -= next) {
             float vg[V], vx[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -780,12 +783,12 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
                 Lanes<T, V>::template store<past.value>(dg, p.at, vg);
                 Lanes<T, V>::template store<past.value>(dx, p.at, vx);
             }
-            end_of_row(kSub - 1 - i);
+            end_of_row(SUB - 1 - i);
         }
     });
     if (!FULL) {
-        zero_rows<T, V>(r.grad_gate, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at, s.lines);
-        zero_rows<T, V>(r.grad_x, out0, D, row0 + rows, min(row0 + kSub, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_gate, out0, D, row0 + rows, min(row0 + SUB, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_x, out0, D, row0 + rows, min(row0 + SUB, r.steps), p.at, s.lines);
     }
     if (r.grad_h0 && starts) {
 #pragma unroll
@@ -793,22 +796,22 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
     }
 }
 
-template <typename T, int V, bool SIGMOID, bool CUT>
+template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
 __global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_bwd(RecurrenceArgs r, RecShape s) {
     __shared__ RecLds<V> lds;
     __shared__ float wave_c[kWaves][64 * V], start_h[kWaves][64 * V];
     const Place<V> p(r, s);
     const int used = (p.len + kRecChunk - 1) / kRecChunk;  // chunks with steps: taken from the last on
     const int k = p.pos < used ? used - 1 - p.pos : p.pos;
-    const int t0 = k * kRecChunk, row0 = t0 + p.row * kSub;
-    if (t0 + p.waves * kSub <= p.len) {
-        backward<T, V, SIGMOID, CUT, true>(r, s, lds, wave_c, start_h, p, k);
+    const int t0 = k * kRecChunk, row0 = t0 + p.row * SUB;
+    if (t0 + p.waves * SUB <= p.len) {
+        backward<T, V, SIGMOID, CUT, true, SUB>(r, s, lds, wave_c, start_h, p, k);
     } else if (t0 < p.len || k == 0) {
-        backward<T, V, SIGMOID, CUT, false>(r, s, lds, wave_c, start_h, p, k);
+        backward<T, V, SIGMOID, CUT, false, SUB>(r, s, lds, wave_c, start_h, p, k);
     } else if (p.mine) {  // padding
         const int64_t out0 = (int64_t)p.b * r.steps * r.channels + p.c0;
-        zero_rows<T, V>(r.grad_gate, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at, s.lines);
-        zero_rows<T, V>(r.grad_x, out0, r.channels, row0, min(row0 + kSub, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_gate, out0, r.channels, row0, min(row0 + SUB, r.steps), p.at, s.lines);
+        zero_rows<T, V>(r.grad_x, out0, r.channels, row0, min(row0 + SUB, r.steps), p.at, s.lines);
     }
 }
 
@@ -884,6 +887,8 @@ struct Forward {
         if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
         if (r.steps == 1)  // serving: no row but the one
             k_recurrence_fwd<T, V, SIGMOID, CUT, 1><<<blocks, kRecThreads, 0, stream>>>(r, s);
+        else if (r.steps <= kFew)
+            k_recurrence_fwd<T, V, SIGMOID, CUT, kFew><<<blocks, kRecThreads, 0, stream>>>(r, s);
         else
             k_recurrence_fwd<T, V, SIGMOID, CUT, kSub><<<blocks, kRecThreads, 0, stream>>>(r, s);
         return hipGetLastError();
@@ -895,7 +900,10 @@ struct Backward {
         RecShape s;
         unsigned blocks;
         if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
-        k_recurrence_bwd<T, V, SIGMOID, CUT><<<blocks, kRecThreads, 0, stream>>>(r, s);
+        if (r.steps <= kFew)
+            k_recurrence_bwd<T, V, SIGMOID, CUT, kFew><<<blocks, kRecThreads, 0, stream>>>(r, s);
+        else
+            k_recurrence_bwd<T, V, SIGMOID, CUT, kSub><<<blocks, kRecThreads, 0, stream>>>(r, s);
         return hipGetLastError();
     }
 };

@@ -75,7 +75,7 @@ def _check(out, ref, what):
                                bound[bad][:3])
 
 
-SHAPES = [(1, 1, 1), (3, 1, 130), (2, 2, 63), (1, 15, 64), (2, 16, 65), (3, 17, 128), (2, 31, 3), (2, 33, 200),
+SHAPES = [(1, 1, 1), (3, 1, 130), (2, 2, 63), (3, 3, 140), (2, 4, 66), (4, 5, 64), (1, 15, 64), (2, 16, 65), (3, 17, 128), (2, 31, 3), (2, 33, 200),
           (1, 64, 257), (2, 65, 66), (3, 127, 70), (3, 128, 64), (4, 129, 37), (1, 255, 130), (4, 300, 96), (2, 1025, 5),
           (1, 4609, 3), (5, 777, 129)]
 
