@@ -103,6 +103,32 @@ def test_norm_and_clip_parity(which, mix):
         _close(to_np(g.double()), h * c, tr.stored(h * c, 3 * EPS * np.abs(h * c), d), "in place")
 
 
+@pytest.mark.parametrize("name", ["mlp", "large"])
+def test_clip_in_place_below_the_norm_keeps_the_bits(name):
+    """A factor of 1: gradients in place stay as they are, others are copied; above the
+    norm's bound the same list is scaled everywhere."""
+    import torch
+    import gaussian_splatting_tile_amd as gs
+    say("[clip in place]", name)
+    types = _types("mixed", len(LISTS[name]))
+    grads = _grads(7, LISTS[name], types)
+    grads[0][:3] = torch.tensor([-0.0, 1e-40, 0.0])  # (1e-40 is subnormal)
+    before = [g.clone() for g in grads]
+    outs = [g if i % 2 == 0 else torch.full_like(g, 7.0) for i, g in enumerate(grads)]
+    norm = tr.grad_norm([to_np(g.double()) for g in grads])
+    lst = gs.GradList(grads, out=outs)
+    lst.clip(float(4.0 * norm))
+    torch.cuda.synchronize()
+    for g, o, b in zip(grads, outs, before):
+        bits = torch.int32 if g.dtype == torch.float32 else torch.int16
+        assert torch.equal(g.view(bits), b.view(bits)) and torch.equal(o.view(bits), b.view(bits))
+    lst.clip(float(0.5 * norm))
+    torch.cuda.synchronize()
+    c = tr.clip_factor(norm, np.float32(0.5 * norm))
+    for o, b, d in zip(outs, before, types):
+        h = to_np(b.double())
+        _close(to_np(o.double()), h * c, tr.stored(h * c, 3 * EPS * np.abs(h * c), d), "scaled")
+
 def test_norm_of_extreme_values():
     import torch
     import gaussian_splatting_tile_amd as gs
