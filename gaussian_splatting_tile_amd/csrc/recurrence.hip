@@ -131,9 +131,10 @@ struct Lanes<T, 2> {
 // sigmoid(z) and 1 - sigmoid(z), each without cancellation: with e = exp(-z)
 // kept below the largest float they are 1 / (1 + e) and e / (1 + e). The
 // hardware's exponential and reciprocal are within an ulp; the product
-// z log2(e) adds a relative |z| 2^-24.
+// z log2(e) adds a relative |z| 2^-24. A NaN passes the bound (a plain minimum
+// would drop it, and a diverged gate with it).
 __device__ __forceinline__ float exp_minus(float z) {
-    return fminf(__builtin_amdgcn_exp2f(z * -1.44269504f), 1e38f);
+    return __builtin_elementwise_minimum(__builtin_amdgcn_exp2f(z * -1.44269504f), 1e38f);
 }
 __device__ __forceinline__ void of_exp_minus(float e, float& a, float& rest) {
     a = __builtin_amdgcn_rcpf(1.0f + e);
