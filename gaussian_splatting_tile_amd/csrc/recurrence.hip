@@ -129,16 +129,17 @@ struct Lanes<T, 2> {
 };
 
 // sigmoid(z) and 1 - sigmoid(z), each without cancellation: with e = exp(-z)
-// kept below the largest float they are 1 / (1 + e) and e / (1 + e). The
-// hardware's exponential and reciprocal are within an ulp; the product
-// z log2(e) adds a relative |z| 2^-24. A NaN passes the bound (a plain minimum
-// would drop it, and a diverged gate with it).
-__device__ __forceinline__ float exp_minus(float z) {
-    return __builtin_elementwise_minimum(__builtin_amdgcn_exp2f(z * -1.44269504f), 1e38f);
-}
+// they are 1 / (1 + e) and e / (1 + e). The hardware's exponential and
+// reciprocal are within an ulp; the product z log2(e) adds a relative |z| 2^-24.
+// Results below 2^-126 are flushed to 0 by both. For z below -86.6 that (or an
+// e of infinity) leaves e times the reciprocal far from 1, so its factors stop
+// at 2^125 and 2^-125: the second value is then 1, and the first is on its way
+// to 0 unhindered (z = -inf is a complete forget). The maximum passes a NaN; a
+// plain one would drop it, and a diverged gate with it.
+__device__ __forceinline__ float exp_minus(float z) { return __builtin_amdgcn_exp2f(z * -1.44269504f); }
 __device__ __forceinline__ void of_exp_minus(float e, float& a, float& rest) {
     a = __builtin_amdgcn_rcpf(1.0f + e);
-    rest = e * a;
+    rest = fminf(e, 0x1p125f) * __builtin_elementwise_maximum(a, 0x1p-125f);
 }
 __device__ __forceinline__ void sigmoids(float z, float& a, float& rest) { of_exp_minus(exp_minus(z), a, rest); }
 
