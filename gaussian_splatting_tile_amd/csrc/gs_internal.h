@@ -226,6 +226,7 @@ struct RecurrenceArgs {
     const uint8_t* restart;
     int batch, steps, channels;
     const float* h0;
+    int64_t h0_batch;  // its stride between sequences; set by the launch
     void* h;         // forward: states
     float* h_last;
     float* ckpt;     // [batch][ceil(steps / 128) - 1][channels]

@@ -62,12 +62,13 @@ struct RecShape {
     int groups;      // of kGroup chunks
     int supers;      // of kGroup groups
     int columns;     // groups of 64 V channels
+    int64_t row;     // columns * 64 V: words of a row of the workspace
     int steps_log2;  // waves of a workgroup along the steps (1 << steps_log2)
     bool lines;      // every row of every tensor is whole 128-byte lines
-    // rows of columns * 64 V, see exchange()
     uint64_t* word;    // [batch][chunks][row] (A, H) or (A, C) of a chunk
     uint64_t* group;   // [batch][groups][row] of a group
-    uint32_t* state;   // [batch][supers][row] state behind a super-group
+    uint32_t* state;   // [batch][supers][row] state behind a super-group; nothing is behind the
+                       // last one, whose row holds a copy of h0 if h_last is to replace it
     int patience;      // polls; 0: waits for nothing and computes every word itself
 };
 
@@ -410,7 +411,7 @@ struct Alone {
         Run f = in_turn(pos, 0);
 #pragma unroll 1
         for (int i = 1; i < kWaves; ++i) f = then(f, in_turn(pos, i));
-        if (!BACK && pos == 0) f.H = apply(f, r.h0 ? r.h0[(int64_t)b * r.channels + c] : 0.0f);
+        if (!BACK && pos == 0) f.H = apply(f, r.h0 ? r.h0[b * r.h0_batch + c] : 0.0f);
         return f;
     }
     __device__ Run group(int g) const {
@@ -539,7 +540,8 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
     }
     float h[V];  // the state in front of the sequence, then of the wave's steps
 #pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = p.pos == 0 && p.row == 0 && r.h0 ? r.h0[state0 + v] : 0.0f;
+    for (int v = 0; v < V; ++v)
+        h[v] = p.pos == 0 && p.row == 0 && r.h0 ? r.h0[p.b * r.h0_batch + p.c0 + p.at + v] : 0.0f;
     const uint32_t cut = CUT ? restarts<SUB>(r, p.b, row0, p.len) : 0u;
     if (SUB == kSub && p.waves > 1) {  // fewer rows a thread: fewer steps than a wave holds
         Run own[V];
@@ -837,11 +839,13 @@ __global__ void k_recurrence_pass(const float* from, float* to, int64_t n) {
 
 int chunks_of(int steps) { return std::max(1, (int)(((int64_t)steps + kRecChunk - 1) / kRecChunk)); }
 
-size_t layout(int batch, int steps, int channels, int columns, RecShape* s, void* base) {
+// columns of `column` channels each
+size_t layout(int batch, int steps, int channels, int columns, int column, RecShape* s, void* base) {
     s->chunks = chunks_of(steps);
     s->groups = (s->chunks + kGroup - 1) / kGroup;
     s->supers = (s->groups + kGroup - 1) / kGroup;
     s->columns = columns;
+    s->row = (int64_t)columns * column;
     s->steps_log2 = 0;
     while ((kSub << s->steps_log2) < std::min(steps, kRecChunk)) ++s->steps_log2;
     s->word = s->group = nullptr;
@@ -857,9 +861,19 @@ size_t layout(int batch, int steps, int channels, int columns, RecShape* s, void
     return words * 8 + states * 4;
 }
 
-// Fills the workspace with ones, 16 bytes a thread.
-__global__ void k_recurrence_clear(uint32_t* p, size_t words) {
-    const size_t i = ((size_t)blockIdx.x * kRecThreads + threadIdx.x) * 4;
+// Fills the workspace with ones, 16 bytes a thread, and the last super-group's
+// row of each sequence with h0, unless that is NULL. Rows are a multiple of 64
+// words, so a thread's four words are in one row.
+__global__ void k_recurrence_clear(uint32_t* p, size_t words, RecShape s, const float* h0, int batch, int channels) {
+    const size_t i = ((size_t)blockIdx.x * kRecThreads + threadIdx.x) * 4, first = s.state - p;
+    if (h0 && i >= first && i < words) {
+        const size_t row = (i - first) / s.row, c = (i - first) % s.row, b = row / s.supers;
+        if (row % s.supers == (size_t)s.supers - 1 && b < (size_t)batch) {
+            for (int j = 0; j < 4; ++j)
+                p[i + j] = c + j < (size_t)channels ? __float_as_uint(h0[b * channels + c + j]) : 0u;
+            return;
+        }
+    }
     if (i + 4 <= words) {
         *(uint4*)(p + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
     } else {
@@ -877,12 +891,17 @@ uint64_t strides_of(const RecurrenceArgs& r) {
     return (uint64_t)r.channels | (uint64_t)(r.gate_batch | r.gate_step | r.x_batch | r.x_step);
 }
 
-// Lays out the launch (and clears its workspace); gives its workgroups.
+// Lays out the launch (and clears its workspace); gives its workgroups. Where
+// h_last takes h0's place, workgroups that run later than they are numbered, or
+// compute for themselves what they wait for, would find the final state: from
+// then on r.h0 is a copy in the workspace. (A single chunk reads it before
+// anything is written.)
 template <int V>
-hipError_t prepare(const RecurrenceArgs& r, int bytes_each, void* scratch, RecShape* s, unsigned* blocks,
+hipError_t prepare(RecurrenceArgs& r, int bytes_each, void* scratch, RecShape* s, unsigned* blocks,
                    hipStream_t stream) {
-    const size_t bytes = layout(r.batch, r.steps, r.channels, (r.channels + 64 * V - 1) / (64 * V), s, scratch);
+    const size_t bytes = layout(r.batch, r.steps, r.channels, (r.channels + 64 * V - 1) / (64 * V), 64 * V, s, scratch);
     s->lines = !((starts_of(r) | (strides_of(r) * bytes_each)) & 127);
+    r.h0_batch = r.channels;
     if (s->chunks == 1) {
         const int across = kWaves >> s->steps_log2;
         *blocks = (unsigned)r.batch * ((s->columns + across - 1) / across);
@@ -890,14 +909,19 @@ hipError_t prepare(const RecurrenceArgs& r, int bytes_each, void* scratch, RecSh
     }
     *blocks = (unsigned)r.batch * s->columns * s->chunks;
     const size_t threads = (bytes + 15) / 16;
+    const float* const replaced = r.h0 == r.h_last ? r.h0 : nullptr;
     k_recurrence_clear<<<(unsigned)((threads + kRecThreads - 1) / kRecThreads), kRecThreads, 0, stream>>>(
-        (uint32_t*)scratch, bytes / 4);
+        (uint32_t*)scratch, bytes / 4, *s, replaced, r.batch, r.channels);
+    if (replaced) {
+        r.h0 = (const float*)(s->state + (s->supers - 1) * s->row);
+        r.h0_batch = s->supers * s->row;
+    }
     return hipGetLastError();
 }
 
 template <typename T, int V, bool SIGMOID, bool CUT>
 struct Forward {
-    static hipError_t launch(const RecurrenceArgs& r, void* scratch, hipStream_t stream) {
+    static hipError_t launch(RecurrenceArgs r, void* scratch, hipStream_t stream) {
         RecShape s;
         unsigned blocks;
         if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
@@ -912,7 +936,7 @@ struct Forward {
 };
 template <typename T, int V, bool SIGMOID, bool CUT>
 struct Backward {
-    static hipError_t launch(const RecurrenceArgs& r, void* scratch, hipStream_t stream) {
+    static hipError_t launch(RecurrenceArgs r, void* scratch, hipStream_t stream) {
         RecShape s;
         unsigned blocks;
         if (hipError_t e = prepare<V>(r, sizeof(T), scratch, &s, &blocks, stream)) return e;
@@ -955,7 +979,7 @@ bool recurrence_fits(const gs_recurrence& r) {
 size_t recurrence_scratch_bytes(const gs_recurrence& r) {
     RecShape s;
     if (r.batch == 0 || r.channels == 0) return 0;
-    return layout(r.batch, r.steps, r.channels, (r.channels + 63) / 64, &s, nullptr);
+    return layout(r.batch, r.steps, r.channels, (r.channels + 63) / 64, 64, &s, nullptr);
 }
 
 hipError_t launch_recurrence_fwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream) {

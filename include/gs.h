@@ -642,10 +642,12 @@ size_t gs_recurrence_scratch_bytes(const gs_recurrence* r);
 /* gs_recurrence_fwd - the states of every step.
  *   gate, x     as described above
  *   h0          [B][D] float32, or NULL (zero)
- *   h           out [B][T][D], each state rounded once to dtype
+ *   h           out [B][T][D], each state rounded once to dtype; must not
+ *               overlap gate or x (which are read again where a chunk of
+ *               steps recomputes what the chunks before it have not given yet)
  *   h_last      out [B][D] float32, or NULL: the state behind the last step
- *               (h0 for a sequence of length 0). May be h0 itself: a serving
- *               loop calls this with T = 1 and keeps one state buffer.
+ *               (h0 for a sequence of length 0). May be h0 itself, at any T: a
+ *               serving loop calls this with T = 1 and keeps one state buffer.
  *   ckpt        out [B][ceil(T / 128) - 1][D] float32, or NULL: row k is the
  *               state in front of step 128 (k + 1), for gs_recurrence_bwd;
  *               rows at or behind the length are not written. Not needed
