@@ -24,6 +24,10 @@
 //    which word came first, so results are the same bits every time. A word
 //    carries its own validity (all ones: not there yet; a NaN of that pattern
 //    is stored as another one), so no fence is needed.
+//  * A product of gates is a float32 over at most 128 steps: a group's A, over
+//    1024, can leave the range where no state does (gates that decay by 1e-28
+//    and then grow by 1e42). A state that such an A would lose walks the words
+//    of the group's chunks.
 //  * No workgroup depends on another one's progress: one that has waited
 //    kPatience polls for a word computes it from the inputs itself, by the
 //    same formula (Alone, below). With workgroups started in order that never
@@ -184,6 +188,32 @@ __device__ __forceinline__ float apply(const Run& f, float h) {
 __device__ __forceinline__ Run then(const Run& f, const Run& g) {
     const bool dropped = __float_as_uint(f.A) == kDropped || __float_as_uint(g.A) == kDropped;
     return {dropped ? __uint_as_float(kDropped) : f.A * g.A + 0.0f, apply(g, f.H)};
+}
+// A group's run, from its chunks' in turn. Its A is a product over 1024 steps,
+// eight floats: in float64 none of the products between leaves the range.
+struct GroupRun {
+    double A;
+    float H;
+    bool dropped;
+    __device__ __forceinline__ GroupRun(const Run& f)
+        : A(f.A), H(f.H), dropped(__float_as_uint(f.A) == kDropped) {}
+    __device__ __forceinline__ void then(const Run& g) {
+        A *= (double)g.A;
+        H = apply(g, H);
+        dropped |= __float_as_uint(g.A) == kDropped;
+    }
+    __device__ __forceinline__ Run run() const { return {dropped ? __uint_as_float(kDropped) : (float)A + 0.0f, H}; }
+};
+// Whether a group's A left float32's range and says too little about what is
+// left of a state h in front: A is infinite (or NaN), or below the normal
+// numbers and its error, up to 2^-150, times h reaches 2^-126. The group's chunks
+// are walked then. (Always walking would take eight times the words; A of most
+// forgetting gates is 0 over 1024 steps, and their states are not so large.)
+constexpr float kLarge = 0x1p24f;
+__device__ __forceinline__ bool too_long(const Run& f, float h) {
+    const float a = fabsf(f.A);
+    return __float_as_uint(f.A) != kDropped && h != 0.0f &&
+           (!(a < __builtin_inff()) || (a < 0x1p-126f && !(fabsf(h) < kLarge)));
 }
 
 constexpr uint32_t kNaN = 0x7fc00000u;
@@ -415,10 +445,17 @@ struct Alone {
         return f;
     }
     __device__ Run group(int g) const {
-        Run f = chunk(g * kGroup);
+        GroupRun f = chunk(g * kGroup);
 #pragma unroll 1
-        for (int j = 1; j < kGroup; ++j) f = then(f, chunk(g * kGroup + j));
-        return f;
+        for (int j = 1; j < kGroup; ++j) f.then(chunk(g * kGroup + j));
+        return f.run();
+    }
+    __device__ float through_group(int g, float e) const {
+        const Run f = group(g);
+        if (!too_long(f, e)) return apply(f, e);
+#pragma unroll 1
+        for (int j = 0; j < kGroup; ++j) e = apply(chunk(g * kGroup + j), e);
+        return e;
     }
     __device__ float state(int sg) const {
         float e = 0.0f;
@@ -426,7 +463,7 @@ struct Alone {
         for (int s = 0; s <= sg; ++s) {
             const int last = s * kGroup + kGroup - 1;  // group
 #pragma unroll 1
-            for (int g = s * kGroup; g < last; ++g) e = apply(group(g), e);
+            for (int g = s * kGroup; g < last; ++g) e = through_group(g, e);
 #pragma unroll 1
             for (int j = 0; j < kGroup - 1; ++j) e = apply(chunk(last * kGroup + j), e);
 #pragma unroll 1
@@ -480,9 +517,10 @@ __device__ __forceinline__ void exchange(RecLds<V>& lds, const RecurrenceArgs& r
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int i = lane * V + v;
-                Run all = lds.chunk[0][i];
-                for (int w = 1; w < kGroup - 1; ++w) all = then(all, lds.chunk[w][i]);
-                publish(group + gj * D + v * 64, then(all, f[v]));
+                GroupRun all = lds.chunk[0][i];
+                for (int w = 1; w < kGroup - 1; ++w) all.then(lds.chunk[w][i]);
+                all.then(f[v]);
+                publish(group + gj * D + v * 64, all.run());
             }
         }
     }
@@ -502,12 +540,50 @@ __device__ __forceinline__ void exchange(RecLds<V>& lds, const RecurrenceArgs& r
     __syncthreads();
 }
 
-// What enters the chunk at channel i of the workgroup (pos > 0).
-template <int V>
-__device__ __forceinline__ float entering(const RecLds<V>& lds, const Place<V>& p, int i) {
+// h through the groups in front of the chunk's, walking the chunks of those
+// whose A is too long (all lanes of a wave).
+template <typename T, int V, bool SIGMOID, bool CUT, bool BACK>
+__device__ __forceinline__ float walk_groups(const RecLds<V>& lds, const RecurrenceArgs& r, const RecShape& s,
+                                             const Place<V>& p, int v, float h) {
+    const int lane = threadIdx.x & 63, i = lane * V + v, gj = p.pos / kGroup % kGroup;
+    const Alone<T, SIGMOID, CUT, BACK> alone{r, p.b, p.len, p.c0 + p.at + v};
+    const int first = (p.pos / kGroup - gj) * kGroup;
+    const uint64_t* const words = s.word + ((int64_t)p.b * s.chunks + first) * s.row + p.c0 + v * 64 + lane;
+#pragma unroll 1
+    for (int w = 0; w < gj; ++w) {
+        const Run f = lds.group[w][i];
+        const bool walk = too_long(f, h);
+        float through = apply(f, h);
+        if (__any(walk)) {
+            float e = h;
+#pragma unroll 1
+            for (int k = w * kGroup; k < (w + 1) * kGroup; ++k) {
+                const uint64_t* const word = words + k * s.row;
+                const auto help = [&] { return word_of(alone.chunk(first + k)); };
+                e = apply(run_of(settle_word(word, word_at(word), s.patience, help)), e);
+            }
+            if (walk) through = e;
+        }
+        h = through;
+    }
+    return h;
+}
+
+// What enters the chunk at channel v of the lane (pos > 0; all lanes of a wave).
+template <typename T, int V, bool SIGMOID, bool CUT, bool BACK>
+__device__ __forceinline__ float entering(const RecLds<V>& lds, const RecurrenceArgs& r, const RecShape& s,
+                                          const Place<V>& p, int v) {
+    const int i = (threadIdx.x & 63) * V + v;
     const int j = p.pos % kGroup, gj = p.pos / kGroup % kGroup;
-    float h = lds.enter[i];
-    for (int w = 0; w < gj; ++w) h = apply(lds.group[w][i], h);
+    const float e = lds.enter[i];
+    float h = e;
+    // no A is too long for a state below 2^24 that it leaves below 2^24
+    bool large = !(fabsf(h) < kLarge);
+    for (int w = 0; w < gj; ++w) {
+        h = apply(lds.group[w][i], h);
+        large |= !(fabsf(h) < kLarge);
+    }
+    if (__builtin_expect(__any(large), 0)) h = walk_groups<T, V, SIGMOID, CUT, BACK>(lds, r, s, p, v, e);
     for (int w = 0; w < j; ++w) h = apply(lds.chunk[w][i], h);
     return h;
 }
@@ -579,7 +655,7 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int i = lane * V + v;
-                float e = p.pos ? entering<V>(lds, p, i) : h[v];
+                float e = p.pos ? entering<T, V, SIGMOID, CUT, false>(lds, r, s, p, v) : h[v];
                 if (p.pos && p.mine && r.ckpt)
                     r.ckpt[((int64_t)p.b * (s.chunks - 1) + p.pos - 1) * D + p.c0 + p.at + v] = e;
                 for (int w = p.first; w < p.first + p.waves; ++w) {
@@ -728,7 +804,7 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int i = lane * V + v;
-                float e = p.pos ? entering<V>(lds, p, i) : 0.0f;
+                float e = p.pos ? entering<T, V, SIGMOID, CUT, true>(lds, r, s, p, v) : 0.0f;
                 for (int w = p.first + p.waves - 1; w >= p.first; --w) {
                     lds.start[w][i] = e;
                     e = apply(Run{lds.wave[w][i].A, wave_c[w][i]}, e);

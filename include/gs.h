@@ -617,9 +617,11 @@ gs_status gs_appearance_bwd(const gs_camera* cam, int32_t n, const float* means,
  *   lengths     [B] int32, or NULL (every length is T); values outside
  *               [0, T] are clamped to it
  *   restart     [B][T] uint8, or NULL
- * All other arrays are contiguous, [B][T][D] or [B][D]. Products of gates
- * over GS_RECURRENCE_CHUNK steps are formed in float32; gates above 1 whose
- * product overflows there give a state that is not finite.
+ * All other arrays are contiguous, [B][T][D] or [B][D]. Products of the gates
+ * of consecutive steps, of any run within steps 128 k .. 128 k + 127 and of
+ * no longer one, are formed in float32. Where gates above 1 overflow such a
+ * product the states and gradients behind it need not be finite (a state that
+ * is exactly 0 stays 0), and one that underflows counts as 0.
  * ------------------------------------------------------------------- */
 #define GS_GATE_LINEAR 0
 #define GS_GATE_SIGMOID 1
