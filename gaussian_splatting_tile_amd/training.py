@@ -29,6 +29,41 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _on(stream, call, given=None):
+    """call() with `stream` current, so that what it allocates is ordered with what it launches
+    there. Tensors that it returns (other than those of the dict `given`) may be used and
+    dropped on the caller's stream, once that is ordered behind `stream`: their memory is not
+    handed out again before the caller's work on them."""
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call()
+    given = [] if given is None else [id(t) for t in given.values()]
+    for t in out.values() if isinstance(out, dict) else [out]:
+        if t is not None and id(t) not in given:
+            t.record_stream(caller)
+    return out
+
+
+def _elsewhere(stream):
+    return stream is not None and stream.cuda_stream != torch.cuda.current_stream(stream.device).cuda_stream
+
+
+class _Held:
+    """Tensors that an object made on the stream of its construction and uses on others too."""
+
+    def _hold(self, tensors):
+        self._held, self._streams = tensors, {_stream(None, self.device)}
+
+    def _call_stream(self, stream):
+        """The raw handle of a call's stream. The tensors are not handed out again before the work on it is done."""
+        raw = _stream(stream, self.device)
+        if raw not in self._streams:
+            for t in self._held:
+                t.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+            self._streams.add(raw)
+        return raw
+
+
 def _ptr(t, shape, dtype, name):
     """The address of a contiguous device tensor of this shape (None: any) and type (None: any)."""
     if t is None:
@@ -69,15 +104,13 @@ def _recurrence(gate, x, gating, lengths, restart):
     return r, B, T, D
 
 
-def _scratch(lib, r, scratch, device, stream):
+def _scratch(lib, r, scratch, device):
     """The workspace's tensor (kept until the call is enqueued), address and size."""
     if r.steps <= _lib.GS_RECURRENCE_CHUNK:
         return None, None, 0
     if scratch is None:
         need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
         scratch = torch.empty((need,), dtype=torch.uint8, device=device)
-        if stream is not None:  # freed by this function's caller, in the order of the current stream
-            scratch.record_stream(stream)
     return scratch, _ptr(scratch, None, None, "scratch"), scratch.numel() * scratch.element_size()
 
 
@@ -101,7 +134,11 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
     lengths int32 [B]; restart uint8 [B, T]. Returns dict h [B, T, D], h_last float32 [B, D] and
     ckpt (float32 [B, recurrence_ckpt_rows(T), D] with checkpoints, for recurrence_bwd; else
     None). `out` may give any of them; out["h_last"] may be h0 itself (one state buffer for
-    step-by-step serving, T = 1)."""
+    step-by-step serving, T = 1). With `stream` (not the current one) the call allocates and
+    runs on it: order it behind whatever wrote the inputs, and the use of what it returns behind
+    it. Calls that share a `scratch` must not overlap."""
+    if _elsewhere(stream):
+        return _on(stream, lambda: recurrence_fwd(gate, x, h0, gating, lengths, restart, checkpoints, out, scratch), out)
     lib = _lib.load()
     r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
     dev, f32, whole, state = gate.device, torch.float32, (B, T, D), (B, D)
@@ -120,7 +157,7 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
         pl = _ptr(h_last, state, f32, "h_last")
     if ckpt is None and checkpoints:
         ckpt = gate.new_empty((B, recurrence_ckpt_rows(T), D), dtype=f32)
-    scratch, ps, nbytes = _scratch(lib, r, scratch, dev, stream)
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
     _lib.check(lib.gs_recurrence_fwd(
         ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), ph, pl,
         None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), ps, nbytes,
@@ -132,14 +169,17 @@ def recurrence_bwd(gate, x, grad_h, h0=None, ckpt=None, grad_last=None, gating=G
                    restart=None, out=None, scratch=None, stream=None):
     """gs_recurrence_bwd: gradients of recurrence_fwd, which gave `ckpt` (needed when T > 128).
     grad_h [B, T, D] of gate's type; grad_last float32 [B, D] or None. Returns dict grad_gate,
-    grad_x [B, T, D], grad_h0 float32 [B, D]."""
+    grad_x [B, T, D], grad_h0 float32 [B, D]. `stream` and `scratch` as for recurrence_fwd."""
+    if _elsewhere(stream):
+        return _on(stream, lambda: recurrence_bwd(gate, x, grad_h, h0, ckpt, grad_last, gating, lengths, restart, out,
+                                                  scratch), out)
     lib = _lib.load()
     r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
     dev, f32, t, whole, state = gate.device, torch.float32, gate.dtype, (B, T, D), (B, D)
     if out is None:
         out = dict(grad_gate=gate.new_empty(whole), grad_x=gate.new_empty(whole),
                    grad_h0=gate.new_empty(state, dtype=f32))
-    scratch, ps, nbytes = _scratch(lib, r, scratch, dev, stream)
+    scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
     _lib.check(lib.gs_recurrence_bwd(
         ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"),
         None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
@@ -158,11 +198,12 @@ def _device_of(tensors, name):
     return dev
 
 
-class GradList:
+class GradList(_Held):
     """A list of gradients (float32, bfloat16 or float16, each contiguous, types mixed as
     wanted) whose global norm is taken and clipped. Holds the tensors, their description for
     the C call and the workspace, so a step's call only launches. Clipping writes to `out`
-    (default: in place)."""
+    (default: in place). Calls of one list share its workspace and must not overlap; on another
+    stream than that of the construction they are ordered behind it by the caller."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -180,6 +221,7 @@ class GradList:
         self._lib = _lib.load()
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=self.device)
         self._pscratch = self.scratch.data_ptr()
+        self._hold([self.scratch])
 
     def _norm(self, out):
         if out is not None:
@@ -189,44 +231,45 @@ class GradList:
 
     def norm(self, kind=NORM_L2, out=None, stream=None):
         """gs_grad_norm: the global norm, a float32 tensor of no dimensions on the device."""
+        if out is None and _elsewhere(stream):
+            return _on(stream, lambda: self.norm(kind))
         out, po = self._norm(out)
         _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), po, self._pscratch,
-                                          _stream(stream, self.device)))
+                                          self._call_stream(stream)))
         return out
 
     def clip(self, max_norm, kind=NORM_L2, out=None, stream=None):
         """gs_clip_grads: scales by min(1, max_norm / (norm + 1e-6)); returns the norm before."""
+        if out is None and _elsewhere(stream):
+            return _on(stream, lambda: self.clip(max_norm, kind))
         out, po = self._norm(out)
         _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm), po, self._pscratch,
-                                           _stream(stream, self.device)))
+                                           self._call_stream(stream)))
         return out
-
-
-def _once(grads, out, stream):
-    """A list for one call, whose workspace outlives the call on its stream."""
-    lst = GradList(grads, out)
-    if stream is not None:
-        lst.scratch.record_stream(stream)
-    return lst
 
 
 def grad_norm(grads, kind=NORM_L2, stream=None):
     """The global norm of a list of gradients (GradList(grads).norm())."""
-    return _once(grads, None, stream).norm(kind, stream=stream)
+    if _elsewhere(stream):
+        return _on(stream, lambda: grad_norm(grads, kind))
+    return GradList(grads).norm(kind)
 
 
 def clip_grads(grads, max_norm, kind=NORM_L2, out=None, stream=None):
     """Clips a list of gradients by their global norm, in place or into `out`; returns the norm."""
-    return _once(grads, out, stream).clip(max_norm, kind, stream=stream)
+    if _elsewhere(stream):
+        return _on(stream, lambda: clip_grads(grads, max_norm, kind, out))
+    return GradList(grads, out).clip(max_norm, kind)
 
 
-class Adam:
+class Adam(_Held):
     """gs_adam_step over a fixed list of parameters and gradient buffers: Adam with decoupled
     weight decay, the gradients clipped on the way by their global norm (max_norm > 0). lr and
     weight_decay are numbers or one number per tensor (`set_lr` changes them); the moments
     (exp_avg, exp_avg_sq, float32) start at 0 and the device step counter at `step` unless
     given. With skip_nonfinite a step whose gradients hold an infinity or a NaN changes
-    nothing."""
+    nothing. Steps of one object must not overlap; on another stream than that of the
+    construction they are ordered behind it by the caller."""
 
     def __init__(self, params, grads, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, max_norm=0.0,
                  skip_nonfinite=False, exp_avg=None, exp_avg_sq=None, step=0):
@@ -262,6 +305,8 @@ class Adam:
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=dev)
         self._fixed = (ctypes.byref(self._cfg), self._list, n, self.steps.data_ptr(),
                        self.norm.data_ptr() if self._want_norm else None, self.scratch.data_ptr())
+        self._hold([self.scratch, self.steps, self.norm] + (self.exp_avg if exp_avg is None else []) +
+                   (self.exp_avg_sq if exp_avg_sq is None else []))
 
     def _each(self, v, name):
         v = [float(v)] * self._n if isinstance(v, (int, float)) else [float(x) for x in v]
@@ -277,5 +322,5 @@ class Adam:
     def step(self, stream=None):
         """One update. Returns the gradients' global norm before clipping (a device tensor that
         the next step overwrites), or None when nothing asks for it."""
-        _lib.check(self._lib.gs_adam_step(*self._fixed, _stream(stream, self.device)))
+        _lib.check(self._lib.gs_adam_step(*self._fixed, self._call_stream(stream)))
         return self.norm if self._want_norm else None
