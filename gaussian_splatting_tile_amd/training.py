@@ -29,6 +29,11 @@ def _stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _of_device(stream, device):
+    if stream.device != device:
+        raise ValueError(f"stream belongs to {stream.device}, the tensors are on {device}")
+
+
 def _on(stream, call, given=None):
     """call() with `stream` current, so that what it allocates is ordered with what it launches
     there. Tensors that it returns (other than those of the dict `given`) may be used and
@@ -44,8 +49,21 @@ def _on(stream, call, given=None):
     return out
 
 
-def _elsewhere(stream):
-    return stream is not None and stream.cuda_stream != torch.cuda.current_stream(stream.device).cuda_stream
+def _elsewhere(stream, device):
+    """Whether a call on `device` is asked to run on another stream than the current one."""
+    if stream is None:
+        return False
+    _of_device(stream, device)
+    return stream.cuda_stream != torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(device, call, *args):
+    """A library call that launches: with the tensors' device current."""
+    if torch._C._cuda_getDevice() == device.index:
+        _lib.check(call(*args))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(call(*args))
 
 
 class _Held:
@@ -56,6 +74,8 @@ class _Held:
 
     def _call_stream(self, stream):
         """The raw handle of a call's stream. The tensors are not handed out again before the work on it is done."""
+        if stream is not None:
+            _of_device(stream, self.device)
         raw = _stream(stream, self.device)
         if raw not in self._streams:
             for t in self._held:
@@ -64,12 +84,13 @@ class _Held:
         return raw
 
 
-def _ptr(t, shape, dtype, name):
-    """The address of a contiguous device tensor of this shape (None: any) and type (None: any)."""
+def _ptr(t, shape, dtype, name, device):
+    """The address of a contiguous tensor of device number `device`, of this shape (None: any)
+    and type (None: any)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device tensor")
+    if not isinstance(t, torch.Tensor) or t.get_device() != device:
+        raise TypeError(f"{name} must be a tensor on cuda:{device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -94,13 +115,14 @@ def _recurrence(gate, x, gating, lengths, restart):
     if not gate.is_cuda:
         raise TypeError("gate and x must be device tensors")
     B, T, D = shape
+    index = gate.get_device()
     gb, gt, gd = gate.stride()
     xb, xt, xd = x.stride()
     if D > 1 and (gd != 1 or xd != 1):
         raise ValueError("gate and x must have contiguous channels (last stride 1)")
     r = _lib.GsRecurrence(_dtype(gate, "gate and x"), int(gating), B, T, D, gb, gt, xb, xt,
-                          _ptr(lengths, (B,), torch.int32, "lengths"),
-                          _ptr(restart, (B, T), torch.uint8, "restart"))
+                          _ptr(lengths, (B,), torch.int32, "lengths", index),
+                          _ptr(restart, (B, T), torch.uint8, "restart", index))
     return r, B, T, D
 
 
@@ -111,7 +133,7 @@ def _scratch(lib, r, scratch, device):
     if scratch is None:
         need = int(lib.gs_recurrence_scratch_bytes(ctypes.byref(r)))
         scratch = torch.empty((need,), dtype=torch.uint8, device=device)
-    return scratch, _ptr(scratch, None, None, "scratch"), scratch.numel() * scratch.element_size()
+    return scratch, _ptr(scratch, None, None, "scratch", device.index), scratch.numel() * scratch.element_size()
 
 
 def recurrence_scratch_bytes(batch: int, steps: int, channels: int) -> int:
@@ -137,11 +159,12 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
     step-by-step serving, T = 1). With `stream` (not the current one) the call allocates and
     runs on it: order it behind whatever wrote the inputs, and the use of what it returns behind
     it. Calls that share a `scratch` must not overlap."""
-    if _elsewhere(stream):
+    if _elsewhere(stream, gate.device):
         return _on(stream, lambda: recurrence_fwd(gate, x, h0, gating, lengths, restart, checkpoints, out, scratch), out)
     lib = _lib.load()
     r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
     dev, f32, whole, state = gate.device, torch.float32, (B, T, D), (B, D)
+    n = dev.index
     h = h_last = ckpt = None
     if out is not None:
         h, h_last, ckpt = out.get("h"), out.get("h_last"), out.get("ckpt")
@@ -149,19 +172,19 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
         h = gate.new_empty(whole)
         ph = h.data_ptr()
     else:
-        ph = _ptr(h, whole, gate.dtype, "h")
+        ph = _ptr(h, whole, gate.dtype, "h", n)
     if h_last is None:
         h_last = gate.new_empty(state, dtype=f32)
         pl = h_last.data_ptr()
     else:
-        pl = _ptr(h_last, state, f32, "h_last")
+        pl = _ptr(h_last, state, f32, "h_last", n)
     if ckpt is None and checkpoints:
         ckpt = gate.new_empty((B, recurrence_ckpt_rows(T), D), dtype=f32)
     scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
-    _lib.check(lib.gs_recurrence_fwd(
-        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"), ph, pl,
-        None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"), ps, nbytes,
-        _stream(stream, dev)))
+    _launch(
+        dev, lib.gs_recurrence_fwd, ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0", n), ph,
+        pl, None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt", n), ps, nbytes,
+        _stream(stream, dev))
     return dict(h=h, h_last=h_last, ckpt=ckpt)
 
 
@@ -170,22 +193,23 @@ def recurrence_bwd(gate, x, grad_h, h0=None, ckpt=None, grad_last=None, gating=G
     """gs_recurrence_bwd: gradients of recurrence_fwd, which gave `ckpt` (needed when T > 128).
     grad_h [B, T, D] of gate's type; grad_last float32 [B, D] or None. Returns dict grad_gate,
     grad_x [B, T, D], grad_h0 float32 [B, D]. `stream` and `scratch` as for recurrence_fwd."""
-    if _elsewhere(stream):
+    if _elsewhere(stream, gate.device):
         return _on(stream, lambda: recurrence_bwd(gate, x, grad_h, h0, ckpt, grad_last, gating, lengths, restart, out,
                                                   scratch), out)
     lib = _lib.load()
     r, B, T, D = _recurrence(gate, x, gating, lengths, restart)
     dev, f32, t, whole, state = gate.device, torch.float32, gate.dtype, (B, T, D), (B, D)
+    n = dev.index
     if out is None:
         out = dict(grad_gate=gate.new_empty(whole), grad_x=gate.new_empty(whole),
                    grad_h0=gate.new_empty(state, dtype=f32))
     scratch, ps, nbytes = _scratch(lib, r, scratch, dev)
-    _lib.check(lib.gs_recurrence_bwd(
-        ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0"),
-        None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt"),
-        _ptr(grad_h, whole, t, "grad_h"), _ptr(grad_last, state, f32, "grad_last"),
-        _ptr(out["grad_gate"], whole, t, "grad_gate"), _ptr(out["grad_x"], whole, t, "grad_x"),
-        _ptr(out.get("grad_h0"), state, f32, "grad_h0"), ps, nbytes, _stream(stream, dev)))
+    _launch(
+        dev, lib.gs_recurrence_bwd, ctypes.byref(r), gate.data_ptr(), x.data_ptr(), _ptr(h0, state, f32, "h0", n),
+        None if ckpt is None else _ptr(ckpt, (B, recurrence_ckpt_rows(T), D), f32, "ckpt", n),
+        _ptr(grad_h, whole, t, "grad_h", n), _ptr(grad_last, state, f32, "grad_last", n),
+        _ptr(out["grad_gate"], whole, t, "grad_gate", n), _ptr(out["grad_x"], whole, t, "grad_x", n),
+        _ptr(out.get("grad_h0"), state, f32, "grad_h0", n), ps, nbytes, _stream(stream, dev))
     return out
 
 
@@ -213,10 +237,11 @@ class GradList(_Held):
             raise ValueError("out must hold one tensor for each gradient")
         self._n = len(self.grads)
         self._list = (_lib.GsGradTensor * self._n)()
+        n = self.device.index
         for d, g, o in zip(self._list, self.grads, self.out):
             if o.shape != g.shape:
                 raise ValueError("out must have the shapes of grads")
-            d.grad, d.out = _ptr(g, None, None, "grad"), _ptr(o, None, g.dtype, "out")
+            d.grad, d.out = _ptr(g, None, None, "grad", n), _ptr(o, None, g.dtype, "out", n)
             d.count, d.dtype = g.numel(), _dtype(g, "grad")
         self._lib = _lib.load()
         self.scratch = torch.empty((int(self._lib.gs_grad_scratch_bytes()),), dtype=torch.uint8, device=self.device)
@@ -225,39 +250,41 @@ class GradList(_Held):
 
     def _norm(self, out):
         if out is not None:
-            return out, _ptr(out, (), torch.float32, "out")
+            return out, _ptr(out, (), torch.float32, "out", self.device.index)
         out = torch.empty((), dtype=torch.float32, device=self.device)
         return out, out.data_ptr()
 
     def norm(self, kind=NORM_L2, out=None, stream=None):
         """gs_grad_norm: the global norm, a float32 tensor of no dimensions on the device."""
-        if out is None and _elsewhere(stream):
+        if out is None and _elsewhere(stream, self.device):
             return _on(stream, lambda: self.norm(kind))
         out, po = self._norm(out)
-        _lib.check(self._lib.gs_grad_norm(self._list, self._n, int(kind), po, self._pscratch,
-                                          self._call_stream(stream)))
+        _launch(self.device, self._lib.gs_grad_norm, self._list, self._n, int(kind), po, self._pscratch,
+                self._call_stream(stream))
         return out
 
     def clip(self, max_norm, kind=NORM_L2, out=None, stream=None):
         """gs_clip_grads: scales by min(1, max_norm / (norm + 1e-6)); returns the norm before."""
-        if out is None and _elsewhere(stream):
+        if out is None and _elsewhere(stream, self.device):
             return _on(stream, lambda: self.clip(max_norm, kind))
         out, po = self._norm(out)
-        _lib.check(self._lib.gs_clip_grads(self._list, self._n, int(kind), float(max_norm), po, self._pscratch,
-                                           self._call_stream(stream)))
+        _launch(self.device, self._lib.gs_clip_grads, self._list, self._n, int(kind), float(max_norm), po,
+                self._pscratch, self._call_stream(stream))
         return out
 
 
 def grad_norm(grads, kind=NORM_L2, stream=None):
     """The global norm of a list of gradients (GradList(grads).norm())."""
-    if _elsewhere(stream):
+    grads = list(grads)
+    if stream is not None and _elsewhere(stream, _device_of(grads, "grads")):
         return _on(stream, lambda: grad_norm(grads, kind))
     return GradList(grads).norm(kind)
 
 
 def clip_grads(grads, max_norm, kind=NORM_L2, out=None, stream=None):
     """Clips a list of gradients by their global norm, in place or into `out`; returns the norm."""
-    if _elsewhere(stream):
+    grads = list(grads)
+    if stream is not None and _elsewhere(stream, _device_of(grads, "grads")):
         return _on(stream, lambda: clip_grads(grads, max_norm, kind, out))
     return GradList(grads, out).clip(max_norm, kind)
 
@@ -295,8 +322,8 @@ class Adam(_Held):
         for d, p, g, m, v in zip(self._list, self.params, self.grads, self.exp_avg, self.exp_avg_sq):
             if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
                 raise ValueError("a gradient or moment does not have its parameter's shape")
-            d.param, d.grad = _ptr(p, None, None, "param"), _ptr(g, None, None, "grad")
-            d.m, d.v = _ptr(m, None, f32, "exp_avg"), _ptr(v, None, f32, "exp_avg_sq")
+            d.param, d.grad = _ptr(p, None, None, "param", dev.index), _ptr(g, None, None, "grad", dev.index)
+            d.m, d.v = _ptr(m, None, f32, "exp_avg", dev.index), _ptr(v, None, f32, "exp_avg_sq", dev.index)
             d.count, d.param_dtype, d.grad_dtype = p.numel(), _dtype(p, "param"), _dtype(g, "grad")
         self.set_lr(lr)
         for d, wd in zip(self._list, self._each(weight_decay, "weight_decay")):
@@ -322,5 +349,5 @@ class Adam(_Held):
     def step(self, stream=None):
         """One update. Returns the gradients' global norm before clipping (a device tensor that
         the next step overwrites), or None when nothing asks for it."""
-        _lib.check(self._lib.gs_adam_step(*self._fixed, self._call_stream(stream)))
+        _launch(self.device, self._lib.gs_adam_step, *self._fixed, self._call_stream(stream))
         return self.norm if self._want_norm else None

@@ -123,3 +123,27 @@ def test_objects_may_be_dropped_behind_their_calls():
                 torch.full(shape, 7, dtype=dtype, device="cuda")
         torch.cuda.synchronize()
         assert torch.equal(p, q) and torch.equal(clipped, out) and torch.equal(norm, want)
+
+
+def test_calls_make_their_device_current(monkeypatch):
+    """Where another device than the tensors' is current, the launch runs with theirs."""
+    import torch
+    import gaussian_splatting_tile_amd as gs
+    say("[device of a call]")
+    x = torch.randn((2, 300, 64), device="cuda")
+    want = gs.recurrence_fwd(x, x, gating=gs.GATE_SIGMOID, checkpoints=True)
+    norm = gs.grad_norm([x])
+    entered, real = [], torch.cuda.device.__enter__
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    monkeypatch.setattr(torch.cuda.device, "__enter__", lambda self: (entered.append(self.idx), real(self))[1])
+    got = gs.recurrence_fwd(x, x, gating=gs.GATE_SIGMOID, checkpoints=True)
+    assert entered == [x.device.index]
+    back = gs.recurrence_bwd(x, x, x, ckpt=got["ckpt"], gating=gs.GATE_SIGMOID)
+    p = torch.ones_like(x)
+    adam = gs.Adam([p], [back["grad_x"]], max_norm=1.0)
+    again = gs.grad_norm([x])
+    adam.step()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert entered == [x.device.index] * 4
+    assert torch.equal(got["h"], want["h"]) and torch.equal(again, norm) and int(adam.steps) == 1
