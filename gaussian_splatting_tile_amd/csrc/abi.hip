@@ -709,6 +709,10 @@ gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void
                      "gs_recurrence_bwd launch");
 }
 
+// For tests of the way without waiting, which no timing reaches at will; not
+// in gs.h. It changes no result.
+int gs_test_recurrence_patience(int polls) { return gs::set_recurrence_patience(polls); }
+
 size_t gs_grad_scratch_bytes(void) { return gs::optim_scratch_bytes(); }
 
 gs_status gs_grad_norm(const gs_grad_tensor* tensors, int32_t n_tensors, int32_t kind, float* norm, void* scratch,

@@ -239,6 +239,9 @@ struct RecurrenceArgs {
 // Whether the work items of one call (64 channels of 128 steps) fit one launch.
 bool recurrence_fits(const gs_recurrence& r);
 size_t recurrence_scratch_bytes(const gs_recurrence& r);
+// Polls of a wait of the calls that follow; 0: none waits, every chunk computes
+// what it needs itself; negative: the usual number. Gives the number before.
+int set_recurrence_patience(int polls);
 hipError_t launch_recurrence_fwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream);
 hipError_t launch_recurrence_bwd(const RecurrenceArgs& r, int dtype, bool sigmoid, void* scratch, hipStream_t stream);
 

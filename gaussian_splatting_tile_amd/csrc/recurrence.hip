@@ -40,7 +40,7 @@
 //    states it needs are recomputed from the forward's checkpoints (one
 //    float32 row per 128 steps), in LDS and registers as in the forward.
 #include <algorithm>
-#include <cstdlib>
+#include <atomic>
 #include <type_traits>
 
 #include "gs_internal.h"
@@ -913,6 +913,8 @@ __global__ void k_recurrence_pass(const float* from, float* to, int64_t n) {
     if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
+std::atomic<int> g_patience{kPatience};
+
 int chunks_of(int steps) { return std::max(1, (int)(((int64_t)steps + kRecChunk - 1) / kRecChunk)); }
 
 // columns of `column` channels each
@@ -926,8 +928,7 @@ size_t layout(int batch, int steps, int channels, int columns, int column, RecSh
     while ((kSub << s->steps_log2) < std::min(steps, kRecChunk)) ++s->steps_log2;
     s->word = s->group = nullptr;
     s->state = nullptr;
-    const char* const patience = getenv("GS_RECURRENCE_PATIENCE");  // for tests of the way without waiting
-    s->patience = patience ? atoi(patience) : kPatience;
+    s->patience = g_patience.load(std::memory_order_relaxed);
     if (s->chunks == 1) return 0;
     const size_t row = (size_t)batch * (((size_t)channels + 127) / 128 * 128);
     const size_t words = row * (s->chunks + s->groups), states = row * s->supers;
@@ -1045,6 +1046,8 @@ hipError_t pass_through(const RecurrenceArgs& r, const float* from, float* to, h
 }
 
 }  // namespace
+
+int set_recurrence_patience(int polls) { return g_patience.exchange(polls < 0 ? kPatience : polls); }
 
 bool recurrence_fits(const gs_recurrence& r) {
     const int64_t most = ((int64_t)1 << 32) / kRecThreads - 1;  // a grid has less than 2^32 threads
