@@ -739,8 +739,8 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
     if (!cfg) return fail(GS_ERR_INVALID, "gs_adam_step: cfg is NULL");
     if (!(cfg->beta1 >= 0.0 && cfg->beta1 < 1.0 && cfg->beta2 >= 0.0 && cfg->beta2 < 1.0))
         return fail(GS_ERR_INVALID, "gs_adam_step: beta1 %g or beta2 %g outside [0, 1)", cfg->beta1, cfg->beta2);
-    if (!(cfg->eps > 0.0) || !std::isfinite(cfg->eps))
-        return fail(GS_ERR_INVALID, "gs_adam_step: eps %g is not positive and finite", cfg->eps);
+    if (!((float)cfg->eps > 0.0f) || !std::isfinite((float)cfg->eps))
+        return fail(GS_ERR_INVALID, "gs_adam_step: eps %g is not positive and finite in float32", cfg->eps);
     if (!(cfg->max_norm >= 0.0f) || !std::isfinite(cfg->max_norm))
         return fail(GS_ERR_INVALID, "gs_adam_step: max_norm %g is negative or not finite", cfg->max_norm);
     if (cfg->flags & ~(uint32_t)GS_ADAM_SKIP_NONFINITE)

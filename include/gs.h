@@ -727,7 +727,8 @@ gs_status gs_clip_grads(const gs_grad_tensor* tensors, int32_t n_tensors, int32_
  *           - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
  * computed in float32, param rounded once to its type.
  *
- *   cfg       (host) 0 <= beta1, beta2 < 1; eps > 0; max_norm >= 0, finite;
+ *   cfg       (host) 0 <= beta1, beta2 < 1; eps > 0 and finite, also as a
+ *             float32; max_norm >= 0, finite;
  *             flags: GS_ADAM_SKIP_NONFINITE leaves params, moments and step
  *             as they are when the norm of the gradients is not finite
  *   tensors   (host) array of n_tensors descriptions, read during the call:
