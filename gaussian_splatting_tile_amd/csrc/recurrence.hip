@@ -206,14 +206,14 @@ struct GroupRun {
 };
 // Whether a group's A left float32's range and says too little about what is
 // left of a state h in front: A is infinite (or NaN), or below the normal
-// numbers and its error, up to 2^-150, times h reaches 2^-126. The group's chunks
-// are walked then. (Always walking would take eight times the words; A of most
-// forgetting gates is 0 over 1024 steps, and their states are not so large.)
+// numbers and its error, up to 2^-150, times h reaches both 2^-126 and the last
+// bit of H. The group's chunks are walked then. (Over 1024 steps A is 0 for most
+// forgetting gates; walking always takes 65536 x 1024 bf16 from 101 to 240 us.)
 constexpr float kLarge = 0x1p24f;
 __device__ __forceinline__ bool too_long(const Run& f, float h) {
-    const float a = fabsf(f.A);
+    const float a = fabsf(f.A), m = fabsf(h);
     return __float_as_uint(f.A) != kDropped && h != 0.0f &&
-           (!(a < __builtin_inff()) || (a < 0x1p-126f && !(fabsf(h) < kLarge)));
+           (!(a < __builtin_inff()) || (a < 0x1p-126f && !(m < kLarge) && !(fabsf(f.H) >= m * 0x1p-125f)));
 }
 
 constexpr uint32_t kNaN = 0x7fc00000u;
@@ -938,12 +938,22 @@ size_t layout(int batch, int steps, int channels, int columns, int column, RecSh
     return words * 8 + states * 4;
 }
 
-// Fills the workspace with ones, 16 bytes a thread, and the last super-group's
-// row of each sequence with h0, unless that is NULL. Rows are a multiple of 64
-// words, so a thread's four words are in one row.
-__global__ void k_recurrence_clear(uint32_t* p, size_t words, RecShape s, const float* h0, int batch, int channels) {
-    const size_t i = ((size_t)blockIdx.x * kRecThreads + threadIdx.x) * 4, first = s.state - p;
-    if (h0 && i >= first && i < words) {
+// Fills words of the workspace with ones, 16 bytes a thread.
+__device__ __forceinline__ void fill_ones(uint32_t* p, size_t words, size_t i) {
+    if (i + 4 <= words) {
+        *(uint4*)(p + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
+    } else {
+        for (size_t j = i; j < words; ++j) p[j] = ~0u;
+    }
+}
+__device__ __forceinline__ size_t clear_at() { return ((size_t)blockIdx.x * kRecThreads + threadIdx.x) * 4; }
+__global__ void k_recurrence_clear(uint32_t* p, size_t words) { fill_ones(p, words, clear_at()); }
+// ... and the last super-group's row of each sequence with h0. Rows are a
+// multiple of 64 words, so a thread's four words are in one row.
+__global__ void k_recurrence_clear_keep(uint32_t* p, size_t words, RecShape s, const float* h0, int batch,
+                                        int channels) {
+    const size_t i = clear_at(), first = s.state - p;
+    if (i >= first && i < words) {
         const size_t row = (i - first) / s.row, c = (i - first) % s.row, b = row / s.supers;
         if (row % s.supers == (size_t)s.supers - 1 && b < (size_t)batch) {
             for (int j = 0; j < 4; ++j)
@@ -951,11 +961,7 @@ __global__ void k_recurrence_clear(uint32_t* p, size_t words, RecShape s, const 
             return;
         }
     }
-    if (i + 4 <= words) {
-        *(uint4*)(p + i) = make_uint4(~0u, ~0u, ~0u, ~0u);
-    } else {
-        for (size_t j = i; j < words; ++j) p[j] = ~0u;
-    }
+    fill_ones(p, words, i);
 }
 
 // The low bits of where the rows of any tensor start: of the tensors' addresses
@@ -986,12 +992,14 @@ hipError_t prepare(RecurrenceArgs& r, int bytes_each, void* scratch, RecShape* s
     }
     *blocks = (unsigned)r.batch * s->columns * s->chunks;
     const size_t threads = (bytes + 15) / 16;
-    const float* const replaced = r.h0 == r.h_last ? r.h0 : nullptr;
-    k_recurrence_clear<<<(unsigned)((threads + kRecThreads - 1) / kRecThreads), kRecThreads, 0, stream>>>(
-        (uint32_t*)scratch, bytes / 4, *s, replaced, r.batch, r.channels);
-    if (replaced) {
+    const unsigned clears = (unsigned)((threads + kRecThreads - 1) / kRecThreads);
+    if (r.h0 && r.h0 == r.h_last) {
+        k_recurrence_clear_keep<<<clears, kRecThreads, 0, stream>>>((uint32_t*)scratch, bytes / 4, *s, r.h0, r.batch,
+                                                                    r.channels);
         r.h0 = (const float*)(s->state + (s->supers - 1) * s->row);
         r.h0_batch = s->supers * s->row;
+    } else {
+        k_recurrence_clear<<<clears, kRecThreads, 0, stream>>>((uint32_t*)scratch, bytes / 4);
     }
     return hipGetLastError();
 }

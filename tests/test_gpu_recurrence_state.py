@@ -125,3 +125,23 @@ def test_a_large_state_outlives_a_product_that_underflows(monkeypatch, dtype):
     monkeypatch.delenv("GS_RECURRENCE_PATIENCE")
     host, dev = _of_gates(dtype, gate, 0.0, 1e37)
     _both_ways(monkeypatch, host, dev, dtype, "backward")
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_large_states_of_ordinary_gates(monkeypatch, dtype, sigmoid):
+    """States of 1e9 over gates whose product over 1024 steps is 0 in float32: what comes in later
+    is as large, so nothing is lost with the product."""
+    import torch
+    say(f"[recurrence large states {dtype} sigmoid={sigmoid}]")
+    host, dev = _inputs(12, 2, 3100, 66, dtype, sigmoid, ragged=True, restarts=True)
+    for k in ("x", "grad_h", "h0", "grad_last"):
+        dev[k] = dev[k] * 2.0 ** 30
+        host[k] = to_np(dev[k].double())
+    ref = _oracle(host, dtype, sigmoid)
+    got = _run(dev, sigmoid)
+    _check(got, ref, "large")
+    monkeypatch.setenv("GS_RECURRENCE_PATIENCE", "0")
+    alone = _run(dev, sigmoid)
+    for k in ("h", "h_last", "grad_gate", "grad_x", "grad_h0"):
+        assert torch.equal(got[k], alone[k]), k
