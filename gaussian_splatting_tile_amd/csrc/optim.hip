@@ -13,9 +13,11 @@
 // A first pass leaves one partial sum per workgroup in the workspace; every
 // workgroup of the second pass adds the partials again in the same order, so
 // neither atomics nor a third launch is needed. The second pass walks the
-// tiles from the last to the first: the end of the list is what the first
-// pass left in the cache behind the L2s. Small lists take one launch of one
-// workgroup instead.
+// tiles from the last to the first, as the end of the list is what the first
+// pass read last; it makes little difference (against ascending: 300 tensors
+// clipped in 67.5 and 67.8 us, a clipped update of 120 tensors in 100.8 and
+// 101.9, of 59M float32 parameters in 288 and 284). Small lists take one launch
+// of one workgroup instead.
 #include <algorithm>
 #include <type_traits>
 
@@ -34,7 +36,7 @@ constexpr int kOptSlots = 2048;      // partial sums of all launches of a call
 // Workgroups of a second-pass launch: one for each tile up to a bound that
 // only keeps the grid within limits. Fewer that take several tiles each were
 // slower (a clipped update of 59M float32 parameters: 320 us with 2048, 298
-// without the bound at that step, 286 now).
+// without the bound at that step, 287 now).
 constexpr int kOptBlocks = 1 << 22;
 constexpr int kSmallThreads = 1024;  // small lists: a wave shares a tile
 constexpr int kSmallTile = 2048;
@@ -60,8 +62,8 @@ struct OptTable {
 // Elements e .. e + U - 1 of a tensor of `count`, all of which are there if
 // WHOLE; else (at its ends) the others read as 0 and are not written. p is
 // aligned to its type only: an access is still one instruction. STREAM: what
-// is not used again soon and is kept from pushing the gradients out of the
-// cache between the two passes (a clipped update of 59M float32 parameters when
+// is not used again soon and should not push the gradients out of the caches
+// between the two passes (a clipped update of 59M float32 parameters when
 // it took 353 us in all: 373 without; on the gradients themselves it costs
 // 13%).
 template <typename T, int U>
@@ -376,9 +378,9 @@ __device__ __forceinline__ void for_tiles(const OptTable<D>& t, uint32_t begin, 
 
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-// sum g^2 (or max |g|) of a workgroup's share. Bound by memory, reads alone:
-// 59M float32 in 44 us, 5.4 TB/s; 9.4M in 9.0 us (4.2 TB/s), of which 3 are the
-// launch and the first latency. Two workgroups of 1024 threads to a unit rather
+// sum g^2 (or max |g|) of a workgroup's share. Bound by memory, reads alone
+// (medians here and below): 59M float32 in 45 us, 5.2 TB/s; 9.4M in 9.2 us (4.1
+// TB/s), of which 3 are the launch and the first latency. Two workgroups of 1024 threads to a unit rather
 // than one per tile: each leaves a partial that the whole second pass reads
 // again, and 512 of them are two loads a thread there.
 __global__ __launch_bounds__(kNormThreads) void k_norm_partial(OptTable<NormTensor> t, OptScratch* s, int slot0,
@@ -401,9 +403,9 @@ __global__ __launch_bounds__(kOptThreads) void k_norm_total(const OptScratch* s,
 }
 
 // out = c g, c = min(1, max_norm / (norm + 1e-6)). Bound by memory: 9.4M float32
-// in 13.8 us, 5.5 TB/s read and written; half of what it reads comes from the
-// cache behind the L2s. With a factor of 1 gradients in place stay untouched
-// (the whole call on 59M float32 138 -> 61 us).
+// in 14.6 us, 5.2 TB/s read and written. Its first loads wait for the partials'
+// reduction. With a factor of 1 gradients in place stay untouched (the whole
+// call on 59M float32 138 -> 61 us).
 __global__ __launch_bounds__(kOptThreads) void k_clip(OptTable<ClipTensor> t, const OptScratch* s, int slots, int kind,
                                                       float max_norm, float* norm) {
     const double n = total_norm(s, slots, kind);
@@ -416,8 +418,9 @@ __global__ __launch_bounds__(kOptThreads) void k_clip(OptTable<ClipTensor> t, co
 
 // m = b1 m + (1 - b1) c g, v = b2 v + (1 - b2) (c g)^2, p = keep p - lr (m / bc1)
 // / (sqrt(v / bc2) + eps), in float32 from one reading of each. Bound by memory:
-// 59M float32 parameters (1.65 GB) in 243 us, 6.8 TB/s with the gradients partly
-// from the cache behind the L2s; 40 bf16 tensors in 49 us. The division and the
+// 59M float32 parameters (1.65 GB) in 245 us, 6.7 TB/s (above a copy's rate of
+// 5.2: where its bytes come from was not measured); 40 bf16 tensors in 49 us. The
+// division and the
 // root are correctly rounded: their operations hide behind the rows.
 __global__ __launch_bounds__(kOptThreads) void k_adam(OptTable<AdamTensor> t, const OptScratch* s, int slots,
                                                       gs_adam cfg, int64_t* step, float* norm, bool last) {

@@ -695,10 +695,11 @@ __device__ __forceinline__ void forward(const RecurrenceArgs& r, const RecShape&
 }
 
 // Forward. Rows of whole sequences in a wave are bound by memory: 16 steps of
-// 1.28M float32 channels in 42 us, 5.8 TB/s; 8 x 2048 x 2048 bf16 (ragged) in 29
-// to 32 us. 65536 x 1024 bf16 takes 97 to 100 us, 4.0 TB/s: the same rows copied
-// take 72, the rest is the exchange between chunks. One step (64 x 2048 bf16) is
-// one launch of 3.1 us: latency. Six waves a SIMD let three workgroups share a
+// 1.28M float32 channels in 42.8 us, 5.7 TB/s; 8 x 2048 x 2048 bf16 (ragged,
+// SIGMOID) in 32 us, of which some 1.5 are the second of the two instructions
+// that bound the factors of 1 - a. 65536 x 1024 bf16 takes 100 us, 4.0 TB/s: the
+// same rows copied take 72, the rest is the exchange between chunks. One step
+// (64 x 2048 bf16) is one launch of 3.0 us: latency. (Medians.) Six waves a SIMD let three workgroups share a
 // unit, so that one's loads fill another's exchange.
 template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
 __global__ __launch_bounds__(kRecThreads, 6) void k_recurrence_fwd(RecurrenceArgs r, RecShape s) {
@@ -883,11 +884,11 @@ __device__ __forceinline__ void backward(const RecurrenceArgs& r, const RecShape
 }
 
 // Backward: three tensors in, two out. Bound by memory while rows move: 8 x 2048
-// x 2048 bf16 (ragged) in 48 to 52 us, 4.6 TB/s; all rows there (LINEAR) 79 us,
+// x 2048 bf16 (ragged) in 52 to 53 us, 4.5 TB/s; all rows there (LINEAR) 79 us,
 // 4.2 TB/s. A thread's 16 rows of three inputs and what it keeps of the walk
-// (weight, e) take 84 to 92 registers, so two workgroups share a unit; a third,
+// (weight, e) take 85 to 92 registers, so two workgroups share a unit; a third,
 // with 80 registers, gains nothing (83 us), and two channels a lane spill (99
-// against 85 us forward and backward). 3 x 1001 x 777 float32 takes 16 us: eight
+// against 85 us forward and backward). 3 x 1001 x 777 float32 takes 17 us: eight
 // chunks in turn.
 template <typename T, int V, bool SIGMOID, bool CUT, int SUB>
 __global__ __launch_bounds__(kRecThreads, 4) void k_recurrence_bwd(RecurrenceArgs r, RecShape s) {
