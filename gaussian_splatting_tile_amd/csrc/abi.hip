@@ -666,6 +666,8 @@ gs_status gs_recurrence_fwd(const gs_recurrence* r, const void* gate, const void
         return fail(GS_ERR_INVALID, "gs_recurrence_fwd: scratch of %zu bytes is smaller than the required %zu",
                     scratch ? scratch_bytes : (size_t)0, need);
     if (need && !aligned(8, scratch)) return fail(GS_ERR_INVALID, "gs_recurrence_fwd: scratch is not 8-byte aligned");
+    if (need && (h == gate || h == x))
+        return fail(GS_ERR_INVALID, "gs_recurrence_fwd: h overlaps gate or x");
     gs::RecurrenceArgs a = recurrence_args(*r);
     a.gate = gate;
     a.x = x;
@@ -695,6 +697,11 @@ gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void
         return fail(GS_ERR_INVALID, "gs_recurrence_bwd: scratch of %zu bytes is smaller than the required %zu",
                     scratch ? scratch_bytes : (size_t)0, need);
     if (need && !aligned(8, scratch)) return fail(GS_ERR_INVALID, "gs_recurrence_bwd: scratch is not 8-byte aligned");
+    if (need) {
+        for (const void* in : {gate, x, grad_h})
+            if (grad_gate == in || grad_x == in)
+                return fail(GS_ERR_INVALID, "gs_recurrence_bwd: a gradient overlaps an input");
+    }
     gs::RecurrenceArgs a = recurrence_args(*r);
     a.gate = gate;
     a.x = x;

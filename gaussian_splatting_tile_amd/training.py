@@ -156,9 +156,9 @@ def recurrence_fwd(gate, x, h0=None, gating=GATE_LINEAR, lengths=None, restart=N
     lengths int32 [B]; restart uint8 [B, T]. Returns dict h [B, T, D], h_last float32 [B, D] and
     ckpt (float32 [B, recurrence_ckpt_rows(T), D] with checkpoints, for recurrence_bwd; else
     None). `out` may give any of them; out["h_last"] may be h0 itself (one state buffer for
-    step-by-step serving, T = 1). With `stream` (not the current one) the call allocates and
-    runs on it: order it behind whatever wrote the inputs, and the use of what it returns behind
-    it. Calls that share a `scratch` must not overlap."""
+    step-by-step serving, T = 1), no other output may overlap an input. With `stream` (not the
+    current one) the call allocates and runs on it: order it behind whatever wrote the inputs,
+    and the use of what it returns behind it. Calls that share a `scratch` must not overlap."""
     if _elsewhere(stream, gate.device):
         return _on(stream, lambda: recurrence_fwd(gate, x, h0, gating, lengths, restart, checkpoints, out, scratch), out)
     lib = _lib.load()

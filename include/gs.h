@@ -646,7 +646,8 @@ size_t gs_recurrence_scratch_bytes(const gs_recurrence* r);
  *   h0          [B][D] float32, or NULL (zero)
  *   h           out [B][T][D], each state rounded once to dtype; must not
  *               overlap gate or x (which are read again where a chunk of
- *               steps recomputes what the chunks before it have not given yet)
+ *               steps recomputes what the chunks before it have not given yet;
+ *               refused where it is one of them and T > 128)
  *   h_last      out [B][D] float32, or NULL: the state behind the last step
  *               (h0 for a sequence of length 0). May be h0 itself, at any T: a
  *               serving loop calls this with T = 1 and keeps one state buffer.
@@ -673,7 +674,7 @@ gs_status gs_recurrence_fwd(const gs_recurrence* r, const void* gate, const void
  *   grad_last   [B][D] float32, or NULL (zero)
  *   grad_gate, grad_x  out [B][T][D]
  *   grad_h0     out [B][D] float32, or NULL
- * Outputs must not overlap inputs. */
+ * Outputs must not overlap inputs (refused as in the forward). */
 gs_status gs_recurrence_bwd(const gs_recurrence* r, const void* gate, const void* x, const float* h0,
                             const float* ckpt, const void* grad_h, const float* grad_last, void* grad_gate,
                             void* grad_x, float* grad_h0, void* scratch, size_t scratch_bytes, void* stream);
