@@ -16,6 +16,9 @@ GS_GATE_LINEAR, GS_GATE_SIGMOID = range(2)
 GS_RECURRENCE_CHUNK = 128
 GS_NORM_L2, GS_NORM_MAX = range(2)
 GS_ADAM_SKIP_NONFINITE = 1
+GS_DELTA_CHUNK, GS_DELTA_MAX_DIM = 64, 128
+GS_BLOCK_NORM_NONE, GS_BLOCK_NORM_RMS, GS_BLOCK_NORM_LAYER = range(3)
+GS_BLOCK_GATE_NONE, GS_BLOCK_GATE_SIGMOID, GS_BLOCK_GATE_SILU = range(3)
 STATUS_NAMES = {0: "GS_OK", 1: "GS_ERR_INVALID", 2: "GS_ERR_CAPACITY", 3: "GS_ERR_OVERFLOW",
                 4: "GS_ERR_HIP"}
 
@@ -27,7 +30,8 @@ EXPORTS = ("gs_constants", "gs_last_error", "gs_version", "gs_preprocess", "gs_p
            "gs_preprocess_views", "gs_bin_and_sort_views_async", "gs_appearance_fwd",
            "gs_appearance_bwd", "gs_bin_and_sort_async_noalloc", "gs_recurrence_scratch_bytes",
            "gs_recurrence_fwd", "gs_recurrence_bwd", "gs_grad_scratch_bytes", "gs_grad_norm", "gs_clip_grads",
-           "gs_adam_step")
+           "gs_adam_step", "gs_delta_rule_scratch_bytes", "gs_delta_rule_fwd", "gs_delta_rule_bwd",
+           "gs_block_norm_fwd", "gs_block_norm_scratch_bytes", "gs_block_norm_bwd")
 
 
 class GsCamera(ctypes.Structure):
@@ -58,6 +62,26 @@ class GsAdamTensor(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("count", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class GsDeltaRule(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("key_heads", ctypes.c_int32), ("heads", ctypes.c_int32), ("key_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("q_batch", ctypes.c_int64),
+                ("q_step", ctypes.c_int64), ("q_head", ctypes.c_int64), ("k_batch", ctypes.c_int64),
+                ("k_step", ctypes.c_int64), ("k_head", ctypes.c_int64), ("v_batch", ctypes.c_int64),
+                ("v_step", ctypes.c_int64), ("v_head", ctypes.c_int64), ("decay_batch", ctypes.c_int64),
+                ("decay_step", ctypes.c_int64), ("beta_batch", ctypes.c_int64), ("beta_step", ctypes.c_int64),
+                ("lengths", ctypes.c_void_p), ("restart", ctypes.c_void_p)]
+
+
+class GsBlockNorm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("gating", ctypes.c_int32), ("pre", ctypes.c_int32), ("inner", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("eps", ctypes.c_float), ("outer", ctypes.c_int64),
+                ("y_outer", ctypes.c_int64), ("y_inner", ctypes.c_int64), ("gate_outer", ctypes.c_int64),
+                ("gate_inner", ctypes.c_int64), ("residual_outer", ctypes.c_int64),
+                ("residual_inner", ctypes.c_int64)]
 
 
 class GsError(RuntimeError):
@@ -147,6 +171,20 @@ def load() -> ctypes.CDLL:
     lib.gs_clip_grads.argtypes = [P, I32, I32, ctypes.c_float, P, P, P]
     lib.gs_adam_step.restype = ctypes.c_int
     lib.gs_adam_step.argtypes = [ctypes.POINTER(GsAdam), P, I32, P, P, P, P]
+    DEL = ctypes.POINTER(GsDeltaRule)
+    lib.gs_delta_rule_scratch_bytes.restype = SIZE
+    lib.gs_delta_rule_scratch_bytes.argtypes = [DEL, I32]
+    lib.gs_delta_rule_fwd.restype = ctypes.c_int
+    lib.gs_delta_rule_fwd.argtypes = [DEL] + [P] * 10 + [SIZE, P]
+    lib.gs_delta_rule_bwd.restype = ctypes.c_int
+    lib.gs_delta_rule_bwd.argtypes = [DEL] + [P] * 16 + [SIZE, P]
+    NRM = ctypes.POINTER(GsBlockNorm)
+    lib.gs_block_norm_scratch_bytes.restype = SIZE
+    lib.gs_block_norm_scratch_bytes.argtypes = [NRM]
+    lib.gs_block_norm_fwd.restype = ctypes.c_int
+    lib.gs_block_norm_fwd.argtypes = [NRM] + [P] * 11
+    lib.gs_block_norm_bwd.restype = ctypes.c_int
+    lib.gs_block_norm_bwd.argtypes = [NRM] + [P] * 19 + [SIZE, P]
     _lib = lib
     return lib
 

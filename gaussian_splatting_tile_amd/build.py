@@ -14,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -43,10 +45,25 @@ def sources() -> list:
 
 def build(verbose: bool = True) -> str:
     tmp = LIB + ".tmp"
-    cmd = [hipcc()] + compile_flags() + ["-shared", "-o", tmp] + sources()
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def compile_one(job):
+        source, obj = job
+        cmd = [hipcc()] + compile_flags() + ["-c", "-o", obj, source]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+        return obj
+
+    # the sources are compiled side by side, the longest-running first
+    with tempfile.TemporaryDirectory() as work:
+        jobs = [(s, os.path.join(work, os.path.basename(s) + ".o"))
+                for s in sorted(sources(), key=os.path.getsize, reverse=True)]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            objects = list(pool.map(compile_one, jobs))
+        cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-o", tmp] + sorted(objects)
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB
 

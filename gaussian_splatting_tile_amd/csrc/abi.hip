@@ -95,6 +95,78 @@ gs::RecurrenceArgs recurrence_args(const gs_recurrence& r) {
     return a;
 }
 
+gs_status check_delta_rule(const gs_delta_rule* r, const char* who) {
+    if (!r) return fail(GS_ERR_INVALID, "%s: the description is NULL", who);
+    if (!type_bytes(r->dtype)) return fail(GS_ERR_INVALID, "%s: unknown dtype %d", who, r->dtype);
+    if (r->batch < 0 || r->steps < 0 || (int64_t)r->batch * r->steps > (1 << 30) || r->steps > (1 << 30))
+        return fail(GS_ERR_INVALID, "%s: batch %d and steps %d negative, or more than 2^30 in all", who, r->batch,
+                    r->steps);
+    if (r->key_heads < 1 || r->heads < 1 || r->heads > 4096 || r->heads % r->key_heads)
+        return fail(GS_ERR_INVALID, "%s: heads %d is not a multiple of key_heads %d in [1, 4096]", who, r->heads,
+                    r->key_heads);
+    if (r->key_dim < 1 || r->value_dim < 1 || r->key_dim > GS_DELTA_MAX_DIM || r->value_dim > GS_DELTA_MAX_DIM)
+        return fail(GS_ERR_INVALID, "%s: key_dim %d or value_dim %d outside [1, %d]", who, r->key_dim, r->value_dim,
+                    GS_DELTA_MAX_DIM);
+    const int64_t chunks = ((int64_t)r->steps + GS_DELTA_CHUNK - 1) / GS_DELTA_CHUNK;
+    const int64_t each = (int64_t)r->heads * (chunks > 0 ? chunks : 1);
+    if (r->batch > 0 && each > (1 << 24) / r->batch)
+        return fail(GS_ERR_INVALID, "%s: %d sequences of %d steps and %d heads are too many for one call", who, r->batch,
+                    r->steps, r->heads);
+    if (!std::isfinite(r->scale)) return fail(GS_ERR_INVALID, "%s: scale is not finite", who);
+    for (int64_t s : {r->q_batch, r->q_step, r->q_head, r->k_batch, r->k_step, r->k_head, r->v_batch, r->v_step,
+                      r->v_head, r->decay_batch, r->decay_step, r->beta_batch, r->beta_step})
+        if (s < 0) return fail(GS_ERR_INVALID, "%s: a stride is negative", who);
+    if ((uintptr_t)r->lengths & 3) return fail(GS_ERR_INVALID, "%s: lengths is not 4-byte aligned", who);
+    return GS_OK;
+}
+
+gs_status check_scratch(const void* scratch, size_t bytes, size_t need, size_t to, const char* who) {
+    if (need && (!scratch || bytes < need))
+        return fail(GS_ERR_INVALID, "%s: scratch of %zu bytes is smaller than the required %zu", who,
+                    scratch ? bytes : (size_t)0, need);
+    if (need && ((uintptr_t)scratch & (to - 1)))
+        return fail(GS_ERR_INVALID, "%s: scratch is not %zu-byte aligned", who, to);
+    return GS_OK;
+}
+
+gs_status check_block_norm(const gs_block_norm* d, const char* who) {
+    if (!d) return fail(GS_ERR_INVALID, "%s: the description is NULL", who);
+    if (!type_bytes(d->dtype) || !type_bytes(d->weight_dtype))
+        return fail(GS_ERR_INVALID, "%s: unknown dtype %d or weight_dtype %d", who, d->dtype, d->weight_dtype);
+    for (int32_t k : {d->post, d->pre})
+        if (k != GS_BLOCK_NORM_NONE && k != GS_BLOCK_NORM_RMS && k != GS_BLOCK_NORM_LAYER)
+            return fail(GS_ERR_INVALID, "%s: unknown norm %d", who, k);
+    if (d->gating != GS_BLOCK_GATE_NONE && d->gating != GS_BLOCK_GATE_SIGMOID && d->gating != GS_BLOCK_GATE_SILU)
+        return fail(GS_ERR_INVALID, "%s: unknown gating %d", who, d->gating);
+    if (d->outer < 0 || d->outer > (1 << 30) || d->inner < 1 || d->outer * d->inner > (1 << 30))
+        return fail(GS_ERR_INVALID, "%s: outer %lld negative, inner %d below 1, or more than 2^30 rows in all", who,
+                    (long long)d->outer, d->inner);
+    if (d->width < 1 || d->width > GS_BLOCK_NORM_MAX_WIDTH)
+        return fail(GS_ERR_INVALID, "%s: width %d outside [1, %d]", who, d->width, GS_BLOCK_NORM_MAX_WIDTH);
+    if (!(d->eps >= 0.0f) || !std::isfinite(d->eps))
+        return fail(GS_ERR_INVALID, "%s: eps %g is negative or not finite", who, d->eps);
+    for (int64_t s : {d->y_outer, d->y_inner, d->gate_outer, d->gate_inner, d->residual_outer, d->residual_inner})
+        if (s < 0) return fail(GS_ERR_INVALID, "%s: a stride is negative", who);
+    return GS_OK;
+}
+
+// The inputs that both directions of the block norms take.
+gs_status check_block_inputs(const gs_block_norm& d, const gs::BlockNormArgs& a, const char* who) {
+    if (!a.y || (d.gating != GS_BLOCK_GATE_NONE && !a.gate))
+        return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
+    if (d.gating == GS_BLOCK_GATE_NONE && a.gate) return fail(GS_ERR_INVALID, "%s: gate is given without gating", who);
+    if (d.post == GS_BLOCK_NORM_NONE && (a.post_weight || a.post_bias))
+        return fail(GS_ERR_INVALID, "%s: post_weight or post_bias is given without the post norm", who);
+    if (d.pre == GS_BLOCK_NORM_NONE && (a.pre_weight || a.pre_bias))
+        return fail(GS_ERR_INVALID, "%s: pre_weight or pre_bias is given without the pre norm", who);
+    if (!aligned(type_bytes(d.dtype), a.y, a.gate, a.residual, a.out, a.norm, a.grad_out, a.grad_norm, a.grad_y,
+                 a.grad_gate, a.grad_residual) ||
+        !aligned(type_bytes(d.weight_dtype), a.post_weight, a.post_bias, a.scale, a.pre_weight, a.pre_bias) ||
+        !aligned(4, a.sums[0], a.sums[1], a.sums[2], a.sums[3], a.sums[4]))
+        return fail(GS_ERR_INVALID, "%s: a buffer is not aligned to its type", who);
+    return GS_OK;
+}
+
 // Checks that the lists of gs_grad_norm, gs_clip_grads and gs_adam_step share.
 gs_status check_list(const void* tensors, int32_t n, const void* scratch, const char* who) {
     if (n < 0 || n > GS_MAX_TENSORS)
@@ -770,6 +842,155 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
     }
     return hip_check(gs::launch_adam_step(*cfg, tensors, n_tensors, step, norm, scratch, (hipStream_t)stream),
                      "gs_adam_step launch");
+}
+
+size_t gs_delta_rule_scratch_bytes(const gs_delta_rule* r, int32_t backward) {
+    g_last_error.clear();
+    if (check_delta_rule(r, "gs_delta_rule_scratch_bytes")) return 0;
+    return gs::delta_rule_scratch_bytes(*r, backward != 0);
+}
+
+gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* beta, const float* h0, void* o, float* h_last,
+                            float* ckpt, void* scratch, size_t scratch_bytes, void* stream) {
+    const char* const who = "gs_delta_rule_fwd";
+    g_last_error.clear();
+    if (gs_status s = check_delta_rule(r, who)) return s;
+    if (r->batch == 0) return GS_OK;
+    if (r->steps > 0 && (!q || !k || !v || !log_decay || !beta || !o))
+        return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
+    if (!aligned(type_bytes(r->dtype), q, k, v, o) || !aligned(4, log_decay, beta, h0, h_last, ckpt))
+        return fail(GS_ERR_INVALID, "%s: a buffer is not aligned to its type", who);
+    if (gs_status s = check_scratch(scratch, scratch_bytes, gs::delta_rule_scratch_bytes(*r, false), 16, who)) return s;
+    for (const void* in : {q, k, v})
+        if (o && o == in) return fail(GS_ERR_INVALID, "%s: o overlaps an input", who);
+    gs::DeltaArgs a{};
+    a.r = *r;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.log_decay = log_decay;
+    a.beta = beta;
+    a.h0 = h0;
+    a.o = o;
+    a.h_last = h_last;
+    a.ckpt = ckpt;
+    return hip_check(gs::launch_delta_rule_fwd(a, scratch, (hipStream_t)stream), "gs_delta_rule_fwd launch");
+}
+
+gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* beta, const float* h0, const float* ckpt,
+                            const void* grad_o, const float* grad_last, void* grad_q, void* grad_k, void* grad_v,
+                            float* grad_log_decay, float* grad_beta, float* grad_h0, void* scratch,
+                            size_t scratch_bytes, void* stream) {
+    const char* const who = "gs_delta_rule_bwd";
+    g_last_error.clear();
+    if (gs_status s = check_delta_rule(r, who)) return s;
+    if (r->batch == 0) return GS_OK;
+    if (r->steps > 0 && (!q || !k || !v || !log_decay || !beta || !grad_o || !grad_q || !grad_k || !grad_v ||
+                         !grad_log_decay || !grad_beta))
+        return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
+    if (r->steps > GS_DELTA_CHUNK && !ckpt)
+        return fail(GS_ERR_INVALID, "%s: ckpt is NULL with more than %d steps", who, GS_DELTA_CHUNK);
+    if (!aligned(type_bytes(r->dtype), q, k, v, grad_o, grad_q, grad_k, grad_v) ||
+        !aligned(4, log_decay, beta, h0, ckpt, grad_last, grad_log_decay, grad_beta, grad_h0))
+        return fail(GS_ERR_INVALID, "%s: a buffer is not aligned to its type", who);
+    if (gs_status s = check_scratch(scratch, scratch_bytes, gs::delta_rule_scratch_bytes(*r, true), 16, who)) return s;
+    for (const void* in : {q, k, v, grad_o, (const void*)log_decay, (const void*)beta, (const void*)h0})
+        for (const void* out : {(const void*)grad_q, (const void*)grad_k, (const void*)grad_v,
+                                (const void*)grad_log_decay, (const void*)grad_beta, (const void*)grad_h0})
+            if (in && in == out) return fail(GS_ERR_INVALID, "%s: a gradient overlaps an input", who);
+    gs::DeltaArgs a{};
+    a.r = *r;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.log_decay = log_decay;
+    a.beta = beta;
+    a.h0 = h0;
+    a.ckpt_in = ckpt;
+    a.grad_o = grad_o;
+    a.grad_last = grad_last;
+    a.grad_q = grad_q;
+    a.grad_k = grad_k;
+    a.grad_v = grad_v;
+    a.grad_log_decay = grad_log_decay;
+    a.grad_beta = grad_beta;
+    a.grad_h0 = grad_h0;
+    return hip_check(gs::launch_delta_rule_bwd(a, scratch, (hipStream_t)stream), "gs_delta_rule_bwd launch");
+}
+
+gs_status gs_block_norm_fwd(const gs_block_norm* d, const void* y, const void* gate, const void* residual,
+                            const void* post_weight, const void* post_bias, const void* scale, const void* pre_weight,
+                            const void* pre_bias, void* out, void* norm, void* stream) {
+    const char* const who = "gs_block_norm_fwd";
+    g_last_error.clear();
+    if (gs_status s = check_block_norm(d, who)) return s;
+    if (d->outer == 0) return GS_OK;
+    const bool pre = d->pre != GS_BLOCK_NORM_NONE;
+    if (pre ? !norm : !out) return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
+    gs::BlockNormArgs a{*d, y, gate, residual, post_weight, post_bias, scale, pre_weight, pre_bias};
+    a.out = out;
+    a.norm = pre ? norm : nullptr;
+    if (gs_status s = check_block_inputs(*d, a, who)) return s;
+    if (pre) {
+        for (const void* p : {y, gate, residual, (const void*)out})
+            if (p == norm) return fail(GS_ERR_INVALID, "%s: norm overlaps out or an input", who);
+    }
+    const int64_t w = d->width, o = w * d->inner;
+    auto contiguous = [&](int64_t so, int64_t si) {
+        return (d->outer == 1 || so == o) && (d->inner == 1 || si == w);
+    };
+    if ((out == y && !contiguous(d->y_outer, d->y_inner)) ||
+        (out && out == gate && !contiguous(d->gate_outer, d->gate_inner)) ||
+        (out && out == residual && !contiguous(d->residual_outer, d->residual_inner)))
+        return fail(GS_ERR_INVALID, "%s: out replaces an input that is not contiguous", who);
+    return hip_check(gs::launch_block_norm_fwd(a, (hipStream_t)stream), "gs_block_norm_fwd launch");
+}
+
+size_t gs_block_norm_scratch_bytes(const gs_block_norm* d) {
+    g_last_error.clear();
+    if (check_block_norm(d, "gs_block_norm_scratch_bytes")) return 0;
+    return gs::block_norm_scratch_bytes(*d);
+}
+
+gs_status gs_block_norm_bwd(const gs_block_norm* d, const void* y, const void* gate, const void* residual,
+                            const void* post_weight, const void* post_bias, const void* scale, const void* pre_weight,
+                            const void* pre_bias, const void* grad_out, const void* grad_norm, void* grad_y,
+                            void* grad_gate, void* grad_residual, float* grad_post_weight, float* grad_post_bias,
+                            float* grad_scale, float* grad_pre_weight, float* grad_pre_bias, void* scratch,
+                            size_t scratch_bytes, void* stream) {
+    const char* const who = "gs_block_norm_bwd";
+    g_last_error.clear();
+    if (gs_status s = check_block_norm(d, who)) return s;
+    gs::BlockNormArgs a{*d, y, gate, residual, post_weight, post_bias, scale, pre_weight, pre_bias};
+    const bool pre = d->pre != GS_BLOCK_NORM_NONE;
+    a.grad_out = grad_out;
+    a.grad_norm = pre ? grad_norm : nullptr;
+    a.grad_y = grad_y;
+    a.grad_gate = d->gating != GS_BLOCK_GATE_NONE ? grad_gate : nullptr;
+    a.grad_residual = grad_residual;
+    const bool post = d->post != GS_BLOCK_NORM_NONE;
+    if ((!post && (grad_post_weight || grad_post_bias)) || (!pre && (grad_pre_weight || grad_pre_bias)))
+        return fail(GS_ERR_INVALID, "%s: the gradient of a weight is asked for without its norm", who);
+    float* const sums[5] = {grad_post_weight, grad_post_bias, grad_scale, grad_pre_weight, grad_pre_bias};
+    bool any = false;
+    for (int i = 0; i < 5; ++i) any |= (a.sums[i] = sums[i]) != nullptr;
+    if (d->outer == 0 && !any) return GS_OK;
+    if (d->outer > 0) {
+        if (!grad_y || (pre ? !grad_norm : !grad_out)) return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
+        if (gs_status s = check_block_inputs(*d, a, who)) return s;
+        for (const void* in : {y, gate, residual})
+            for (const void* out : {(const void*)grad_y, (const void*)a.grad_gate, (const void*)grad_residual})
+                if (in && in == out) return fail(GS_ERR_INVALID, "%s: a gradient overlaps an input", who);
+        if (grad_y == a.grad_gate || grad_y == grad_residual || (grad_residual && grad_residual == a.grad_gate))
+            return fail(GS_ERR_INVALID, "%s: two gradients are one buffer", who);
+        if (any)
+            if (gs_status s = check_scratch(scratch, scratch_bytes, gs::block_norm_scratch_bytes(*d), 4, who)) return s;
+    } else if (!aligned(4, sums[0], sums[1], sums[2], sums[3], sums[4])) {
+        return fail(GS_ERR_INVALID, "%s: a buffer is not aligned to its type", who);
+    }
+    return hip_check(gs::launch_block_norm_bwd(a, (float*)scratch, (hipStream_t)stream), "gs_block_norm_bwd launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,789 @@
+// Gated delta rule, forward and backward (include/gs.h, gs_delta_rule_*).
+//
+// A sequence is cut into chunks of 64 steps. Inside a chunk, with S the state
+// in front, gamma_i the product of the decays up to step i, D_ij that of the
+// decays behind j up to i (0 across a restart), the steps' u solve
+//   (I + A) U = R,  A_ij = beta_i D_ij k_i.k_j (j < i),  R = beta (V - gamma K S)
+// and with M = (I + A)^-1, P_ij = scale D_ij q_i.k_j (j <= i), e_j = D_{63,j}:
+//   U = M R;  O = scale gamma Q S + P U;  S' = gamma_63 S + K^T (e U).
+// Backwards, with dS the gradient of S' and dO that of O:
+//   dU = P^T dO + e K dS;  dR = M^T dU;  dV = beta dR
+//   dS <- gamma_63 dS + Q^T (scale gamma dO) - K^T (beta gamma dR)
+// and, D included in both, Pd = scale D (dO U^T), Ad = -beta D (dR U^T) (j < i):
+//   dQ = scale gamma (dO S^T) + Pd K
+//   dK = Pd^T Q + Ad K + Ad^T K - beta gamma (dR S^T) + e (U dS^T)
+//   dbeta_i = dR_i.(v_i - gamma_i S^T k_i) + sum_j Ad_ij k_i.k_j / beta_i
+// The decay of step t lies between all j < t <= i, so with
+// X_ij = Pd_ij q_i.k_j + Ad_ij k_i.k_j
+//   dlog_decay_t = sum_{j < t <= i} X_ij + sum_{i >= t} f_i + sum_{j < t} b_j + gamma_63 <S, dS>
+//   f_i = q_i.(scale gamma dO S^T)_i - k_i.(beta gamma dR S^T)_i,  b_j = k_j.(e U dS^T)_j
+// formed as these sums, without differences of larger ones.
+#include <algorithm>
+
+#include "gs_internal.h"
+
+namespace gs {
+namespace {
+
+constexpr int kC = GS_DELTA_CHUNK;
+constexpr int kTiles = 10;               // lower 16 x 16 tiles of a chunk's 64 x 64 matrix
+constexpr int kLower = kTiles * 256;     // their floats
+constexpr int kPitch = kC + 4;           // of a 64 x 64 matrix in LDS
+
+typedef __bf16 bf16;
+typedef _Float16 f16;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ constexpr int tri(int i, int j) { return i * (i + 1) / 2 + j; }
+
+// Products of 16 x 16 tiles over 16: lane (i, g) of a wave holds A[i][4g + r] in a[r], B[4g + r][i] in b[r]
+// and C[4g + r][i] in c[r], so one product's result is the next one's right operand as it stands.
+__device__ __forceinline__ f32x4 mma(f32x4 a, f32x4 b, f32x4 c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[r], b[r], c, 0, 0, 0);
+    return c;
+}
+
+struct Chunk {
+    double G[kC];       // log2 of the product of the decays up to each step
+    float gamma[kC];    // that product, 0 behind a restart
+    float end[kC];      // product of the decays behind each step, 0 in front of a restart
+    float beta[kC];
+    int seg[kC];        // restarts up to each step
+    float whole;        // product of all decays, 0 with a restart
+};
+
+__device__ __forceinline__ int length_of(const gs_delta_rule& r, int b) {
+    return r.lengths ? min(max(r.lengths[b], 0), r.steps) : r.steps;
+}
+
+// By one wave, a lane a step. A decay that is 0 in float32 acts as a restart, so every sum is finite.
+__device__ __forceinline__ void load_gates(const DeltaArgs& a, int b, int h, int t0, int len, Chunk& s) {
+    const int lane = threadIdx.x & 63, t = t0 + lane;
+    const bool live = t < len;
+    float g = live ? a.log_decay[b * a.r.decay_batch + t * a.r.decay_step + h] : 0.0f;
+    const float beta = live ? a.beta[b * a.r.beta_batch + t * a.r.beta_step + h] : 0.0f;
+    const bool cut = live && (g < -104.0f || (a.r.restart && a.r.restart[(int64_t)b * a.r.steps + t]));
+    const uint64_t cuts = __ballot(cut);
+    const int seg = __popcll(cuts & (~0ull >> (63 - lane))), segs = __popcll(cuts);
+    double G = cut ? 0.0 : (double)g * 1.4426950408889634;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const double p = __shfl_up(G, m);
+        if (lane >= m) G += p;
+    }
+    const double last = __shfl(G, 63);
+    s.G[lane] = G;
+    s.seg[lane] = seg;
+    s.beta[lane] = beta;
+    s.gamma[lane] = seg == 0 ? __builtin_amdgcn_exp2f((float)G) : 0.0f;
+    s.end[lane] = seg == segs ? __builtin_amdgcn_exp2f((float)(last - G)) : 0.0f;
+    if (lane == 63) s.whole = segs == 0 ? __builtin_amdgcn_exp2f((float)G) : 0.0f;
+}
+
+__device__ __forceinline__ float decay(const Chunk& s, int i, int j) {
+    return s.seg[i] == s.seg[j] ? __builtin_amdgcn_exp2f((float)(s.G[i] - s.G[j])) : 0.0f;
+}
+
+// 64 rows of a [B][T][heads][dim] tensor as float32 in LDS, 0 at padding and past dim.
+template <int DK, typename T>
+__device__ __forceinline__ void load_rows(const T* p, int64_t step, int rows, int dim, float* to, int threads) {
+    for (int e = threadIdx.x; e < kC * DK; e += threads) {
+        const int t = e / DK, d = e % DK;
+        to[t * (DK + 4) + d] = t < rows && d < dim ? (float)p[t * step + d] : 0.0f;
+    }
+}
+
+template <int DK>
+__device__ __forceinline__ f32x4 row4(const float* m, int row, int col) {
+    return *(const f32x4*)(m + row * (DK + 4) + col);
+}
+__device__ __forceinline__ f32x4 col4(const float* m, int pitch, int row, int col) {
+    const float* const p = m + row * pitch + col;
+    return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
+}
+
+// M = (I + A)^-1 of every chunk and head: its lower 16 x 16 tiles, row-major, in
+// to[b][chunk][h][10][16][16]. The diagonal tiles by forward substitution, the
+// others from them, M21 = -M22 A21 M11 for pairs of tiles and of pairs.
+template <typename T, int DK>
+__global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs a, int chunks, float* to) {
+    __shared__ float K[kC * (DK + 4)];
+    __shared__ float M[kC * kPitch];
+    __shared__ Chunk s;
+    const int h = blockIdx.x % a.r.heads, c = blockIdx.x / a.r.heads % chunks, b = blockIdx.x / a.r.heads / chunks;
+    const int len = length_of(a.r, b), t0 = c * kC;
+    if (t0 >= len) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int kh = h / (a.r.heads / a.r.key_heads);
+    const T* const k = (const T*)a.k + b * a.r.k_batch + t0 * a.r.k_step + kh * a.r.k_head;
+    load_rows<DK>(k, a.r.k_step, len - t0, a.r.key_dim, K, 256);
+    if (w == 0) load_gates(a, b, h, t0, len, s);
+    __syncthreads();
+    for (int cj = 0; cj <= w; ++cj) {
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt)
+            acc = mma(row4<DK>(K, 16 * w + n, 16 * kt + 4 * g), row4<DK>(K, 16 * cj + n, 16 * kt + 4 * g), acc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * w + 4 * g + r, j = 16 * cj + n;
+            M[i * kPitch + j] = i > j ? s.beta[i] * decay(s, i, j) * acc[r] : 0.0f;
+        }
+    }
+    __syncthreads();
+    {
+        float x[16];
+        const float* const A = M + 16 * w * (kPitch + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float t = i == n ? 1.0f : 0.0f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) t = fmaf(-A[i * kPitch + j], x[j], t);
+            x[i] = t;
+        }
+        __syncthreads();
+        if (lane < 16)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) M[(16 * w + i) * kPitch + 16 * w + n] = x[i];
+    }
+    __syncthreads();
+    auto tile = [&](int i, int j) { return *(const f32x4*)(M + (16 * i + n) * kPitch + 16 * j + 4 * g); };
+    auto right = [&](int i, int j) { return col4(M, kPitch, 16 * i + 4 * g, 16 * j + n); };
+    const f32x4 zero = {0, 0, 0, 0};
+    auto put = [&](int i, int j, f32x4 v) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) M[(16 * i + 4 * g + r) * kPitch + 16 * j + n] = -v[r];
+    };
+    if (w < 2) {
+        const f32x4 x = mma(tile(2 * w + 1, 2 * w), right(2 * w, 2 * w), zero);
+        put(2 * w + 1, 2 * w, mma(tile(2 * w + 1, 2 * w + 1), x, zero));
+    }
+    __syncthreads();
+    f32x4 y2 = zero, y3 = zero;
+    if (w < 2) {
+        f32x4 x2 = zero, x3 = zero;
+        for (int q = w; q < 2; ++q) {
+            const f32x4 m = right(q, w);
+            x2 = mma(tile(2, q), m, x2);
+            x3 = mma(tile(3, q), m, x3);
+        }
+        y2 = mma(tile(2, 2), x2, zero);
+        y3 = mma(tile(3, 3), x3, mma(tile(3, 2), x2, zero));
+    }
+    __syncthreads();
+    if (w < 2) {
+        put(2, w, y2);
+        put(3, w, y3);
+    }
+    __syncthreads();
+    float* const out = to + (int64_t)blockIdx.x * kLower;
+    for (int e = threadIdx.x; e < kLower; e += 256) {
+        const int q = e >> 8, i = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, j = q - tri(i, 0);
+        out[e] = M[(16 * i + (e >> 4 & 15)) * kPitch + 16 * j + (e & 15)];
+    }
+}
+
+// P of a chunk into LDS, its tiles spread over the waves of the workgroup.
+template <int DK>
+__device__ __forceinline__ void chunk_p(const float* Q, const float* K, const Chunk& s, float scale, float* P, int waves) {
+    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    for (int q = threadIdx.x >> 6; q < kTiles; q += waves) {
+        const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, tj = q - tri(ti, 0);
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int kt = 0; kt < DK / 16; ++kt)
+            acc = mma(row4<DK>(Q, 16 * ti + n, 16 * kt + 4 * g), row4<DK>(K, 16 * tj + n, 16 * kt + 4 * g), acc);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
+            P[i * kPitch + j] = i >= j ? scale * decay(s, i, j) * acc[r] : 0.0f;
+        }
+    }
+}
+
+constexpr int kChainWaves = 4;
+
+// The states, chunk after chunk, 16 columns of the values a wave: S stays in
+// its registers as C tiles, which are the right operands of K S and Q S.
+template <typename T, int DK>
+__global__ __launch_bounds__(64 * kChainWaves) void k_delta_fwd(DeltaArgs a, int chunks, const float* inverse) {
+    constexpr int KT = DK / 16, kThreads = 64 * kChainWaves;
+    __shared__ float K[kC * (DK + 4)];
+    __shared__ float Q[kC * (DK + 4)];
+    __shared__ float P[kC * kPitch];
+    __shared__ Chunk s;
+    const gs_delta_rule& d = a.r;
+    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
+    const bool on = col < d.value_dim;
+    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
+    const int64_t head = (int64_t)b * d.heads + h, state = head * d.key_dim * d.value_dim + col;
+    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
+    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
+    const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head + col;
+    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
+    const int64_t o_step = (int64_t)d.heads * d.value_dim;
+    f32x4 S[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * kt + 4 * g + r;
+            S[kt][r] = a.h0 && on && row < d.key_dim ? a.h0[state + (int64_t)row * d.value_dim] : 0.0f;
+        }
+    for (int c = 0; c < mine; ++c) {
+        const int t0 = c * kC, rows = len - t0;
+        __syncthreads();
+        load_rows<DK>(k + t0 * d.k_step, d.k_step, rows, d.key_dim, K, kThreads);
+        load_rows<DK>(q + t0 * d.q_step, d.q_step, rows, d.key_dim, Q, kThreads);
+        if (w == 0) load_gates(a, b, h, t0, len, s);
+        __syncthreads();
+        chunk_p<DK>(Q, K, s, d.scale, P, kChainWaves);
+        f32x4 R[4], U[4];
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r;
+                const float x = on && i < rows ? (float)v[(t0 + i) * d.v_step] : 0.0f;
+                R[ti][r] = s.beta[i] * (x - s.gamma[i] * acc[r]);
+            }
+        }
+        const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower + n * 16 + 4 * g;
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            U[ti] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int tj = 0; tj <= ti; ++tj) U[ti] = mma(*(const f32x4*)(M + tri(ti, tj) * 256), R[tj], U[ti]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(Q, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] *= d.scale * s.gamma[16 * ti + 4 * g + r];
+#pragma unroll
+            for (int tj = 0; tj <= ti; ++tj) acc = mma(*(const f32x4*)(P + (16 * ti + n) * kPitch + 16 * tj + 4 * g), U[tj], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = t0 + 16 * ti + 4 * g + r;
+                if (on && t < d.steps) o[t * o_step] = (T)acc[r];
+            }
+        }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) U[ti][r] *= s.end[16 * ti + 4 * g + r];
+        const float whole = s.whole;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            S[kt] *= whole;
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj) S[kt] = mma(col4(K, DK + 4, 16 * tj + 4 * g, 16 * kt + n), U[tj], S[kt]);
+        }
+        if (a.ckpt && t0 + kC < len) {
+            float* const to = a.ckpt + ((((int64_t)b * (chunks - 1) + c) * d.heads + h) * d.key_dim) * d.value_dim + col;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * kt + 4 * g + r;
+                    if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[kt][r];
+                }
+        }
+    }
+    for (int t = mine * kC + g; t < d.steps; t += 4)
+        if (on) o[t * o_step] = (T)0.0f;
+    if (a.h_last)
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * kt + 4 * g + r;
+                if (on && row < d.key_dim) a.h_last[state + (int64_t)row * d.value_dim] = S[kt][r];
+            }
+}
+
+// The gradients of the states, from the last chunk to the first, 16 columns a
+// wave; behind[b][chunk][h] receives the one behind each chunk.
+template <typename T, int DK>
+__global__ __launch_bounds__(64 * kChainWaves) void k_delta_bwd(DeltaArgs a, int chunks, const float* inverse, float* behind) {
+    constexpr int KT = DK / 16, kThreads = 64 * kChainWaves;
+    __shared__ float K[kC * (DK + 4)];
+    __shared__ float Q[kC * (DK + 4)];
+    __shared__ float P[kC * kPitch];
+    __shared__ Chunk s;
+    const gs_delta_rule& d = a.r;
+    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
+    const bool on = col < d.value_dim;
+    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
+    const int64_t head = (int64_t)b * d.heads + h, state = head * d.key_dim * d.value_dim + col;
+    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
+    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
+    const int64_t o_step = (int64_t)d.heads * d.value_dim;
+    const int64_t first = ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
+    const T* const go = (const T*)a.grad_o + first;
+    T* const gv = (T*)a.grad_v + first;
+    f32x4 S[KT];
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = 16 * kt + 4 * g + r;
+            S[kt][r] = a.grad_last && on && row < d.key_dim ? a.grad_last[state + (int64_t)row * d.value_dim] : 0.0f;
+        }
+    for (int t = mine * kC + g; t < d.steps; t += 4)
+        if (on) gv[t * o_step] = (T)0.0f;
+    for (int c = mine - 1; c >= 0; --c) {
+        const int t0 = c * kC, rows = len - t0;
+        float* const to = behind + (((int64_t)b * chunks + c) * d.heads + h) * d.key_dim * d.value_dim + col;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * kt + 4 * g + r;
+                if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[kt][r];
+            }
+        __syncthreads();
+        load_rows<DK>(k + t0 * d.k_step, d.k_step, rows, d.key_dim, K, kThreads);
+        load_rows<DK>(q + t0 * d.q_step, d.q_step, rows, d.key_dim, Q, kThreads);
+        if (w == 0) load_gates(a, b, h, t0, len, s);
+        __syncthreads();
+        chunk_p<DK>(Q, K, s, d.scale, P, kChainWaves);
+        f32x4 dO[4], dU[4], dR[4];
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r;
+                dO[ti][r] = on && i < rows ? (float)go[(t0 + i) * o_step] : 0.0f;
+                dU[ti][r] = s.end[i] * acc[r];
+            }
+        }
+        __syncthreads();
+        const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower + 64 * g + n;
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int tj = ti; tj < 4; ++tj) dU[ti] = mma(col4(P, kPitch, 16 * tj + 4 * g, 16 * ti + n), dO[tj], dU[ti]);
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            dR[ti] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int tj = ti; tj < 4; ++tj) dR[ti] = mma(col4(M + tri(tj, ti) * 256, 16, 0, 0), dU[tj], dR[ti]);
+        }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r, t = t0 + i;
+                const float x = s.beta[i] * dR[ti][r];
+                if (on && t < d.steps) gv[t * o_step] = (T)x;
+                dR[ti][r] = -s.gamma[i] * x;
+                dO[ti][r] *= d.scale * s.gamma[i];
+            }
+        const float whole = s.whole;
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            S[kt] *= whole;
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj) {
+                S[kt] = mma(col4(Q, DK + 4, 16 * tj + 4 * g, 16 * kt + n), dO[tj], S[kt]);
+                S[kt] = mma(col4(K, DK + 4, 16 * tj + 4 * g, 16 * kt + n), dR[tj], S[kt]);
+            }
+        }
+    }
+    if (a.grad_h0)
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * kt + 4 * g + r;
+                if (on && row < d.key_dim) a.grad_h0[state + (int64_t)row * d.value_dim] = S[kt][r];
+            }
+}
+
+constexpr int kGradWaves = 8;
+constexpr int kV = GS_DELTA_MAX_DIM;
+
+// The gradients of a chunk's queries, keys and gates from the states in front
+// and the gradients behind, for all heads of a key head, one after another.
+// First a wave takes 16 columns of the values (U and dR, to LDS), then 16 of
+// the keys.
+template <typename T, int DK>
+__global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int chunks, const float* inverse, const float* behind) {
+    constexpr int KT = DK / 16, kThreads = 64 * kGradWaves;
+    __shared__ float K[kC * (DK + 4)];
+    __shared__ float U[kC * (kV + 4)];
+    __shared__ float E[kC * (kV + 4)];   // dR
+    __shared__ float P[kC * kPitch];     // P, then Pd
+    __shared__ float A[kC * kPitch];     // Ad
+    __shared__ float X[kC * (kC + 1)];
+    __shared__ float betas[kGradWaves][kC], front[kGradWaves][kC], after[kGradWaves][kC], dots[kGradWaves];
+    __shared__ Chunk s;
+    const gs_delta_rule& d = a.r;
+    const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
+    const int64_t first = (((int64_t)b * d.steps + t0) * d.key_heads + kh) * d.key_dim;
+    T* const gq = (T*)a.grad_q + first;
+    T* const gk = (T*)a.grad_k + first;
+    const int64_t k_step = (int64_t)d.key_heads * d.key_dim, o_step = (int64_t)d.heads * d.value_dim;
+    const int all = min(kC, d.steps - t0);  // steps of the chunk, padding included
+    if (rows <= 0) {
+        for (int e = threadIdx.x; e < all * d.key_dim; e += kThreads) {
+            const int64_t at = e / d.key_dim * k_step + e % d.key_dim;
+            gq[at] = gk[at] = (T)0.0f;
+        }
+        for (int e = threadIdx.x; e < all * group; e += kThreads) {
+            const int64_t at = ((int64_t)b * d.steps + t0 + e / group) * d.heads + kh * group + e % group;
+            a.grad_log_decay[at] = a.grad_beta[at] = 0.0f;
+        }
+        return;
+    }
+    const T* const q = (const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head;
+    const T* const k = (const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head;
+    auto q4 = [&](int row, int at) {
+        f32x4 x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = row < rows && at + r < d.key_dim ? (float)q[row * d.q_step + at + r] : 0.0f;
+        return x;
+    };
+    auto qcol = [&](int row, int at) {
+        f32x4 x;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = row + r < rows && at < d.key_dim ? (float)q[(row + r) * d.q_step + at] : 0.0f;
+        return x;
+    };
+    load_rows<DK>(k, d.k_step, rows, d.key_dim, K, kThreads);
+    const f32x4 zero = {0, 0, 0, 0};
+    f32x4 dq[4], dk[4];
+#pragma unroll
+    for (int ti = 0; ti < 4; ++ti) dq[ti] = dk[ti] = zero;
+    for (int hh = 0; hh < group; ++hh) {
+        const int h = kh * group + hh;
+        const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
+        const float* const S0 = c == 0 ? (a.h0 ? a.h0 + head * size : nullptr)
+                                       : a.ckpt_in + (((int64_t)b * (chunks - 1) + c - 1) * d.heads + h) * size;
+        const float* const dS = behind + (((int64_t)b * chunks + c) * d.heads + h) * size;
+        const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower;
+        const T* const v = (const T*)a.v + b * d.v_batch + t0 * d.v_step + h * d.v_head;
+        const T* const go = (const T*)a.grad_o + (((int64_t)b * d.steps + t0) * d.heads + h) * d.value_dim;
+        __syncthreads();
+        if (w == 0) load_gates(a, b, h, t0, len, s);
+        __syncthreads();
+        for (int p = w; p < kTiles; p += kGradWaves) {
+            const int ti = p >= 6 ? 3 : p >= 3 ? 2 : p >= 1 ? 1 : 0, tj = p - tri(ti, 0);
+            f32x4 acc = zero;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+                acc = mma(q4(16 * ti + n, 16 * kt + 4 * g), row4<DK>(K, 16 * tj + n, 16 * kt + 4 * g), acc);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
+                P[i * kPitch + j] = i >= j ? d.scale * decay(s, i, j) * acc[r] : 0.0f;
+            }
+        }
+        __syncthreads();
+        {
+            const int col = 16 * w + n;
+            const bool on = col < d.value_dim;
+            f32x4 S[KT], Z[KT];
+            float dot = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * kt + 4 * g + r;
+                    const bool in = on && row < d.key_dim;
+                    S[kt][r] = in && S0 ? S0[(int64_t)row * d.value_dim + col] : 0.0f;
+                    Z[kt][r] = in ? dS[(int64_t)row * d.value_dim + col] : 0.0f;
+                    dot = fmaf(S[kt][r], Z[kt][r], dot);
+                }
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) dot += __shfl_xor(dot, m);
+            if (lane == 0) dots[w] = dot;
+            f32x4 R[4], e[4], dO[4], dU[4], dR[4], u[4];
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                f32x4 x = zero, y = zero;
+#pragma unroll
+                for (int kt = 0; kt < KT; ++kt) {
+                    const f32x4 kk = row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g);
+                    x = mma(kk, S[kt], x);
+                    y = mma(kk, Z[kt], y);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * ti + 4 * g + r;
+                    const bool in = on && i < rows;
+                    e[ti][r] = (in ? (float)v[i * d.v_step + col] : 0.0f) - s.gamma[i] * x[r];
+                    R[ti][r] = s.beta[i] * e[ti][r];
+                    dO[ti][r] = in ? (float)go[i * o_step + col] : 0.0f;
+                    dU[ti][r] = s.end[i] * y[r];
+                }
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                u[ti] = zero;
+#pragma unroll
+                for (int tj = 0; tj <= ti; ++tj)
+                    u[ti] = mma(*(const f32x4*)(M + tri(ti, tj) * 256 + n * 16 + 4 * g), R[tj], u[ti]);
+#pragma unroll
+                for (int tj = ti; tj < 4; ++tj) dU[ti] = mma(col4(P, kPitch, 16 * tj + 4 * g, 16 * ti + n), dO[tj], dU[ti]);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                dR[ti] = zero;
+#pragma unroll
+                for (int tj = ti; tj < 4; ++tj) dR[ti] = mma(col4(M + tri(tj, ti) * 256 + 64 * g + n, 16, 0, 0), dU[tj], dR[ti]);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * ti + 4 * g + r;
+                    U[i * (kV + 4) + col] = u[ti][r];
+                    E[i * (kV + 4) + col] = dR[ti][r];
+                    float t = dR[ti][r] * e[ti][r];
+#pragma unroll
+                    for (int m = 1; m < 16; m <<= 1) t += __shfl_xor(t, m);
+                    if (n == 0) betas[w][i] = t;
+                }
+        }
+        __syncthreads();
+        auto o4 = [&](int row, int at) {
+            f32x4 x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[r] = row < rows && at + r < d.value_dim ? (float)go[row * o_step + at + r] : 0.0f;
+            return x;
+        };
+        const int vt = (d.value_dim + 15) / 16;
+        float part[2][4] = {};  // of the gradient of beta, from the tiles of this wave
+        for (int p = w, turn = 0; p < kTiles; p += kGradWaves, ++turn) {
+            const int ti = p >= 6 ? 3 : p >= 3 ? 2 : p >= 1 ? 1 : 0, tj = p - tri(ti, 0);
+            f32x4 dp = zero, da = zero, qk = zero, kk = zero;
+            for (int ct = 0; ct < vt; ++ct) {
+                const f32x4 u = row4<kV>(U, 16 * tj + n, 16 * ct + 4 * g);
+                dp = mma(o4(16 * ti + n, 16 * ct + 4 * g), u, dp);
+                da = mma(row4<kV>(E, 16 * ti + n, 16 * ct + 4 * g), u, da);
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) {
+                const f32x4 x = row4<DK>(K, 16 * tj + n, 16 * kt + 4 * g);
+                qk = mma(q4(16 * ti + n, 16 * kt + 4 * g), x, qk);
+                kk = mma(row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g), x, kk);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
+                const float D = i >= j ? decay(s, i, j) : 0.0f;
+                const float pd = d.scale * D * dp[r], ad = i > j ? -D * da[r] : 0.0f;
+                P[i * kPitch + j] = pd;
+                A[i * kPitch + j] = s.beta[i] * ad;
+                X[i * (kC + 1) + j] = pd * qk[r] + s.beta[i] * ad * kk[r];
+                float t = ad * kk[r];
+#pragma unroll
+                for (int m = 1; m < 16; m <<= 1) t += __shfl_xor(t, m);
+                part[turn][r] = t;
+            }
+        }
+        f32x4 aq[4], ar[4], au[4];
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) aq[ti] = ar[ti] = au[ti] = zero;
+        const int row = 16 * w + n;  // of the keys
+        if (w < KT) {
+            for (int ct = 0; ct < vt; ++ct) {
+                f32x4 x, y;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = 16 * ct + 4 * g + r;
+                    const bool in = row < d.key_dim && at < d.value_dim;
+                    x[r] = in && S0 ? S0[(int64_t)row * d.value_dim + at] : 0.0f;
+                    y[r] = in ? dS[(int64_t)row * d.value_dim + at] : 0.0f;
+                }
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    aq[ti] = mma(o4(16 * ti + n, 16 * ct + 4 * g), x, aq[ti]);
+                    ar[ti] = mma(row4<kV>(E, 16 * ti + n, 16 * ct + 4 * g), x, ar[ti]);
+                    au[ti] = mma(row4<kV>(U, 16 * ti + n, 16 * ct + 4 * g), y, au[ti]);
+                }
+            }
+        }
+        __syncthreads();
+        // what tile (ti, tj) adds to the gradient of beta: rows of ti, in the order of tj, behind the values' part
+        for (int q = 0; q < kTiles; ++q) {
+            if (q % kGradWaves == w && n == 0) {
+                const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) betas[0][16 * ti + 4 * g + r] += part[q / kGradWaves][r];
+            }
+            __syncthreads();
+        }
+        if (w < KT) {
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                f32x4 x, y, fr, af;
+                const f32x4 qq = qcol(16 * ti + 4 * g, row), kk = col4(K, DK + 4, 16 * ti + 4 * g, row);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * ti + 4 * g + r;
+                    x[r] = d.scale * s.gamma[i] * aq[ti][r];
+                    const float m = s.beta[i] * s.gamma[i] * ar[ti][r], z = s.end[i] * au[ti][r];
+                    y[r] = z - m;
+                    fr[r] = qq[r] * x[r] - kk[r] * m;
+                    af[r] = kk[r] * z;
+#pragma unroll
+                    for (int t = 1; t < 16; t <<= 1) {
+                        fr[r] += __shfl_xor(fr[r], t);
+                        af[r] += __shfl_xor(af[r], t);
+                    }
+                    if (n == 0) {
+                        front[w][i] = fr[r];
+                        after[w][i] = af[r];
+                    }
+                }
+#pragma unroll
+                for (int tj = 0; tj < 4; ++tj) {
+                    const f32x4 k4 = col4(K, DK + 4, 16 * tj + 4 * g, row);
+                    if (tj <= ti) {
+                        x = mma(*(const f32x4*)(P + (16 * ti + n) * kPitch + 16 * tj + 4 * g), k4, x);
+                        y = mma(*(const f32x4*)(A + (16 * ti + n) * kPitch + 16 * tj + 4 * g), k4, y);
+                    }
+                    if (tj >= ti) {
+                        y = mma(col4(P, kPitch, 16 * tj + 4 * g, 16 * ti + n), qcol(16 * tj + 4 * g, row), y);
+                        y = mma(col4(A, kPitch, 16 * tj + 4 * g, 16 * ti + n), k4, y);
+                    }
+                }
+                dq[ti] += x;
+                dk[ti] += y;
+            }
+        }
+        // X: sums over j < t of every row, in place
+        if (w == kGradWaves - 1) {
+            float t = 0.0f;
+            for (int j = 0; j < lane; ++j) {
+                const float x = X[lane * (kC + 1) + j];
+                X[lane * (kC + 1) + j] = t;
+                t += x;
+            }
+            X[lane * (kC + 1) + lane] = t;
+        }
+        __syncthreads();
+        if (w == 0) {
+            float f = 0.0f, af = 0.0f, be = 0.0f, dot = 0.0f;
+            for (int x = 0; x < kGradWaves; ++x) {
+                be += betas[x][lane];
+                dot += dots[x];
+            }
+            for (int x = 0; x < KT; ++x) {
+                f += front[x][lane];
+                af += after[x][lane];
+            }
+            float all_f = f, all_a = af;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const float p = __shfl_down(all_f, m), o = __shfl_up(all_a, m);
+                if (lane + m < 64) all_f += p;
+                if (lane >= m) all_a += o;
+            }
+            all_a = __shfl_up(all_a, 1);
+            float t = 0.0f;
+            for (int i = lane; i < kC; ++i) t += X[i * (kC + 1) + lane];
+            t += all_f + (lane ? all_a : 0.0f) + s.whole * dot;
+            if (lane < all) {
+                const int64_t at = ((int64_t)b * d.steps + t0 + lane) * d.heads + h;
+                const bool live = lane < rows;
+                // the decay of a restart is not applied
+                const bool cut = lane ? s.seg[lane] != s.seg[lane - 1] : s.seg[0] != 0;
+                a.grad_log_decay[at] = live && !cut ? t : 0.0f;
+                a.grad_beta[at] = live ? be : 0.0f;
+            }
+        }
+    }
+    const int row = 16 * w + n;
+    if (w < KT && row < d.key_dim)
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r;
+                if (i < all) {
+                    gq[i * k_step + row] = (T)dq[ti][r];
+                    gk[i * k_step + row] = (T)dk[ti][r];
+                }
+            }
+}
+
+int chunks_of(const gs_delta_rule& r) { return (r.steps + kC - 1) / kC; }
+size_t inverse_floats(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * kLower; }
+
+template <typename T, int DK>
+hipError_t forward(const DeltaArgs& a, float* scratch, hipStream_t stream) {
+    const gs_delta_rule& r = a.r;
+    const int chunks = chunks_of(r);
+    if (chunks) k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, scratch);
+    const int wide = 16 * kChainWaves;
+    k_delta_fwd<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
+        a, chunks, scratch);
+    return hipGetLastError();
+}
+
+template <typename T, int DK>
+hipError_t backward(const DeltaArgs& a, float* scratch, hipStream_t stream) {
+    const gs_delta_rule& r = a.r;
+    const int chunks = chunks_of(r);
+    float* const behind = scratch + inverse_floats(r);
+    if (chunks) k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, scratch);
+    const int wide = 16 * kChainWaves;
+    k_delta_bwd<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
+        a, chunks, scratch, behind);
+    if (chunks)
+        k_delta_grad<T, DK><<<r.batch * chunks * r.key_heads, 64 * kGradWaves, 0, stream>>>(a, chunks, scratch, behind);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t run(const DeltaArgs& a, float* scratch, bool back, hipStream_t stream) {
+    if (a.r.key_dim <= 64)
+        return back ? backward<T, 64>(a, scratch, stream) : forward<T, 64>(a, scratch, stream);
+    return back ? backward<T, 128>(a, scratch, stream) : forward<T, 128>(a, scratch, stream);
+}
+
+hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream) {
+    switch (a.r.dtype) {
+        case GS_F32: return run<float>(a, (float*)scratch, back, stream);
+        case GS_BF16: return run<bf16>(a, (float*)scratch, back, stream);
+        default: return run<f16>(a, (float*)scratch, back, stream);
+    }
+}
+
+}  // namespace
+
+size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
+    size_t floats = inverse_floats(r);
+    if (backward) floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
+    return floats * sizeof(float);
+}
+
+hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
+    return run(a, scratch, false, stream);
+}
+
+hipError_t launch_delta_rule_bwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
+    return run(a, scratch, true, stream);
+}
+
+}  // namespace gs

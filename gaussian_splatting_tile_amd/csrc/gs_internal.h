@@ -255,4 +255,36 @@ hipError_t launch_clip_grads(const gs_grad_tensor* tensors, int n, int kind, flo
 hipError_t launch_adam_step(const gs_adam& cfg, const gs_adam_tensor* tensors, int n, int64_t* step, float* norm,
                             void* scratch, hipStream_t stream);
 
+// Norms around a block: the arguments of one call, by value to its kernels.
+struct BlockNormArgs {
+    gs_block_norm d;
+    const void *y, *gate, *residual;
+    const void *post_weight, *post_bias, *scale, *pre_weight, *pre_bias;
+    void *out, *norm;                   // forward
+    const void *grad_out, *grad_norm;   // backward
+    void *grad_y, *grad_gate, *grad_residual;
+    float* sums[5];                     // gradients of post_weight, post_bias, scale, pre_weight, pre_bias
+};
+size_t block_norm_scratch_bytes(const gs_block_norm& d);
+hipError_t launch_block_norm_fwd(const BlockNormArgs& a, hipStream_t stream);
+hipError_t launch_block_norm_bwd(const BlockNormArgs& a, float* scratch, hipStream_t stream);
+
+// Gated delta rule: the arguments of one call, by value to its kernels.
+struct DeltaArgs {
+    gs_delta_rule r;
+    const void *q, *k, *v;
+    const float *log_decay, *beta, *h0;
+    void* o;  // forward
+    float* h_last;
+    float* ckpt;
+    const float* ckpt_in;  // backward
+    const void* grad_o;
+    const float* grad_last;
+    void *grad_q, *grad_k, *grad_v;
+    float *grad_log_decay, *grad_beta, *grad_h0;
+};
+size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward);
+hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream);
+hipError_t launch_delta_rule_bwd(const DeltaArgs& a, void* scratch, hipStream_t stream);
+
 }  // namespace gs

@@ -759,6 +759,165 @@ typedef struct {
 gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_t n_tensors, int64_t* step,
                        float* norm, void* scratch, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Gated delta rule: per sequence b and head h a matrix S of key_dim x
+ * value_dim that forgets by a decay and learns, at every step, the part of
+ * the value that it does not yet return for the key. With a_t =
+ * exp(log_decay_t), S_{-1} = h0:
+ *
+ *   S_t = a_t S_{t-1} + k_t u_t^T,  u_t = beta_t (v_t - a_t S_{t-1}^T k_t)
+ *   o_t = scale S_t^T q_t                         t = 0 .. len_b - 1
+ *
+ * Head h uses the queries and keys of key head h / (heads / key_heads). At a
+ * step with restart set the previous state is dropped (S_{t-1} = 0); a decay
+ * that is 0 in float32 (log_decay below -104, or -inf) drops it too. Steps at
+ * or behind len_b are padding: nothing of them is read, and o and the
+ * gradients are 0 there.
+ *
+ *   dtype       GS_F32, GS_BF16 or GS_F16: q, k, v, o and their gradients
+ *   batch, steps             B, T >= 0; B T at most 2^30
+ *   key_heads, heads         Hk >= 1, H a multiple of Hk; H at most 4096, and
+ *                            B H ceil(T / 64) at most 2^24
+ *   key_dim, value_dim       1 .. GS_DELTA_MAX_DIM
+ *   scale       of the queries, finite
+ *   *_batch, *_step, *_head  strides of q [B][T][Hk][key_dim], k (the same)
+ *               and v [B][T][H][value_dim] in elements, >= 0, a head's
+ *               elements contiguous; decay and beta strides of log_decay and
+ *               beta, float32 [B][T][H], heads contiguous
+ *   lengths     [B] int32, or NULL (every length is T); values outside
+ *               [0, T] are clamped to it
+ *   restart     [B][T] uint8, or NULL
+ * All other arrays are contiguous. Products of 16-bit inputs and float32
+ * values keep 24 bits of both, sums and states are float32, sums of
+ * log_decay float64. Products of decays above 1 (log_decay above 0) are
+ * formed over at most 64 steps and may leave float32's range there.
+ * ------------------------------------------------------------------- */
+#define GS_DELTA_CHUNK 64
+#define GS_DELTA_MAX_DIM 128
+typedef struct {
+    int32_t dtype;
+    int32_t batch, steps, key_heads, heads, key_dim, value_dim;
+    float scale;
+    int64_t q_batch, q_step, q_head, k_batch, k_step, k_head, v_batch, v_step, v_head;
+    int64_t decay_batch, decay_step, beta_batch, beta_step;
+    const int32_t* lengths;
+    const uint8_t* restart;
+} gs_delta_rule;
+
+/* gs_delta_rule_scratch_bytes - workspace of gs_delta_rule_fwd (backward = 0)
+ * or gs_delta_rule_bwd (1) for this description (16-byte aligned; 0 for
+ * invalid arguments). It needs no clearing. Calls that share one workspace
+ * must not overlap. */
+size_t gs_delta_rule_scratch_bytes(const gs_delta_rule* r, int32_t backward);
+
+/* gs_delta_rule_fwd - the outputs of every step and the last state.
+ *   h0          [B][H][key_dim][value_dim] float32, or NULL (zero)
+ *   o           out [B][T][H][value_dim]
+ *   h_last      out [B][H][key_dim][value_dim] float32, or NULL: the state
+ *               behind the last step (h0 for a sequence of length 0). May be
+ *               h0 itself: a serving loop keeps one state buffer.
+ *   ckpt        out [B][ceil(T / 64) - 1][H][key_dim][value_dim] float32, or
+ *               NULL: row c is the state in front of step 64 (c + 1), for
+ *               gs_delta_rule_bwd; rows at or behind the length are not
+ *               written. Not needed when T <= 64.
+ * o must not overlap an input. Two calls on the same inputs give the same
+ * bits. */
+gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* beta, const float* h0, void* o, float* h_last,
+                            float* ckpt, void* scratch, size_t scratch_bytes, void* stream);
+
+/* gs_delta_rule_bwd - gradients of gs_delta_rule_fwd. With dS the gradient of
+ * the state, from the last step (grad_last) to the first, and
+ * e = v - a S_{t-1}^T k:
+ *   dS += scale q do^T;  du = dS^T k;  dk = dS (beta e) - a S_{t-1} (beta du)
+ *   dv = beta du;  dbeta = du . e;  dq = scale S_t do;  dS -= k (beta du)^T
+ *   dlog_decay = a <dS, S_{t-1}>;  dS = a dS      (both 0 at a restart)
+ * grad_q and grad_k are summed over the heads of a key head, in their order.
+ * The states are recomputed from the checkpoints.
+ *   grad_o      [B][T][H][value_dim];  grad_last  like h0, or NULL (zero)
+ *   grad_q, grad_k  out [B][T][Hk][key_dim];  grad_v  out like grad_o
+ *   grad_log_decay, grad_beta  out [B][T][H] float32
+ *   grad_h0     out like h0, or NULL
+ * Outputs must not overlap inputs. */
+gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
+                            const float* log_decay, const float* beta, const float* h0, const float* ckpt,
+                            const void* grad_o, const float* grad_last, void* grad_q, void* grad_k, void* grad_v,
+                            float* grad_log_decay, float* grad_beta, float* grad_h0, void* scratch,
+                            size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * The norms around a block of a network, over rows of `width` elements, with
+ * what lies between them: the block's output y is normalised (post), gated,
+ * scaled and added to the residual stream, and the sum normalised for the
+ * next block (pre). Every part can be left out:
+ *
+ *   t    = post(y) = (y - m) / sqrt(var + eps) post_weight + post_bias
+ *   out  = residual + scale act(gate) t
+ *   norm = pre(out), formed from the sum before its rounding
+ *
+ * GS_BLOCK_NORM_RMS: m = 0 and var the mean square; GS_BLOCK_NORM_LAYER: the
+ * mean and the variance of the row; GS_BLOCK_NORM_NONE: the identity, and for
+ * pre no norm. act: GS_BLOCK_GATE_SIGMOID sigma(z), GS_BLOCK_GATE_SILU
+ * z sigma(z), GS_BLOCK_GATE_NONE 1.
+ *
+ *   dtype        GS_F32, GS_BF16 or GS_F16: every array of rows
+ *   weight_dtype of the weights, biases and scale, each [width] or NULL (1, 0, 1)
+ *   outer, inner rows are numbered [outer][inner] (tokens and heads; inner >= 1);
+ *                outer inner at most 2^30
+ *   width        1 .. GS_BLOCK_NORM_MAX_WIDTH
+ *   eps          >= 0, finite
+ *   y_*, gate_*, residual_*  strides of the rows in elements, >= 0; a row's
+ *                elements are contiguous
+ * All other arrays are contiguous. Sums are float32. Two calls on the same
+ * inputs give the same bits.
+ * ------------------------------------------------------------------- */
+#define GS_BLOCK_NORM_NONE 0
+#define GS_BLOCK_NORM_RMS 1
+#define GS_BLOCK_NORM_LAYER 2
+#define GS_BLOCK_GATE_NONE 0
+#define GS_BLOCK_GATE_SIGMOID 1
+#define GS_BLOCK_GATE_SILU 2
+#define GS_BLOCK_NORM_MAX_WIDTH 16384
+typedef struct {
+    int32_t dtype, weight_dtype;
+    int32_t post, gating, pre;
+    int32_t inner, width;
+    float eps;
+    int64_t outer;
+    int64_t y_outer, y_inner, gate_outer, gate_inner, residual_outer, residual_inner;
+} gs_block_norm;
+
+/* gs_block_norm_fwd
+ *   y, gate (NULL with GS_BLOCK_GATE_NONE), residual (or NULL)  rows
+ *   post_weight, post_bias, scale, pre_weight, pre_bias  [width], or NULL
+ *   out          out rows, or NULL (only with pre); may be y, gate or
+ *                residual itself where that is contiguous
+ *   norm         out rows (required with pre, not looked at without)
+ * out and norm must not overlap each other or, otherwise, an input. */
+gs_status gs_block_norm_fwd(const gs_block_norm* d, const void* y, const void* gate, const void* residual,
+                            const void* post_weight, const void* post_bias, const void* scale, const void* pre_weight,
+                            const void* pre_bias, void* out, void* norm, void* stream);
+
+/* gs_block_norm_bwd - gradients of gs_block_norm_fwd; the rows are recomputed
+ * from the inputs.
+ *   grad_out     rows, or NULL (zero; only with pre)
+ *   grad_norm    rows (required with pre, not looked at without)
+ *   grad_y       out rows; grad_gate and grad_residual out rows, or NULL
+ *   grad_post_weight .. grad_pre_bias  out [width] float32, or NULL: sums over
+ *                the rows, in an order that depends on the sizes only
+ *   scratch, scratch_bytes  workspace of gs_block_norm_scratch_bytes(d) bytes,
+ *                4-byte aligned; no clearing needed, not shared by
+ *                overlapping calls. Not looked at when no sum is asked for.
+ * grad_y, grad_gate and grad_residual may each be grad_out or grad_norm
+ * itself, and must not overlap anything otherwise. */
+size_t gs_block_norm_scratch_bytes(const gs_block_norm* d);
+gs_status gs_block_norm_bwd(const gs_block_norm* d, const void* y, const void* gate, const void* residual,
+                            const void* post_weight, const void* post_bias, const void* scale, const void* pre_weight,
+                            const void* pre_bias, const void* grad_out, const void* grad_norm, void* grad_y,
+                            void* grad_gate, void* grad_residual, float* grad_post_weight, float* grad_post_bias,
+                            float* grad_scale, float* grad_pre_weight, float* grad_pre_bias, void* scratch,
+                            size_t scratch_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
