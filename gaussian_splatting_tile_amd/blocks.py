@@ -204,7 +204,7 @@ def block_norm_fwd(y, residual=None, gate=None, gating=BLOCK_GATE_NONE, scale=No
     (weight, bias). Norms: BLOCK_NORM_NONE, BLOCK_NORM_RMS, BLOCK_NORM_LAYER; gating: BLOCK_GATE_NONE,
     BLOCK_GATE_SIGMOID, BLOCK_GATE_SILU. y, gate, residual [..., width] of one shape and type (float32, bfloat16 or
     float16), rows at any one stride, or two (tokens and heads of a part of a projection); weights, biases and scale
-    [width] of one type. Returns dict out (None unless want_out) and norm (None without pre). `out` may give them;
+    [width], all float32 or all of y's type. Returns dict out (None unless want_out) and norm (None without pre). `out` may give them;
     out["out"] may be y, gate or residual itself. `stream` as for delta_rule_fwd."""
     if _elsewhere(stream, y.device):
         return _on(stream, lambda: block_norm_fwd(y, residual, gate, gating, scale, post, post_weight, post_bias, pre,

@@ -133,6 +133,8 @@ gs_status check_block_norm(const gs_block_norm* d, const char* who) {
     if (!d) return fail(GS_ERR_INVALID, "%s: the description is NULL", who);
     if (!type_bytes(d->dtype) || !type_bytes(d->weight_dtype))
         return fail(GS_ERR_INVALID, "%s: unknown dtype %d or weight_dtype %d", who, d->dtype, d->weight_dtype);
+    if (d->weight_dtype != GS_F32 && d->weight_dtype != d->dtype)
+        return fail(GS_ERR_INVALID, "%s: weight_dtype %d is neither GS_F32 nor dtype %d", who, d->weight_dtype, d->dtype);
     for (int32_t k : {d->post, d->pre})
         if (k != GS_BLOCK_NORM_NONE && k != GS_BLOCK_NORM_RMS && k != GS_BLOCK_NORM_LAYER)
             return fail(GS_ERR_INVALID, "%s: unknown norm %d", who, k);

@@ -29,45 +29,93 @@ struct Geometry {
     int block;    // threads of a workgroup
     int grid;
     int64_t rows;
-    bool wide;    // 16-byte accesses
-    int per;      // elements of a thread
+    int per;      // elements of a thread, at most
 };
 
 typedef __bf16 bf16;
 typedef _Float16 f16;
 
+// Aligned to an element only: the hardware takes 16-byte accesses at any address.
 template <typename T, int N>
 struct Pack {
-    typedef T type __attribute__((ext_vector_type(N)));
+    typedef T type __attribute__((ext_vector_type(N), aligned(sizeof(T))));
 };
 template <typename T>
 struct Pack<T, 1> {
     typedef T type;
 };
 
-// A thread's elements of a row: NV groups of V neighbours.
+// A thread's elements of a row: NV groups of V neighbours. The last group of a
+// row whose width is no multiple of V is read where it ends with the row and
+// moved to its place, and stored element by element; so rows of odd widths are
+// read in 16-byte pieces as well (rows narrower than one have V = 1).
 template <typename T, int V, int NV>
 struct Rows {
-    static constexpr int NE = V * NV;
+    static constexpr int NE = V * NV, NVs = NV;
     typedef typename Pack<T, V>::type P;
+    struct Raw {
+        P r[NV];
+        __device__ __forceinline__ float operator[](int i) const {
+            if constexpr (V == 1)
+                return (float)r[i];
+            else
+                return (float)r[i / V][i % V];
+        }
+    };
     int lane, lanes, width;
 
     __device__ __forceinline__ int at(int j) const { return (j * lanes + lane) * V; }
-    __device__ __forceinline__ void load(const void* base, int64_t row, float fill, float (&v)[NE]) const {
+    __device__ __forceinline__ bool in(int i) const { return at(i / V) + i % V < width; }
+    // the elements of a group move down by the ones it was read too early; what is behind them counts for nothing
+    template <typename Q>
+    static __device__ __forceinline__ Q moved(Q r, int by) {
+        if constexpr (sizeof(Q) == 16 && V == 8) {
+            typedef uint32_t U4 __attribute__((ext_vector_type(4)));
+            U4 u = __builtin_bit_cast(U4, r);
+            if (by & 4) u = U4{u[2], u[3], 0, 0};
+            if (by & 2) u = U4{u[1], u[2], u[3], 0};
+            if (by & 1)
+                u = U4{__builtin_amdgcn_alignbit(u[1], u[0], 16), __builtin_amdgcn_alignbit(u[2], u[1], 16),
+                       __builtin_amdgcn_alignbit(u[3], u[2], 16), u[3] >> 16};
+            return __builtin_bit_cast(Q, u);
+        } else if constexpr (V == 8) {
+            if (by & 4) r = Q{r[4], r[5], r[6], r[7], 0, 0, 0, 0};
+            if (by & 2) r = Q{r[2], r[3], r[4], r[5], r[6], r[7], 0, 0};
+            if (by & 1) r = Q{r[1], r[2], r[3], r[4], r[5], r[6], r[7], 0};
+        } else if constexpr (V == 4) {
+            if (by & 2) r = Q{r[2], r[3], 0, 0};
+            if (by & 1) r = Q{r[1], r[2], r[3], 0};
+        }
+        return r;
+    }
+    // group j of a row of W at p, 0 past the width
+    template <typename W>
+    __device__ __forceinline__ typename Pack<W, V>::type group(const W* p, int j) const {
+        typedef typename Pack<W, V>::type Q;
+        Q q{};
+        const int from = V == 1 ? at(j) : min(at(j), width - V);
+        if (at(j) < width) {
+            q = *(const Q*)((const char*)p + (uint32_t)(from * (int)sizeof(W)));
+            if constexpr (V > 1)
+                if (from != at(j)) q = moved(q, at(j) - from);
+        }
+        return q;
+    }
+    // Loads first, all of them, and the moves behind them.
+    __device__ __forceinline__ void load(const void* base, int64_t row, Raw& v) const {
         const T* const p = (const T*)base + row;
-        P r[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (at(j) < width) r[j] = *(const P*)(p + at(j));
+        for (int j = 0; j < NV; ++j) {
+            v.r[j] = P{};
+            const int from = V == 1 ? at(j) : min(at(j), width - V);
+            if (at(j) < width) v.r[j] = *(const P*)((const char*)p + (uint32_t)(from * (int)sizeof(T)));
+        }
+    }
+    __device__ __forceinline__ void settle(Raw& v) const {
+        if (V > 1 && width % V)
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if constexpr (V == 1)
-                    v[j] = at(j) < width ? (float)r[j] : fill;
-                else
-                    v[j * V + i] = at(j) < width ? (float)r[j][i] : fill;
-            }
+            for (int j = 0; j < NV; ++j)
+                if (at(j) < width && at(j) + V > width) v.r[j] = moved(v.r[j], at(j) + V - width);
     }
     __device__ __forceinline__ void store(void* base, int64_t row, const float (&v)[NE]) const {
         T* const p = (T*)base + row;
@@ -81,22 +129,36 @@ struct Rows {
                 else
                     r[i] = (T)v[j * V + i];
             }
-            if (at(j) < width) *(P*)(p + at(j)) = r;
+            if (at(j) + V <= width) {
+                *(P*)((char*)p + (uint32_t)(at(j) * (int)sizeof(T))) = r;
+            } else if constexpr (V > 1) {
+                for (int i = 0; i < V - 1; ++i)
+                    if (at(j) + i < width) p[at(j) + i] = (T)v[j * V + i];
+            }
         }
     }
-    // A vector of weights of type `dtype`, `fill` where there is none.
+    // A vector of weights, of type float32 or that of the rows; `fill` where there is none.
     __device__ __forceinline__ void weights(const void* w, int dtype, float fill, float (&v)[NE]) const {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+        for (int e = 0; e < NE; ++e) v[e] = fill;
+        if (!w) return;
+        auto take = [&](auto* p) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = at(j) + i;
-                float x = fill;
-                if (w && k < width)
-                    x = dtype == GS_F32 ? ((const float*)w)[k]
-                                        : dtype == GS_BF16 ? (float)((const bf16*)w)[k] : (float)((const f16*)w)[k];
-                v[j * V + i] = x;
+            for (int j = 0; j < NV; ++j) {
+                const auto q = group(p, j);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    if constexpr (V == 1)
+                        v[j] = (float)q;
+                    else
+                        v[j * V + i] = (float)q[i];
+                }
             }
+        };
+        if (sizeof(T) == 4 || dtype == GS_F32)
+            take((const float*)w);
+        else
+            take((const T*)w);
     }
 };
 
@@ -140,7 +202,7 @@ __device__ __forceinline__ float normalise(const R& rows, RowSum& sum, int kind,
         sum(m, none);
         m *= inv;
 #pragma unroll
-        for (int i = 0; i < R::NE; ++i) x[i] = rows.at(i / (R::NE / R::NVs)) < rows.width ? x[i] - m : 0.0f;
+        for (int i = 0; i < R::NE; ++i) x[i] = rows.in(i) ? x[i] - m : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < R::NE; ++i) s = fmaf(x[i], x[i], s);
@@ -169,50 +231,63 @@ __device__ __forceinline__ void normalise_back(const R& rows, RowSum& sum, int k
     for (int i = 0; i < R::NE; ++i) g[i] = r * (g[i] - b - xhat[i] * a);
 }
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
-
-template <typename T, int V, int NV>
-struct RowsN : Rows<T, V, NV> {
-    static constexpr int NVs = NV;
-};
+// 1 / (1 + exp(-z)); the hardware's exponential and reciprocal are within an ulp, the product z log2(e) adds |z| 2^-24.
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
+}
 
 __device__ __forceinline__ int64_t row_at(int64_t row, int inner, int64_t so, int64_t si) {
     const int64_t o = row / inner;
     return o * so + (row - o * inner) * si;
 }
 
-template <typename T, int V, int NV>
-__global__ __launch_bounds__(1024) void k_block_norm_fwd(BlockNormArgs a, Geometry g) {
-    typedef RowsN<T, V, NV> R;
+// Rows of up to 2048 elements: 256 threads that keep the weights in registers.
+// Longer ones: 512 or 1024 threads, whose registers do not hold them; they are
+// read again for every row, from the caches.
+template <typename T, int V, int NV, int BLOCK>
+__global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geometry g) {
+    typedef Rows<T, V, NV> R;
     constexpr int NE = R::NE;
+    constexpr bool KEEP = BLOCK == 256;
     __shared__ float lds[2][16][2];
     const gs_block_norm& d = a.d;
     R rows;
-    rows.lanes = g.lanes;
-    rows.lane = threadIdx.x & (g.lanes - 1);
+    // a row of more than 2048 elements has the workgroup to itself
+    const int lanes = KEEP ? g.lanes : BLOCK, sets = BLOCK / lanes;
+    rows.lanes = lanes;
+    rows.lane = threadIdx.x & (lanes - 1);
     rows.width = d.width;
-    RowSum sum{lds, g.lanes, 0};
-    const int sets = blockDim.x / g.lanes;
+    RowSum sum{lds, lanes, 0};
     float w[NE], b[NE], s[NE], w2[NE], b2[NE];
-    rows.weights(a.post_weight, d.weight_dtype, 1.0f, w);
-    rows.weights(a.post_bias, d.weight_dtype, 0.0f, b);
-    rows.weights(a.scale, d.weight_dtype, 1.0f, s);
-    rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
-    rows.weights(a.pre_bias, d.weight_dtype, 0.0f, b2);
+    auto weights = [&](bool first, bool second) {
+        if (first) {
+            rows.weights(a.post_weight, d.weight_dtype, 1.0f, w);
+            rows.weights(a.post_bias, d.weight_dtype, 0.0f, b);
+            rows.weights(a.scale, d.weight_dtype, 1.0f, s);
+        }
+        if (second) {
+            rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
+            rows.weights(a.pre_bias, d.weight_dtype, 0.0f, b2);
+        }
+    };
+    if constexpr (KEEP) weights(true, true);
     for (int64_t base = (int64_t)blockIdx.x * sets; base < g.rows; base += (int64_t)gridDim.x * sets) {
-        const int64_t row = base + threadIdx.x / g.lanes;
+        const int64_t row = KEEP ? base + threadIdx.x / lanes : base;
         const bool here = row < g.rows;
         rows.width = here ? d.width : 0;
-        float x[NE], z[NE], res[NE];
-        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), 0.0f, x);
-        if (d.gating != GS_BLOCK_GATE_NONE)
-            rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), 0.0f, z);
-        if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), 0.0f, res);
-        if (d.post != GS_BLOCK_NORM_NONE) {
-            rows.width = d.width;
-            normalise(rows, sum, d.post, d.eps, x);
-        }
-        if (!here) rows.width = 0;
+        typename R::Raw y{}, z{}, res{};
+        float x[NE];
+        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), y);
+        if (d.gating != GS_BLOCK_GATE_NONE) rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), z);
+        if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), res);
+        rows.width = d.width;
+        rows.settle(y);
+        rows.settle(z);
+        rows.settle(res);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) x[i] = y[i];
+        if (d.post != GS_BLOCK_NORM_NONE) normalise(rows, sum, d.post, d.eps, x);
+        if constexpr (!KEEP) weights(true, false);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
             x[i] = fmaf(x[i], w[i], b[i]);
@@ -220,12 +295,14 @@ __global__ __launch_bounds__(1024) void k_block_norm_fwd(BlockNormArgs a, Geomet
             x[i] = a.residual ? fmaf(s[i], x[i], res[i]) : s[i] * x[i];
         }
         const int64_t at = row * d.width;
+        if (!here) rows.width = 0;
         if (a.out) rows.store(a.out, at, x);
         if (d.pre != GS_BLOCK_NORM_NONE) {
             rows.width = d.width;
+            if constexpr (!KEEP) weights(false, true);
             // what lies past the width holds the biases
 #pragma unroll
-            for (int i = 0; i < NE; ++i) x[i] = rows.at(i / V) < d.width ? x[i] : 0.0f;
+            for (int i = 0; i < NE; ++i) x[i] = rows.in(i) ? x[i] : 0.0f;
             normalise(rows, sum, d.pre, d.eps, x);
 #pragma unroll
             for (int i = 0; i < NE; ++i) x[i] = fmaf(x[i], w2[i], b2[i]);
@@ -234,104 +311,116 @@ __global__ __launch_bounds__(1024) void k_block_norm_fwd(BlockNormArgs a, Geomet
     }
 }
 
-// The sums of a workgroup go to partial[workgroup][5][width].
-template <typename T, int V, int NV, bool BIAS>
-__global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a, Geometry g, float* partial) {
-    typedef RowsN<T, V, NV> R;
+// The sums of a workgroup go to partial[workgroup][5][width]. BIAS: with a bias
+// of the post norm, or the gradient of one asked for.
+template <typename T, int V, int NV, int BLOCK, bool BIAS>
+__global__ __launch_bounds__(BLOCK) void k_block_norm_bwd(BlockNormArgs a, Geometry g, float* partial) {
+    typedef Rows<T, V, NV> R;
     constexpr int NE = R::NE;
+    constexpr bool KEEP = BLOCK == 256;
     __shared__ float lds[2][16][2];
     const gs_block_norm& d = a.d;
     R rows;
-    rows.lanes = g.lanes;
-    rows.lane = threadIdx.x & (g.lanes - 1);
+    // a row of more than 2048 elements has the workgroup to itself
+    const int lanes = KEEP ? g.lanes : BLOCK, sets = BLOCK / lanes;
+    rows.lanes = lanes;
+    rows.lane = threadIdx.x & (lanes - 1);
     rows.width = d.width;
-    RowSum sum{lds, g.lanes, 0};
-    const int sets = blockDim.x / g.lanes;
+    RowSum sum{lds, lanes, 0};
     float w[NE], b[NE], s[NE], w2[NE];
-    rows.weights(a.post_weight, d.weight_dtype, 1.0f, w);
-    rows.weights(a.post_bias, d.weight_dtype, 0.0f, b);
-    rows.weights(a.scale, d.weight_dtype, 1.0f, s);
-    rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
+    auto weights = [&] {
+        rows.weights(a.post_weight, d.weight_dtype, 1.0f, w);
+        if constexpr (BIAS) rows.weights(a.post_bias, d.weight_dtype, 0.0f, b);
+        rows.weights(a.scale, d.weight_dtype, 1.0f, s);
+    };
+    if constexpr (KEEP) {
+        weights();
+        rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
+    }
     constexpr int NS = BIAS ? 5 : 3;
     float acc[NS][NE];  // post_weight, scale, pre_weight, post_bias, pre_bias
 #pragma unroll
     for (int k = 0; k < NS; ++k)
 #pragma unroll
         for (int i = 0; i < NE; ++i) acc[k][i] = 0.0f;
+    const bool gated = d.gating != GS_BLOCK_GATE_NONE, silu = d.gating == GS_BLOCK_GATE_SILU;
+    const bool pre = d.pre != GS_BLOCK_NORM_NONE;
     for (int64_t base = (int64_t)blockIdx.x * sets; base < g.rows; base += (int64_t)gridDim.x * sets) {
-        const int64_t row = base + threadIdx.x / g.lanes;
+        const int64_t row = KEEP ? base + threadIdx.x / lanes : base;
         const bool here = row < g.rows;
         const int64_t at = row * d.width;
         rows.width = here ? d.width : 0;
-        float x[NE], z[NE], c[NE], u[NE], dn[NE];
-        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), 0.0f, x);
-        const bool gated = d.gating != GS_BLOCK_GATE_NONE, pre = d.pre != GS_BLOCK_NORM_NONE;
-        if (gated) rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), 0.0f, z);
+        typename R::Raw y{}, z{}, res{}, gn{}, go{};
+        float x[NE], u[NE], dn[NE];
+        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), y);
+        if (gated) rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), z);
         if (pre) {
-            if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), 0.0f, u);
-            rows.load(a.grad_norm, at, 0.0f, dn);
+            if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), res);
+            rows.load(a.grad_norm, at, gn);
         }
-        float up[NE];
-        if (a.grad_out) rows.load(a.grad_out, at, 0.0f, up);
+        if (a.grad_out) rows.load(a.grad_out, at, go);
         rows.width = d.width;
+        rows.settle(y);
+        rows.settle(z);
+        rows.settle(res);
+        rows.settle(gn);
+        rows.settle(go);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) x[i] = y[i];
         float r = 1.0f;
         if (d.post != GS_BLOCK_NORM_NONE) r = normalise(rows, sum, d.post, d.eps, x);
-        float act[NE];
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            const float t = fmaf(x[i], w[i], b[i]);
-            act[i] = 1.0f;
-            c[i] = t;
-            if (gated) {
-                const float sg = sigmoid(z[i]);
-                const bool silu = d.gating == GS_BLOCK_GATE_SILU;
-                act[i] = silu ? z[i] * sg : sg;
-                c[i] = act[i] * t;
-                // the derivative of the gate's factor, times what it multiplies
-                z[i] = t * (silu ? sg * fmaf(z[i], 1.0f - sg, 1.0f) : sg * (1.0f - sg));
-            }
-        }
+        if constexpr (!KEEP) weights();
+        // the post norm's output, and that with the gate's factor
+        auto normed = [&](int i) {
+            float t = x[i] * w[i];
+            if constexpr (BIAS) t += b[i];
+            return t;
+        };
+        auto factor = [&](int i, float sg) { return silu ? z[i] * sg : sg; };
         if (pre) {
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-                const float v = a.residual ? fmaf(s[i], c[i], u[i]) : s[i] * c[i];
-                u[i] = here && rows.at(i / V) < d.width ? v : 0.0f;
+                float v = normed(i);
+                if (gated) v *= factor(i, sigmoid(z[i]));
+                v = a.residual ? fmaf(s[i], v, res[i]) : s[i] * v;
+                u[i] = here && rows.in(i) ? v : 0.0f;
             }
             const float r2 = normalise(rows, sum, d.pre, d.eps, u);
+            if constexpr (!KEEP) rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-                acc[2][i] = fmaf(dn[i], u[i], acc[2][i]);
-                if constexpr (BIAS) acc[4][i] += dn[i];
-                dn[i] *= w2[i];
+                acc[2][i] = fmaf(gn[i], u[i], acc[2][i]);
+                if constexpr (BIAS) acc[4][i] += gn[i];
+                dn[i] = gn[i] * w2[i];
             }
             normalise_back(rows, sum, d.pre, r2, u, dn);
 #pragma unroll
-            for (int i = 0; i < NE; ++i) dn[i] = a.grad_out ? dn[i] + up[i] : dn[i];
+            for (int i = 0; i < NE; ++i) dn[i] = a.grad_out ? dn[i] + go[i] : dn[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < NE; ++i) dn[i] = up[i];
+            for (int i = 0; i < NE; ++i) dn[i] = go[i];
         }
         // past the width (and past the rows) everything upstream is 0, but for a layer norm's mean
 #pragma unroll
-        for (int i = 0; i < NE; ++i) dn[i] = here && rows.at(i / V) < d.width ? dn[i] : 0.0f;
+        for (int i = 0; i < NE; ++i) dn[i] = here && rows.in(i) ? dn[i] : 0.0f;
         if (!here) rows.width = 0;
         if (a.grad_residual) rows.store(a.grad_residual, at, dn);
 #pragma unroll
         for (int i = 0; i < NE; ++i) {
-            acc[1][i] = fmaf(dn[i], c[i], acc[1][i]);
-            dn[i] *= s[i];
+            float t = normed(i), f = 1.0f;
+            const float ds = dn[i] * s[i];
             if (gated) {
-                z[i] *= dn[i];
-                dn[i] *= act[i];
+                const float sg = sigmoid(z[i]);
+                f = factor(i, sg);
+                u[i] = ds * t * (silu ? sg * fmaf(z[i], 1.0f - sg, 1.0f) : sg * (1.0f - sg));
             }
-        }
-        if (gated && a.grad_gate) rows.store(a.grad_gate, at, z);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) {
+            acc[1][i] = fmaf(dn[i], f * t, acc[1][i]);
+            dn[i] = ds * f;
             acc[0][i] = fmaf(dn[i], x[i], acc[0][i]);
             if constexpr (BIAS) acc[3][i] += dn[i];
             dn[i] *= w[i];
         }
+        if (gated && a.grad_gate) rows.store(a.grad_gate, at, u);
         if (d.post != GS_BLOCK_NORM_NONE) {
             rows.width = d.width;
             normalise_back(rows, sum, d.post, r, x, dn);
@@ -349,17 +438,17 @@ __global__ __launch_bounds__(1024) void k_block_norm_bwd(BlockNormArgs a, Geomet
         if (sets == 1) {
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                if (rows.at(i / V) < d.width) to[rows.at(i / V) + i % V] = acc[k][i];
+                if (rows.in(i)) to[rows.at(i / V) + i % V] = acc[k][i];
         } else {  // the rows a workgroup holds at once, through LDS in their order
             __syncthreads();
 #pragma unroll
-            for (int i = 0; i < NE; ++i) join[i * blockDim.x + threadIdx.x] = acc[k][i];
+            for (int i = 0; i < NE; ++i) join[i * BLOCK + threadIdx.x] = acc[k][i];
             __syncthreads();
-            for (int e = threadIdx.x; e < NE * g.lanes; e += blockDim.x) {
-                const int i = e / g.lanes, lane = e & (g.lanes - 1);
+            for (int e = threadIdx.x; e < NE * lanes; e += BLOCK) {
+                const int i = e / lanes, lane = e & (lanes - 1);
                 float t = 0.0f;
-                for (int q = 0; q < sets; ++q) t += join[i * blockDim.x + q * g.lanes + lane];
-                const int col = ((i / V) * g.lanes + lane) * V + i % V;
+                for (int q = 0; q < sets; ++q) t += join[i * BLOCK + q * lanes + lane];
+                const int col = ((i / V) * lanes + lane) * V + i % V;
                 if (col < d.width) to[col] = t;
             }
         }
@@ -391,15 +480,9 @@ __global__ __launch_bounds__(1024) void k_block_norm_sums(const float* partial, 
     }
 }
 
-template <typename... P>
-bool aligned16(P... p) {
-    return !((0 | ... | (uintptr_t)p) & 15);
-}
-
-Geometry geometry(const gs_block_norm& d, bool wide, bool backward) {
+Geometry geometry(const gs_block_norm& d, bool backward) {
     Geometry g;
     g.rows = d.outer * d.inner;
-    g.wide = wide;
     g.per = d.width > 8192 ? 16 : 8;
     int lanes = 8;
     while ((int64_t)lanes * g.per < d.width) lanes *= 2;
@@ -412,75 +495,53 @@ Geometry geometry(const gs_block_norm& d, bool wide, bool backward) {
     return g;
 }
 
-// Whether rows can be read and written in 16-byte pieces.
-bool wide_rows(const BlockNormArgs& a) {
-    const gs_block_norm& d = a.d;
-    const int v = d.dtype == GS_F32 ? 4 : 8;
-    int64_t all = d.width | d.y_outer | d.y_inner;
-    if (d.gating != GS_BLOCK_GATE_NONE) all |= d.gate_outer | d.gate_inner;
-    if (a.residual) all |= d.residual_outer | d.residual_inner;
-    if (all & (v - 1)) return false;
-    return aligned16(a.y, a.gate, a.residual, a.out, a.norm, a.grad_out, a.grad_norm, a.grad_y, a.grad_gate,
-                     a.grad_residual);
-}
-
-template <typename T, int V>
-hipError_t forward(const BlockNormArgs& a, const Geometry& g, hipStream_t stream) {
-    if (g.per == 8)
-        k_block_norm_fwd<T, V, 8 / V><<<g.grid, g.block, 0, stream>>>(a, g);
+template <typename T, int V, int NV, int BLOCK>
+hipError_t go(const BlockNormArgs& a, const Geometry& g, float* scratch, bool back, hipStream_t stream) {
+    if (!back)
+        k_block_norm_fwd<T, V, NV, BLOCK><<<g.grid, BLOCK, 0, stream>>>(a, g);
+    else if (a.post_bias || a.sums[1] || a.sums[4])
+        k_block_norm_bwd<T, V, NV, BLOCK, true><<<g.grid, BLOCK, 0, stream>>>(a, g, scratch);
     else
-        k_block_norm_fwd<T, V, 16 / V><<<g.grid, g.block, 0, stream>>>(a, g);
-    return hipGetLastError();
-}
-
-template <typename T, int V, bool BIAS>
-hipError_t backward(const BlockNormArgs& a, const Geometry& g, float* scratch, hipStream_t stream) {
-    if (g.per == 8)
-        k_block_norm_bwd<T, V, 8 / V, BIAS><<<g.grid, g.block, 0, stream>>>(a, g, scratch);
-    else
-        k_block_norm_bwd<T, V, 16 / V, BIAS><<<g.grid, g.block, 0, stream>>>(a, g, scratch);
+        k_block_norm_bwd<T, V, NV, BLOCK, false><<<g.grid, BLOCK, 0, stream>>>(a, g, scratch);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t forward_of(const BlockNormArgs& a, const Geometry& g, hipStream_t stream) {
-    return g.wide ? forward<T, 16 / sizeof(T)>(a, g, stream) : forward<T, 1>(a, g, stream);
+hipError_t go(const BlockNormArgs& a, const Geometry& g, float* scratch, bool back, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    if (a.d.width < V) return go<T, 1, 1, 256>(a, g, scratch, back, stream);
+    if (g.block == 256) return go<T, V, 8 / V, 256>(a, g, scratch, back, stream);
+    if (g.block == 512) return go<T, V, 8 / V, 512>(a, g, scratch, back, stream);
+    if (g.per == 8) return go<T, V, 8 / V, 1024>(a, g, scratch, back, stream);
+    return go<T, V, 16 / V, 1024>(a, g, scratch, back, stream);
 }
 
-template <typename T>
-hipError_t backward_of(const BlockNormArgs& a, const Geometry& g, float* scratch, hipStream_t stream) {
-    if (a.sums[1] || a.sums[4])
-        return g.wide ? backward<T, 16 / sizeof(T), true>(a, g, scratch, stream) : backward<T, 1, true>(a, g, scratch, stream);
-    return g.wide ? backward<T, 16 / sizeof(T), false>(a, g, scratch, stream) : backward<T, 1, false>(a, g, scratch, stream);
+hipError_t launch(const BlockNormArgs& a, const Geometry& g, float* scratch, bool back, hipStream_t stream) {
+    switch (a.d.dtype) {
+        case GS_F32: return go<float>(a, g, scratch, back, stream);
+        case GS_BF16: return go<bf16>(a, g, scratch, back, stream);
+        default: return go<f16>(a, g, scratch, back, stream);
+    }
 }
 
 }  // namespace
 
 size_t block_norm_scratch_bytes(const gs_block_norm& d) {
     if (d.outer == 0) return 0;
-    return (size_t)geometry(d, false, true).grid * 5 * d.width * sizeof(float);
+    return (size_t)geometry(d, true).grid * 5 * d.width * sizeof(float);
 }
 
 hipError_t launch_block_norm_fwd(const BlockNormArgs& a, hipStream_t stream) {
-    const Geometry g = geometry(a.d, wide_rows(a), false);
-    switch (a.d.dtype) {
-        case GS_F32: return forward_of<float>(a, g, stream);
-        case GS_BF16: return forward_of<bf16>(a, g, stream);
-        default: return forward_of<f16>(a, g, stream);
-    }
+    return launch(a, geometry(a.d, false), nullptr, false, stream);
 }
 
 hipError_t launch_block_norm_bwd(const BlockNormArgs& a, float* scratch, hipStream_t stream) {
-    Geometry g = geometry(a.d, wide_rows(a), true);
+    Geometry g = geometry(a.d, true);
     hipError_t e = hipSuccess;
     if (a.d.outer == 0)
         g.grid = 0;  // the sums of no rows are 0
     else
-    switch (a.d.dtype) {
-        case GS_F32: e = backward_of<float>(a, g, scratch, stream); break;
-        case GS_BF16: e = backward_of<bf16>(a, g, scratch, stream); break;
-        default: e = backward_of<f16>(a, g, scratch, stream); break;
-    }
+        e = launch(a, g, scratch, true, stream);
     SumArgs s;
     bool any = false;
     for (int k = 0; k < 5; ++k) any |= (s.to[k] = a.sums[k]) != nullptr;

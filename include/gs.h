@@ -861,7 +861,8 @@ gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k
  * z sigma(z), GS_BLOCK_GATE_NONE 1.
  *
  *   dtype        GS_F32, GS_BF16 or GS_F16: every array of rows
- *   weight_dtype of the weights, biases and scale, each [width] or NULL (1, 0, 1)
+ *   weight_dtype of the weights, biases and scale, each [width] or NULL (1, 0, 1):
+ *                GS_F32 or dtype
  *   outer, inner rows are numbered [outer][inner] (tokens and heads; inner >= 1);
  *                outer inner at most 2^30
  *   width        1 .. GS_BLOCK_NORM_MAX_WIDTH
