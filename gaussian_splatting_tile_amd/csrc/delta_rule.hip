@@ -727,6 +727,151 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             }
 }
 
+// A few steps (one new token, a few drafted ones): the state is read and
+// written once, and that is the bound. A workgroup holds `slice` columns of one
+// head's state in registers, V neighbouring columns a lane and the rows spread
+// over lanes and waves. Both sums over the rows that a step needs, S^T k and
+// S^T q, are formed of the state in front of it (o = a S^T q + (q.k) u), so a
+// step has one exchange through LDS. Everything the steps read is fetched
+// before the first one.
+constexpr int kFewSteps = 16;
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void k_delta_steps(DeltaArgs a, int slice, int lanes) {
+    constexpr int NR = 64 / V;
+    typedef float Vec __attribute__((ext_vector_type(V)));
+    const gs_delta_rule& d = a.r;
+    __shared__ float ks[kFewSteps][kV], qs[kFewSteps][kV], vs[kFewSteps][kV], gates[kFewSteps][2], qk[kFewSteps];
+    __shared__ float part[2][4][2][kV];
+    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
+    const int len = length_of(d, b), c0 = blockIdx.y * slice, cols = min(slice, d.value_dim - c0);
+    const int lane = threadIdx.x & (lanes - 1), group = threadIdx.x / lanes, groups = 256 / lanes;
+    const int wave = threadIdx.x >> 6, col = lane * V;
+    const bool on = col < cols;  // and so are its V - 1 neighbours
+    const int64_t state = ((int64_t)b * d.heads + h) * d.key_dim * d.value_dim + c0 + col;
+    Vec S[NR];
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        if (j * groups >= d.key_dim) break;
+        const int row = j * groups + group;
+        S[j] = Vec{};
+        if (a.h0 && on && row < d.key_dim) S[j] = *(const Vec*)(a.h0 + state + (int64_t)row * d.value_dim);
+    }
+    for (int e = threadIdx.x; e < len * d.key_dim; e += 256) {
+        const int t = e / d.key_dim, i = e - t * d.key_dim;
+        ks[t][i] = (float)((const T*)a.k)[b * d.k_batch + t * d.k_step + kh * d.k_head + i];
+        qs[t][i] = (float)((const T*)a.q)[b * d.q_batch + t * d.q_step + kh * d.q_head + i];
+    }
+    for (int e = threadIdx.x; e < len * cols; e += 256) {
+        const int t = e / cols, i = e - t * cols;
+        vs[t][i] = (float)((const T*)a.v)[b * d.v_batch + t * d.v_step + h * d.v_head + c0 + i];
+    }
+    if ((int)threadIdx.x < len) {
+        const int t = threadIdx.x;
+        const bool cut = d.restart && d.restart[(int64_t)b * d.steps + t];
+        const float g = a.log_decay[b * d.decay_batch + t * d.decay_step + h];
+        gates[t][0] = cut || g < -104.0f ? 0.0f : expf(g);
+        gates[t][1] = a.beta[b * d.beta_batch + t * d.beta_step + h];
+    }
+    __syncthreads();
+    for (int t = wave; t < len; t += 4) {
+        float x = 0.0f;
+        for (int i = threadIdx.x & 63; i < d.key_dim; i += 64) x = fmaf(ks[t][i], qs[t][i], x);
+        for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m);
+        if ((threadIdx.x & 63) == 0) qk[t] = x;
+    }
+    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim + c0 + col;
+    const int64_t o_step = (int64_t)d.heads * d.value_dim;
+    for (int t = 0; t < len; ++t) {
+        Vec x{}, y{};
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            if (j * groups >= d.key_dim) break;
+            const int row = min(j * groups + group, d.key_dim - 1);  // rows past the last one hold 0
+            const float kk = ks[t][row], qq = qs[t][row];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i] = fmaf(S[j][i], kk, x[i]);
+                y[i] = fmaf(S[j][i], qq, y[i]);
+            }
+        }
+        for (int m = lanes; m < 64; m <<= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                x[i] += __shfl_xor(x[i], m);
+                y[i] += __shfl_xor(y[i], m);
+            }
+        // a wave's sums: where a row takes several waves, of its own columns
+        const int turn = t & 1;
+        if ((int)(threadIdx.x & 63) < lanes && on) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                part[turn][wave][0][col + i] = x[i];
+                part[turn][wave][1][col + i] = y[i];
+            }
+        }
+        __syncthreads();
+        const float decay = gates[t][0], beta = gates[t][1], dot = qk[t];
+        const int first = lanes > 64 ? wave & (lanes / 64 - 1) : 0, by = lanes > 64 ? lanes / 64 : 1;
+        Vec u{};
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float sx = 0.0f, sy = 0.0f;
+                for (int w = first; w < 4; w += by) {
+                    sx += part[turn][w][0][col + i];
+                    sy += part[turn][w][1][col + i];
+                }
+                // a state that is dropped is dropped whatever it holds
+                u[i] = beta * (vs[t][col + i] - (decay == 0.0f ? 0.0f : decay * sx));
+                x[i] = d.scale * fmaf(dot, u[i], decay == 0.0f ? 0.0f : decay * sy);
+            }
+            if (group == 0)
+#pragma unroll
+                for (int i = 0; i < V; ++i) o[t * o_step + i] = (T)x[i];
+        }
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            if (j * groups >= d.key_dim) break;
+            const int row = j * groups + group;
+            const float kk = row < d.key_dim ? ks[t][row] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) S[j][i] = fmaf(kk, u[i], decay == 0.0f ? 0.0f : decay * S[j][i]);
+        }
+    }
+    if (on && group == 0)
+        for (int t = len; t < d.steps; ++t)
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[t * o_step + i] = (T)0.0f;
+    if (a.h_last && on)
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            if (j * groups >= d.key_dim) break;
+            const int row = j * groups + group;
+            if (row < d.key_dim) *(Vec*)(a.h_last + state + (int64_t)row * d.value_dim) = S[j];
+        }
+}
+
+template <typename T>
+hipError_t steps(const DeltaArgs& a, hipStream_t stream) {
+    const gs_delta_rule& r = a.r;
+    const bool wide = r.value_dim % 4 == 0 && !(((uintptr_t)a.h0 | (uintptr_t)a.h_last) & 15);
+    // columns of a workgroup: all, but fewer where that leaves compute units without work
+    int slice = r.value_dim;
+    const int most = wide ? 128 : 64;
+    if (slice > most) slice = most;
+    while (slice > 16 && (int64_t)r.batch * r.heads * ((r.value_dim + slice - 1) / slice) < 512) slice = (slice / 2 + 3) & ~3;
+    const int v = wide ? 4 : 1;
+    int lanes = 1;
+    while (lanes * v < slice) lanes *= 2;
+    const dim3 grid(r.batch * r.heads, (r.value_dim + slice - 1) / slice);
+    if (wide)
+        k_delta_steps<T, 4><<<grid, 256, 0, stream>>>(a, slice, lanes);
+    else
+        k_delta_steps<T, 1><<<grid, 256, 0, stream>>>(a, slice, lanes);
+    return hipGetLastError();
+}
+
 int chunks_of(const gs_delta_rule& r) { return (r.steps + kC - 1) / kC; }
 size_t inverse_floats(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * kLower; }
 
@@ -773,12 +918,20 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 }  // namespace
 
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
+    if (!backward && r.steps <= kFewSteps) return 0;
     size_t floats = inverse_floats(r);
     if (backward) floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
     return floats * sizeof(float);
 }
 
 hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
+    if (a.r.steps <= kFewSteps) {
+        switch (a.r.dtype) {
+            case GS_F32: return steps<float>(a, stream);
+            case GS_BF16: return steps<bf16>(a, stream);
+            default: return steps<f16>(a, stream);
+        }
+    }
     return run(a, scratch, false, stream);
 }
 
