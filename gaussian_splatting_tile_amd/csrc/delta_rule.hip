@@ -204,113 +204,6 @@ __device__ __forceinline__ void chunk_p(const float* Q, const float* K, const Ch
 
 constexpr int kChainWaves = 4;
 
-// The states, chunk after chunk, 16 columns of the values a wave: S stays in
-// its registers as C tiles, which are the right operands of K S and Q S.
-template <typename T, int DK>
-__global__ __launch_bounds__(64 * kChainWaves) void k_delta_fwd(DeltaArgs a, int chunks, const float* inverse) {
-    constexpr int KT = DK / 16, kThreads = 64 * kChainWaves;
-    __shared__ float K[kC * (DK + 4)];
-    __shared__ float Q[kC * (DK + 4)];
-    __shared__ float P[kC * kPitch];
-    __shared__ Chunk s;
-    const gs_delta_rule& d = a.r;
-    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
-    const bool on = col < d.value_dim;
-    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
-    const int64_t head = (int64_t)b * d.heads + h, state = head * d.key_dim * d.value_dim + col;
-    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
-    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
-    const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head + col;
-    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
-    const int64_t o_step = (int64_t)d.heads * d.value_dim;
-    f32x4 S[KT];
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * kt + 4 * g + r;
-            S[kt][r] = a.h0 && on && row < d.key_dim ? a.h0[state + (int64_t)row * d.value_dim] : 0.0f;
-        }
-    for (int c = 0; c < mine; ++c) {
-        const int t0 = c * kC, rows = len - t0;
-        __syncthreads();
-        load_rows<DK>(k + t0 * d.k_step, d.k_step, rows, d.key_dim, K, kThreads);
-        load_rows<DK>(q + t0 * d.q_step, d.q_step, rows, d.key_dim, Q, kThreads);
-        if (w == 0) load_gates(a, b, h, t0, len, s);
-        __syncthreads();
-        chunk_p<DK>(Q, K, s, d.scale, P, kChainWaves);
-        f32x4 R[4], U[4];
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * ti + 4 * g + r;
-                const float x = on && i < rows ? (float)v[(t0 + i) * d.v_step] : 0.0f;
-                R[ti][r] = s.beta[i] * (x - s.gamma[i] * acc[r]);
-            }
-        }
-        const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower + n * 16 + 4 * g;
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            U[ti] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int tj = 0; tj <= ti; ++tj) U[ti] = mma(*(const f32x4*)(M + tri(ti, tj) * 256), R[tj], U[ti]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(Q, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] *= d.scale * s.gamma[16 * ti + 4 * g + r];
-#pragma unroll
-            for (int tj = 0; tj <= ti; ++tj) acc = mma(*(const f32x4*)(P + (16 * ti + n) * kPitch + 16 * tj + 4 * g), U[tj], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = t0 + 16 * ti + 4 * g + r;
-                if (on && t < d.steps) o[t * o_step] = (T)acc[r];
-            }
-        }
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) U[ti][r] *= s.end[16 * ti + 4 * g + r];
-        const float whole = s.whole;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            S[kt] *= whole;
-#pragma unroll
-            for (int tj = 0; tj < 4; ++tj) S[kt] = mma(col4(K, DK + 4, 16 * tj + 4 * g, 16 * kt + n), U[tj], S[kt]);
-        }
-        if (a.ckpt && t0 + kC < len) {
-            float* const to = a.ckpt + ((((int64_t)b * (chunks - 1) + c) * d.heads + h) * d.key_dim) * d.value_dim + col;
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * kt + 4 * g + r;
-                    if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[kt][r];
-                }
-        }
-    }
-    for (int t = mine * kC + g; t < d.steps; t += 4)
-        if (on) o[t * o_step] = (T)0.0f;
-    if (a.h_last)
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * kt + 4 * g + r;
-                if (on && row < d.key_dim) a.h_last[state + (int64_t)row * d.value_dim] = S[kt][r];
-            }
-}
-
 // The gradients of the states, from the last chunk to the first, 16 columns a
 // wave; behind[b][chunk][h] receives the one behind each chunk.
 template <typename T, int DK>
@@ -412,6 +305,468 @@ __global__ __launch_bounds__(64 * kChainWaves) void k_delta_bwd(DeltaArgs a, int
             for (int r = 0; r < 4; ++r) {
                 const int row = 16 * kt + 4 * g + r;
                 if (on && row < d.key_dim) a.grad_h0[state + (int64_t)row * d.value_dim] = S[kt][r];
+            }
+}
+
+// ---------------------------------------------------------------------------
+// 24 bits of float32 on the 16-bit matrix instructions. A float32 value is the
+// sum of three bfloat16 ones (planes), each the rounding of what the ones
+// before it leave; products of planes i and j with i + j <= 2 make up the
+// product to 2^-24, at 6/16 of the cost of the float32 instruction. A bfloat16
+// input is one plane, a float16 one two, exactly, so products with inputs cost
+// 3 or 5 of 16. In lane (i, g) of a wave a tile's right operand is 8 values of
+// column i, its left operand 8 of row i, for the same 8 terms of the sum; the
+// result holds rows 4g + r of column i. Which 8 terms is free as long as both
+// sides agree: with the terms 4g + r of two tiles in a row, two results are a
+// right operand as they stand.
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+template <int N>
+struct Planes {
+    bf16x8 p[N];
+};
+
+template <int N>
+__device__ __forceinline__ Planes<N> split(const float (&x)[8]) {
+    Planes<N> out;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        f32x2 v = {x[e], x[e + 1]};
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const bf16x2 h = __builtin_convertvector(v, bf16x2);
+            out.p[k][e] = h[0];
+            out.p[k][e + 1] = h[1];
+            if (k + 1 < N) {
+                v[0] -= (float)h[0];
+                v[1] -= (float)h[1];
+            }
+        }
+    }
+    return out;
+}
+template <int N>
+__device__ __forceinline__ Planes<N> split(f32x4 a, f32x4 b) {
+    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split<N>(x);
+}
+
+// c[t] += A[t] B for COUNT left operands, the planes' products up to i + j <= MOST, smallest first.
+template <int MOST, int COUNT, int NA, int NB>
+__device__ __forceinline__ void products(const Planes<NA> (&A)[COUNT], const Planes<NB>& B, f32x4* c) {
+#pragma unroll
+    for (int sum = MOST; sum >= 0; --sum)
+#pragma unroll
+        for (int i = 0; i <= sum; ++i)
+            if (i < NA && sum - i < NB)
+#pragma unroll
+                for (int t = 0; t < COUNT; ++t)
+                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[t].p[i], B.p[sum - i], c[t], 0, 0, 0);
+}
+
+template <typename T>
+constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+template <>
+constexpr int kPlanes<f16> = 2;
+
+// 64 rows of an input in LDS, plane after plane, in 16-byte pieces; piece c of
+// row t lies at c ^ t (within the row), so that the same piece of 16 rows
+// covers all banks.
+template <typename T, int DK>
+struct Operand {
+    static constexpr int N = kPlanes<T>, PIECES = DK / 8, PLANE = kC * DK, SIZE = N * PLANE;
+    static __device__ __forceinline__ int at(int t, int c) { return t * DK + (c ^ (t & (PIECES - 1))) * 8; }
+    // the rows 16 tile + i, terms 32 s + 8 g ..
+    static __device__ __forceinline__ Planes<N> row(const bf16* m, int tile, int s) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+        Planes<N> x;
+#pragma unroll
+        for (int k = 0; k < N; ++k) x.p[k] = *(const bf16x8*)(m + k * PLANE + at(16 * tile + n, 4 * s + g));
+        return x;
+    }
+    // the transposed rows: dimensions 32 s + 8 (i / 4) + 4 h + i % 4, terms the steps 4g + r of tiles 2p and 2p + 1
+    static __device__ __forceinline__ Planes<N> column(const bf16* m, int s, int h, int p) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+        typedef short i16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) i16x4* Lds;
+        Planes<N> x;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int t = 32 * p + 4 * g + n / 4;
+            const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(t, 4 * s + (n & 3)) + 4 * h));
+            const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(t + 16, 4 * s + (n & 3)) + 4 * h));
+            const bf16x4 lo = __builtin_bit_cast(bf16x4, a), hi = __builtin_bit_cast(bf16x4, b);
+            x.p[k] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+        return x;
+    }
+};
+
+// A thread's share of the rows on their way from memory to LDS. 8 elements at a time, at any alignment; rows at or
+// behind `rows` and elements past `dim` are 0.
+template <typename T, int DK, int THREADS>
+struct Fetch {
+    static constexpr int JOBS = kC * DK / 8 / THREADS;
+    typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    T8 x[JOBS];
+    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int dim) {
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int e = threadIdx.x + j * THREADS, t = e / (DK / 8), d = e % (DK / 8) * 8;
+            x[j] = T8{};
+            if (t < rows) {
+                const T* const from = p + t * step + d;
+                if (d + 8 <= dim)
+                    x[j] = *(const T8*)from;
+                else
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (d + i < dim) x[j][i] = from[i];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(bf16* m) const {
+        typedef Operand<T, DK> O;
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int e = threadIdx.x + j * THREADS, t = e / (DK / 8), c = e % (DK / 8);
+            Planes<O::N> y;
+            if constexpr (O::N == 1) {
+                y.p[0] = __builtin_bit_cast(bf16x8, x[j]);
+            } else {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i] = (float)x[j][i];
+                y = split<O::N>(f);
+            }
+#pragma unroll
+            for (int k = 0; k < O::N; ++k) *(bf16x8*)(m + k * O::PLANE + O::at(t, c)) = y.p[k];
+        }
+    }
+};
+
+// What the chunks' kernels share of a chunk and head, made once: the left
+// operands M and P in the order in which lanes take them (the pairs of tiles
+// (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), three planes of M, and of P two where
+// its product with U is rounded to bfloat16's 8 bits), then per step gamma, e, beta
+// and, in its place 0, gamma of the whole chunk.
+constexpr int kPairs = 6;
+template <int NP>  // planes of P
+struct Record {
+    static constexpr int N = NP;
+    bf16 M[kPairs * 3 * 512];
+    bf16 P[kPairs * NP * 512];
+    float gamma[kC], end[kC], beta[kC], whole[kC];
+};
+template <typename T>
+using RecordOf = Record<kPlanes<T> == 1 ? 2 : 3>;
+static_assert(sizeof(Record<2>) % 16 == 0 && sizeof(Record<3>) % 16 == 0, "records are copied in 16-byte pieces");
+
+__device__ __forceinline__ constexpr int pair_row(int f) { return f < 2 ? f : f < 4 ? 2 : 3; }
+__device__ __forceinline__ constexpr int pair_col(int f) { return f == 3 || f == 5; }
+
+constexpr int kPrepThreads = 256;
+
+// Records of a chunk for all heads of a key head: K K^T and Q K^T once, then
+// per head the decays, M by forward substitution in the diagonal tiles and
+// M21 = -M22 A21 M11 for pairs of tiles and of pairs, in float32.
+template <typename T, int DK>
+__global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int chunks, RecordOf<T>* to) {
+    typedef Operand<T, DK> O;
+    __shared__ bf16 K[O::SIZE];
+    __shared__ bf16 Q[O::SIZE];
+    __shared__ float M[kC * kPitch];
+    __shared__ float P[kC * kPitch];
+    __shared__ Chunk s;
+    const gs_delta_rule& d = a.r;
+    const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
+    const int len = length_of(d, b), t0 = c * kC, group = d.heads / d.key_heads;
+    if (t0 >= len) return;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    {
+        Fetch<T, DK, kPrepThreads> k, q;
+        k.load((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, len - t0, d.key_dim);
+        q.load((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, len - t0, d.key_dim);
+        k.store(K);
+        q.store(Q);
+    }
+    for (int e = threadIdx.x; e < 512; e += kPrepThreads) {  // the tiles over the diagonal that pairs take along
+        const int i = (e >> 4 & 15) + (e >> 8) * 32, j = (e & 15) + (e >> 8) * 32 + 16;
+        M[i * kPitch + j] = P[i * kPitch + j] = 0.0f;
+    }
+    __syncthreads();
+    const f32x4 zero = {0, 0, 0, 0};
+    f32x4 kk[4], qk[4];  // of row tile w
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero;
+#pragma unroll
+    for (int x = 0; x < DK / 32; ++x) {
+        const Planes<O::N> left[2] = {O::row(K, w, x), O::row(Q, w, x)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w) {
+                f32x4 t[2] = {kk[j], qk[j]};
+                products<2>(left, O::row(K, j, x), t);
+                kk[j] = t[0];
+                qk[j] = t[1];
+            }
+    }
+    for (int hh = 0; hh < group; ++hh) {
+        const int h = kh * group + hh;
+        RecordOf<T>* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
+        if (hh) __syncthreads();
+        if (w == 0) load_gates(a, b, h, t0, len, s);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j <= w)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * w + 4 * g + r, col = 16 * j + n;
+                    const float D = row >= col ? decay(s, row, col) : 0.0f;
+                    M[row * kPitch + col] = row > col ? s.beta[row] * D * kk[j][r] : 0.0f;
+                    P[row * kPitch + col] = d.scale * D * qk[j][r];
+                }
+        __syncthreads();
+        {
+            float x[16];
+            const float* const A = M + 16 * w * (kPitch + 1);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float t = i == n ? 1.0f : 0.0f;
+#pragma unroll
+                for (int j = 0; j < i; ++j) t = fmaf(-A[i * kPitch + j], x[j], t);
+                x[i] = t;
+            }
+            __syncthreads();
+            if (lane < 16)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) M[(16 * w + i) * kPitch + 16 * w + n] = x[i];
+        }
+        __syncthreads();
+        auto tile = [&](int i, int j) { return *(const f32x4*)(M + (16 * i + n) * kPitch + 16 * j + 4 * g); };
+        auto right = [&](int i, int j) { return col4(M, kPitch, 16 * i + 4 * g, 16 * j + n); };
+        auto put = [&](int i, int j, f32x4 v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) M[(16 * i + 4 * g + r) * kPitch + 16 * j + n] = -v[r];
+        };
+        if (w < 2) {
+            const f32x4 x = mma(tile(2 * w + 1, 2 * w), right(2 * w, 2 * w), zero);
+            put(2 * w + 1, 2 * w, mma(tile(2 * w + 1, 2 * w + 1), x, zero));
+        }
+        __syncthreads();
+        f32x4 y2 = zero, y3 = zero;
+        if (w < 2) {
+            f32x4 x2 = zero, x3 = zero;
+            for (int q = w; q < 2; ++q) {
+                const f32x4 m = right(q, w);
+                x2 = mma(tile(2, q), m, x2);
+                x3 = mma(tile(3, q), m, x3);
+            }
+            y2 = mma(tile(2, 2), x2, zero);
+            y3 = mma(tile(3, 3), x3, mma(tile(3, 2), x2, zero));
+        }
+        __syncthreads();
+        if (w < 2) {
+            put(2, w, y2);
+            put(3, w, y3);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < kPairs * 64; e += kPrepThreads) {
+            const int f = e >> 6, at = (16 * pair_row(f) + n) * kPitch + 32 * pair_col(f) + 4 * g;
+            const Planes<3> m = split<3>(*(const f32x4*)(M + at), *(const f32x4*)(M + at + 16));
+            const Planes<RecordOf<T>::N> p = split<RecordOf<T>::N>(*(const f32x4*)(P + at), *(const f32x4*)(P + at + 16));
+#pragma unroll
+            for (int k = 0; k < 3; ++k) *(bf16x8*)(out->M + (f * 3 + k) * 512 + lane * 8) = m.p[k];
+#pragma unroll
+            for (int k = 0; k < RecordOf<T>::N; ++k) *(bf16x8*)(out->P + (f * RecordOf<T>::N + k) * 512 + lane * 8) = p.p[k];
+        }
+        if (w == 1) {
+            out->gamma[lane] = s.gamma[lane];
+            out->end[lane] = s.end[lane];
+            out->beta[lane] = s.beta[lane];
+            out->whole[lane] = s.whole;
+        }
+    }
+}
+
+// A record on its way from memory to LDS.
+template <typename Record, int THREADS>
+struct FetchRecord {
+    static constexpr int JOBS = (sizeof(Record) / 16 + THREADS - 1) / THREADS;
+    f32x4 x[JOBS];
+    __device__ __forceinline__ void load(const Record* p) {
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int e = threadIdx.x + j * THREADS;
+            if (e < (int)sizeof(Record) / 16) x[j] = ((const f32x4*)p)[e];
+        }
+    }
+    __device__ __forceinline__ void store(Record* p) const {
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int e = threadIdx.x + j * THREADS;
+            if (e < (int)sizeof(Record) / 16) ((f32x4*)p)[e] = x[j];
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ Planes<N> operand(const bf16* m, int f) {
+    Planes<N> x;
+#pragma unroll
+    for (int k = 0; k < N; ++k) x.p[k] = *(const bf16x8*)(m + (f * N + k) * 512 + (threadIdx.x & 63) * 8);
+    return x;
+}
+
+// The dimension of the keys that row 4g + r of tile t of a state's column stands for.
+__device__ __forceinline__ int key_row(int t, int g, int r) { return 32 * (t / 2) + 8 * g + 4 * (t & 1) + r; }
+
+// The states, chunk after chunk, 16 columns of the values a wave: S and what
+// follows from it (R, U) never leave its registers, each product's result is
+// the next one's right operand. What the waves share is fetched a chunk ahead.
+template <typename T, int DK>
+__global__ __launch_bounds__(64 * kChainWaves) void k_delta_chain(DeltaArgs a, int chunks, const RecordOf<T>* records) {
+    typedef RecordOf<T> Record;
+    constexpr int NP = Record::N;
+    constexpr int KT = DK / 16, KS = DK / 32, kThreads = 64 * kChainWaves;
+    typedef Operand<T, DK> O;
+    __shared__ bf16 K[O::SIZE];
+    __shared__ bf16 Q[O::SIZE];
+    __shared__ Record rec;
+    const gs_delta_rule& d = a.r;
+    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
+    const bool on = col < d.value_dim;
+    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
+    const int64_t state = ((int64_t)b * d.heads + h) * d.key_dim * d.value_dim + col;
+    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
+    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
+    const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head + col;
+    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
+    const int64_t o_step = (int64_t)d.heads * d.value_dim;
+    const Record* const mine_rec = records + (int64_t)b * chunks * d.heads + h;
+    f32x4 S[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int row = key_row(t, g, r);
+            S[t][r] = a.h0 && on && row < d.key_dim ? a.h0[state + (int64_t)row * d.value_dim] : 0.0f;
+        }
+    Fetch<T, DK, kThreads> fk, fq;
+    FetchRecord<Record, kThreads> fr;
+    T fv[16];
+    auto fetch = [&](int c) {
+        const int t0 = c * kC, rows = len - t0;
+        fr.load(mine_rec + (int64_t)c * d.heads);
+        fk.load(k + t0 * d.k_step, d.k_step, rows, d.key_dim);
+        fq.load(q + t0 * d.q_step, d.q_step, rows, d.key_dim);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int i = 16 * (e / 4) + 4 * g + e % 4;
+            fv[e] = on && i < rows ? v[(t0 + i) * d.v_step] : (T)0.0f;
+        }
+    };
+    if (mine > 0) fetch(0);
+    const f32x4 zero = {0, 0, 0, 0};
+    for (int c = 0; c < mine; ++c) {
+        const int t0 = c * kC;
+        __syncthreads();
+        fr.store(&rec);
+        fk.store(K);
+        fq.store(Q);
+        float V[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) V[e] = (float)fv[e];
+        __syncthreads();
+        if (c + 1 < mine) fetch(c + 1);
+        f32x4 x[4], y[4];  // K S and Q S
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) x[ti] = y[ti] = zero;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const Planes<3> sp = split<3>(S[2 * s], S[2 * s + 1]);
+            Planes<O::N> A[4];
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s);
+            products<2>(A, sp, x);
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
+            products<NP - 1>(A, sp, y);
+        }
+        f32x4 gamma[4];
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            gamma[ti] = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g);
+            const f32x4 beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x[ti][r] = beta[r] * (V[4 * ti + r] - gamma[ti][r] * x[ti][r]);
+        }
+        f32x4 U[4];
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) U[ti] = zero;
+        const Planes<3> R0 = split<3>(x[0], x[1]), R1 = split<3>(x[2], x[3]);
+        {
+            const Planes<3> A[4] = {operand<3>(rec.M, 0), operand<3>(rec.M, 1), operand<3>(rec.M, 2), operand<3>(rec.M, 4)};
+            products<2>(A, R0, U);
+            const Planes<3> B[2] = {operand<3>(rec.M, 3), operand<3>(rec.M, 5)};
+            products<2>(B, R1, U + 2);
+        }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[ti][r] *= d.scale * gamma[ti][r];
+        {
+            const Planes<NP> U0 = split<NP>(U[0], U[1]), U1 = split<NP>(U[2], U[3]);
+            const Planes<NP> A[4] = {operand<NP>(rec.P, 0), operand<NP>(rec.P, 1), operand<NP>(rec.P, 2), operand<NP>(rec.P, 4)};
+            products<NP - 1>(A, U0, y);
+            const Planes<NP> B[2] = {operand<NP>(rec.P, 3), operand<NP>(rec.P, 5)};
+            products<NP - 1>(B, U1, y + 2);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int t = t0 + 16 * (e / 4) + 4 * g + e % 4;
+            if (on && t < d.steps) o[t * o_step] = (T)y[e / 4][e % 4];
+        }
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
+        const float whole = rec.whole[0];
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S[t] *= whole;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const Planes<3> up = split<3>(U[2 * p], U[2 * p + 1]);
+#pragma unroll
+            for (int s = 0; s < KS; s += 2) {
+                const Planes<O::N> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
+                products<2>(A, up, S + 2 * s);
+            }
+        }
+        if (a.ckpt && t0 + kC < len) {
+            float* const to = a.ckpt + ((((int64_t)b * (chunks - 1) + c) * d.heads + h) * d.key_dim) * d.value_dim + col;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = key_row(t, g, r);
+                    if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[t][r];
+                }
+        }
+    }
+    for (int t = mine * kC + g; t < d.steps; t += 4)
+        if (on) o[t * o_step] = (T)0.0f;
+    if (a.h_last)
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = key_row(t, g, r);
+                if (on && row < d.key_dim) a.h_last[state + (int64_t)row * d.value_dim] = S[t][r];
             }
 }
 
@@ -876,13 +1231,14 @@ int chunks_of(const gs_delta_rule& r) { return (r.steps + kC - 1) / kC; }
 size_t inverse_floats(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * kLower; }
 
 template <typename T, int DK>
-hipError_t forward(const DeltaArgs& a, float* scratch, hipStream_t stream) {
+hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const int chunks = chunks_of(r);
-    if (chunks) k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, scratch);
+    RecordOf<T>* const records = (RecordOf<T>*)scratch;
+    k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, records);
     const int wide = 16 * kChainWaves;
-    k_delta_fwd<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
-        a, chunks, scratch);
+    k_delta_chain<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
+        a, chunks, records);
     return hipGetLastError();
 }
 
@@ -919,8 +1275,10 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
+    if (!backward)
+        return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Record<2>) : sizeof(Record<3>));
     size_t floats = inverse_floats(r);
-    if (backward) floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
+    floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
     return floats * sizeof(float);
 }
 
