@@ -116,6 +116,9 @@ gs_status check_delta_rule(const gs_delta_rule* r, const char* who) {
     for (int64_t s : {r->q_batch, r->q_step, r->q_head, r->k_batch, r->k_step, r->k_head, r->v_batch, r->v_step,
                       r->v_head, r->decay_batch, r->decay_step, r->beta_batch, r->beta_step})
         if (s < 0) return fail(GS_ERR_INVALID, "%s: a stride is negative", who);
+    // a chunk's rows are addressed by 32-bit offsets in bytes
+    for (int64_t s : {r->q_step, r->k_step, r->v_step, (int64_t)r->heads * r->value_dim})
+        if (s > (1 << 22)) return fail(GS_ERR_INVALID, "%s: a step stride of %lld is over 2^22", who, (long long)s);
     if ((uintptr_t)r->lengths & 3) return fail(GS_ERR_INVALID, "%s: lengths is not 4-byte aligned", who);
     return GS_OK;
 }

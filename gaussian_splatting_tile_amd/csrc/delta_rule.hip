@@ -19,6 +19,7 @@
 //   f_i = q_i.(scale gamma dO S^T)_i - k_i.(beta gamma dR S^T)_i,  b_j = k_j.(e U dS^T)_j
 // formed as these sums, without differences of larger ones.
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_internal.h"
 
@@ -405,26 +406,54 @@ struct Operand {
     }
 };
 
-// A thread's share of the rows on their way from memory to LDS. 8 elements at a time, at any alignment; rows at or
-// behind `rows` and elements past `dim` are 0.
+// A uniform base and a 32-bit offset in bytes.
+template <typename V, typename T>
+__device__ __forceinline__ V& at_bytes(T* p, uint32_t off) {
+    typedef std::conditional_t<std::is_const_v<T>, const char, char> Byte;
+    return *(V*)((Byte*)p + off);
+}
+
+// The same value, which the compiler does not know: what is computed of it is
+// computed where it is used, not held in registers through a loop.
+template <typename T>
+__device__ __forceinline__ T here(T x) {
+    asm volatile("" : "+s"(x));
+    return x;
+}
+
+// A thread's share of the rows on their way from memory to LDS, 8 elements at a
+// time, at any alignment, without branches: a row at or behind `rows` is read
+// as the last one of them (its beta of 0 and its place behind all others keep
+// it out of every result that is stored), elements past `dim` are 0.
 template <typename T, int DK, int THREADS>
 struct Fetch {
-    static constexpr int JOBS = kC * DK / 8 / THREADS;
+    static constexpr int JOBS = kC * DK / 8 / THREADS, PIECES = DK / 8;
+    static_assert(THREADS % PIECES == 0, "a thread's pieces lie at one place of their rows");
     typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
     T8 x[JOBS];
     __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int dim) {
+        const int d = threadIdx.x % PIECES * 8, t = threadIdx.x / PIECES;
+        constexpr int BY = THREADS / PIECES;
+        step = here(step);
+        if (dim == DK && rows >= kC) {
+            const uint32_t off = (uint32_t)(t * (int)step + d) * (uint32_t)sizeof(T);
+#pragma unroll
+            for (int j = 0; j < JOBS; ++j) {
+                x[j] = at_bytes<const T8>(p, off);
+                p += BY * step;
+            }
+            return;
+        }
+        const int last = min(rows, kC) - 1;
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
-            const int e = threadIdx.x + j * THREADS, t = e / (DK / 8), d = e % (DK / 8) * 8;
+            const T* const from = p + min(t + j * BY, last) * step + d;
             x[j] = T8{};
-            if (t < rows) {
-                const T* const from = p + t * step + d;
-                if (d + 8 <= dim)
-                    x[j] = *(const T8*)from;
-                else
+            if (d + 8 <= dim) {
+                x[j] = *(const T8*)from;
+            } else if (d < dim) {
 #pragma unroll
-                    for (int i = 0; i < 7; ++i)
-                        if (d + i < dim) x[j][i] = from[i];
+                for (int i = 0; i < 7; ++i) x[j][i] = d + i < dim ? from[min(i, dim - 1 - d)] : (T)0.0f;
             }
         }
     }
@@ -432,7 +461,7 @@ struct Fetch {
         typedef Operand<T, DK> O;
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
-            const int e = threadIdx.x + j * THREADS, t = e / (DK / 8), c = e % (DK / 8);
+            const int t = threadIdx.x / PIECES + j * (THREADS / PIECES), c = threadIdx.x % PIECES;
             Planes<O::N> y;
             if constexpr (O::N == 1) {
                 y.p[0] = __builtin_bit_cast(bf16x8, x[j]);
@@ -593,24 +622,19 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
     }
 }
 
-// A record on its way from memory to LDS.
+// A record on its way from memory to LDS; the threads that have none of the last pieces copy the last one too.
 template <typename Record, int THREADS>
 struct FetchRecord {
-    static constexpr int JOBS = (sizeof(Record) / 16 + THREADS - 1) / THREADS;
+    static constexpr int PIECES = sizeof(Record) / 16, JOBS = (PIECES + THREADS - 1) / THREADS;
     f32x4 x[JOBS];
     __device__ __forceinline__ void load(const Record* p) {
 #pragma unroll
-        for (int j = 0; j < JOBS; ++j) {
-            const int e = threadIdx.x + j * THREADS;
-            if (e < (int)sizeof(Record) / 16) x[j] = ((const f32x4*)p)[e];
-        }
+        for (int j = 0; j < JOBS; ++j)
+            x[j] = at_bytes<const f32x4>(p, (uint32_t)min((int)threadIdx.x + j * THREADS, PIECES - 1) * 16u);
     }
     __device__ __forceinline__ void store(Record* p) const {
 #pragma unroll
-        for (int j = 0; j < JOBS; ++j) {
-            const int e = threadIdx.x + j * THREADS;
-            if (e < (int)sizeof(Record) / 16) ((f32x4*)p)[e] = x[j];
-        }
+        for (int j = 0; j < JOBS; ++j) ((f32x4*)p)[min((int)threadIdx.x + j * THREADS, PIECES - 1)] = x[j];
     }
 };
 
@@ -625,149 +649,296 @@ __device__ __forceinline__ Planes<N> operand(const bf16* m, int f) {
 // The dimension of the keys that row 4g + r of tile t of a state's column stands for.
 __device__ __forceinline__ int key_row(int t, int g, int r) { return 32 * (t / 2) + 8 * g + 4 * (t & 1) + r; }
 
+// A column of a state in registers: rows in the order of key_row, zero past the dimensions.
+template <int KT>
+struct Column {
+    f32x4 t[KT];
+    __device__ __forceinline__ void load(const float* p, bool on, const gs_delta_rule& d) {
+        const int g = threadIdx.x >> 4 & 3;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = key_row(k, g, r);
+                t[k][r] = p && on && row < d.key_dim ? p[row * d.value_dim] : 0.0f;
+            }
+    }
+    // p: a matrix with rows of `pitch`
+    __device__ __forceinline__ void store(float* p, int col, int pitch, const gs_delta_rule& d) const {
+        const int g = threadIdx.x >> 4 & 3;
+        pitch = here(pitch);
+        if (d.key_dim == 16 * KT) {
+            const uint32_t first = (8 * g * pitch + col) * 4;
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    at_bytes<float>(p, first) = t[k][r];
+                    p += (k & 1) && r == 3 ? 25 * pitch : pitch;
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = key_row(k, g, r);
+                    if (row < d.key_dim) p[row * pitch + col] = t[k][r];
+                }
+        }
+    }
+};
+
+// The values of a chunk in a column, as results lie: rows 16 t + 4g + r.
+template <typename T>
+struct Values {
+    T x[16];
+    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int col) {
+        const int g = threadIdx.x >> 4 & 3;
+        step = here(step);
+        if (rows >= kC) {
+            const uint32_t off = (uint32_t)(4 * g * (int)step + col) * (uint32_t)sizeof(T);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                x[e] = at_bytes<const T>(p, off);
+                p += e % 4 == 3 ? 13 * step : step;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = p[min(16 * (e / 4) + 4 * g + e % 4, rows - 1) * step + col];
+        }
+    }
+    // rows from `rows` on are 0, those from `all` on are not there
+    static __device__ __forceinline__ void store(T* p, int64_t step, int rows, int all, int col, const f32x4 (&v)[4]) {
+        const int g = threadIdx.x >> 4 & 3;
+        step = here(step);
+        if (rows >= kC) {
+            const uint32_t off = (uint32_t)(4 * g * (int)step + col) * (uint32_t)sizeof(T);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                at_bytes<T>(p, off) = (T)v[e / 4][e % 4];
+                p += e % 4 == 3 ? 13 * step : step;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int i = 16 * (e / 4) + 4 * g + e % 4;
+                if (i < all) p[i * step + col] = i < rows ? (T)v[e / 4][e % 4] : (T)0.0f;
+            }
+        }
+    }
+};
+
 // The states, chunk after chunk, 16 columns of the values a wave: S and what
 // follows from it (R, U) never leave its registers, each product's result is
 // the next one's right operand. What the waves share is fetched a chunk ahead.
-template <typename T, int DK>
-__global__ __launch_bounds__(64 * kChainWaves) void k_delta_chain(DeltaArgs a, int chunks, const RecordOf<T>* records) {
+//
+// Where there are few sequences and heads, a sequence is cut into segments that
+// run side by side. A segment takes a state S to Phi S + B, so a first pass
+// without outputs (OUT false) gives B (from a state of 0) and Phi (as columns
+// of a state that starts as the identity, without values), a short walk over
+// the segments (k_delta_join) the state in front of each, and the pass with
+// outputs starts from those.
+struct Segments {
+    int count, chunks;  // of a sequence; of a segment
+    float* front;       // [b][h][segment][key_dim][value_dim] B, then the state in front
+    float* phi;         // [b][h][segment][key_dim][key_dim]
+};
+
+template <typename T, int DK, int WAVES, bool OUT>
+__global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const RecordOf<T>* records, Segments seg) {
     typedef RecordOf<T> Record;
-    constexpr int NP = Record::N;
-    constexpr int KT = DK / 16, KS = DK / 32, kThreads = 64 * kChainWaves;
+    constexpr int NP = Record::N, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
     typedef Operand<T, DK> O;
     __shared__ bf16 K[O::SIZE];
-    __shared__ bf16 Q[O::SIZE];
+    __shared__ bf16 Q[OUT ? O::SIZE : 8];
     __shared__ Record rec;
     const gs_delta_rule& d = a.r;
     const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
-    const bool on = col < d.value_dim;
-    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
-    const int64_t state = ((int64_t)b * d.heads + h) * d.key_dim * d.value_dim + col;
+    // behind the values' columns, in workgroups of their own, those of Phi
+    const int blocks = (d.value_dim + 16 * WAVES - 1) / (16 * WAVES);
+    const bool values = OUT || (int)blockIdx.y < blocks;
+    const int col = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16 + n;
+    const bool on = col < (values ? d.value_dim : d.key_dim);
+    const int len = length_of(d, b), z = blockIdx.z;
+    const int c0 = z * seg.chunks, c1 = min((len + kC - 1) / kC, c0 + seg.chunks);
+    const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
     const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
     const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
-    const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head + col;
-    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
+    const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head;
     const int64_t o_step = (int64_t)d.heads * d.value_dim;
-    const Record* const mine_rec = records + (int64_t)b * chunks * d.heads + h;
-    f32x4 S[KT];
+    T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
+    const Record* const first = records + (int64_t)b * chunks * d.heads + h;
+    Column<KT> S;
+    if constexpr (OUT) {
+        const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
+        S.load(from ? from + col : nullptr, on, d);
+    } else {
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = key_row(t, g, r);
-            S[t][r] = a.h0 && on && row < d.key_dim ? a.h0[state + (int64_t)row * d.value_dim] : 0.0f;
-        }
+            for (int r = 0; r < 4; ++r) S.t[t][r] = !values && key_row(t, g, r) == col ? 1.0f : 0.0f;
+    }
     Fetch<T, DK, kThreads> fk, fq;
     FetchRecord<Record, kThreads> fr;
-    T fv[16];
+    Values<T> fv;
     auto fetch = [&](int c) {
         const int t0 = c * kC, rows = len - t0;
-        fr.load(mine_rec + (int64_t)c * d.heads);
+        fr.load(first + (int64_t)c * d.heads);
         fk.load(k + t0 * d.k_step, d.k_step, rows, d.key_dim);
-        fq.load(q + t0 * d.q_step, d.q_step, rows, d.key_dim);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int i = 16 * (e / 4) + 4 * g + e % 4;
-            fv[e] = on && i < rows ? v[(t0 + i) * d.v_step] : (T)0.0f;
-        }
+        if constexpr (OUT) fq.load(q + t0 * d.q_step, d.q_step, rows, d.key_dim);
+        if (values) fv.load(v + t0 * d.v_step, d.v_step, rows, min(col, d.value_dim - 1));
     };
-    if (mine > 0) fetch(0);
+    if (c0 < c1) fetch(c0);
     const f32x4 zero = {0, 0, 0, 0};
-    for (int c = 0; c < mine; ++c) {
+    for (int c = c0; c < c1; ++c) {
         const int t0 = c * kC;
         __syncthreads();
         fr.store(&rec);
         fk.store(K);
-        fq.store(Q);
-        float V[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) V[e] = (float)fv[e];
+        if constexpr (OUT) fq.store(Q);
         __syncthreads();
-        if (c + 1 < mine) fetch(c + 1);
         f32x4 x[4], y[4];  // K S and Q S
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) x[ti] = y[ti] = zero;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const Planes<3> sp = split<3>(S[2 * s], S[2 * s + 1]);
+            const Planes<3> sp = split<3>(S.t[2 * s], S.t[2 * s + 1]);
             Planes<O::N> A[4];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s);
             products<2>(A, sp, x);
+            if constexpr (OUT) {
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
-            products<NP - 1>(A, sp, y);
+                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
+                products<NP - 1>(A, sp, y);
+            }
         }
-        f32x4 gamma[4];
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) {
-            gamma[ti] = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g);
-            const f32x4 beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
+            const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) x[ti][r] = beta[r] * (V[4 * ti + r] - gamma[ti][r] * x[ti][r]);
+            for (int r = 0; r < 4; ++r) {
+                x[ti][r] = beta[r] * fmaf(-gamma[r], x[ti][r], values ? (float)fv.x[4 * ti + r] : 0.0f);
+                if constexpr (OUT) y[ti][r] *= d.scale * gamma[r];
+            }
         }
+        if (c + 1 < c1) fetch(c + 1);
         f32x4 U[4];
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] = zero;
-        const Planes<3> R0 = split<3>(x[0], x[1]), R1 = split<3>(x[2], x[3]);
         {
+            const Planes<3> R0 = split<3>(x[0], x[1]);
             const Planes<3> A[4] = {operand<3>(rec.M, 0), operand<3>(rec.M, 1), operand<3>(rec.M, 2), operand<3>(rec.M, 4)};
             products<2>(A, R0, U);
+            const Planes<3> R1 = split<3>(x[2], x[3]);
             const Planes<3> B[2] = {operand<3>(rec.M, 3), operand<3>(rec.M, 5)};
             products<2>(B, R1, U + 2);
         }
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) y[ti][r] *= d.scale * gamma[ti][r];
-        {
-            const Planes<NP> U0 = split<NP>(U[0], U[1]), U1 = split<NP>(U[2], U[3]);
+        if constexpr (OUT) {
+            const Planes<NP> U0 = split<NP>(U[0], U[1]);
             const Planes<NP> A[4] = {operand<NP>(rec.P, 0), operand<NP>(rec.P, 1), operand<NP>(rec.P, 2), operand<NP>(rec.P, 4)};
             products<NP - 1>(A, U0, y);
+            const Planes<NP> U1 = split<NP>(U[2], U[3]);
             const Planes<NP> B[2] = {operand<NP>(rec.P, 3), operand<NP>(rec.P, 5)};
             products<NP - 1>(B, U1, y + 2);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int t = t0 + 16 * (e / 4) + 4 * g + e % 4;
-            if (on && t < d.steps) o[t * o_step] = (T)y[e / 4][e % 4];
+            if (on) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col, y);
         }
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
         const float whole = rec.whole[0];
 #pragma unroll
-        for (int t = 0; t < KT; ++t) S[t] *= whole;
+        for (int t = 0; t < KT; ++t) S.t[t] *= whole;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const Planes<3> up = split<3>(U[2 * p], U[2 * p + 1]);
 #pragma unroll
             for (int s = 0; s < KS; s += 2) {
                 const Planes<O::N> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
-                products<2>(A, up, S + 2 * s);
+                products<2>(A, up, S.t + 2 * s);
             }
         }
-        if (a.ckpt && t0 + kC < len) {
-            float* const to = a.ckpt + ((((int64_t)b * (chunks - 1) + c) * d.heads + h) * d.key_dim) * d.value_dim + col;
+        if (OUT && a.ckpt && t0 + kC < len && on)
+            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col, d.value_dim, d);
+    }
+    if constexpr (OUT) {
+        // the steps of the segment that are padding behind its last chunk
+        const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
+        if (on)
+            for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col] = (T)0.0f;
+        if (a.h_last && on && z + 1 == seg.count) S.store(a.h_last + head * size, col, d.value_dim, d);
+    } else if (on) {
+        if (values)
+            S.store(seg.front + (head * seg.count + z) * size, col, d.value_dim, d);
+        else
+            S.store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col, d.key_dim, d);
+    }
+}
+
+// The state in front of every segment, in place of its B: S <- Phi S + B from
+// segment to segment, 16 columns a wave.
+constexpr int kJoinWaves = 8;
+
+template <int DK>
+__global__ __launch_bounds__(64 * kJoinWaves) void k_delta_join(DeltaArgs a, Segments seg) {
+    constexpr int KT = DK / 16, KS = DK / 32, kThreads = 64 * kJoinWaves;
+    typedef Operand<float, DK> O;
+    __shared__ bf16 F[DK / kC][O::SIZE];
+    const gs_delta_rule& d = a.r;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int col = w * 16 + n;
+    const bool on = col < d.value_dim;
+    const int64_t head = blockIdx.x, size = (int64_t)d.key_dim * d.value_dim;
+    Column<KT> S, B;
+    S.load(a.h0 ? a.h0 + head * size + col : nullptr, on, d);
+    Fetch<float, DK, kThreads> f[DK / kC];
+    float* front = seg.front + head * seg.count * size;
+    const float* phi = seg.phi + head * seg.count * d.key_dim * d.key_dim;
+    // rows past the dimensions are copies of the last one here, and their results are not stored
+    auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < DK / kC; ++i)
+            f[i].load(phi + (int64_t)min(i * kC, d.key_dim - 1) * d.key_dim, d.key_dim, max(d.key_dim - i * kC, 1), d.key_dim);
+        B.load(front + col, on, d);
+    };
+    fetch();
+    for (int z = 0; z < seg.count; ++z) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < DK / kC; ++i) f[i].store(F[i]);
+        __syncthreads();
+        if (on) S.store(front, col, d.value_dim, d);
+        if (z + 1 == seg.count) break;
+        Column<KT> N = B;
+        front += size;
+        phi += d.key_dim * d.key_dim;
+        if (z + 2 < seg.count) fetch();
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const Planes<3> sp = split<3>(S.t[2 * s], S.t[2 * s + 1]);
+#pragma unroll
+            for (int t = 0; t < KT; t += 4) {
+                Planes<3> A[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // row n of result tile t + i stands for this dimension
+                    const int row = key_row(t + i, n >> 2, n & 3);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        A[i].p[k] = *(const bf16x8*)(F[row / kC] + k * O::PLANE + O::at(row % kC, 4 * s + g));
+                }
+                products<2>(A, sp, N.t + t);
+            }
+        }
+        S = N;
+        // rows past the dimensions stay 0
+        if (d.key_dim < DK)
 #pragma unroll
             for (int t = 0; t < KT; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = key_row(t, g, r);
-                    if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[t][r];
-                }
-        }
+                for (int r = 0; r < 4; ++r)
+                    if (key_row(t, g, r) >= d.key_dim) S.t[t][r] = 0.0f;
     }
-    for (int t = mine * kC + g; t < d.steps; t += 4)
-        if (on) o[t * o_step] = (T)0.0f;
-    if (a.h_last)
-#pragma unroll
-        for (int t = 0; t < KT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = key_row(t, g, r);
-                if (on && row < d.key_dim) a.h_last[state + (int64_t)row * d.value_dim] = S[t][r];
-            }
 }
 
 constexpr int kGradWaves = 8;
@@ -1230,16 +1401,52 @@ hipError_t steps(const DeltaArgs& a, hipStream_t stream) {
 int chunks_of(const gs_delta_rule& r) { return (r.steps + kC - 1) / kC; }
 size_t inverse_floats(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * kLower; }
 
+size_t record_bytes(const gs_delta_rule& r) {
+    return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Record<2>) : sizeof(Record<3>));
+}
+
+// Segments of a sequence: enough workgroups for the chip, each of them long
+// enough for the walk over them and the first pass (more than the work of the
+// second) to pay.
+constexpr int kUnits = 256;  // compute units
+Segments segments_of(const gs_delta_rule& r) {
+    Segments s{1, chunks_of(r), nullptr, nullptr};
+    const int64_t heads = (int64_t)r.batch * r.heads;
+    if (heads > kUnits / 3 || s.chunks < 32) return s;
+    const int most = (int)std::min<int64_t>((kUnits + heads - 1) / heads, 32);
+    s.chunks = std::max((s.chunks + most - 1) / most, 8);
+    s.count = (chunks_of(r) + s.chunks - 1) / s.chunks;
+    return s;
+}
+size_t segment_bytes(const gs_delta_rule& r) {
+    const Segments s = segments_of(r);
+    return s.count == 1 ? 0 : (size_t)r.batch * r.heads * s.count * r.key_dim * (r.value_dim + r.key_dim) * sizeof(float);
+}
+
+template <typename T, int DK, int WAVES>
+hipError_t chain(const DeltaArgs& a, void* scratch, hipStream_t stream) {
+    const gs_delta_rule& r = a.r;
+    const int chunks = chunks_of(r), wide = 16 * WAVES, heads = r.batch * r.heads;
+    const RecordOf<T>* const records = (const RecordOf<T>*)scratch;
+    const int blocks = (r.value_dim + wide - 1) / wide;
+    Segments seg = segments_of(r);
+    if (seg.count > 1) {
+        seg.front = (float*)((char*)scratch + record_bytes(r));
+        seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
+        k_delta_chain<T, DK, WAVES, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * WAVES, 0, stream>>>(
+            a, chunks, records, seg);
+        k_delta_join<DK><<<heads, 64 * kJoinWaves, 0, stream>>>(a, seg);
+    }
+    k_delta_chain<T, DK, WAVES, true><<<dim3(heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(a, chunks, records, seg);
+    return hipGetLastError();
+}
+
 template <typename T, int DK>
 hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const int chunks = chunks_of(r);
-    RecordOf<T>* const records = (RecordOf<T>*)scratch;
-    k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, records);
-    const int wide = 16 * kChainWaves;
-    k_delta_chain<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
-        a, chunks, records);
-    return hipGetLastError();
+    k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, (RecordOf<T>*)scratch);
+    return r.value_dim > 64 ? chain<T, DK, 8>(a, scratch, stream) : chain<T, DK, 4>(a, scratch, stream);
 }
 
 template <typename T, int DK>
@@ -1275,8 +1482,7 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
-    if (!backward)
-        return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Record<2>) : sizeof(Record<3>));
+    if (!backward) return record_bytes(r) + segment_bytes(r);
     size_t floats = inverse_floats(r);
     floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
     return floats * sizeof(float);

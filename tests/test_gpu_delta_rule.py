@@ -90,6 +90,21 @@ def test_against_oracle(B, T, Hk, H, dk, dv, flags, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B,T,Hk,H,dk,dv,flags", [
+    (1, 2048, 1, 1, 64, 64, ""), (1, 2100, 1, 2, 128, 128, "p"), (2, 2500, 1, 1, 40, 72, "lr"), (3, 2049, 1, 1, 100, 16, "l"),
+])
+def test_long_sequences(B, T, Hk, H, dk, dv, flags, dtype):
+    """Few sequences of many chunks: cut into segments that run side by side."""
+    d, up = make(B, T, Hk, H, dk, dv, dtype, T + dk, "l" in flags, "r" in flags, "p" in flags)
+    h = d["h0"].clone()
+    out = run(d, up)
+    check(out, blocks.delta_rule(**host(d), **host(up)), dtype)
+    import gaussian_splatting_tile_amd as gs
+    again = gs.delta_rule_fwd(**dict(d, h0=h), out=dict(h_last=h))
+    assert (h == out["h_last"]).all() and (again["o"] == out["o"]).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [1, 3, 70])
 def test_without_state_and_upstream_state(T, dtype):
     d, up = make(2, T, 2, 2, 64, 32, dtype, 5, state=False)
