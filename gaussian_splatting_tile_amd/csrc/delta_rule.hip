@@ -310,86 +310,125 @@ __global__ __launch_bounds__(64 * kChainWaves) void k_delta_bwd(DeltaArgs a, int
 }
 
 // ---------------------------------------------------------------------------
-// 24 bits of float32 on the 16-bit matrix instructions. A float32 value is the
-// sum of three bfloat16 ones (planes), each the rounding of what the ones
-// before it leave; products of planes i and j with i + j <= 2 make up the
-// product to 2^-24, at 6/16 of the cost of the float32 instruction. A bfloat16
-// input is one plane, a float16 one two, exactly, so products with inputs cost
-// 3 or 5 of 16. In lane (i, g) of a wave a tile's right operand is 8 values of
-// column i, its left operand 8 of row i, for the same 8 terms of the sum; the
-// result holds rows 4g + r of column i. Which 8 terms is free as long as both
-// sides agree: with the terms 4g + r of two tiles in a row, two results are a
-// right operand as they stand.
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+// Float32 values on the 16-bit matrix instructions. Scaled by a power of two to
+// at most 1, a value is the sum of two float16 ones (planes), the rounding of
+// it and that of the rest: 22 bits, or 2^-25 of the largest value that shares
+// the scale. Left operands are scaled by rows, right ones by columns, so the
+// scales leave every sum as one factor. Inputs of 16 bits are one plane
+// (bfloat16's 8 bits fit float16's 11), float32 ones two; a product of two
+// planes leaves out the product of the rests. An instruction takes 1/16 of the
+// float32 one's time for the same product, so float32 results cost 2/16
+// (16-bit inputs) or 3/16.
+//
+// In lane (i, g) of a wave a tile's right operand is 8 values of column i, its
+// left operand 8 of row i, for the same 8 terms of the sum; the result holds
+// rows 4g + r of column i. Which 8 terms is free as long as both sides agree:
+// with the terms 4g + r of two tiles in a row, two results are a right operand
+// as they stand.
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef f16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 template <int N>
 struct Planes {
-    bf16x8 p[N];
+    f16x8 p[N];
 };
 
 template <int N>
-__device__ __forceinline__ Planes<N> split(const float (&x)[8]) {
+__device__ __forceinline__ Planes<N> split(f32x4 a, f32x4 b, float scale) {
     Planes<N> out;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-        f32x2 v = {x[e], x[e + 1]};
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const bf16x2 h = __builtin_convertvector(v, bf16x2);
-            out.p[k][e] = h[0];
-            out.p[k][e + 1] = h[1];
-            if (k + 1 < N) {
-                v[0] -= (float)h[0];
-                v[1] -= (float)h[1];
-            }
+        const f32x2 v = e < 4 ? f32x2{a[e], a[e + 1]} : f32x2{b[e - 4], b[e - 3]};
+        const f16x2 h = __builtin_convertvector(f32x2{v[0] * scale, v[1] * scale}, f16x2);
+        out.p[0][e] = h[0];
+        out.p[0][e + 1] = h[1];
+        if constexpr (N > 1) {
+            const f32x2 rest = {fmaf(v[0], scale, -(float)h[0]), fmaf(v[1], scale, -(float)h[1])};
+            const f16x2 l = __builtin_convertvector(rest, f16x2);
+            out.p[1][e] = l[0];
+            out.p[1][e + 1] = l[1];
         }
     }
     return out;
 }
+
+// A power of two that brings values of this largest size to [1/2, 1), and its inverse.
+struct Scale {
+    float by, back;
+    __device__ __forceinline__ explicit Scale(float largest) {
+        const int e = min(max(__builtin_amdgcn_frexp_expf(largest), -126), 127);
+        by = __builtin_amdgcn_ldexpf(1.0f, -e);
+        back = __builtin_amdgcn_ldexpf(1.0f, e);
+    }
+};
+
 template <int N>
-__device__ __forceinline__ Planes<N> split(f32x4 a, f32x4 b) {
-    const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-    return split<N>(x);
+__device__ __forceinline__ float largest(const f32x4 (&v)[N]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int t = 0; t < N; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(v[t][r]));
+    return m;
+}
+// Over the four lanes that hold a column of a result.
+__device__ __forceinline__ float over_column(float m) {
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    m = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+}
+// Over N neighbouring lanes (N = 8 or 16).
+template <int N>
+__device__ __forceinline__ float over_lanes(float m) {
+    auto with = [&](auto ctrl) {
+        m = fmaxf(m, __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(m), decltype(ctrl)::value, 0xf, 0xf, true)));
+    };
+    with(std::integral_constant<int, 0xB1>{});   // quad_perm 1 0 3 2
+    with(std::integral_constant<int, 0x4E>{});   // quad_perm 2 3 0 1
+    with(std::integral_constant<int, 0x141>{});  // row_half_mirror
+    if constexpr (N == 16) with(std::integral_constant<int, 0x140>{});  // row_mirror
+    return m;
 }
 
-// c[t] += A[t] B for COUNT left operands, the planes' products up to i + j <= MOST, smallest first.
-template <int MOST, int COUNT, int NA, int NB>
+// c[t] += A[t] B for COUNT left operands, the planes' products but that of the rests, smaller ones first.
+template <int COUNT, int NA, int NB>
 __device__ __forceinline__ void products(const Planes<NA> (&A)[COUNT], const Planes<NB>& B, f32x4* c) {
 #pragma unroll
-    for (int sum = MOST; sum >= 0; --sum)
+    for (int sum = 1; sum >= 0; --sum)
 #pragma unroll
         for (int i = 0; i <= sum; ++i)
             if (i < NA && sum - i < NB)
 #pragma unroll
                 for (int t = 0; t < COUNT; ++t)
-                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(A[t].p[i], B.p[sum - i], c[t], 0, 0, 0);
+                    c[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[t].p[i], B.p[sum - i], c[t], 0, 0, 0);
 }
 
+// Planes of an input, and of P and what it multiplies where that is rounded to bfloat16's 8 bits, float16's 11 or not.
 template <typename T>
-constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-template <>
-constexpr int kPlanes<f16> = 2;
+constexpr int kPlanes = sizeof(T) == 4 ? 2 : 1;
+template <typename T>
+constexpr int kOutPlanes = std::is_same_v<T, bf16> ? 1 : 2;
 
-// 64 rows of an input in LDS, plane after plane, in 16-byte pieces; piece c of
-// row t lies at c ^ t (within the row), so that the same piece of 16 rows
-// covers all banks.
-template <typename T, int DK>
+// 64 rows of an input, plane after plane, in 16-byte pieces; piece c of row t
+// lies at c ^ t (within the row), so that the same piece of 16 rows covers all
+// banks of LDS.
+template <int NX, int DK>
 struct Operand {
-    static constexpr int N = kPlanes<T>, PIECES = DK / 8, PLANE = kC * DK, SIZE = N * PLANE;
+    static constexpr int N = NX, PIECES = DK / 8, PLANE = kC * DK, SIZE = N * PLANE;
     static __device__ __forceinline__ int at(int t, int c) { return t * DK + (c ^ (t & (PIECES - 1))) * 8; }
     // the rows 16 tile + i, terms 32 s + 8 g ..
-    static __device__ __forceinline__ Planes<N> row(const bf16* m, int tile, int s) {
+    static __device__ __forceinline__ Planes<N> row(const f16* m, int tile, int s) {
         const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
         Planes<N> x;
 #pragma unroll
-        for (int k = 0; k < N; ++k) x.p[k] = *(const bf16x8*)(m + k * PLANE + at(16 * tile + n, 4 * s + g));
+        for (int k = 0; k < N; ++k) x.p[k] = *(const f16x8*)(m + k * PLANE + at(16 * tile + n, 4 * s + g));
         return x;
     }
     // the transposed rows: dimensions 32 s + 8 (i / 4) + 4 h + i % 4, terms the steps 4g + r of tiles 2p and 2p + 1
-    static __device__ __forceinline__ Planes<N> column(const bf16* m, int s, int h, int p) {
+    static __device__ __forceinline__ Planes<N> column(const f16* m, int s, int h, int p) {
         const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
         typedef short i16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) i16x4* Lds;
@@ -399,8 +438,8 @@ struct Operand {
             const int t = 32 * p + 4 * g + n / 4;
             const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(t, 4 * s + (n & 3)) + 4 * h));
             const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(t + 16, 4 * s + (n & 3)) + 4 * h));
-            const bf16x4 lo = __builtin_bit_cast(bf16x4, a), hi = __builtin_bit_cast(bf16x4, b);
-            x.p[k] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            const f16x4 lo = __builtin_bit_cast(f16x4, a), hi = __builtin_bit_cast(f16x4, b);
+            x.p[k] = f16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
         return x;
     }
@@ -421,107 +460,90 @@ __device__ __forceinline__ T here(T x) {
     return x;
 }
 
-// A thread's share of the rows on their way from memory to LDS, 8 elements at a
-// time, at any alignment, without branches: a row at or behind `rows` is read
-// as the last one of them (its beta of 0 and its place behind all others keep
-// it out of every result that is stored), elements past `dim` are 0.
-template <typename T, int DK, int THREADS>
-struct Fetch {
-    static constexpr int JOBS = kC * DK / 8 / THREADS, PIECES = DK / 8;
-    static_assert(THREADS % PIECES == 0, "a thread's pieces lie at one place of their rows");
-    typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-    T8 x[JOBS];
-    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int dim) {
-        const int d = threadIdx.x % PIECES * 8, t = threadIdx.x / PIECES;
-        constexpr int BY = THREADS / PIECES;
-        step = here(step);
-        if (dim == DK && rows >= kC) {
-            const uint32_t off = (uint32_t)(t * (int)step + d) * (uint32_t)sizeof(T);
-#pragma unroll
-            for (int j = 0; j < JOBS; ++j) {
-                x[j] = at_bytes<const T8>(p, off);
-                p += BY * step;
-            }
-            return;
-        }
-        const int last = min(rows, kC) - 1;
-#pragma unroll
-        for (int j = 0; j < JOBS; ++j) {
-            const T* const from = p + min(t + j * BY, last) * step + d;
-            x[j] = T8{};
-            if (d + 8 <= dim) {
-                x[j] = *(const T8*)from;
-            } else if (d < dim) {
-#pragma unroll
-                for (int i = 0; i < 7; ++i) x[j][i] = d + i < dim ? from[min(i, dim - 1 - d)] : (T)0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ void store(bf16* m) const {
-        typedef Operand<T, DK> O;
-#pragma unroll
-        for (int j = 0; j < JOBS; ++j) {
-            const int t = threadIdx.x / PIECES + j * (THREADS / PIECES), c = threadIdx.x % PIECES;
-            Planes<O::N> y;
-            if constexpr (O::N == 1) {
-                y.p[0] = __builtin_bit_cast(bf16x8, x[j]);
-            } else {
-                float f[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) f[i] = (float)x[j][i];
-                y = split<O::N>(f);
-            }
-#pragma unroll
-            for (int k = 0; k < O::N; ++k) *(bf16x8*)(m + k * O::PLANE + O::at(t, c)) = y.p[k];
-        }
-    }
+// What the chunks' kernels share, made once, in the form in which they take it.
+// Of a chunk and key head: the planes of keys and queries, rows scaled.
+template <int NX, int DK>
+struct Keys {
+    f16 K[NX * kC * DK], Q[NX * kC * DK];
 };
-
-// What the chunks' kernels share of a chunk and head, made once: the left
-// operands M and P in the order in which lanes take them (the pairs of tiles
-// (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), three planes of M, and of P two where
-// its product with U is rounded to bfloat16's 8 bits), then per step gamma, e, beta
-// and, in its place 0, gamma of the whole chunk.
+// Of a chunk and head: left operands in the order in which lanes take them (the
+// pairs of tiles (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), or (0,0) (0,1) (1,0)
+// (1,1) (2,1) (3,1) of transposed ones), and per step, with the scales of the
+// keys' and queries' rows in them, gamma of K S, scale gamma of Q S, e of K^T U,
+// and beta.
 constexpr int kPairs = 6;
-template <int NP>  // planes of P
-struct Record {
-    static constexpr int N = NP;
-    bf16 M[kPairs * 3 * 512];
-    bf16 P[kPairs * NP * 512];
-    float gamma[kC], end[kC], beta[kC], whole[kC];
+constexpr int kPair = 512;  // elements of a pair's plane
+template <int NP>
+struct Forward {
+    f16 M[kPairs * 2 * kPair];
+    f16 P[kPairs * NP * kPair];
+    float gamma[kC], query[kC], end[kC], beta[kC];
+    float misc[kC];  // 0: gamma of the chunk, 1 and 2: the inverse scales of M and P
 };
 template <typename T>
-using RecordOf = Record<kPlanes<T> == 1 ? 2 : 3>;
-static_assert(sizeof(Record<2>) % 16 == 0 && sizeof(Record<3>) % 16 == 0, "records are copied in 16-byte pieces");
+using ForwardOf = Forward<kOutPlanes<T>>;
 
 __device__ __forceinline__ constexpr int pair_row(int f) { return f < 2 ? f : f < 4 ? 2 : 3; }
 __device__ __forceinline__ constexpr int pair_col(int f) { return f == 3 || f == 5; }
 
 constexpr int kPrepThreads = 256;
 
-// Records of a chunk for all heads of a key head: K K^T and Q K^T once, then
-// per head the decays, M by forward substitution in the diagonal tiles and
-// M21 = -M22 A21 M11 for pairs of tiles and of pairs, in float32.
+// Records of a chunk for all heads of a key head: the rows of keys and queries
+// (0 at padding), K K^T and Q K^T, then per head the decays, and M by forward
+// substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
+// and of pairs, in float32.
 template <typename T, int DK>
-__global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int chunks, RecordOf<T>* to) {
-    typedef Operand<T, DK> O;
-    __shared__ bf16 K[O::SIZE];
-    __shared__ bf16 Q[O::SIZE];
+__global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
+                                                                ForwardOf<T>* to) {
+    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>;
+    typedef Operand<NX, DK> O;
+    __shared__ Keys<NX, DK> kq;
     __shared__ float M[kC * kPitch];
     __shared__ float P[kC * kPitch];
+    __shared__ float k_back[kC], q_back[kC], most[2][4];
     __shared__ Chunk s;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
-    const int len = length_of(d, b), t0 = c * kC, group = d.heads / d.key_heads;
-    if (t0 >= len) return;
+    const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
+    if (rows <= 0) return;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    {
-        Fetch<T, DK, kPrepThreads> k, q;
-        k.load((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, len - t0, d.key_dim);
-        q.load((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, len - t0, d.key_dim);
-        k.store(K);
-        q.store(Q);
-    }
+    auto stage = [&](const T* p, int64_t step, f16* m, f16* out, float* back) {
+        typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+        constexpr int PIECES = O::PIECES, BY = kPrepThreads / PIECES, JOBS = kC / BY;
+        const int at = threadIdx.x % PIECES, dim = at * 8;
+        T8 x[JOBS];
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int t = threadIdx.x / PIECES + j * BY;
+            const T* const from = p + min(t, rows - 1) * step + dim;
+            x[j] = T8{};
+            if (dim + 8 <= d.key_dim) {
+                x[j] = *(const T8*)from;
+            } else if (dim < d.key_dim) {
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (dim + i < d.key_dim) x[j][i] = from[i];
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < JOBS; ++j) {
+            const int t = threadIdx.x / PIECES + j * BY;
+            f32x4 v[2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i / 4][i % 4] = t < rows ? (float)x[j][i] : 0.0f;
+            const Scale scale(over_lanes<PIECES>(largest(v)));
+            const Planes<NX> y = split<NX>(v[0], v[1], scale.by);
+#pragma unroll
+            for (int k = 0; k < NX; ++k) {
+                *(f16x8*)(m + k * O::PLANE + O::at(t, at)) = y.p[k];
+                *(f16x8*)(out + k * O::PLANE + O::at(t, at)) = y.p[k];
+            }
+            if (at == 0) back[t] = scale.back;
+        }
+    };
+    Keys<NX, DK>* const key = keys + ((int64_t)b * chunks + c) * d.key_heads + kh;
+    stage((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, kq.K, key->K, k_back);
+    stage((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, kq.Q, key->Q, q_back);
     for (int e = threadIdx.x; e < 512; e += kPrepThreads) {  // the tiles over the diagonal that pairs take along
         const int i = (e >> 4 & 15) + (e >> 8) * 32, j = (e & 15) + (e >> 8) * 32 + 16;
         M[i * kPitch + j] = P[i * kPitch + j] = 0.0f;
@@ -533,19 +555,19 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
     for (int j = 0; j < 4; ++j) kk[j] = qk[j] = zero;
 #pragma unroll
     for (int x = 0; x < DK / 32; ++x) {
-        const Planes<O::N> left[2] = {O::row(K, w, x), O::row(Q, w, x)};
+        const Planes<NX> left[2] = {O::row(kq.K, w, x), O::row(kq.Q, w, x)};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j <= w) {
                 f32x4 t[2] = {kk[j], qk[j]};
-                products<2>(left, O::row(K, j, x), t);
+                products(left, O::row(kq.K, j, x), t);
                 kk[j] = t[0];
                 qk[j] = t[1];
             }
     }
     for (int hh = 0; hh < group; ++hh) {
         const int h = kh * group + hh;
-        RecordOf<T>* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
+        ForwardOf<T>* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
         if (hh) __syncthreads();
         if (w == 0) load_gates(a, b, h, t0, len, s);
         __syncthreads();
@@ -555,9 +577,9 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = 16 * w + 4 * g + r, col = 16 * j + n;
-                    const float D = row >= col ? decay(s, row, col) : 0.0f;
-                    M[row * kPitch + col] = row > col ? s.beta[row] * D * kk[j][r] : 0.0f;
-                    P[row * kPitch + col] = d.scale * D * qk[j][r];
+                    const float D = row >= col ? decay(s, row, col) * k_back[col] : 0.0f;
+                    M[row * kPitch + col] = row > col ? s.beta[row] * k_back[row] * D * kk[j][r] : 0.0f;
+                    P[row * kPitch + col] = d.scale * q_back[row] * D * qk[j][r];
                 }
         __syncthreads();
         {
@@ -604,46 +626,80 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
             put(3, w, y3);
         }
         __syncthreads();
-        for (int e = threadIdx.x; e < kPairs * 64; e += kPrepThreads) {
-            const int f = e >> 6, at = (16 * pair_row(f) + n) * kPitch + 32 * pair_col(f) + 4 * g;
-            const Planes<3> m = split<3>(*(const f32x4*)(M + at), *(const f32x4*)(M + at + 16));
-            const Planes<RecordOf<T>::N> p = split<RecordOf<T>::N>(*(const f32x4*)(P + at), *(const f32x4*)(P + at + 16));
-#pragma unroll
-            for (int k = 0; k < 3; ++k) *(bf16x8*)(out->M + (f * 3 + k) * 512 + lane * 8) = m.p[k];
-#pragma unroll
-            for (int k = 0; k < RecordOf<T>::N; ++k) *(bf16x8*)(out->P + (f * RecordOf<T>::N + k) * 512 + lane * 8) = p.p[k];
+        f32x4 m[4], p[4];  // this thread's operands: pair w of all, pair 4 + w of the first two waves
+        auto take = [&](int f, f32x4* to, const float* from) {
+            const int at = (16 * pair_row(f) + n) * kPitch + 32 * pair_col(f) + 4 * g;
+            to[0] = *(const f32x4*)(from + at);
+            to[1] = *(const f32x4*)(from + at + 16);
+        };
+        take(w, m, M);
+        take(w, p, P);
+        if (w < 2) {
+            take(4 + w, m + 2, M);
+            take(4 + w, p + 2, P);
+        } else {
+            m[2] = m[3] = p[2] = p[3] = zero;
         }
-        if (w == 1) {
-            out->gamma[lane] = s.gamma[lane];
-            out->end[lane] = s.end[lane];
+        const float mm = over_column(over_lanes<16>(largest(m))), pm = over_column(over_lanes<16>(largest(p)));
+        if (lane == 0) {
+            most[0][w] = mm;
+            most[1][w] = pm;
+        }
+        __syncthreads();
+        const Scale ms(fmaxf(fmaxf(most[0][0], most[0][1]), fmaxf(most[0][2], most[0][3])));
+        const Scale ps(fmaxf(fmaxf(most[1][0], most[1][1]), fmaxf(most[1][2], most[1][3])));
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+            if (f == 0 || w < 2) {
+                const Planes<2> x = split<2>(m[2 * f], m[2 * f + 1], ms.by);
+                const Planes<NP> y = split<NP>(p[2 * f], p[2 * f + 1], ps.by);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) *(f16x8*)(out->M + ((4 * f + w) * 2 + k) * kPair + lane * 8) = x.p[k];
+#pragma unroll
+                for (int k = 0; k < NP; ++k) *(f16x8*)(out->P + ((4 * f + w) * NP + k) * kPair + lane * 8) = y.p[k];
+            }
+        if (w == 2) {
+            out->gamma[lane] = s.gamma[lane] * k_back[lane];
+            out->query[lane] = d.scale * s.gamma[lane] * q_back[lane];
+            out->end[lane] = s.end[lane] * k_back[lane];
             out->beta[lane] = s.beta[lane];
-            out->whole[lane] = s.whole;
+            out->misc[lane] = lane == 0 ? s.whole : lane == 1 ? ms.back : ps.back;
         }
     }
 }
 
-// A record on its way from memory to LDS; the threads that have none of the last pieces copy the last one too.
-template <typename Record, int THREADS>
-struct FetchRecord {
-    static constexpr int PIECES = sizeof(Record) / 16, JOBS = (PIECES + THREADS - 1) / THREADS;
+// 16-byte pieces on their way from memory to LDS; the threads that have none of the last ones copy the last one too.
+template <int BYTES, int THREADS>
+struct Copy {
+    static_assert(BYTES % 16 == 0, "whole pieces");
+    static constexpr int PIECES = BYTES / 16, JOBS = (PIECES + THREADS - 1) / THREADS;
     f32x4 x[JOBS];
-    __device__ __forceinline__ void load(const Record* p) {
+    __device__ __forceinline__ void load(const void* p) {
 #pragma unroll
         for (int j = 0; j < JOBS; ++j)
-            x[j] = at_bytes<const f32x4>(p, (uint32_t)min((int)threadIdx.x + j * THREADS, PIECES - 1) * 16u);
+            x[j] = at_bytes<const f32x4>((const char*)p, (uint32_t)min((int)threadIdx.x + j * THREADS, PIECES - 1) * 16u);
     }
-    __device__ __forceinline__ void store(Record* p) const {
+    __device__ __forceinline__ void store(void* p) const {
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) ((f32x4*)p)[min((int)threadIdx.x + j * THREADS, PIECES - 1)] = x[j];
     }
 };
 
 template <int N>
-__device__ __forceinline__ Planes<N> operand(const bf16* m, int f) {
+__device__ __forceinline__ Planes<N> operand(const f16* m, int f) {
     Planes<N> x;
 #pragma unroll
-    for (int k = 0; k < N; ++k) x.p[k] = *(const bf16x8*)(m + (f * N + k) * 512 + (threadIdx.x & 63) * 8);
+    for (int k = 0; k < N; ++k) x.p[k] = *(const f16x8*)(m + (f * N + k) * kPair + (threadIdx.x & 63) * 8);
     return x;
+}
+
+// c += A B over the steps, A a lower triangular matrix of a record, B two columns' planes.
+template <int NA, int NB>
+__device__ __forceinline__ void lower(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4]) {
+    const Planes<NA> A[4] = {operand<NA>(m, 0), operand<NA>(m, 1), operand<NA>(m, 2), operand<NA>(m, 4)};
+    products(A, B[0], c);
+    const Planes<NA> C[2] = {operand<NA>(m, 3), operand<NA>(m, 5)};
+    products(C, B[1], c + 2);
 }
 
 // The dimension of the keys that row 4g + r of tile t of a state's column stands for.
@@ -664,7 +720,7 @@ struct Column {
             }
     }
     // p: a matrix with rows of `pitch`
-    __device__ __forceinline__ void store(float* p, int col, int pitch, const gs_delta_rule& d) const {
+    __device__ __forceinline__ void store(float* p, int col, int pitch, const gs_delta_rule& d, float scale) const {
         const int g = threadIdx.x >> 4 & 3;
         pitch = here(pitch);
         if (d.key_dim == 16 * KT) {
@@ -673,7 +729,7 @@ struct Column {
             for (int k = 0; k < KT; ++k)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    at_bytes<float>(p, first) = t[k][r];
+                    at_bytes<float>(p, first) = t[k][r] * scale;
                     p += (k & 1) && r == 3 ? 25 * pitch : pitch;
                 }
         } else {
@@ -682,7 +738,7 @@ struct Column {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int row = key_row(k, g, r);
-                    if (row < d.key_dim) p[row * pitch + col] = t[k][r];
+                    if (row < d.key_dim) p[row * pitch + col] = t[k][r] * scale;
                 }
         }
     }
@@ -704,7 +760,10 @@ struct Values {
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = p[min(16 * (e / 4) + 4 * g + e % 4, rows - 1) * step + col];
+            for (int e = 0; e < 16; ++e) {
+                const int i = 16 * (e / 4) + 4 * g + e % 4;
+                x[e] = i < rows ? p[i * step + col] : (T)0.0f;
+            }
         }
     }
     // rows from `rows` on are 0, those from `all` on are not there
@@ -728,10 +787,6 @@ struct Values {
     }
 };
 
-// The states, chunk after chunk, 16 columns of the values a wave: S and what
-// follows from it (R, U) never leave its registers, each product's result is
-// the next one's right operand. What the waves share is fetched a chunk ahead.
-//
 // Where there are few sequences and heads, a sequence is cut into segments that
 // run side by side. A segment takes a state S to Phi S + B, so a first pass
 // without outputs (OUT false) gives B (from a state of 0) and Phi (as columns
@@ -744,50 +799,71 @@ struct Segments {
     float* phi;         // [b][h][segment][key_dim][key_dim]
 };
 
-template <typename T, int DK, int WAVES, bool OUT>
-__global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const RecordOf<T>* records, Segments seg) {
-    typedef RecordOf<T> Record;
-    constexpr int NP = Record::N, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
-    typedef Operand<T, DK> O;
-    __shared__ bf16 K[O::SIZE];
-    __shared__ bf16 Q[OUT ? O::SIZE : 8];
+constexpr int kWaves = 4;  // of a workgroup of the chains
+
+// The states, chunk after chunk, CT times 16 columns of the values a wave: S and
+// what follows from it (R, U) never leave its registers, each product's result
+// is the next one's right operand. What the waves share is fetched a chunk
+// ahead. The columns of S are held scaled to at most about 1, S = unit * S.t.
+template <typename T, int DK, int CT, bool OUT>
+__global__ __launch_bounds__(64 * kWaves, CT == 1 ? 2 : 1) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
+                                                               const ForwardOf<T>* records, Segments seg) {
+    typedef ForwardOf<T> Record;
+    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * kWaves;
+    typedef Operand<NX, DK> O;
+    constexpr int KEYS = OUT ? sizeof(Keys<NX, DK>) : sizeof(Keys<NX, DK>) / 2;  // without outputs no queries
+    __shared__ alignas(16) char kq[KEYS];
     __shared__ Record rec;
+    const f16* const K = (const f16*)kq;
+    const f16* const Q = K + O::SIZE;
     const gs_delta_rule& d = a.r;
     const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
     // behind the values' columns, in workgroups of their own, those of Phi
-    const int blocks = (d.value_dim + 16 * WAVES - 1) / (16 * WAVES);
+    constexpr int WIDE = 16 * CT * kWaves;
+    const int blocks = (d.value_dim + WIDE - 1) / WIDE;
     const bool values = OUT || (int)blockIdx.y < blocks;
-    const int col = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16 + n;
-    const bool on = col < (values ? d.value_dim : d.key_dim);
+    const int wide = values ? d.value_dim : d.key_dim;
+    int col[CT];
+    bool on[CT];
+#pragma unroll
+    for (int x = 0; x < CT; ++x) {
+        col[x] = ((values ? blockIdx.y : blockIdx.y - blocks) * kWaves + w) * 16 * CT + 16 * x + n;
+        on[x] = col[x] < wide;
+    }
     const int len = length_of(d, b), z = blockIdx.z;
     const int c0 = z * seg.chunks, c1 = min((len + kC - 1) / kC, c0 + seg.chunks);
     const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
-    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
-    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
     const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head;
     const int64_t o_step = (int64_t)d.heads * d.value_dim;
     T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
     const Record* const first = records + (int64_t)b * chunks * d.heads + h;
-    Column<KT> S;
-    if constexpr (OUT) {
-        const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
-        S.load(from ? from + col : nullptr, on, d);
-    } else {
+    const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
+    Column<KT> S[CT];
+    float unit[CT];
 #pragma unroll
-        for (int t = 0; t < KT; ++t)
+    for (int x = 0; x < CT; ++x) {
+        unit[x] = 1.0f;
+        if constexpr (OUT) {
+            const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
+            S[x].load(from ? from + col[x] : nullptr, on[x], d);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S.t[t][r] = !values && key_row(t, g, r) == col ? 1.0f : 0.0f;
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[x].t[t][r] = !values && key_row(t, g, r) == col[x] ? 1.0f : 0.0f;
+        }
     }
-    Fetch<T, DK, kThreads> fk, fq;
-    FetchRecord<Record, kThreads> fr;
-    Values<T> fv;
+    Copy<KEYS, kThreads> fk;
+    Copy<sizeof(Record), kThreads> fr;
+    Values<T> fv[CT];
     auto fetch = [&](int c) {
-        const int t0 = c * kC, rows = len - t0;
+        const int t0 = c * kC;
         fr.load(first + (int64_t)c * d.heads);
-        fk.load(k + t0 * d.k_step, d.k_step, rows, d.key_dim);
-        if constexpr (OUT) fq.load(q + t0 * d.q_step, d.q_step, rows, d.key_dim);
-        if (values) fv.load(v + t0 * d.v_step, d.v_step, rows, min(col, d.value_dim - 1));
+        fk.load(first_keys + (int64_t)c * d.key_heads);
+        if (values)
+#pragma unroll
+            for (int x = 0; x < CT; ++x) fv[x].load(v + t0 * d.v_step, d.v_step, len - t0, min(col[x], d.value_dim - 1));
     };
     if (c0 < c1) fetch(c0);
     const f32x4 zero = {0, 0, 0, 0};
@@ -795,150 +871,171 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         const int t0 = c * kC;
         __syncthreads();
         fr.store(&rec);
-        fk.store(K);
-        if constexpr (OUT) fq.store(Q);
+        fk.store(kq);
         __syncthreads();
-        f32x4 x[4], y[4];  // K S and Q S
+        f32x4 R[CT][4], y[CT][4];  // K S, then R; Q S
+        float big[CT];
 #pragma unroll
-        for (int ti = 0; ti < 4; ++ti) x[ti] = y[ti] = zero;
+        for (int x = 0; x < CT; ++x) {
+            big[x] = over_column(largest(S[x].t));
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) R[x][ti] = y[x][ti] = zero;
+        }
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            const Planes<3> sp = split<3>(S.t[2 * s], S.t[2 * s + 1]);
-            Planes<O::N> A[4];
+            Planes<2> sp[CT];
+#pragma unroll
+            for (int x = 0; x < CT; ++x) sp[x] = split<2>(S[x].t[2 * s], S[x].t[2 * s + 1], Scale(big[x]).by);
+            Planes<NX> A[4];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s);
-            products<2>(A, sp, x);
+#pragma unroll
+            for (int x = 0; x < CT; ++x) products(A, sp[x], R[x]);
             if constexpr (OUT) {
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
-                products<NP - 1>(A, sp, y);
+#pragma unroll
+                for (int x = 0; x < CT; ++x) {
+                    if constexpr (NP == 2) {
+                        products(A, sp[x], y[x]);
+                    } else {
+                        const Planes<1> high = {{sp[x].p[0]}};
+                        products(A, high, y[x]);
+                    }
+                }
             }
         }
 #pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
+        for (int x = 0; x < CT; ++x) {
+            const float back = unit[x] * Scale(big[x]).back;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                x[ti][r] = beta[r] * fmaf(-gamma[r], x[ti][r], values ? (float)fv.x[4 * ti + r] : 0.0f);
-                if constexpr (OUT) y[ti][r] *= d.scale * gamma[r];
+            for (int ti = 0; ti < 4; ++ti) {
+                const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
+                f32x4 query;
+                if constexpr (OUT) query = *(const f32x4*)(rec.query + 16 * ti + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    R[x][ti][r] = beta[r] * fmaf(-gamma[r] * back, R[x][ti][r], values ? (float)fv[x].x[4 * ti + r] : 0.0f);
+                    if constexpr (OUT) y[x][ti][r] *= query[r] * back;
+                }
             }
         }
         if (c + 1 < c1) fetch(c + 1);
-        f32x4 U[4];
+        const float whole = rec.misc[0];
 #pragma unroll
-        for (int ti = 0; ti < 4; ++ti) U[ti] = zero;
-        {
-            const Planes<3> R0 = split<3>(x[0], x[1]);
-            const Planes<3> A[4] = {operand<3>(rec.M, 0), operand<3>(rec.M, 1), operand<3>(rec.M, 2), operand<3>(rec.M, 4)};
-            products<2>(A, R0, U);
-            const Planes<3> R1 = split<3>(x[2], x[3]);
-            const Planes<3> B[2] = {operand<3>(rec.M, 3), operand<3>(rec.M, 5)};
-            products<2>(B, R1, U + 2);
+        for (int x = 0; x < CT; ++x) {
+            f32x4 U[4] = {zero, zero, zero, zero};
+            {
+                const Scale rs(over_column(largest(R[x])));
+                const Planes<2> B[2] = {split<2>(R[x][0], R[x][1], rs.by), split<2>(R[x][2], R[x][3], rs.by)};
+                lower<2>(rec.M, B, U);
+                const float back = rs.back * rec.misc[1];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
+            }
+            if constexpr (OUT) {
+                const Scale us(over_column(largest(U)));
+                const Planes<NP> B[2] = {split<NP>(U[0], U[1], us.by), split<NP>(U[2], U[3], us.by)};
+                f32x4 pu[4] = {zero, zero, zero, zero};
+                lower<NP>(rec.P, B, pu);
+                const float back = us.back * rec.misc[2];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) pu[ti][r] = fmaf(pu[ti][r], back, y[x][ti][r]);
+                if (on[x]) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col[x], pu);
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
+            const Scale es(fmaxf(over_column(largest(U)), big[x] * whole * unit[x]));
+            const float keep = whole * unit[x] * es.by;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) S[x].t[t] *= keep;
+            unit[x] = es.back;
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) R[x][ti] = U[ti] * es.by;
         }
-        if constexpr (OUT) {
-            const Planes<NP> U0 = split<NP>(U[0], U[1]);
-            const Planes<NP> A[4] = {operand<NP>(rec.P, 0), operand<NP>(rec.P, 1), operand<NP>(rec.P, 2), operand<NP>(rec.P, 4)};
-            products<NP - 1>(A, U0, y);
-            const Planes<NP> U1 = split<NP>(U[2], U[3]);
-            const Planes<NP> B[2] = {operand<NP>(rec.P, 3), operand<NP>(rec.P, 5)};
-            products<NP - 1>(B, U1, y + 2);
-            if (on) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col, y);
-        }
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
-        const float whole = rec.whole[0];
-#pragma unroll
-        for (int t = 0; t < KT; ++t) S.t[t] *= whole;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const Planes<3> up = split<3>(U[2 * p], U[2 * p + 1]);
+            Planes<2> up[CT];
+#pragma unroll
+            for (int x = 0; x < CT; ++x) up[x] = split<2>(R[x][2 * p], R[x][2 * p + 1], 1.0f);
 #pragma unroll
             for (int s = 0; s < KS; s += 2) {
-                const Planes<O::N> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
-                products<2>(A, up, S.t + 2 * s);
+                const Planes<NX> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
+#pragma unroll
+                for (int x = 0; x < CT; ++x) products(A, up[x], S[x].t + 2 * s);
             }
         }
-        if (OUT && a.ckpt && t0 + kC < len && on)
-            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col, d.value_dim, d);
+        if (OUT && a.ckpt && t0 + kC < len)
+#pragma unroll
+            for (int x = 0; x < CT; ++x)
+                if (on[x])
+                    S[x].store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col[x], d.value_dim, d, unit[x]);
     }
-    if constexpr (OUT) {
-        // the steps of the segment that are padding behind its last chunk
-        const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
-        if (on)
-            for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col] = (T)0.0f;
-        if (a.h_last && on && z + 1 == seg.count) S.store(a.h_last + head * size, col, d.value_dim, d);
-    } else if (on) {
-        if (values)
-            S.store(seg.front + (head * seg.count + z) * size, col, d.value_dim, d);
-        else
-            S.store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col, d.key_dim, d);
+#pragma unroll
+    for (int x = 0; x < CT; ++x) {
+        if (!on[x]) continue;
+        if constexpr (OUT) {
+            // the steps of the segment that are padding behind its last chunk
+            const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
+            for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col[x]] = (T)0.0f;
+            if (a.h_last && z + 1 == seg.count) S[x].store(a.h_last + head * size, col[x], d.value_dim, d, unit[x]);
+        } else if (values) {
+            S[x].store(seg.front + (head * seg.count + z) * size, col[x], d.value_dim, d, unit[x]);
+        } else {
+            S[x].store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col[x], d.key_dim, d, unit[x]);
+        }
     }
 }
 
 // The state in front of every segment, in place of its B: S <- Phi S + B from
-// segment to segment, 16 columns a wave.
-constexpr int kJoinWaves = 8;
-
+// segment to segment (from the last to the first with BACK, with the transposed
+// Phi), 16 columns a workgroup and 16 rows a wave, on the float32 matrix
+// instructions. Bound by the latency of a step: Phi is fetched two ahead.
 template <int DK>
-__global__ __launch_bounds__(64 * kJoinWaves) void k_delta_join(DeltaArgs a, Segments seg) {
-    constexpr int KT = DK / 16, KS = DK / 32, kThreads = 64 * kJoinWaves;
-    typedef Operand<float, DK> O;
-    __shared__ bf16 F[DK / kC][O::SIZE];
+__global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg) {
+    constexpr int KT = DK / 16, PITCH = DK + 4;
+    __shared__ float L[2][16 * PITCH];  // S by columns
     const gs_delta_rule& d = a.r;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col = w * 16 + n;
+    const int col = blockIdx.y * 16 + n, row = 16 * w + 4 * g, left = 16 * w + n;
     const bool on = col < d.value_dim;
     const int64_t head = blockIdx.x, size = (int64_t)d.key_dim * d.value_dim;
-    Column<KT> S, B;
-    S.load(a.h0 ? a.h0 + head * size + col : nullptr, on, d);
-    Fetch<float, DK, kThreads> f[DK / kC];
-    float* front = seg.front + head * seg.count * size;
-    const float* phi = seg.phi + head * seg.count * d.key_dim * d.key_dim;
-    // rows past the dimensions are copies of the last one here, and their results are not stored
-    auto fetch = [&] {
+    float* const front = seg.front + head * seg.count * size;
+    const float* const phi = seg.phi + head * seg.count * d.key_dim * d.key_dim;
+    f32x4 A[2][KT], B[2], S;
+    auto fetch = [&](int z, int at) {
 #pragma unroll
-        for (int i = 0; i < DK / kC; ++i)
-            f[i].load(phi + (int64_t)min(i * kC, d.key_dim - 1) * d.key_dim, d.key_dim, max(d.key_dim - i * kC, 1), d.key_dim);
-        B.load(front + col, on, d);
-    };
-    fetch();
-    for (int z = 0; z < seg.count; ++z) {
-        __syncthreads();
+        for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
-        for (int i = 0; i < DK / kC; ++i) f[i].store(F[i]);
-        __syncthreads();
-        if (on) S.store(front, col, d.value_dim, d);
-        if (z + 1 == seg.count) break;
-        Column<KT> N = B;
-        front += size;
-        phi += d.key_dim * d.key_dim;
-        if (z + 2 < seg.count) fetch();
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const Planes<3> sp = split<3>(S.t[2 * s], S.t[2 * s + 1]);
-#pragma unroll
-            for (int t = 0; t < KT; t += 4) {
-                Planes<3> A[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // row n of result tile t + i stands for this dimension
-                    const int row = key_row(t + i, n >> 2, n & 3);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        A[i].p[k] = *(const bf16x8*)(F[row / kC] + k * O::PLANE + O::at(row % kC, 4 * s + g));
-                }
-                products<2>(A, sp, N.t + t);
+            for (int r = 0; r < 4; ++r) {
+                const int k = 16 * kt + 4 * g + r;
+                const bool in = left < d.key_dim && k < d.key_dim;
+                A[at][kt][r] = in ? phi[((int64_t)z * d.key_dim + left) * d.key_dim + k] : 0.0f;
             }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) B[at][r] = on && row + r < d.key_dim ? front[z * size + (row + r) * d.value_dim + col] : 0.0f;
+    };
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        S[r] = a.h0 && on && row + r < d.key_dim ? a.h0[head * size + (row + r) * d.value_dim + col] : 0.0f;
+    fetch(0, 0);
+    for (int z = 0; z < seg.count; z += 2)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            if (z + x >= seg.count) break;
+            if (z + x + 1 < seg.count) fetch(z + x + 1, x ^ 1);
+            *(f32x4*)(L[x] + n * PITCH + row) = S;
+            __syncthreads();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (on && row + r < d.key_dim) front[(z + x) * size + (row + r) * d.value_dim + col] = S[r];
+            f32x4 acc[2] = {B[x], {0, 0, 0, 0}};
+#pragma unroll
+            for (int kt = 0; kt < KT; ++kt) acc[kt & 1] = mma(A[x][kt], *(const f32x4*)(L[x] + n * PITCH + 16 * kt + 4 * g), acc[kt & 1]);
+            S = acc[0] + acc[1];
         }
-        S = N;
-        // rows past the dimensions stay 0
-        if (d.key_dim < DK)
-#pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (key_row(t, g, r) >= d.key_dim) S.t[t][r] = 0.0f;
-    }
 }
 
 constexpr int kGradWaves = 8;
@@ -1401,8 +1498,13 @@ hipError_t steps(const DeltaArgs& a, hipStream_t stream) {
 int chunks_of(const gs_delta_rule& r) { return (r.steps + kC - 1) / kC; }
 size_t inverse_floats(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * kLower; }
 
+int padded(int dim) { return dim <= 64 ? 64 : 128; }
+size_t key_bytes(const gs_delta_rule& r) {
+    const size_t row = (size_t)2 * kC * padded(r.key_dim) * sizeof(f16) * (r.dtype == GS_F32 ? 2 : 1);
+    return (size_t)r.batch * chunks_of(r) * r.key_heads * row;
+}
 size_t record_bytes(const gs_delta_rule& r) {
-    return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Record<2>) : sizeof(Record<3>));
+    return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Forward<1>) : sizeof(Forward<2>));
 }
 
 // Segments of a sequence: enough workgroups for the chip, each of them long
@@ -1423,21 +1525,22 @@ size_t segment_bytes(const gs_delta_rule& r) {
     return s.count == 1 ? 0 : (size_t)r.batch * r.heads * s.count * r.key_dim * (r.value_dim + r.key_dim) * sizeof(float);
 }
 
-template <typename T, int DK, int WAVES>
+template <typename T, int DK, int CT>
 hipError_t chain(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
-    const int chunks = chunks_of(r), wide = 16 * WAVES, heads = r.batch * r.heads;
-    const RecordOf<T>* const records = (const RecordOf<T>*)scratch;
+    const int chunks = chunks_of(r), wide = 16 * CT * kWaves, heads = r.batch * r.heads;
+    const auto* const keys = (const Keys<kPlanes<T>, DK>*)scratch;
+    const auto* const records = (const ForwardOf<T>*)((char*)scratch + key_bytes(r));
     const int blocks = (r.value_dim + wide - 1) / wide;
     Segments seg = segments_of(r);
     if (seg.count > 1) {
-        seg.front = (float*)((char*)scratch + record_bytes(r));
+        seg.front = (float*)((char*)records + record_bytes(r));
         seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
-        k_delta_chain<T, DK, WAVES, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * WAVES, 0, stream>>>(
-            a, chunks, records, seg);
-        k_delta_join<DK><<<heads, 64 * kJoinWaves, 0, stream>>>(a, seg);
+        k_delta_chain<T, DK, CT, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * kWaves, 0, stream>>>(
+            a, chunks, keys, records, seg);
+        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg);
     }
-    k_delta_chain<T, DK, WAVES, true><<<dim3(heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(a, chunks, records, seg);
+    k_delta_chain<T, DK, CT, true><<<dim3(heads, blocks, seg.count), 64 * kWaves, 0, stream>>>(a, chunks, keys, records, seg);
     return hipGetLastError();
 }
 
@@ -1445,8 +1548,11 @@ template <typename T, int DK>
 hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const int chunks = chunks_of(r);
-    k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, (RecordOf<T>*)scratch);
-    return r.value_dim > 64 ? chain<T, DK, 8>(a, scratch, stream) : chain<T, DK, 4>(a, scratch, stream);
+    k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(
+        a, chunks, (Keys<kPlanes<T>, DK>*)scratch, (ForwardOf<T>*)((char*)scratch + key_bytes(r)));
+    // two columns a lane where that leaves a workgroup for every compute unit
+    const int64_t groups = (int64_t)r.batch * r.heads * segments_of(r).count;
+    return r.value_dim > 64 && groups >= kUnits * 100 ? chain<T, DK, 2>(a, scratch, stream) : chain<T, DK, 1>(a, scratch, stream);
 }
 
 template <typename T, int DK>
@@ -1482,7 +1588,7 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
-    if (!backward) return record_bytes(r) + segment_bytes(r);
+    if (!backward) return key_bytes(r) + record_bytes(r) + segment_bytes(r);
     size_t floats = inverse_floats(r);
     floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
     return floats * sizeof(float);

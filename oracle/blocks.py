@@ -14,12 +14,21 @@ may be off by 16 such deviations; the rounding to a 16-bit type adds half a
 unit in its last place, at least half its smallest subnormal. A norm's sums are
 longer (16384 terms), but each thread adds at most 16 of them one by one and
 the rest as a tree, so the same bound holds for them.
+
+The bfloat16 outputs of the delta rule are sums of products whose factors are
+rounded to float16's 11 bits: the state in front of a chunk of 64 steps, the
+chunk's u, and the factors of u. A rounding is off by at most float16's unit
+roundoff 2^-11 of the factor, 2^-11 / sqrt(3) in the root mean square; two
+factors of a term make 2^-11 sqrt(2 / 3) of it, and a sum of such terms is off
+by as much of the root of the sum of their squares. LOST is 6 times that;
+delta_rule gives those roots ("terms") when asked.
 """
 from __future__ import annotations
 
 import numpy as np
 
 TOL = 2.0 ** -18
+LOST = 6 * 2.0 ** -11 * (2 / 3) ** 0.5
 # unit roundoff and half of the smallest subnormal
 TYPES = {"f32": (2.0 ** -24, 2.0 ** -150), "bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}
 
@@ -41,7 +50,8 @@ def off(got, want, dtype="f32", sums=1.0, size=0.0, lost=0.0):
     return max(worst, np.sqrt(np.mean(err * err)) / (TOL * sums * rms + 1e-300))
 
 
-def delta_rule(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, restart=None, grad_o=None, grad_last=None):
+def delta_rule(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, restart=None, grad_o=None, grad_last=None,
+               terms=False):
     """gs_delta_rule_fwd, and gs_delta_rule_bwd when grad_o is given, step by step. Returns a dict."""
     B, T, Hk, dk = q.shape
     H, dv = v.shape[2:]
@@ -69,6 +79,17 @@ def delta_rule(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, rest
         states.append(S)
         o[:, t] = np.einsum("bhkv,bhk->bhv", S, q[:, t])
     out = dict(o=o, h_last=S)
+    if terms:
+        size = np.zeros_like(o)
+        for t in range(T):
+            c = t - t % 64
+            a = np.concatenate([np.cumprod(alpha[:, t:c:-1], 1)[:, ::-1], np.ones((B, 1, H))], 1)  # behind j, j = c .. t
+            front = alpha[:, c] * a[:, 0]
+            size[:, t] = np.einsum("bhkv,bhk->bhv", before[c] ** 2, q[:, t] ** 2) * front[..., None] ** 2
+            p = a * np.einsum("bjhk,bhk->bjh", k[:, c:t + 1], q[:, t])
+            u = beta[:, c:t + 1, :, None] * np.stack(errs[c:t + 1], 1)
+            size[:, t] += np.einsum("bjh,bjhv->bhv", p ** 2, u ** 2)
+        out["terms"] = np.sqrt(size)
     if grad_o is None:
         return out
     go = np.where(live[:, :, None, None], grad_o, 0.0).astype(np.float64)
