@@ -203,112 +203,6 @@ __device__ __forceinline__ void chunk_p(const float* Q, const float* K, const Ch
     }
 }
 
-constexpr int kChainWaves = 4;
-
-// The gradients of the states, from the last chunk to the first, 16 columns a
-// wave; behind[b][chunk][h] receives the one behind each chunk.
-template <typename T, int DK>
-__global__ __launch_bounds__(64 * kChainWaves) void k_delta_bwd(DeltaArgs a, int chunks, const float* inverse, float* behind) {
-    constexpr int KT = DK / 16, kThreads = 64 * kChainWaves;
-    __shared__ float K[kC * (DK + 4)];
-    __shared__ float Q[kC * (DK + 4)];
-    __shared__ float P[kC * kPitch];
-    __shared__ Chunk s;
-    const gs_delta_rule& d = a.r;
-    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.y * kChainWaves + w) * 16 + n;
-    const bool on = col < d.value_dim;
-    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
-    const int64_t head = (int64_t)b * d.heads + h, state = head * d.key_dim * d.value_dim + col;
-    const T* const q = (const T*)a.q + b * d.q_batch + kh * d.q_head;
-    const T* const k = (const T*)a.k + b * d.k_batch + kh * d.k_head;
-    const int64_t o_step = (int64_t)d.heads * d.value_dim;
-    const int64_t first = ((int64_t)b * d.steps * d.heads + h) * d.value_dim + col;
-    const T* const go = (const T*)a.grad_o + first;
-    T* const gv = (T*)a.grad_v + first;
-    f32x4 S[KT];
-#pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int row = 16 * kt + 4 * g + r;
-            S[kt][r] = a.grad_last && on && row < d.key_dim ? a.grad_last[state + (int64_t)row * d.value_dim] : 0.0f;
-        }
-    for (int t = mine * kC + g; t < d.steps; t += 4)
-        if (on) gv[t * o_step] = (T)0.0f;
-    for (int c = mine - 1; c >= 0; --c) {
-        const int t0 = c * kC, rows = len - t0;
-        float* const to = behind + (((int64_t)b * chunks + c) * d.heads + h) * d.key_dim * d.value_dim + col;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * kt + 4 * g + r;
-                if (on && row < d.key_dim) to[(int64_t)row * d.value_dim] = S[kt][r];
-            }
-        __syncthreads();
-        load_rows<DK>(k + t0 * d.k_step, d.k_step, rows, d.key_dim, K, kThreads);
-        load_rows<DK>(q + t0 * d.q_step, d.q_step, rows, d.key_dim, Q, kThreads);
-        if (w == 0) load_gates(a, b, h, t0, len, s);
-        __syncthreads();
-        chunk_p<DK>(Q, K, s, d.scale, P, kChainWaves);
-        f32x4 dO[4], dU[4], dR[4];
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int kt = 0; kt < KT; ++kt) acc = mma(row4<DK>(K, 16 * ti + n, 16 * kt + 4 * g), S[kt], acc);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * ti + 4 * g + r;
-                dO[ti][r] = on && i < rows ? (float)go[(t0 + i) * o_step] : 0.0f;
-                dU[ti][r] = s.end[i] * acc[r];
-            }
-        }
-        __syncthreads();
-        const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower + 64 * g + n;
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-            for (int tj = ti; tj < 4; ++tj) dU[ti] = mma(col4(P, kPitch, 16 * tj + 4 * g, 16 * ti + n), dO[tj], dU[ti]);
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti) {
-            dR[ti] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int tj = ti; tj < 4; ++tj) dR[ti] = mma(col4(M + tri(tj, ti) * 256, 16, 0, 0), dU[tj], dR[ti]);
-        }
-#pragma unroll
-        for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int i = 16 * ti + 4 * g + r, t = t0 + i;
-                const float x = s.beta[i] * dR[ti][r];
-                if (on && t < d.steps) gv[t * o_step] = (T)x;
-                dR[ti][r] = -s.gamma[i] * x;
-                dO[ti][r] *= d.scale * s.gamma[i];
-            }
-        const float whole = s.whole;
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt) {
-            S[kt] *= whole;
-#pragma unroll
-            for (int tj = 0; tj < 4; ++tj) {
-                S[kt] = mma(col4(Q, DK + 4, 16 * tj + 4 * g, 16 * kt + n), dO[tj], S[kt]);
-                S[kt] = mma(col4(K, DK + 4, 16 * tj + 4 * g, 16 * kt + n), dR[tj], S[kt]);
-            }
-        }
-    }
-    if (a.grad_h0)
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * kt + 4 * g + r;
-                if (on && row < d.key_dim) a.grad_h0[state + (int64_t)row * d.value_dim] = S[kt][r];
-            }
-}
-
 // ---------------------------------------------------------------------------
 // Float32 values on the 16-bit matrix instructions. Scaled by a power of two to
 // at most 1, a value is the sum of two float16 ones (planes), the rounding of
@@ -475,6 +369,7 @@ constexpr int kPairs = 6;
 constexpr int kPair = 512;  // elements of a pair's plane
 template <int NP>
 struct Forward {
+    static constexpr int N = NP;
     f16 M[kPairs * 2 * kPair];
     f16 P[kPairs * NP * kPair];
     float gamma[kC], query[kC], end[kC], beta[kC];
@@ -482,9 +377,18 @@ struct Forward {
 };
 template <typename T>
 using ForwardOf = Forward<kOutPlanes<T>>;
+// Of the backward's: M, and M and P transposed, and per step gamma, e, beta and
+// the inverse scales of the keys' and queries' rows.
+struct Backward {
+    f16 M[kPairs * 2 * kPair], MT[kPairs * 2 * kPair], PT[kPairs * 2 * kPair];
+    float gamma[kC], end[kC], beta[kC], k_back[kC], q_back[kC];
+    float misc[kC];  // as Forward's
+};
 
 __device__ __forceinline__ constexpr int pair_row(int f) { return f < 2 ? f : f < 4 ? 2 : 3; }
 __device__ __forceinline__ constexpr int pair_col(int f) { return f == 3 || f == 5; }
+__device__ __forceinline__ constexpr int upper_row(int f) { return f < 2 ? 0 : f < 4 ? 1 : f - 2; }
+__device__ __forceinline__ constexpr int upper_col(int f) { return f == 1 || f >= 3; }
 
 constexpr int kPrepThreads = 256;
 
@@ -492,10 +396,11 @@ constexpr int kPrepThreads = 256;
 // (0 at padding), K K^T and Q K^T, then per head the decays, and M by forward
 // substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
 // and of pairs, in float32.
-template <typename T, int DK>
+template <typename T, int DK, typename Record>
 __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
-                                                                ForwardOf<T>* to) {
-    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>;
+                                                                Record* to) {
+    constexpr bool BACK = std::is_same_v<Record, Backward>;
+    constexpr int NX = kPlanes<T>;
     typedef Operand<NX, DK> O;
     __shared__ Keys<NX, DK> kq;
     __shared__ float M[kC * kPitch];
@@ -567,7 +472,7 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
     }
     for (int hh = 0; hh < group; ++hh) {
         const int h = kh * group + hh;
-        ForwardOf<T>* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
+        Record* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
         if (hh) __syncthreads();
         if (w == 0) load_gates(a, b, h, t0, len, s);
         __syncthreads();
@@ -651,17 +556,34 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
 #pragma unroll
         for (int f = 0; f < 2; ++f)
             if (f == 0 || w < 2) {
-                const Planes<2> x = split<2>(m[2 * f], m[2 * f + 1], ms.by);
-                const Planes<NP> y = split<NP>(p[2 * f], p[2 * f + 1], ps.by);
+                const int pair = 4 * f + w;
+                auto put_planes = [&](f16* to, const auto& x, int planes) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k) *(f16x8*)(out->M + ((4 * f + w) * 2 + k) * kPair + lane * 8) = x.p[k];
-#pragma unroll
-                for (int k = 0; k < NP; ++k) *(f16x8*)(out->P + ((4 * f + w) * NP + k) * kPair + lane * 8) = y.p[k];
+                    for (int k = 0; k < planes; ++k) *(f16x8*)(to + (pair * planes + k) * kPair + lane * 8) = x.p[k];
+                };
+                put_planes(out->M, split<2>(m[2 * f], m[2 * f + 1], ms.by), 2);
+                if constexpr (BACK) {
+                    auto transposed = [&](const float* from, float scale) {
+                        const int row = 32 * upper_col(pair) + 4 * g, col = 16 * upper_row(pair) + n;
+                        return split<2>(col4(from, kPitch, row, col), col4(from, kPitch, row + 16, col), scale);
+                    };
+                    put_planes(out->MT, transposed(M, ms.by), 2);
+                    put_planes(out->PT, transposed(P, ps.by), 2);
+                } else {
+                    put_planes(out->P, split<Record::N>(p[2 * f], p[2 * f + 1], ps.by), Record::N);
+                }
             }
         if (w == 2) {
-            out->gamma[lane] = s.gamma[lane] * k_back[lane];
-            out->query[lane] = d.scale * s.gamma[lane] * q_back[lane];
-            out->end[lane] = s.end[lane] * k_back[lane];
+            if constexpr (BACK) {
+                out->gamma[lane] = s.gamma[lane];
+                out->end[lane] = s.end[lane];
+                out->k_back[lane] = k_back[lane];
+                out->q_back[lane] = q_back[lane];
+            } else {
+                out->gamma[lane] = s.gamma[lane] * k_back[lane];
+                out->query[lane] = d.scale * s.gamma[lane] * q_back[lane];
+                out->end[lane] = s.end[lane] * k_back[lane];
+            }
             out->beta[lane] = s.beta[lane];
             out->misc[lane] = lane == 0 ? s.whole : lane == 1 ? ms.back : ps.back;
         }
@@ -700,6 +622,15 @@ __device__ __forceinline__ void lower(const f16* m, const Planes<NB> (&B)[2], f3
     products(A, B[0], c);
     const Planes<NA> C[2] = {operand<NA>(m, 3), operand<NA>(m, 5)};
     products(C, B[1], c + 2);
+}
+
+// The same of an upper triangular one.
+template <int NA, int NB>
+__device__ __forceinline__ void upper(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4]) {
+    const Planes<NA> A[2] = {operand<NA>(m, 0), operand<NA>(m, 2)};
+    products(A, B[0], c);
+    const Planes<NA> C[4] = {operand<NA>(m, 1), operand<NA>(m, 3), operand<NA>(m, 4), operand<NA>(m, 5)};
+    products(C, B[1], c);
 }
 
 // The dimension of the keys that row 4g + r of tile t of a state's column stands for.
@@ -799,17 +730,15 @@ struct Segments {
     float* phi;         // [b][h][segment][key_dim][key_dim]
 };
 
-constexpr int kWaves = 4;  // of a workgroup of the chains
-
-// The states, chunk after chunk, CT times 16 columns of the values a wave: S and
+// The states, chunk after chunk, 16 columns of the values a wave: S and
 // what follows from it (R, U) never leave its registers, each product's result
 // is the next one's right operand. What the waves share is fetched a chunk
 // ahead. The columns of S are held scaled to at most about 1, S = unit * S.t.
-template <typename T, int DK, int CT, bool OUT>
-__global__ __launch_bounds__(64 * kWaves, CT == 1 ? 2 : 1) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
+template <typename T, int DK, int WAVES, bool OUT>
+__global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
                                                                const ForwardOf<T>* records, Segments seg) {
     typedef ForwardOf<T> Record;
-    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * kWaves;
+    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
     typedef Operand<NX, DK> O;
     constexpr int KEYS = OUT ? sizeof(Keys<NX, DK>) : sizeof(Keys<NX, DK>) / 2;  // without outputs no queries
     __shared__ alignas(16) char kq[KEYS];
@@ -820,17 +749,10 @@ __global__ __launch_bounds__(64 * kWaves, CT == 1 ? 2 : 1) void k_delta_chain(De
     const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
     // behind the values' columns, in workgroups of their own, those of Phi
-    constexpr int WIDE = 16 * CT * kWaves;
-    const int blocks = (d.value_dim + WIDE - 1) / WIDE;
+    const int blocks = (d.value_dim + 16 * WAVES - 1) / (16 * WAVES);
     const bool values = OUT || (int)blockIdx.y < blocks;
-    const int wide = values ? d.value_dim : d.key_dim;
-    int col[CT];
-    bool on[CT];
-#pragma unroll
-    for (int x = 0; x < CT; ++x) {
-        col[x] = ((values ? blockIdx.y : blockIdx.y - blocks) * kWaves + w) * 16 * CT + 16 * x + n;
-        on[x] = col[x] < wide;
-    }
+    const int col = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16 + n;
+    const bool on = col < (values ? d.value_dim : d.key_dim);
     const int len = length_of(d, b), z = blockIdx.z;
     const int c0 = z * seg.chunks, c1 = min((len + kC - 1) / kC, c0 + seg.chunks);
     const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
@@ -839,31 +761,25 @@ __global__ __launch_bounds__(64 * kWaves, CT == 1 ? 2 : 1) void k_delta_chain(De
     T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
     const Record* const first = records + (int64_t)b * chunks * d.heads + h;
     const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
-    Column<KT> S[CT];
-    float unit[CT];
+    Column<KT> S;
+    float unit = 1.0f;
+    if constexpr (OUT) {
+        const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
+        S.load(from ? from + col : nullptr, on, d);
+    } else {
 #pragma unroll
-    for (int x = 0; x < CT; ++x) {
-        unit[x] = 1.0f;
-        if constexpr (OUT) {
-            const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
-            S[x].load(from ? from + col[x] : nullptr, on[x], d);
-        } else {
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-            for (int t = 0; t < KT; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) S[x].t[t][r] = !values && key_row(t, g, r) == col[x] ? 1.0f : 0.0f;
-        }
+            for (int r = 0; r < 4; ++r) S.t[t][r] = !values && key_row(t, g, r) == col ? 1.0f : 0.0f;
     }
     Copy<KEYS, kThreads> fk;
     Copy<sizeof(Record), kThreads> fr;
-    Values<T> fv[CT];
+    Values<T> fv;
     auto fetch = [&](int c) {
         const int t0 = c * kC;
         fr.load(first + (int64_t)c * d.heads);
         fk.load(first_keys + (int64_t)c * d.key_heads);
-        if (values)
-#pragma unroll
-            for (int x = 0; x < CT; ++x) fv[x].load(v + t0 * d.v_step, d.v_step, len - t0, min(col[x], d.value_dim - 1));
+        if (values) fv.load(v + t0 * d.v_step, d.v_step, len - t0, min(col, d.value_dim - 1));
     };
     if (c0 < c1) fetch(c0);
     const f32x4 zero = {0, 0, 0, 0};
@@ -873,119 +789,90 @@ __global__ __launch_bounds__(64 * kWaves, CT == 1 ? 2 : 1) void k_delta_chain(De
         fr.store(&rec);
         fk.store(kq);
         __syncthreads();
-        f32x4 R[CT][4], y[CT][4];  // K S, then R; Q S
-        float big[CT];
-#pragma unroll
-        for (int x = 0; x < CT; ++x) {
-            big[x] = over_column(largest(S[x].t));
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) R[x][ti] = y[x][ti] = zero;
-        }
+        f32x4 R[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};  // K S, then R; Q S, then O
+        const Scale big(over_column(largest(S.t)));
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-            Planes<2> sp[CT];
-#pragma unroll
-            for (int x = 0; x < CT; ++x) sp[x] = split<2>(S[x].t[2 * s], S[x].t[2 * s + 1], Scale(big[x]).by);
+            const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], big.by);
             Planes<NX> A[4];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s);
-#pragma unroll
-            for (int x = 0; x < CT; ++x) products(A, sp[x], R[x]);
+            products(A, sp, R);
             if constexpr (OUT) {
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
+                Planes<NP> high;
 #pragma unroll
-                for (int x = 0; x < CT; ++x) {
-                    if constexpr (NP == 2) {
-                        products(A, sp[x], y[x]);
-                    } else {
-                        const Planes<1> high = {{sp[x].p[0]}};
-                        products(A, high, y[x]);
-                    }
-                }
+                for (int k = 0; k < NP; ++k) high.p[k] = sp.p[k];
+                products(A, high, y);
             }
         }
+        const float from = unit * big.back;
 #pragma unroll
-        for (int x = 0; x < CT; ++x) {
-            const float back = unit[x] * Scale(big[x]).back;
+        for (int ti = 0; ti < 4; ++ti) {
+            const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) {
-                const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
-                f32x4 query;
-                if constexpr (OUT) query = *(const f32x4*)(rec.query + 16 * ti + 4 * g);
+            for (int r = 0; r < 4; ++r)
+                R[ti][r] = beta[r] * fmaf(-gamma[r] * from, R[ti][r], values ? (float)fv.x[4 * ti + r] : 0.0f);
+            if constexpr (OUT) {
+                const f32x4 query = *(const f32x4*)(rec.query + 16 * ti + 4 * g);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    R[x][ti][r] = beta[r] * fmaf(-gamma[r] * back, R[x][ti][r], values ? (float)fv[x].x[4 * ti + r] : 0.0f);
-                    if constexpr (OUT) y[x][ti][r] *= query[r] * back;
-                }
+                for (int r = 0; r < 4; ++r) y[ti][r] *= query[r] * from;
             }
         }
         if (c + 1 < c1) fetch(c + 1);
-        const float whole = rec.misc[0];
+        f32x4 U[4] = {zero, zero, zero, zero};
+        {
+            const Scale rs(over_column(largest(R)));
+            const Planes<2> B[2] = {split<2>(R[0], R[1], rs.by), split<2>(R[2], R[3], rs.by)};
+            lower<2>(rec.M, B, U);
+            const float back = rs.back * rec.misc[1];
 #pragma unroll
-        for (int x = 0; x < CT; ++x) {
-            f32x4 U[4] = {zero, zero, zero, zero};
-            {
-                const Scale rs(over_column(largest(R[x])));
-                const Planes<2> B[2] = {split<2>(R[x][0], R[x][1], rs.by), split<2>(R[x][2], R[x][3], rs.by)};
-                lower<2>(rec.M, B, U);
-                const float back = rs.back * rec.misc[1];
+            for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
+        }
+        if constexpr (OUT) {
+            const Scale us(over_column(largest(U)));
+            const Planes<NP> B[2] = {split<NP>(U[0], U[1], us.by), split<NP>(U[2], U[3], us.by)};
+            f32x4 x[4] = {zero, zero, zero, zero};
+            lower<NP>(rec.P, B, x);
+            const float back = us.back * rec.misc[2];
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
-            }
-            if constexpr (OUT) {
-                const Scale us(over_column(largest(U)));
-                const Planes<NP> B[2] = {split<NP>(U[0], U[1], us.by), split<NP>(U[2], U[3], us.by)};
-                f32x4 pu[4] = {zero, zero, zero, zero};
-                lower<NP>(rec.P, B, pu);
-                const float back = us.back * rec.misc[2];
+            for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) pu[ti][r] = fmaf(pu[ti][r], back, y[x][ti][r]);
-                if (on[x]) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col[x], pu);
-            }
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
-            const Scale es(fmaxf(over_column(largest(U)), big[x] * whole * unit[x]));
-            const float keep = whole * unit[x] * es.by;
-#pragma unroll
-            for (int t = 0; t < KT; ++t) S[x].t[t] *= keep;
-            unit[x] = es.back;
-#pragma unroll
-            for (int ti = 0; ti < 4; ++ti) R[x][ti] = U[ti] * es.by;
+                for (int r = 0; r < 4; ++r) y[ti][r] = fmaf(x[ti][r], back, y[ti][r]);
+            if (on) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col, y);
         }
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            Planes<2> up[CT];
+        for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
+        // one scale for what is kept of S and what is added
+        const float whole = rec.misc[0] * unit;
+        const Scale es(fmaxf(over_column(largest(U)), whole * big.back));
+        const float keep = whole * es.by;
 #pragma unroll
-            for (int x = 0; x < CT; ++x) up[x] = split<2>(R[x][2 * p], R[x][2 * p + 1], 1.0f);
+        for (int t = 0; t < KT; ++t) S.t[t] *= keep;
+        unit = es.back;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const Planes<2> up = split<2>(U[2 * p], U[2 * p + 1], es.by);
 #pragma unroll
             for (int s = 0; s < KS; s += 2) {
                 const Planes<NX> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
-#pragma unroll
-                for (int x = 0; x < CT; ++x) products(A, up[x], S[x].t + 2 * s);
+                products(A, up, S.t + 2 * s);
             }
         }
-        if (OUT && a.ckpt && t0 + kC < len)
-#pragma unroll
-            for (int x = 0; x < CT; ++x)
-                if (on[x])
-                    S[x].store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col[x], d.value_dim, d, unit[x]);
+        if (OUT && a.ckpt && t0 + kC < len && on)
+            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col, d.value_dim, d, unit);
     }
-#pragma unroll
-    for (int x = 0; x < CT; ++x) {
-        if (!on[x]) continue;
-        if constexpr (OUT) {
-            // the steps of the segment that are padding behind its last chunk
-            const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
-            for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col[x]] = (T)0.0f;
-            if (a.h_last && z + 1 == seg.count) S[x].store(a.h_last + head * size, col[x], d.value_dim, d, unit[x]);
-        } else if (values) {
-            S[x].store(seg.front + (head * seg.count + z) * size, col[x], d.value_dim, d, unit[x]);
-        } else {
-            S[x].store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col[x], d.key_dim, d, unit[x]);
-        }
+    if (!on) return;
+    if constexpr (OUT) {
+        // the steps of the segment that are padding behind its last chunk
+        const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
+        for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col] = (T)0.0f;
+        if (a.h_last && z + 1 == seg.count) S.store(a.h_last + head * size, col, d.value_dim, d, unit);
+    } else if (values) {
+        S.store(seg.front + (head * seg.count + z) * size, col, d.value_dim, d, unit);
+    } else {
+        S.store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col, d.key_dim, d, unit);
     }
 }
 
@@ -1036,6 +923,120 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
             for (int kt = 0; kt < KT; ++kt) acc[kt & 1] = mma(A[x][kt], *(const f32x4*)(L[x] + n * PITCH + 16 * kt + 4 * g), acc[kt & 1]);
             S = acc[0] + acc[1];
         }
+}
+
+// The gradients of the states, from the last chunk to the first, 16 columns a
+// wave, held and scaled as the states of k_delta_chain; behind[b][chunk][h]
+// receives the one behind each chunk.
+template <typename T, int DK, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
+                                                               const Backward* records, float* behind) {
+    constexpr int NX = kPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
+    typedef Operand<NX, DK> O;
+    __shared__ Keys<NX, DK> kq;
+    // of a record: all but M
+    constexpr int SKIP = sizeof(Backward::M);
+    __shared__ alignas(16) char part[sizeof(Backward) - SKIP];
+    const Backward& rec = *(const Backward*)(part - SKIP);
+    const gs_delta_rule& d = a.r;
+    const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int col = (blockIdx.y * WAVES + w) * 16 + n;
+    const bool on = col < d.value_dim;
+    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
+    const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
+    const int64_t o_step = (int64_t)d.heads * d.value_dim, first_o = ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
+    const T* const go = (const T*)a.grad_o + first_o;
+    T* const gv = (T*)a.grad_v + first_o;
+    const Backward* const first = records + (int64_t)b * chunks * d.heads + h;
+    const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
+    Column<KT> S;
+    float unit = 1.0f;
+    S.load(a.grad_last ? a.grad_last + head * size + col : nullptr, on, d);
+    if (on)
+        for (int t = mine * kC + g; t < d.steps; t += 4) gv[t * o_step + col] = (T)0.0f;
+    Copy<sizeof(Keys<NX, DK>), kThreads> fk;
+    Copy<sizeof(Backward) - SKIP, kThreads> fr;
+    Values<T> fo;
+    auto fetch = [&](int c) {
+        const int t0 = c * kC;
+        fr.load((const char*)(first + (int64_t)c * d.heads) + SKIP);
+        fk.load(first_keys + (int64_t)c * d.key_heads);
+        fo.load(go + t0 * o_step, o_step, len - t0, min(col, d.value_dim - 1));
+    };
+    if (mine > 0) fetch(mine - 1);
+    const f32x4 zero = {0, 0, 0, 0};
+    for (int c = mine - 1; c >= 0; --c) {
+        const int t0 = c * kC;
+        if (on) S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, col, d.value_dim, d, unit);
+        __syncthreads();
+        fr.store(part);
+        fk.store(&kq);
+        f32x4 dO[4];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dO[e / 4][e % 4] = (float)fo.x[e];
+        __syncthreads();
+        if (c > 0) fetch(c - 1);
+        const Scale big(over_column(largest(S.t)));
+        f32x4 dU[4] = {zero, zero, zero, zero}, x[4] = {zero, zero, zero, zero};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], big.by);
+            Planes<NX> A[4];
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s);
+            products(A, sp, dU);
+        }
+        {
+            const Scale os(over_column(largest(dO)));
+            const Planes<NX> B[2] = {split<NX>(dO[0], dO[1], os.by), split<NX>(dO[2], dO[3], os.by)};
+            upper<2>(rec.PT, B, x);
+            const float back = os.back * rec.misc[2], from = unit * big.back;
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                const f32x4 end = *(const f32x4*)(rec.end + 16 * ti + 4 * g), kb = *(const f32x4*)(rec.k_back + 16 * ti + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dU[ti][r] = fmaf(end[r] * kb[r] * from, dU[ti][r], back * x[ti][r]);
+            }
+        }
+        f32x4 dR[4] = {zero, zero, zero, zero};
+        {
+            const Scale us(over_column(largest(dU)));
+            const Planes<2> B[2] = {split<2>(dU[0], dU[1], us.by), split<2>(dU[2], dU[3], us.by)};
+            upper<2>(rec.MT, B, dR);
+            const float back = us.back * rec.misc[1];
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                const f32x4 beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g), gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g);
+                const f32x4 kb = *(const f32x4*)(rec.k_back + 16 * ti + 4 * g), qb = *(const f32x4*)(rec.q_back + 16 * ti + 4 * g);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    x[ti][r] = beta[r] * back * dR[ti][r];  // dV
+                    dR[ti][r] = -gamma[r] * kb[r] * x[ti][r];
+                    dO[ti][r] *= d.scale * gamma[r] * qb[r];
+                }
+            }
+        }
+        if (on) Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, col, x);
+        const float whole = rec.misc[0] * unit;
+        const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
+        const float keep = whole * es.by;
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S.t[t] *= keep;
+        unit = es.back;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const Planes<2> op = split<2>(dO[2 * p], dO[2 * p + 1], es.by), rp = split<2>(dR[2 * p], dR[2 * p + 1], es.by);
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Planes<NX> A[2] = {O::column(kq.Q, s, 0, p), O::column(kq.Q, s, 1, p)};
+                products(A, op, S.t + 2 * s);
+                const Planes<NX> B[2] = {O::column(kq.K, s, 0, p), O::column(kq.K, s, 1, p)};
+                products(B, rp, S.t + 2 * s);
+            }
+        }
+    }
+    if (a.grad_h0 && on) S.store(a.grad_h0 + head * size, col, d.value_dim, d, unit);
 }
 
 constexpr int kGradWaves = 8;
@@ -1503,6 +1504,7 @@ size_t key_bytes(const gs_delta_rule& r) {
     const size_t row = (size_t)2 * kC * padded(r.key_dim) * sizeof(f16) * (r.dtype == GS_F32 ? 2 : 1);
     return (size_t)r.batch * chunks_of(r) * r.key_heads * row;
 }
+size_t back_record_bytes(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * sizeof(Backward); }
 size_t record_bytes(const gs_delta_rule& r) {
     return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Forward<1>) : sizeof(Forward<2>));
 }
@@ -1525,10 +1527,10 @@ size_t segment_bytes(const gs_delta_rule& r) {
     return s.count == 1 ? 0 : (size_t)r.batch * r.heads * s.count * r.key_dim * (r.value_dim + r.key_dim) * sizeof(float);
 }
 
-template <typename T, int DK, int CT>
+template <typename T, int DK, int WAVES>
 hipError_t chain(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
-    const int chunks = chunks_of(r), wide = 16 * CT * kWaves, heads = r.batch * r.heads;
+    const int chunks = chunks_of(r), wide = 16 * WAVES, heads = r.batch * r.heads;
     const auto* const keys = (const Keys<kPlanes<T>, DK>*)scratch;
     const auto* const records = (const ForwardOf<T>*)((char*)scratch + key_bytes(r));
     const int blocks = (r.value_dim + wide - 1) / wide;
@@ -1536,11 +1538,11 @@ hipError_t chain(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     if (seg.count > 1) {
         seg.front = (float*)((char*)records + record_bytes(r));
         seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
-        k_delta_chain<T, DK, CT, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * kWaves, 0, stream>>>(
+        k_delta_chain<T, DK, WAVES, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * WAVES, 0, stream>>>(
             a, chunks, keys, records, seg);
         k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg);
     }
-    k_delta_chain<T, DK, CT, true><<<dim3(heads, blocks, seg.count), 64 * kWaves, 0, stream>>>(a, chunks, keys, records, seg);
+    k_delta_chain<T, DK, WAVES, true><<<dim3(heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(a, chunks, keys, records, seg);
     return hipGetLastError();
 }
 
@@ -1550,27 +1552,32 @@ hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const int chunks = chunks_of(r);
     k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(
         a, chunks, (Keys<kPlanes<T>, DK>*)scratch, (ForwardOf<T>*)((char*)scratch + key_bytes(r)));
-    // two columns a lane where that leaves a workgroup for every compute unit
-    const int64_t groups = (int64_t)r.batch * r.heads * segments_of(r).count;
-    return r.value_dim > 64 && groups >= kUnits * 100 ? chain<T, DK, 2>(a, scratch, stream) : chain<T, DK, 1>(a, scratch, stream);
+    return r.value_dim > 64 ? chain<T, DK, 8>(a, scratch, stream) : chain<T, DK, 4>(a, scratch, stream);
 }
 
 template <typename T, int DK>
-hipError_t backward(const DeltaArgs& a, float* scratch, hipStream_t stream) {
+hipError_t backward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const int chunks = chunks_of(r);
-    float* const behind = scratch + inverse_floats(r);
-    if (chunks) k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, scratch);
-    const int wide = 16 * kChainWaves;
-    k_delta_bwd<T, DK><<<dim3(r.batch * r.heads, (r.value_dim + wide - 1) / wide), 64 * kChainWaves, 0, stream>>>(
-        a, chunks, scratch, behind);
+    auto* const keys = (Keys<kPlanes<T>, DK>*)scratch;
+    auto* const records = (Backward*)((char*)scratch + key_bytes(r));
+    float* const inverse = (float*)((char*)records + back_record_bytes(r));
+    float* const behind = inverse + inverse_floats(r);
+    if (chunks) {
+        k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, keys, records);
+        k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, inverse);
+    }
+    if (r.value_dim > 64)
+        k_delta_back<T, DK, 8><<<r.batch * r.heads, 512, 0, stream>>>(a, chunks, keys, records, behind);
+    else
+        k_delta_back<T, DK, 4><<<r.batch * r.heads, 256, 0, stream>>>(a, chunks, keys, records, behind);
     if (chunks)
-        k_delta_grad<T, DK><<<r.batch * chunks * r.key_heads, 64 * kGradWaves, 0, stream>>>(a, chunks, scratch, behind);
+        k_delta_grad<T, DK><<<r.batch * chunks * r.key_heads, 64 * kGradWaves, 0, stream>>>(a, chunks, inverse, behind);
     return hipGetLastError();
 }
 
 template <typename T>
-hipError_t run(const DeltaArgs& a, float* scratch, bool back, hipStream_t stream) {
+hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream) {
     if (a.r.key_dim <= 64)
         return back ? backward<T, 64>(a, scratch, stream) : forward<T, 64>(a, scratch, stream);
     return back ? backward<T, 128>(a, scratch, stream) : forward<T, 128>(a, scratch, stream);
@@ -1578,9 +1585,9 @@ hipError_t run(const DeltaArgs& a, float* scratch, bool back, hipStream_t stream
 
 hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream) {
     switch (a.r.dtype) {
-        case GS_F32: return run<float>(a, (float*)scratch, back, stream);
-        case GS_BF16: return run<bf16>(a, (float*)scratch, back, stream);
-        default: return run<f16>(a, (float*)scratch, back, stream);
+        case GS_F32: return run<float>(a, scratch, back, stream);
+        case GS_BF16: return run<bf16>(a, scratch, back, stream);
+        default: return run<f16>(a, scratch, back, stream);
     }
 }
 
@@ -1589,9 +1596,8 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
     if (!backward) return key_bytes(r) + record_bytes(r) + segment_bytes(r);
-    size_t floats = inverse_floats(r);
-    floats += (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
-    return floats * sizeof(float);
+    return key_bytes(r) + back_record_bytes(r) +
+           (inverse_floats(r) + (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim) * sizeof(float);
 }
 
 hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
