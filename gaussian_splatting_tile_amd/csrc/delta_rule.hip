@@ -346,13 +346,28 @@ __device__ __forceinline__ V& at_bytes(T* p, uint32_t off) {
     return *(V*)((Byte*)p + off);
 }
 
-// The same value, which the compiler does not know: what is computed of it is
-// computed where it is used, not held in registers through a loop.
-template <typename T>
-__device__ __forceinline__ T here(T x) {
-    asm volatile("" : "+s"(x));
-    return x;
-}
+// A uniform base of `bytes` bytes (below 2^31) and 32-bit offsets: what lies at
+// or behind the end is read as 0 and not written, without a branch.
+constexpr uint32_t kNowhere = 0x80000000u;
+struct Buffer {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ Buffer(const void* p, uint32_t bytes)
+        : r(__builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00020000)) {}
+    template <typename T>
+    __device__ __forceinline__ T load(uint32_t off) const {
+        if constexpr (sizeof(T) == 2)
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+        else
+            return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(uint32_t off, T v) const {
+        if constexpr (sizeof(T) == 2)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), r, off, 0, 0);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+    }
+};
 
 // What the chunks' kernels share, made once, in the form in which they take it.
 // Of a chunk and key head: the planes of keys and queries, rows scaled.
@@ -640,80 +655,59 @@ __device__ __forceinline__ int key_row(int t, int g, int r) { return 32 * (t / 2
 template <int KT>
 struct Column {
     f32x4 t[KT];
-    __device__ __forceinline__ void load(const float* p, bool on, const gs_delta_rule& d) {
-        const int g = threadIdx.x >> 4 & 3;
+    // of a matrix with `rows` rows of `pitch`
+    static __device__ __forceinline__ uint32_t offset(int col, int pitch) {
+        return (uint32_t)(8 * (threadIdx.x >> 4 & 3) * pitch + col) * 4u;
+    }
+    __device__ __forceinline__ void load(const float* p, bool on, int col, int rows, int pitch) {
+        const Buffer m(p, p ? rows * pitch * 4 : 0);
+        const uint32_t off = on ? offset(col, pitch) : kNowhere;
+#pragma unroll
+        for (int k = 0; k < KT; ++k)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) t[k][r] = m.load<float>(off + key_row(k, 0, r) * pitch * 4);
+    }
+    __device__ __forceinline__ void store(float* p, bool on, int col, int rows, int pitch, float scale) const {
+        const Buffer m(p, rows * pitch * 4);
+        uint32_t off = on ? offset(col, pitch) : kNowhere;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = key_row(k, g, r);
-                t[k][r] = p && on && row < d.key_dim ? p[row * d.value_dim] : 0.0f;
+                m.store(off, t[k][r] * scale);
+                off += ((k & 1) && r == 3 ? 25 : 1) * pitch * 4;
             }
-    }
-    // p: a matrix with rows of `pitch`
-    __device__ __forceinline__ void store(float* p, int col, int pitch, const gs_delta_rule& d, float scale) const {
-        const int g = threadIdx.x >> 4 & 3;
-        pitch = here(pitch);
-        if (d.key_dim == 16 * KT) {
-            const uint32_t first = (8 * g * pitch + col) * 4;
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    at_bytes<float>(p, first) = t[k][r] * scale;
-                    p += (k & 1) && r == 3 ? 25 * pitch : pitch;
-                }
-        } else {
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = key_row(k, g, r);
-                    if (row < d.key_dim) p[row * pitch + col] = t[k][r] * scale;
-                }
-        }
     }
 };
 
-// The values of a chunk in a column, as results lie: rows 16 t + 4g + r.
+// The values of a chunk in a column, as results lie: rows 16 t + 4g + r; p at the chunk's first row, rows from `rows`
+// on are 0. (Where rows overlap, step < dim, the rows behind the last one may hold something of it instead, which
+// their beta of 0 keeps out.)
 template <typename T>
 struct Values {
     T x[16];
-    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, int col) {
-        const int g = threadIdx.x >> 4 & 3;
-        step = here(step);
-        if (rows >= kC) {
-            const uint32_t off = (uint32_t)(4 * g * (int)step + col) * (uint32_t)sizeof(T);
+    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, bool on, int col, int dim) {
+        const int by = (int)step * (int)sizeof(T);
+        const Buffer m(p, (min(rows, kC) - 1) * by + dim * (int)sizeof(T));
+        uint32_t off = on ? 4 * (threadIdx.x >> 4 & 3) * by + col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                x[e] = at_bytes<const T>(p, off);
-                p += e % 4 == 3 ? 13 * step : step;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int i = 16 * (e / 4) + 4 * g + e % 4;
-                x[e] = i < rows ? p[i * step + col] : (T)0.0f;
-            }
+        for (int e = 0; e < 16; ++e) {
+            x[e] = m.load<T>(off);
+            off += e % 4 == 3 ? 13 * by : by;
         }
     }
     // rows from `rows` on are 0, those from `all` on are not there
-    static __device__ __forceinline__ void store(T* p, int64_t step, int rows, int all, int col, const f32x4 (&v)[4]) {
-        const int g = threadIdx.x >> 4 & 3;
-        step = here(step);
-        if (rows >= kC) {
-            const uint32_t off = (uint32_t)(4 * g * (int)step + col) * (uint32_t)sizeof(T);
+    static __device__ __forceinline__ void store(T* p, int64_t step, int rows, int all, bool on, int col, int dim, f32x4 (&v)[4]) {
+        const int g = threadIdx.x >> 4 & 3, by = (int)step * (int)sizeof(T);
+        if (rows < kC)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                at_bytes<T>(p, off) = (T)v[e / 4][e % 4];
-                p += e % 4 == 3 ? 13 * step : step;
-            }
-        } else {
+            for (int e = 0; e < 16; ++e) v[e / 4][e % 4] = 16 * (e / 4) + 4 * g + e % 4 < rows ? v[e / 4][e % 4] : 0.0f;
+        const Buffer m(p, (min(all, kC) - 1) * by + dim * (int)sizeof(T));
+        uint32_t off = on ? 4 * g * by + col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int i = 16 * (e / 4) + 4 * g + e % 4;
-                if (i < all) p[i * step + col] = i < rows ? (T)v[e / 4][e % 4] : (T)0.0f;
-            }
+        for (int e = 0; e < 16; ++e) {
+            m.store(off, (T)v[e / 4][e % 4]);
+            off += e % 4 == 3 ? 13 * by : by;
         }
     }
 };
@@ -765,7 +759,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
     float unit = 1.0f;
     if constexpr (OUT) {
         const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size : a.h0 ? a.h0 + head * size : nullptr;
-        S.load(from ? from + col : nullptr, on, d);
+        S.load(from, on, col, d.key_dim, d.value_dim);
     } else {
 #pragma unroll
         for (int t = 0; t < KT; ++t)
@@ -779,7 +773,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         const int t0 = c * kC;
         fr.load(first + (int64_t)c * d.heads);
         fk.load(first_keys + (int64_t)c * d.key_heads);
-        if (values) fv.load(v + t0 * d.v_step, d.v_step, len - t0, min(col, d.value_dim - 1));
+        if (values) fv.load(v + t0 * d.v_step, d.v_step, len - t0, on, col, d.value_dim);
     };
     if (c0 < c1) fetch(c0);
     const f32x4 zero = {0, 0, 0, 0};
@@ -788,7 +782,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         __syncthreads();
         fr.store(&rec);
         fk.store(kq);
+        f32x4 V[4];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) V[e / 4][e % 4] = values ? (float)fv.x[e] : 0.0f;
         __syncthreads();
+        if (c + 1 < c1) fetch(c + 1);
         f32x4 R[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};  // K S, then R; Q S, then O
         const Scale big(over_column(largest(S.t)));
 #pragma unroll
@@ -813,14 +811,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             const f32x4 gamma = *(const f32x4*)(rec.gamma + 16 * ti + 4 * g), beta = *(const f32x4*)(rec.beta + 16 * ti + 4 * g);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                R[ti][r] = beta[r] * fmaf(-gamma[r] * from, R[ti][r], values ? (float)fv.x[4 * ti + r] : 0.0f);
+                R[ti][r] = beta[r] * fmaf(-gamma[r] * from, R[ti][r], V[ti][r]);
             if constexpr (OUT) {
                 const f32x4 query = *(const f32x4*)(rec.query + 16 * ti + 4 * g);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[ti][r] *= query[r] * from;
             }
         }
-        if (c + 1 < c1) fetch(c + 1);
         f32x4 U[4] = {zero, zero, zero, zero};
         {
             const Scale rs(over_column(largest(R)));
@@ -840,7 +837,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[ti][r] = fmaf(x[ti][r], back, y[ti][r]);
-            if (on) Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, col, y);
+            Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, y);
         }
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
@@ -860,19 +857,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
                 products(A, up, S.t + 2 * s);
             }
         }
-        if (OUT && a.ckpt && t0 + kC < len && on)
-            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, col, d.value_dim, d, unit);
+        if (OUT && a.ckpt && t0 + kC < len)
+            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit);
     }
-    if (!on) return;
     if constexpr (OUT) {
         // the steps of the segment that are padding behind its last chunk
         const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
-        for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col] = (T)0.0f;
-        if (a.h_last && z + 1 == seg.count) S.store(a.h_last + head * size, col, d.value_dim, d, unit);
-    } else if (values) {
-        S.store(seg.front + (head * seg.count + z) * size, col, d.value_dim, d, unit);
+        if (on)
+            for (int t = max(c0, c1) * kC + g; t < end; t += 4) o[t * o_step + col] = (T)0.0f;
+        if (a.h_last && z + 1 == seg.count) S.store(a.h_last + head * size, on, col, d.key_dim, d.value_dim, unit);
     } else {
-        S.store(seg.phi + (head * seg.count + z) * d.key_dim * d.key_dim, col, d.key_dim, d, unit);
+        const int64_t at = head * seg.count + z;
+        S.store(values ? seg.front + at * size : seg.phi + at * d.key_dim * d.key_dim, on, col, d.key_dim,
+                values ? d.value_dim : d.key_dim, unit);
     }
 }
 
@@ -952,7 +949,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
     const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
     Column<KT> S;
     float unit = 1.0f;
-    S.load(a.grad_last ? a.grad_last + head * size + col : nullptr, on, d);
+    S.load(a.grad_last ? a.grad_last + head * size : nullptr, on, col, d.key_dim, d.value_dim);
     if (on)
         for (int t = mine * kC + g; t < d.steps; t += 4) gv[t * o_step + col] = (T)0.0f;
     Copy<sizeof(Keys<NX, DK>), kThreads> fk;
@@ -962,13 +959,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         const int t0 = c * kC;
         fr.load((const char*)(first + (int64_t)c * d.heads) + SKIP);
         fk.load(first_keys + (int64_t)c * d.key_heads);
-        fo.load(go + t0 * o_step, o_step, len - t0, min(col, d.value_dim - 1));
+        fo.load(go + t0 * o_step, o_step, len - t0, on, col, d.value_dim);
     };
     if (mine > 0) fetch(mine - 1);
     const f32x4 zero = {0, 0, 0, 0};
     for (int c = mine - 1; c >= 0; --c) {
         const int t0 = c * kC;
-        if (on) S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, col, d.value_dim, d, unit);
+        S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit);
         __syncthreads();
         fr.store(part);
         fk.store(&kq);
@@ -1017,7 +1014,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
                 }
             }
         }
-        if (on) Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, col, x);
+        Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x);
         const float whole = rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
         const float keep = whole * es.by;
@@ -1036,7 +1033,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             }
         }
     }
-    if (a.grad_h0 && on) S.store(a.grad_h0 + head * size, col, d.value_dim, d, unit);
+    if (a.grad_h0) S.store(a.grad_h0 + head * size, on, col, d.key_dim, d.value_dim, unit);
 }
 
 constexpr int kGradWaves = 8;
