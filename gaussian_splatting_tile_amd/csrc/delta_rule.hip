@@ -1348,6 +1348,488 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             }
 }
 
+// 16-bit matrices by columns: rows of 64 (steps), 16-byte pieces swizzled by the
+// row, PLANE elements from plane to plane. Results of products are written in
+// groups of four steps; read as operands with lanes along the steps (turned) or
+// along the rows.
+template <int ROWS>
+struct Turned {
+    static constexpr int PLANE = ROWS * kC;
+    static __device__ __forceinline__ int at(int row, int piece) { return row * kC + (piece ^ (row & 7)) * 8; }
+    // steps 16 tile + 4g .. of a row
+    static __device__ __forceinline__ void write(f16* m, int row, int tile, f32x4 v, float scale) {
+        const int g = threadIdx.x >> 4 & 3;
+        f16* const to = m + at(row, 2 * tile + g / 2) + (g & 1) * 4;
+        const f16x2 a = __builtin_convertvector(f32x2{v[0] * scale, v[1] * scale}, f16x2);
+        const f16x2 b = __builtin_convertvector(f32x2{v[2] * scale, v[3] * scale}, f16x2);
+        const f16x2 c = __builtin_convertvector(
+            f32x2{fmaf(v[0], scale, -(float)a[0]), fmaf(v[1], scale, -(float)a[1])}, f16x2);
+        const f16x2 e = __builtin_convertvector(
+            f32x2{fmaf(v[2], scale, -(float)b[0]), fmaf(v[3], scale, -(float)b[1])}, f16x2);
+        *(f16x4*)to = f16x4{a[0], a[1], b[0], b[1]};
+        *(f16x4*)(to + PLANE) = f16x4{c[0], c[1], e[0], e[1]};
+    }
+    // lane i: step 16 tile + i, terms the rows 32 s + 8 g ..
+    static __device__ __forceinline__ Planes<2> turned(const f16* m, int tile, int s) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+        typedef short i16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) i16x4* Lds;
+        Planes<2> x;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int row = 32 * s + 8 * g + n / 4, piece = 2 * tile + (n & 3) / 2, in = (n & 1) * 4;
+            const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(row, piece) + in));
+            const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(m + k * PLANE + at(row + 4, piece) + in));
+            const f16x4 lo = __builtin_bit_cast(f16x4, a), hi = __builtin_bit_cast(f16x4, b);
+            x.p[k] = f16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+        return x;
+    }
+    // lane i: row 16 tile + i, terms the steps 32 p + 8 g ..
+    static __device__ __forceinline__ Planes<2> along(const f16* m, int tile, int p) {
+        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+        Planes<2> x;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) x.p[k] = *(const f16x8*)(m + k * PLANE + at(16 * tile + n, 4 * p + g));
+        return x;
+    }
+};
+
+// Sums over 16 neighbouring lanes, and over the lanes up to each.
+__device__ __forceinline__ float sum_lanes(float x) {
+    auto with = [&](auto ctrl) {
+        x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    with(std::integral_constant<int, 0xB1>{});
+    with(std::integral_constant<int, 0x4E>{});
+    with(std::integral_constant<int, 0x141>{});
+    with(std::integral_constant<int, 0x140>{});
+    return x;
+}
+__device__ __forceinline__ float scan_lanes(float x) {
+    auto with = [&](auto ctrl) {
+        x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+    };
+    with(std::integral_constant<int, 0x111>{});  // row_shr
+    with(std::integral_constant<int, 0x112>{});
+    with(std::integral_constant<int, 0x114>{});
+    with(std::integral_constant<int, 0x118>{});
+    return x;
+}
+__device__ __forceinline__ float sum_column(float m) {
+    auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    m = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    a = __builtin_amdgcn_permlane32_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// k_delta_grad for 16-bit inputs, on float16 planes. A wave takes 16 columns of
+// the values and leaves U and dR in LDS, then tiles of the 64 x 64 matrices and
+// 16 columns of the keys, from rows of S and dS that it reads again.
+template <typename T, int DK>
+__global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, int chunks, const Keys<1, DK>* keys,
+                                                                const Backward* records, const float* behind) {
+    static_assert(sizeof(T) == 2, "one plane of the inputs");
+    constexpr int KT = DK / 16, KS = DK / 32, kThreads = 64 * kGradWaves;
+    typedef Operand<1, DK> O;
+    typedef Operand<1, kV> OV;
+    typedef Turned<kV> TV;
+    typedef Turned<kC> TC;
+    __shared__ Keys<1, DK> kq;
+    __shared__ f16 dOs[OV::SIZE];
+    __shared__ union Shared {
+        f16 ue[2][2 * TV::PLANE];  // U and dR
+        f16 pa[4][2 * TC::PLANE];  // Pd by the keys' scales, by the queries', Ad by the keys' of its columns, of its rows
+    } m;
+    __shared__ Backward rec;
+    __shared__ float o_back[kC], betas[kGradWaves][kC], front[kGradWaves][kC], after[kGradWaves][kC], dots[kGradWaves];
+    __shared__ float most[4][kGradWaves];
+    __shared__ float inside[kTiles][16], across[kTiles][16], tile_beta[kTiles][16];
+    __shared__ Chunk gates;
+    const gs_delta_rule& d = a.r;
+    const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
+    const int all = min(kC, d.steps - t0);  // steps of the chunk, padding included
+    const int64_t first = (((int64_t)b * d.steps + t0) * d.key_heads + kh) * d.key_dim;
+    T* const gq = (T*)a.grad_q + first;
+    T* const gk = (T*)a.grad_k + first;
+    const int64_t k_step = (int64_t)d.key_heads * d.key_dim, o_step = (int64_t)d.heads * d.value_dim;
+    if (rows <= 0) {
+        for (int e = threadIdx.x; e < all * d.key_dim; e += kThreads) {
+            const int64_t at = e / d.key_dim * k_step + e % d.key_dim;
+            gq[at] = gk[at] = (T)0.0f;
+        }
+        for (int e = threadIdx.x; e < all * group; e += kThreads) {
+            const int64_t at = ((int64_t)b * d.steps + t0 + e / group) * d.heads + kh * group + e % group;
+            a.grad_log_decay[at] = a.grad_beta[at] = 0.0f;
+        }
+        return;
+    }
+    const f32x4 zero = {0, 0, 0, 0};
+    f32x4 dq[4] = {zero, zero, zero, zero}, dk[4] = {zero, zero, zero, zero};
+    {
+        Copy<sizeof(kq), kThreads> f;
+        f.load(keys + ((int64_t)b * chunks + c) * d.key_heads + kh);
+        f.store(&kq);
+    }
+    const int vs = (d.value_dim + 31) / 32;  // terms of sums over the values, by 32
+    const int col = 16 * w + n;              // of the values, and the row of a state's transposed columns
+    for (int hh = 0; hh < group; ++hh) {
+        const int h = kh * group + hh;
+        const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
+        const float* const S0 = c == 0 ? (a.h0 ? a.h0 + head * size : nullptr)
+                                       : a.ckpt_in + (((int64_t)b * (chunks - 1) + c - 1) * d.heads + h) * size;
+        const float* const dS = behind + (((int64_t)b * chunks + c) * d.heads + h) * size;
+        const T* const v = (const T*)a.v + b * d.v_batch + t0 * d.v_step + h * d.v_head;
+        const T* const go = (const T*)a.grad_o + (((int64_t)b * d.steps + t0) * d.heads + h) * d.value_dim;
+        Column<KT> S, Z;
+        const bool on = col < d.value_dim;
+        S.load(S0, on, col, d.key_dim, d.value_dim);
+        Z.load(dS, on, col, d.key_dim, d.value_dim);
+        Values<T> fv, fo;
+        fv.load(v, d.v_step, rows, on, col, d.value_dim);
+        fo.load(go, o_step, rows, on, col, d.value_dim);
+        if (hh) __syncthreads();
+        {
+            Copy<sizeof(rec), kThreads> f;
+            f.load(records + ((int64_t)b * chunks + c) * d.heads + h);
+            f.store(&rec);
+        }
+        {  // the rows of dO, scaled
+            typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+            constexpr int PIECES = kV / 8, BY = kThreads / PIECES, JOBS = kC / BY;
+            const int at = threadIdx.x % PIECES, dim = at * 8;
+#pragma unroll
+            for (int j = 0; j < JOBS; ++j) {
+                const int t = threadIdx.x / PIECES + j * BY;
+                T8 x{};
+                if (t < rows) {
+                    const T* const from = go + t * o_step + dim;
+                    if (dim + 8 <= d.value_dim) {
+                        x = *(const T8*)from;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 7; ++i)
+                            if (dim + i < d.value_dim) x[i] = from[i];
+                    }
+                }
+                f32x4 f[2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) f[i / 4][i % 4] = (float)x[i];
+                const Scale scale(over_lanes<PIECES>(largest(f)));
+                *(f16x8*)(dOs + OV::at(t, at)) = split<1>(f[0], f[1], scale.by).p[0];
+                if (at == 0) o_back[t] = scale.back;
+            }
+        }
+        if (w == 0) load_gates(a, b, h, t0, len, gates);
+        __syncthreads();
+        // 16 columns of the values: U and dR
+        f32x4 U[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
+        {
+            float dot = 0.0f;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dot = fmaf(S.t[t][r], Z.t[t][r], dot);
+            dot = sum_column(sum_lanes(dot));
+            if (lane == 0) dots[w] = dot;
+            const Scale ss(over_column(largest(S.t))), zs(over_column(largest(Z.t)));
+            f32x4 x[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero}, e[4];
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], ss.by), zp = split<2>(Z.t[2 * s], Z.t[2 * s + 1], zs.by);
+                Planes<1> A[4];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s);
+                products(A, sp, x);
+                products(A, zp, y);
+            }
+            f32x4 R[4], dO[4], dU[4] = {zero, zero, zero, zero};
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                const int i = 16 * ti + 4 * g;
+                const f32x4 gamma = *(const f32x4*)(rec.gamma + i), beta = *(const f32x4*)(rec.beta + i), kb = *(const f32x4*)(rec.k_back + i);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    e[ti][r] = fmaf(-gamma[r] * kb[r] * ss.back, x[ti][r], (float)fv.x[4 * ti + r]);
+                    R[ti][r] = beta[r] * e[ti][r];
+                    dO[ti][r] = (float)fo.x[4 * ti + r];
+                }
+            }
+            {
+                const Scale rs(over_column(largest(R)));
+                const Planes<2> B[2] = {split<2>(R[0], R[1], rs.by), split<2>(R[2], R[3], rs.by)};
+                lower<2>(rec.M, B, U);
+                const float back = rs.back * rec.misc[1];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
+            }
+            {
+                const Scale os(over_column(largest(dO)));
+                const Planes<1> B[2] = {split<1>(dO[0], dO[1], os.by), split<1>(dO[2], dO[3], os.by)};
+                upper<2>(rec.PT, B, dU);
+                const float back = os.back * rec.misc[2];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    const int i = 16 * ti + 4 * g;
+                    const f32x4 end = *(const f32x4*)(rec.end + i), kb = *(const f32x4*)(rec.k_back + i);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dU[ti][r] = fmaf(end[r] * kb[r] * zs.back, y[ti][r], back * dU[ti][r]);
+                }
+            }
+            {
+                const Scale us(over_column(largest(dU)));
+                const Planes<2> B[2] = {split<2>(dU[0], dU[1], us.by), split<2>(dU[2], dU[3], us.by)};
+                upper<2>(rec.MT, B, E);
+                const float back = us.back * rec.misc[1];
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    E[ti] *= back;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float t = sum_lanes(E[ti][r] * e[ti][r]);
+                        if (n == 0) betas[w][16 * ti + 4 * g + r] = t;
+                    }
+                }
+            }
+            const float um = over_column(over_lanes<16>(largest(U))), em = over_column(over_lanes<16>(largest(E)));
+            if (lane == 0) {
+                most[0][w] = um;
+                most[1][w] = em;
+            }
+        }
+        __syncthreads();
+        auto over_waves = [&](const float* p) {
+            float x = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kGradWaves; ++i) x = fmaxf(x, p[i]);
+            return x;
+        };
+        const Scale us(over_waves(most[0])), es(over_waves(most[1]));
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti) {
+            TV::write(m.ue[0], col, ti, U[ti], us.by);
+            TV::write(m.ue[1], col, ti, E[ti], es.by);
+        }
+        __syncthreads();
+        // 16 columns of the keys: dO S^T, dR S^T, U dS^T
+        f32x4 aq[4] = {zero, zero, zero, zero}, ar[4] = {zero, zero, zero, zero}, au[4] = {zero, zero, zero, zero};
+        float s_back = 0.0f, z_back = 0.0f;
+        if (w < KT) {
+            auto take = [&](const float* p, f32x4 (&x)[8]) {  // row `col` of a state, terms 32 s + 8 g ..
+                const Buffer from(p, p ? (int)size * 4 : 0);
+                const uint32_t off = col < d.key_dim ? (uint32_t)(col * d.value_dim + 8 * g) * 4u : kNowhere;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[2 * s + i / 4][i % 4] = from.load<float>(32 * s + 8 * g + i < d.value_dim ? off + (32 * s + i) * 4 : kNowhere);
+            };
+            f32x4 x[8];
+            take(S0, x);
+            Scale scale(over_column(largest(x)));
+            s_back = scale.back;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s < vs) {
+                    const Planes<2> B = split<2>(x[2 * s], x[2 * s + 1], scale.by);
+                    Planes<1> A[4];
+                    Planes<2> C[4];
+#pragma unroll
+                    for (int ti = 0; ti < 4; ++ti) {
+                        A[ti] = OV::row(dOs, ti, s);
+                        C[ti] = TV::turned(m.ue[1], ti, s);
+                    }
+                    products(A, B, aq);
+                    products(C, B, ar);
+                }
+            take(dS, x);
+            scale = Scale(over_column(largest(x)));
+            z_back = scale.back;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s < vs) {
+                    const Planes<2> B = split<2>(x[2 * s], x[2 * s + 1], scale.by);
+                    Planes<2> C[4];
+#pragma unroll
+                    for (int ti = 0; ti < 4; ++ti) C[ti] = TV::turned(m.ue[0], ti, s);
+                    products(C, B, au);
+                }
+        }
+        // tiles of Pd and Ad, and of what the gates' gradients need of them
+        f32x4 pd[2] = {zero, zero}, ad[2] = {zero, zero};
+        float pm = 0.0f, am = 0.0f;
+#pragma unroll
+        for (int turn = 0; turn < 2; ++turn) {
+            const int q = w + turn * kGradWaves;
+            if (q >= kTiles) continue;
+            const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, tj = q - tri(ti, 0);
+            f32x4 dp = zero, da = zero, qk = zero, kk = zero;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (s < vs) {
+                    const Planes<2> B = TV::turned(m.ue[0], tj, s);
+                    const Planes<1> A[1] = {OV::row(dOs, ti, s)};
+                    const Planes<2> C[1] = {TV::turned(m.ue[1], ti, s)};
+                    products(A, B, &dp);
+                    products(C, B, &da);
+                }
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const Planes<1> B = O::row(kq.K, tj, s);
+                const Planes<1> A[1] = {O::row(kq.Q, ti, s)}, C[1] = {O::row(kq.K, ti, s)};
+                products(A, B, &qk);
+                products(C, B, &kk);
+            }
+            const int j = 16 * tj + n;
+            const float kj = rec.k_back[j];
+            float column = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r;
+                const float D = i >= j ? decay(gates, i, j) : 0.0f;
+                const float p = d.scale * D * us.back * o_back[i] * dp[r], t = i > j ? -D * us.back * es.back * da[r] : 0.0f;
+                const float ki = rec.k_back[i], qi = rec.q_back[i], beta = rec.beta[i];
+                const float tb = t * kk[r] * ki * kj;
+                pd[turn][r] = p;
+                ad[turn][r] = beta * t;
+                pm = fmaxf(pm, fabsf(p) * fmaxf(kj, qi));
+                am = fmaxf(am, fabsf(beta * t) * fmaxf(kj, ki));
+                // sums over the columns up to this one; the decay of step j lies behind them
+                const float x = fmaf(p, qk[r] * qi * kj, beta * tb), up = scan_lanes(x);
+                if (ti > tj || i >= j) column += up - x;
+                if (n == 15) across[q][4 * g + r] = up;
+                const float sum = sum_lanes(tb);
+                if (n == 0) tile_beta[q][4 * g + r] = sum;
+            }
+            column = sum_column(column);
+            if (g == 0) inside[q][n] = column;
+        }
+        pm = over_column(over_lanes<16>(pm));
+        am = over_column(over_lanes<16>(am));
+        if (lane == 0) {
+            most[2][w] = pm;
+            most[3][w] = am;
+        }
+        __syncthreads();
+        const Scale ps(over_waves(most[2])), as(over_waves(most[3]));
+#pragma unroll
+        for (int turn = 0; turn < 2; ++turn) {
+            const int q = w + turn * kGradWaves;
+            if (q >= kTiles) continue;
+            const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, tj = q - tri(ti, 0), row = 16 * tj + n;
+            const float kj = rec.k_back[row];
+            const f32x4 ki = *(const f32x4*)(rec.k_back + 16 * ti + 4 * g), qi = *(const f32x4*)(rec.q_back + 16 * ti + 4 * g);
+            TC::write(m.pa[0], row, ti, pd[turn] * kj, ps.by);
+            TC::write(m.pa[1], row, ti, pd[turn] * qi, ps.by);
+            TC::write(m.pa[2], row, ti, ad[turn] * kj, as.by);
+            TC::write(m.pa[3], row, ti, ad[turn] * ki, as.by);
+        }
+        if (w >= 4)  // the tiles over the diagonal that pairs of tiles take along
+#pragma unroll
+            for (int p = 0; p < 2; ++p) TC::write(m.pa[w - 4], 32 * p + 16 + n, 2 * p, zero, 1.0f);
+        __syncthreads();
+        if (w < KT) {
+            f32x4 xq[4] = {zero, zero, zero, zero}, xp[4] = {zero, zero, zero, zero}, xa[4] = {zero, zero, zero, zero};
+            // a column of the keys' (queries') rows: terms the steps 32 p + 8 g ..
+            auto columns = [&](const f16* from, int p) {
+                typedef short i16x4 __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) i16x4* Lds;
+                const int t = 32 * p + 8 * g + n / 4, piece = 2 * w + (n & 3) / 2, in = (n & 1) * 4;
+                const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(from + O::at(t, piece) + in));
+                const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Lds)(from + O::at(t + 4, piece) + in));
+                const f16x4 lo = __builtin_bit_cast(f16x4, x), hi = __builtin_bit_cast(f16x4, y);
+                return Planes<1>{{f16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}}};
+            };
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const Planes<1> kc = columns(kq.K, p), qc = columns(kq.Q, p);
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti) {
+                    if (p <= ti / 2) {
+                        const Planes<2> A[1] = {TC::turned(m.pa[0], ti, p)}, C[1] = {TC::turned(m.pa[2], ti, p)};
+                        products(A, kc, xq + ti);
+                        products(C, kc, xa + ti);
+                    }
+                    if (p >= ti / 2) {
+                        const Planes<2> A[1] = {TC::along(m.pa[1], ti, p)}, C[1] = {TC::along(m.pa[3], ti, p)};
+                        products(A, qc, xp + ti);
+                        products(C, kc, xa + ti);
+                    }
+                }
+            }
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti) {
+                const int i0 = 16 * ti + 4 * g;
+                const f32x4 gamma = *(const f32x4*)(rec.gamma + i0), beta = *(const f32x4*)(rec.beta + i0), end = *(const f32x4*)(rec.end + i0);
+                const f32x4 kb = *(const f32x4*)(rec.k_back + i0), qb = *(const f32x4*)(rec.q_back + i0), ob = *(const f32x4*)(o_back + i0);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int i = i0 + r, at = O::at(i, 2 * w + n / 8) + (n & 7);
+                    const float kv = (float)kq.K[at] * kb[r], qv = (float)kq.Q[at] * qb[r];
+                    const float x = d.scale * gamma[r] * ob[r] * s_back * aq[ti][r];
+                    const float y = beta[r] * gamma[r] * es.back * s_back * ar[ti][r], z = end[r] * us.back * z_back * au[ti][r];
+                    const float f = sum_lanes(qv * x - kv * y), af = sum_lanes(kv * z);
+                    if (n == 0) {
+                        front[w][i] = f;
+                        after[w][i] = af;
+                    }
+                    dq[ti][r] += fmaf(ps.back, xq[ti][r], x);
+                    dk[ti][r] += fmaf(ps.back, xp[ti][r], fmaf(as.back, xa[ti][r], z - y));
+                }
+            }
+        }
+        __syncthreads();
+        if (w == 0) {
+            const int tt = lane >> 4;
+            float f = 0.0f, af = 0.0f, be = 0.0f, dot = 0.0f, t = 0.0f;
+            for (int x = 0; x < kGradWaves; ++x) {
+                be += betas[x][lane];
+                dot += dots[x];
+            }
+            for (int x = 0; x < KT; ++x) {
+                f += front[x][lane];
+                af += after[x][lane];
+            }
+            for (int tj = 0; tj <= tt; ++tj) be += tile_beta[tri(tt, tj)][n];
+            // between every j < t <= i: in this step's column of tiles, and of whole rows of the columns in front
+            for (int ti = tt; ti < 4; ++ti) t += inside[tri(ti, tt)][n];
+            for (int tj = 0; tj < tt; ++tj)
+                for (int ti = tt; ti < 4; ++ti)
+                    for (int r = ti == tt ? n : 0; r < 16; ++r) t += across[tri(ti, tj)][r];
+            float all_f = f, all_a = af;
+#pragma unroll
+            for (int x = 1; x < 64; x <<= 1) {
+                const float p = __shfl_down(all_f, x), o = __shfl_up(all_a, x);
+                if (lane + x < 64) all_f += p;
+                if (lane >= x) all_a += o;
+            }
+            all_a = __shfl_up(all_a, 1);
+            t += all_f + (lane ? all_a : 0.0f) + gates.whole * dot;
+            if (lane < all) {
+                const int64_t at = ((int64_t)b * d.steps + t0 + lane) * d.heads + h;
+                const bool live = lane < rows;
+                // the decay of a restart is not applied
+                const bool cut = lane ? gates.seg[lane] != gates.seg[lane - 1] : gates.seg[0] != 0;
+                a.grad_log_decay[at] = live && !cut ? t : 0.0f;
+                a.grad_beta[at] = live ? be : 0.0f;
+            }
+        }
+    }
+    if (w < KT && col < d.key_dim)
+#pragma unroll
+        for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int i = 16 * ti + 4 * g + r;
+                if (i < all) {
+                    gq[i * k_step + col] = (T)(i < rows ? dq[ti][r] : 0.0f);
+                    gk[i * k_step + col] = (T)(i < rows ? dk[ti][r] : 0.0f);
+                }
+            }
+}
+
 // A few steps (one new token, a few drafted ones): the state is read and
 // written once, and that is the bound. A workgroup holds `slice` columns of one
 // head's state in registers, V neighbouring columns a lane and the rows spread
@@ -1501,6 +1983,9 @@ size_t key_bytes(const gs_delta_rule& r) {
     const size_t row = (size_t)2 * kC * padded(r.key_dim) * sizeof(f16) * (r.dtype == GS_F32 ? 2 : 1);
     return (size_t)r.batch * chunks_of(r) * r.key_heads * row;
 }
+size_t behind_floats(const gs_delta_rule& r) {
+    return (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim;
+}
 size_t back_record_bytes(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * sizeof(Backward); }
 size_t record_bytes(const gs_delta_rule& r) {
     return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Forward<1>) : sizeof(Forward<2>));
@@ -1558,18 +2043,23 @@ hipError_t backward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const int chunks = chunks_of(r);
     auto* const keys = (Keys<kPlanes<T>, DK>*)scratch;
     auto* const records = (Backward*)((char*)scratch + key_bytes(r));
-    float* const inverse = (float*)((char*)records + back_record_bytes(r));
-    float* const behind = inverse + inverse_floats(r);
-    if (chunks) {
+    float* const behind = (float*)((char*)records + back_record_bytes(r));
+    if (chunks)
         k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, keys, records);
-        k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, inverse);
-    }
     if (r.value_dim > 64)
         k_delta_back<T, DK, 8><<<r.batch * r.heads, 512, 0, stream>>>(a, chunks, keys, records, behind);
     else
         k_delta_back<T, DK, 4><<<r.batch * r.heads, 256, 0, stream>>>(a, chunks, keys, records, behind);
-    if (chunks)
-        k_delta_grad<T, DK><<<r.batch * chunks * r.key_heads, 64 * kGradWaves, 0, stream>>>(a, chunks, inverse, behind);
+    if (chunks) {
+        const int grid = r.batch * chunks * r.key_heads;
+        if constexpr (sizeof(T) == 2) {
+            k_delta_grads<T, DK><<<grid, 64 * kGradWaves, 0, stream>>>(a, chunks, keys, records, behind);
+        } else {
+            float* const inverse = behind + behind_floats(r);
+            k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, inverse);
+            k_delta_grad<T, DK><<<grid, 64 * kGradWaves, 0, stream>>>(a, chunks, inverse, behind);
+        }
+    }
     return hipGetLastError();
 }
 
@@ -1593,8 +2083,8 @@ hipError_t run(const DeltaArgs& a, void* scratch, bool back, hipStream_t stream)
 size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
     if (!backward) return key_bytes(r) + record_bytes(r) + segment_bytes(r);
-    return key_bytes(r) + back_record_bytes(r) +
-           (inverse_floats(r) + (size_t)r.batch * chunks_of(r) * r.heads * r.key_dim * r.value_dim) * sizeof(float);
+    return key_bytes(r) + back_record_bytes(r) + behind_floats(r) * sizeof(float) +
+           (r.dtype == GS_F32 ? inverse_floats(r) * sizeof(float) : 0);
 }
 
 hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
