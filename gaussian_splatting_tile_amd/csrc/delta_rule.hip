@@ -229,6 +229,19 @@ struct Planes {
     f16x8 p[N];
 };
 
+// The place (i, g) of a lane. here(): the same, which the compiler does not
+// know, so that the many addresses that follow from it are formed where they
+// are used and not held in registers through a loop.
+struct Lane {
+    int n, g;
+    __device__ __forceinline__ explicit Lane(int id = threadIdx.x) : n(id & 15), g(id >> 4 & 3) {}
+    static __device__ __forceinline__ Lane here() {
+        int id = threadIdx.x;
+        asm volatile("" : "+v"(id));
+        return Lane(id);
+    }
+};
+
 template <int N>
 __device__ __forceinline__ Planes<N> split(f32x4 a, f32x4 b, float scale) {
     Planes<N> out;
@@ -314,16 +327,16 @@ struct Operand {
     static constexpr int N = NX, PIECES = DK / 8, PLANE = kC * DK, SIZE = N * PLANE;
     static __device__ __forceinline__ int at(int t, int c) { return t * DK + (c ^ (t & (PIECES - 1))) * 8; }
     // the rows 16 tile + i, terms 32 s + 8 g ..
-    static __device__ __forceinline__ Planes<N> row(const f16* m, int tile, int s) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    static __device__ __forceinline__ Planes<N> row(const f16* m, int tile, int s, Lane l = Lane()) {
+        const int n = l.n, g = l.g;
         Planes<N> x;
 #pragma unroll
         for (int k = 0; k < N; ++k) x.p[k] = *(const f16x8*)(m + k * PLANE + at(16 * tile + n, 4 * s + g));
         return x;
     }
     // the transposed rows: dimensions 32 s + 8 (i / 4) + 4 h + i % 4, terms the steps 4g + r of tiles 2p and 2p + 1
-    static __device__ __forceinline__ Planes<N> column(const f16* m, int s, int h, int p) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    static __device__ __forceinline__ Planes<N> column(const f16* m, int s, int h, int p, Lane l = Lane()) {
+        const int n = l.n, g = l.g;
         typedef short i16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) i16x4* Lds;
         Planes<N> x;
@@ -623,28 +636,28 @@ struct Copy {
 };
 
 template <int N>
-__device__ __forceinline__ Planes<N> operand(const f16* m, int f) {
+__device__ __forceinline__ Planes<N> operand(const f16* m, int f, Lane l = Lane()) {
     Planes<N> x;
 #pragma unroll
-    for (int k = 0; k < N; ++k) x.p[k] = *(const f16x8*)(m + (f * N + k) * kPair + (threadIdx.x & 63) * 8);
+    for (int k = 0; k < N; ++k) x.p[k] = *(const f16x8*)(m + (f * N + k) * kPair + (16 * l.g + l.n) * 8);
     return x;
 }
 
 // c += A B over the steps, A a lower triangular matrix of a record, B two columns' planes.
 template <int NA, int NB>
-__device__ __forceinline__ void lower(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4]) {
-    const Planes<NA> A[4] = {operand<NA>(m, 0), operand<NA>(m, 1), operand<NA>(m, 2), operand<NA>(m, 4)};
+__device__ __forceinline__ void lower(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4], Lane l = Lane()) {
+    const Planes<NA> A[4] = {operand<NA>(m, 0, l), operand<NA>(m, 1, l), operand<NA>(m, 2, l), operand<NA>(m, 4, l)};
     products(A, B[0], c);
-    const Planes<NA> C[2] = {operand<NA>(m, 3), operand<NA>(m, 5)};
+    const Planes<NA> C[2] = {operand<NA>(m, 3, l), operand<NA>(m, 5, l)};
     products(C, B[1], c + 2);
 }
 
 // The same of an upper triangular one.
 template <int NA, int NB>
-__device__ __forceinline__ void upper(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4]) {
-    const Planes<NA> A[2] = {operand<NA>(m, 0), operand<NA>(m, 2)};
+__device__ __forceinline__ void upper(const f16* m, const Planes<NB> (&B)[2], f32x4 (&c)[4], Lane l = Lane()) {
+    const Planes<NA> A[2] = {operand<NA>(m, 0, l), operand<NA>(m, 2, l)};
     products(A, B[0], c);
-    const Planes<NA> C[4] = {operand<NA>(m, 1), operand<NA>(m, 3), operand<NA>(m, 4), operand<NA>(m, 5)};
+    const Planes<NA> C[4] = {operand<NA>(m, 1, l), operand<NA>(m, 3, l), operand<NA>(m, 4, l), operand<NA>(m, 5, l)};
     products(C, B[1], c);
 }
 
@@ -656,20 +669,20 @@ template <int KT>
 struct Column {
     f32x4 t[KT];
     // of a matrix with `rows` rows of `pitch`
-    static __device__ __forceinline__ uint32_t offset(int col, int pitch) {
-        return (uint32_t)(8 * (threadIdx.x >> 4 & 3) * pitch + col) * 4u;
+    static __device__ __forceinline__ uint32_t offset(int col, int pitch, Lane l) {
+        return (uint32_t)(8 * l.g * pitch + col) * 4u;
     }
-    __device__ __forceinline__ void load(const float* p, bool on, int col, int rows, int pitch) {
+    __device__ __forceinline__ void load(const float* p, bool on, int col, int rows, int pitch, Lane l = Lane()) {
         const Buffer m(p, p ? rows * pitch * 4 : 0);
-        const uint32_t off = on ? offset(col, pitch) : kNowhere;
+        const uint32_t off = on ? offset(col, pitch, l) : kNowhere;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
             for (int r = 0; r < 4; ++r) t[k][r] = m.load<float>(off + key_row(k, 0, r) * pitch * 4);
     }
-    __device__ __forceinline__ void store(float* p, bool on, int col, int rows, int pitch, float scale) const {
+    __device__ __forceinline__ void store(float* p, bool on, int col, int rows, int pitch, float scale, Lane l = Lane()) const {
         const Buffer m(p, rows * pitch * 4);
-        uint32_t off = on ? offset(col, pitch) : kNowhere;
+        uint32_t off = on ? offset(col, pitch, l) : kNowhere;
 #pragma unroll
         for (int k = 0; k < KT; ++k)
 #pragma unroll
@@ -686,10 +699,10 @@ struct Column {
 template <typename T>
 struct Values {
     T x[16];
-    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, bool on, int col, int dim) {
+    __device__ __forceinline__ void load(const T* p, int64_t step, int rows, bool on, int col, int dim, Lane l = Lane()) {
         const int by = (int)step * (int)sizeof(T);
         const Buffer m(p, (min(rows, kC) - 1) * by + dim * (int)sizeof(T));
-        uint32_t off = on ? 4 * (threadIdx.x >> 4 & 3) * by + col * (uint32_t)sizeof(T) : kNowhere;
+        uint32_t off = on ? 4 * l.g * by + col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
             x[e] = m.load<T>(off);
@@ -697,8 +710,9 @@ struct Values {
         }
     }
     // rows from `rows` on are 0, those from `all` on are not there
-    static __device__ __forceinline__ void store(T* p, int64_t step, int rows, int all, bool on, int col, int dim, f32x4 (&v)[4]) {
-        const int g = threadIdx.x >> 4 & 3, by = (int)step * (int)sizeof(T);
+    static __device__ __forceinline__ void store(T* p, int64_t step, int rows, int all, bool on, int col, int dim, f32x4 (&v)[4],
+                                                 Lane l = Lane()) {
+        const int g = l.g, by = (int)step * (int)sizeof(T);
         if (rows < kC)
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e / 4][e % 4] = 16 * (e / 4) + 4 * g + e % 4 < rows ? v[e / 4][e % 4] : 0.0f;
@@ -745,7 +759,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
     // behind the values' columns, in workgroups of their own, those of Phi
     const int blocks = (d.value_dim + 16 * WAVES - 1) / (16 * WAVES);
     const bool values = OUT || (int)blockIdx.y < blocks;
-    const int col = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16 + n;
+    const int col0 = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16, col = col0 + n;
     const bool on = col < (values ? d.value_dim : d.key_dim);
     const int len = length_of(d, b), z = blockIdx.z;
     const int c0 = z * seg.chunks, c1 = min((len + kC - 1) / kC, c0 + seg.chunks);
@@ -778,6 +792,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
     if (c0 < c1) fetch(c0);
     const f32x4 zero = {0, 0, 0, 0};
     for (int c = c0; c < c1; ++c) {
+        const Lane l = Lane::here();
+        const int g = l.g, col = col0 + l.n;
         const int t0 = c * kC;
         __syncthreads();
         fr.store(&rec);
@@ -794,11 +810,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], big.by);
             Planes<NX> A[4];
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s);
+            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(K, ti, s, l);
             products(A, sp, R);
             if constexpr (OUT) {
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s);
+                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s, l);
                 Planes<NP> high;
 #pragma unroll
                 for (int k = 0; k < NP; ++k) high.p[k] = sp.p[k];
@@ -822,7 +838,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         {
             const Scale rs(over_column(largest(R)));
             const Planes<2> B[2] = {split<2>(R[0], R[1], rs.by), split<2>(R[2], R[3], rs.by)};
-            lower<2>(rec.M, B, U);
+            lower<2>(rec.M, B, U, l);
             const float back = rs.back * rec.misc[1];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
@@ -831,13 +847,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             const Scale us(over_column(largest(U)));
             const Planes<NP> B[2] = {split<NP>(U[0], U[1], us.by), split<NP>(U[2], U[3], us.by)};
             f32x4 x[4] = {zero, zero, zero, zero};
-            lower<NP>(rec.P, B, x);
+            lower<NP>(rec.P, B, x, l);
             const float back = us.back * rec.misc[2];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[ti][r] = fmaf(x[ti][r], back, y[ti][r]);
-            Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, y);
+            Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, y, l);
         }
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
@@ -853,12 +869,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             const Planes<2> up = split<2>(U[2 * p], U[2 * p + 1], es.by);
 #pragma unroll
             for (int s = 0; s < KS; s += 2) {
-                const Planes<NX> A[4] = {O::column(K, s, 0, p), O::column(K, s, 1, p), O::column(K, s + 1, 0, p), O::column(K, s + 1, 1, p)};
+                const Planes<NX> A[4] = {O::column(K, s, 0, p, l), O::column(K, s, 1, p, l), O::column(K, s + 1, 0, p, l), O::column(K, s + 1, 1, p, l)};
                 products(A, up, S.t + 2 * s);
             }
         }
         if (OUT && a.ckpt && t0 + kC < len)
-            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit);
+            S.store(a.ckpt + (((int64_t)b * (chunks - 1) + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit, l);
     }
     if constexpr (OUT) {
         // the steps of the segment that are padding behind its last chunk
@@ -938,7 +954,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
     const gs_delta_rule& d = a.r;
     const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col = (blockIdx.y * WAVES + w) * 16 + n;
+    const int col0 = (blockIdx.y * WAVES + w) * 16, col = col0 + n;
     const bool on = col < d.value_dim;
     const int len = length_of(d, b), mine = (len + kC - 1) / kC;
     const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
@@ -964,8 +980,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
     if (mine > 0) fetch(mine - 1);
     const f32x4 zero = {0, 0, 0, 0};
     for (int c = mine - 1; c >= 0; --c) {
+        const Lane l = Lane::here();
+        const int g = l.g, col = col0 + l.n;
         const int t0 = c * kC;
-        S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit);
+        S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit, l);
         __syncthreads();
         fr.store(part);
         fk.store(&kq);
@@ -981,13 +999,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], big.by);
             Planes<NX> A[4];
 #pragma unroll
-            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s);
+            for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s, l);
             products(A, sp, dU);
         }
         {
             const Scale os(over_column(largest(dO)));
             const Planes<NX> B[2] = {split<NX>(dO[0], dO[1], os.by), split<NX>(dO[2], dO[3], os.by)};
-            upper<2>(rec.PT, B, x);
+            upper<2>(rec.PT, B, x, l);
             const float back = os.back * rec.misc[2], from = unit * big.back;
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
@@ -1000,7 +1018,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         {
             const Scale us(over_column(largest(dU)));
             const Planes<2> B[2] = {split<2>(dU[0], dU[1], us.by), split<2>(dU[2], dU[3], us.by)};
-            upper<2>(rec.MT, B, dR);
+            upper<2>(rec.MT, B, dR, l);
             const float back = us.back * rec.misc[1];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
@@ -1014,7 +1032,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
                 }
             }
         }
-        Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x);
+        Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
         const float whole = rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
         const float keep = whole * es.by;
@@ -1026,9 +1044,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             const Planes<2> op = split<2>(dO[2 * p], dO[2 * p + 1], es.by), rp = split<2>(dR[2 * p], dR[2 * p + 1], es.by);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Planes<NX> A[2] = {O::column(kq.Q, s, 0, p), O::column(kq.Q, s, 1, p)};
+                const Planes<NX> A[2] = {O::column(kq.Q, s, 0, p, l), O::column(kq.Q, s, 1, p, l)};
                 products(A, op, S.t + 2 * s);
-                const Planes<NX> B[2] = {O::column(kq.K, s, 0, p), O::column(kq.K, s, 1, p)};
+                const Planes<NX> B[2] = {O::column(kq.K, s, 0, p, l), O::column(kq.K, s, 1, p, l)};
                 products(B, rp, S.t + 2 * s);
             }
         }
@@ -1357,8 +1375,8 @@ struct Turned {
     static constexpr int PLANE = ROWS * kC;
     static __device__ __forceinline__ int at(int row, int piece) { return row * kC + (piece ^ (row & 7)) * 8; }
     // steps 16 tile + 4g .. of a row
-    static __device__ __forceinline__ void write(f16* m, int row, int tile, f32x4 v, float scale) {
-        const int g = threadIdx.x >> 4 & 3;
+    static __device__ __forceinline__ void write(f16* m, int row, int tile, f32x4 v, float scale, Lane l = Lane()) {
+        const int g = l.g;
         f16* const to = m + at(row, 2 * tile + g / 2) + (g & 1) * 4;
         const f16x2 a = __builtin_convertvector(f32x2{v[0] * scale, v[1] * scale}, f16x2);
         const f16x2 b = __builtin_convertvector(f32x2{v[2] * scale, v[3] * scale}, f16x2);
@@ -1370,8 +1388,8 @@ struct Turned {
         *(f16x4*)(to + PLANE) = f16x4{c[0], c[1], e[0], e[1]};
     }
     // lane i: step 16 tile + i, terms the rows 32 s + 8 g ..
-    static __device__ __forceinline__ Planes<2> turned(const f16* m, int tile, int s) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    static __device__ __forceinline__ Planes<2> turned(const f16* m, int tile, int s, Lane l = Lane()) {
+        const int n = l.n, g = l.g;
         typedef short i16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) i16x4* Lds;
         Planes<2> x;
@@ -1386,8 +1404,8 @@ struct Turned {
         return x;
     }
     // lane i: row 16 tile + i, terms the steps 32 p + 8 g ..
-    static __device__ __forceinline__ Planes<2> along(const f16* m, int tile, int p) {
-        const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3;
+    static __device__ __forceinline__ Planes<2> along(const f16* m, int tile, int p, Lane l = Lane()) {
+        const int n = l.n, g = l.g;
         Planes<2> x;
 #pragma unroll
         for (int k = 0; k < 2; ++k) x.p[k] = *(const f16x8*)(m + k * PLANE + at(16 * tile + n, 4 * p + g));
@@ -1448,7 +1466,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
     __shared__ Chunk gates;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int w = threadIdx.x >> 6;
     const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
     const int all = min(kC, d.steps - t0);  // steps of the chunk, padding included
     const int64_t first = (((int64_t)b * d.steps + t0) * d.key_heads + kh) * d.key_dim;
@@ -1474,8 +1492,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         f.store(&kq);
     }
     const int vs = (d.value_dim + 31) / 32;  // terms of sums over the values, by 32
-    const int col = 16 * w + n;              // of the values, and the row of a state's transposed columns
     for (int hh = 0; hh < group; ++hh) {
+        const Lane l = Lane::here();
+        const int n = l.n, g = l.g, lane = 16 * g + n, col = 16 * w + n;  // of the values, and the row of a state's transposed columns
         const int h = kh * group + hh;
         const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
         const float* const S0 = c == 0 ? (a.h0 ? a.h0 + head * size : nullptr)
@@ -1485,11 +1504,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         const T* const go = (const T*)a.grad_o + (((int64_t)b * d.steps + t0) * d.heads + h) * d.value_dim;
         Column<KT> S, Z;
         const bool on = col < d.value_dim;
-        S.load(S0, on, col, d.key_dim, d.value_dim);
-        Z.load(dS, on, col, d.key_dim, d.value_dim);
+        S.load(S0, on, col, d.key_dim, d.value_dim, l);
+        Z.load(dS, on, col, d.key_dim, d.value_dim, l);
         Values<T> fv, fo;
-        fv.load(v, d.v_step, rows, on, col, d.value_dim);
-        fo.load(go, o_step, rows, on, col, d.value_dim);
+        fv.load(v, d.v_step, rows, on, col, d.value_dim, l);
+        fo.load(go, o_step, rows, on, col, d.value_dim, l);
         if (hh) __syncthreads();
         {
             Copy<sizeof(rec), kThreads> f;
@@ -1541,7 +1560,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                 const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], ss.by), zp = split<2>(Z.t[2 * s], Z.t[2 * s + 1], zs.by);
                 Planes<1> A[4];
 #pragma unroll
-                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s);
+                for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s, l);
                 products(A, sp, x);
                 products(A, zp, y);
             }
@@ -1560,7 +1579,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             {
                 const Scale rs(over_column(largest(R)));
                 const Planes<2> B[2] = {split<2>(R[0], R[1], rs.by), split<2>(R[2], R[3], rs.by)};
-                lower<2>(rec.M, B, U);
+                lower<2>(rec.M, B, U, l);
                 const float back = rs.back * rec.misc[1];
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) U[ti] *= back;
@@ -1568,7 +1587,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             {
                 const Scale os(over_column(largest(dO)));
                 const Planes<1> B[2] = {split<1>(dO[0], dO[1], os.by), split<1>(dO[2], dO[3], os.by)};
-                upper<2>(rec.PT, B, dU);
+                upper<2>(rec.PT, B, dU, l);
                 const float back = os.back * rec.misc[2];
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
@@ -1581,7 +1600,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             {
                 const Scale us(over_column(largest(dU)));
                 const Planes<2> B[2] = {split<2>(dU[0], dU[1], us.by), split<2>(dU[2], dU[3], us.by)};
-                upper<2>(rec.MT, B, E);
+                upper<2>(rec.MT, B, E, l);
                 const float back = us.back * rec.misc[1];
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
@@ -1609,8 +1628,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         const Scale us(over_waves(most[0])), es(over_waves(most[1]));
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) {
-            TV::write(m.ue[0], col, ti, U[ti], us.by);
-            TV::write(m.ue[1], col, ti, E[ti], es.by);
+            TV::write(m.ue[0], col, ti, U[ti], us.by, l);
+            TV::write(m.ue[1], col, ti, E[ti], es.by, l);
         }
         __syncthreads();
         // 16 columns of the keys: dO S^T, dR S^T, U dS^T
@@ -1638,12 +1657,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                     Planes<2> C[4];
 #pragma unroll
                     for (int ti = 0; ti < 4; ++ti) {
-                        A[ti] = OV::row(dOs, ti, s);
-                        C[ti] = TV::turned(m.ue[1], ti, s);
+                        A[ti] = OV::row(dOs, ti, s, l);
+                        C[ti] = TV::turned(m.ue[1], ti, s, l);
                     }
                     products(A, B, aq);
                     products(C, B, ar);
-                }
+                    }
             take(dS, x);
             scale = Scale(over_column(largest(x)));
             z_back = scale.back;
@@ -1653,9 +1672,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                     const Planes<2> B = split<2>(x[2 * s], x[2 * s + 1], scale.by);
                     Planes<2> C[4];
 #pragma unroll
-                    for (int ti = 0; ti < 4; ++ti) C[ti] = TV::turned(m.ue[0], ti, s);
+                    for (int ti = 0; ti < 4; ++ti) C[ti] = TV::turned(m.ue[0], ti, s, l);
                     products(C, B, au);
-                }
+                    }
         }
         // tiles of Pd and Ad, and of what the gates' gradients need of them
         f32x4 pd[2] = {zero, zero}, ad[2] = {zero, zero};
@@ -1669,16 +1688,16 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 if (s < vs) {
-                    const Planes<2> B = TV::turned(m.ue[0], tj, s);
-                    const Planes<1> A[1] = {OV::row(dOs, ti, s)};
-                    const Planes<2> C[1] = {TV::turned(m.ue[1], ti, s)};
+                    const Planes<2> B = TV::turned(m.ue[0], tj, s, l);
+                    const Planes<1> A[1] = {OV::row(dOs, ti, s, l)};
+                    const Planes<2> C[1] = {TV::turned(m.ue[1], ti, s, l)};
                     products(A, B, &dp);
                     products(C, B, &da);
-                }
+                    }
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
-                const Planes<1> B = O::row(kq.K, tj, s);
-                const Planes<1> A[1] = {O::row(kq.Q, ti, s)}, C[1] = {O::row(kq.K, ti, s)};
+                const Planes<1> B = O::row(kq.K, tj, s, l);
+                const Planes<1> A[1] = {O::row(kq.Q, ti, s, l)}, C[1] = {O::row(kq.K, ti, s, l)};
                 products(A, B, &qk);
                 products(C, B, &kk);
             }
@@ -1721,14 +1740,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, tj = q - tri(ti, 0), row = 16 * tj + n;
             const float kj = rec.k_back[row];
             const f32x4 ki = *(const f32x4*)(rec.k_back + 16 * ti + 4 * g), qi = *(const f32x4*)(rec.q_back + 16 * ti + 4 * g);
-            TC::write(m.pa[0], row, ti, pd[turn] * kj, ps.by);
-            TC::write(m.pa[1], row, ti, pd[turn] * qi, ps.by);
-            TC::write(m.pa[2], row, ti, ad[turn] * kj, as.by);
-            TC::write(m.pa[3], row, ti, ad[turn] * ki, as.by);
+            TC::write(m.pa[0], row, ti, pd[turn] * kj, ps.by, l);
+            TC::write(m.pa[1], row, ti, pd[turn] * qi, ps.by, l);
+            TC::write(m.pa[2], row, ti, ad[turn] * kj, as.by, l);
+            TC::write(m.pa[3], row, ti, ad[turn] * ki, as.by, l);
         }
         if (w >= 4)  // the tiles over the diagonal that pairs of tiles take along
 #pragma unroll
-            for (int p = 0; p < 2; ++p) TC::write(m.pa[w - 4], 32 * p + 16 + n, 2 * p, zero, 1.0f);
+            for (int p = 0; p < 2; ++p) TC::write(m.pa[w - 4], 32 * p + 16 + n, 2 * p, zero, 1.0f, l);
         __syncthreads();
         if (w < KT) {
             f32x4 xq[4] = {zero, zero, zero, zero}, xp[4] = {zero, zero, zero, zero}, xa[4] = {zero, zero, zero, zero};
@@ -1748,12 +1767,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
                     if (p <= ti / 2) {
-                        const Planes<2> A[1] = {TC::turned(m.pa[0], ti, p)}, C[1] = {TC::turned(m.pa[2], ti, p)};
+                        const Planes<2> A[1] = {TC::turned(m.pa[0], ti, p, l)}, C[1] = {TC::turned(m.pa[2], ti, p, l)};
                         products(A, kc, xq + ti);
                         products(C, kc, xa + ti);
                     }
                     if (p >= ti / 2) {
-                        const Planes<2> A[1] = {TC::along(m.pa[1], ti, p)}, C[1] = {TC::along(m.pa[3], ti, p)};
+                        const Planes<2> A[1] = {TC::along(m.pa[1], ti, p, l)}, C[1] = {TC::along(m.pa[3], ti, p, l)};
                         products(A, qc, xp + ti);
                         products(C, kc, xa + ti);
                     }
@@ -1817,6 +1836,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             }
         }
     }
+    const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, col = 16 * w + n;
     if (w < KT && col < d.key_dim)
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti)
