@@ -698,14 +698,23 @@ struct Column {
 // their beta of 0 keeps out.)
 template <typename T>
 struct Values {
-    T x[16];
+    uint32_t x[16];  // a register each: packed, they would be waited for where they are fetched
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (sizeof(T) == 2)
+            return (float)__builtin_bit_cast(T, (uint16_t)x[e]);
+        else
+            return __uint_as_float(x[e]);
+    }
     __device__ __forceinline__ void load(const T* p, int64_t step, int rows, bool on, int col, int dim, Lane l = Lane()) {
         const int by = (int)step * (int)sizeof(T);
         const Buffer m(p, (min(rows, kC) - 1) * by + dim * (int)sizeof(T));
         uint32_t off = on ? 4 * l.g * by + col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-            x[e] = m.load<T>(off);
+            if constexpr (sizeof(T) == 2)
+                x[e] = m.load<uint16_t>(off);
+            else
+                x[e] = m.load<uint32_t>(off);
             off += e % 4 == 3 ? 13 * by : by;
         }
     }
@@ -787,9 +796,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         const int t0 = c * kC;
         fr.load(first + (int64_t)c * d.heads);
         fk.load(first_keys + (int64_t)c * d.key_heads);
+        __builtin_amdgcn_sched_barrier(0);  // the values last: when they are there, so is the rest
         if (values) fv.load(v + t0 * d.v_step, d.v_step, len - t0, on, col, d.value_dim);
     };
-    if (c0 < c1) fetch(c0);
+    // The values are taken over before the chunk's stores: behind them they would be waited for together.
+    f32x4 V[4];
+    auto take = [&] {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) V[e / 4][e % 4] = values ? fv[e] : 0.0f;
+    };
+    if (c0 < c1) {
+        fetch(c0);
+        take();
+    }
     const f32x4 zero = {0, 0, 0, 0};
     for (int c = c0; c < c1; ++c) {
         const Lane l = Lane::here();
@@ -798,9 +817,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         __syncthreads();
         fr.store(&rec);
         fk.store(kq);
-        f32x4 V[4];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) V[e / 4][e % 4] = values ? (float)fv.x[e] : 0.0f;
         __syncthreads();
         if (c + 1 < c1) fetch(c + 1);
         f32x4 R[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};  // K S, then R; Q S, then O
@@ -853,10 +869,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             for (int ti = 0; ti < 4; ++ti)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[ti][r] = fmaf(x[ti][r], back, y[ti][r]);
+            take();
             Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, y, l);
         }
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
+        if constexpr (!OUT) take();
         // one scale for what is kept of S and what is added
         const float whole = rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(largest(U)), whole * big.back));
@@ -890,50 +908,54 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 }
 
 // The state in front of every segment, in place of its B: S <- Phi S + B from
-// segment to segment (from the last to the first with BACK, with the transposed
-// Phi), 16 columns a workgroup and 16 rows a wave, on the float32 matrix
-// instructions. Bound by the latency of a step: Phi is fetched two ahead.
+// segment to segment, 16 columns a workgroup and 16 rows a wave, on the float32
+// matrix instructions. Bound by the latency of a step: Phi is fetched three
+// steps ahead.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg) {
-    constexpr int KT = DK / 16, PITCH = DK + 4;
+    constexpr int KT = DK / 16, PITCH = DK + 4, AHEAD = 4;
     __shared__ float L[2][16 * PITCH];  // S by columns
     const gs_delta_rule& d = a.r;
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
     const int col = blockIdx.y * 16 + n, row = 16 * w + 4 * g, left = 16 * w + n;
-    const bool on = col < d.value_dim;
-    const int64_t head = blockIdx.x, size = (int64_t)d.key_dim * d.value_dim;
+    const int64_t head = blockIdx.x;
+    const int size = d.key_dim * d.value_dim, square = d.key_dim * d.key_dim;
     float* const front = seg.front + head * seg.count * size;
-    const float* const phi = seg.phi + head * seg.count * d.key_dim * d.key_dim;
-    f32x4 A[2][KT], B[2], S;
-    auto fetch = [&](int z, int at) {
+    const float* const phi = seg.phi + head * seg.count * square;
+    const uint32_t at = col < d.value_dim ? (uint32_t)(row * d.value_dim + col) * 4u : kNowhere;
+    const uint32_t from = (uint32_t)(left * d.key_dim + 4 * g) * 4u;
+    f32x4 A[AHEAD][KT], B[AHEAD], S;
+    // What is read past a row's end meets rows of S that are 0.
+    auto fetch = [&](int z, f32x4 (&x)[KT], f32x4& y) {
+        const Buffer p(phi + (int64_t)z * square, square * 4), f(front + (int64_t)z * size, size * 4);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
+            x[kt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.r, from + 64 * kt, 0, 0));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int k = 16 * kt + 4 * g + r;
-                const bool in = left < d.key_dim && k < d.key_dim;
-                A[at][kt][r] = in ? phi[((int64_t)z * d.key_dim + left) * d.key_dim + k] : 0.0f;
-            }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) B[at][r] = on && row + r < d.key_dim ? front[z * size + (row + r) * d.value_dim + col] : 0.0f;
+        for (int r = 0; r < 4; ++r) y[r] = f.load<float>(at + r * d.value_dim * 4);
     };
+    {
+        const Buffer h(a.h0 + head * size, a.h0 ? size * 4 : 0);
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-        S[r] = a.h0 && on && row + r < d.key_dim ? a.h0[head * size + (row + r) * d.value_dim + col] : 0.0f;
-    fetch(0, 0);
-    for (int z = 0; z < seg.count; z += 2)
+        for (int r = 0; r < 4; ++r) S[r] = h.load<float>(at + r * d.value_dim * 4);
+    }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x + 1 < AHEAD; ++x)
+        if (x < seg.count) fetch(x, A[x], B[x]);
+    for (int z = 0; z < seg.count; z += AHEAD)
+#pragma unroll
+        for (int x = 0; x < AHEAD; ++x) {
             if (z + x >= seg.count) break;
-            if (z + x + 1 < seg.count) fetch(z + x + 1, x ^ 1);
-            *(f32x4*)(L[x] + n * PITCH + row) = S;
+            if (z + x + AHEAD - 1 < seg.count) fetch(z + x + AHEAD - 1, A[(x + AHEAD - 1) % AHEAD], B[(x + AHEAD - 1) % AHEAD]);
+            float* const s = L[x & 1];
+            *(f32x4*)(s + n * PITCH + row) = S;
             __syncthreads();
+            const Buffer f(front + (int64_t)(z + x) * size, size * 4);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                if (on && row + r < d.key_dim) front[(z + x) * size + (row + r) * d.value_dim + col] = S[r];
+            for (int r = 0; r < 4; ++r) f.store(at + r * d.value_dim * 4, S[r]);
             f32x4 acc[2] = {B[x], {0, 0, 0, 0}};
 #pragma unroll
-            for (int kt = 0; kt < KT; ++kt) acc[kt & 1] = mma(A[x][kt], *(const f32x4*)(L[x] + n * PITCH + 16 * kt + 4 * g), acc[kt & 1]);
+            for (int kt = 0; kt < KT; ++kt) acc[kt & 1] = mma(A[x][kt], *(const f32x4*)(s + n * PITCH + 16 * kt + 4 * g), acc[kt & 1]);
             S = acc[0] + acc[1];
         }
 }
@@ -975,9 +997,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         const int t0 = c * kC;
         fr.load((const char*)(first + (int64_t)c * d.heads) + SKIP);
         fk.load(first_keys + (int64_t)c * d.key_heads);
+        __builtin_amdgcn_sched_barrier(0);  // the values last: when they are there, so is the rest
         fo.load(go + t0 * o_step, o_step, len - t0, on, col, d.value_dim);
     };
-    if (mine > 0) fetch(mine - 1);
+    // taken over before a chunk's stores, with which they would be waited for
+    f32x4 next[4];
+    auto take = [&] {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) next[e / 4][e % 4] = fo[e];
+    };
+    if (mine > 0) {
+        fetch(mine - 1);
+        take();
+    }
     const f32x4 zero = {0, 0, 0, 0};
     for (int c = mine - 1; c >= 0; --c) {
         const Lane l = Lane::here();
@@ -987,9 +1019,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         __syncthreads();
         fr.store(part);
         fk.store(&kq);
-        f32x4 dO[4];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) dO[e / 4][e % 4] = (float)fo.x[e];
+        f32x4 dO[4] = {next[0], next[1], next[2], next[3]};
         __syncthreads();
         if (c > 0) fetch(c - 1);
         const Scale big(over_column(largest(S.t)));
@@ -1032,6 +1062,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
                 }
             }
         }
+        take();
         Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
         const float whole = rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
@@ -1571,9 +1602,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                 const f32x4 gamma = *(const f32x4*)(rec.gamma + i), beta = *(const f32x4*)(rec.beta + i), kb = *(const f32x4*)(rec.k_back + i);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    e[ti][r] = fmaf(-gamma[r] * kb[r] * ss.back, x[ti][r], (float)fv.x[4 * ti + r]);
+                    e[ti][r] = fmaf(-gamma[r] * kb[r] * ss.back, x[ti][r], fv[4 * ti + r]);
                     R[ti][r] = beta[r] * e[ti][r];
-                    dO[ti][r] = (float)fo.x[4 * ti + r];
+                    dO[ti][r] = fo[4 * ti + r];
                 }
             }
             {
