@@ -425,21 +425,26 @@ constexpr int kPrepThreads = 256;
 // substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
 // and of pairs, in float32.
 template <typename T, int DK, typename Record>
-__global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
+__global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
                                                                 Record* to) {
     constexpr bool BACK = std::is_same_v<Record, Backward>;
     constexpr int NX = kPlanes<T>;
     typedef Operand<NX, DK> O;
-    __shared__ Keys<NX, DK> kq;
-    __shared__ float M[kC * kPitch];
-    __shared__ float P[kC * kPitch];
+    // the rows until their products are in registers, then M and P
+    __shared__ union Shared {
+        Keys<NX, DK> kq;
+        float mp[2][kC * kPitch];
+    } sh;
+    Keys<NX, DK>& kq = sh.kq;
+    float* const M = sh.mp[0];
+    float* const P = sh.mp[1];
     __shared__ float k_back[kC], q_back[kC], most[2][4];
     __shared__ Chunk s;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
     const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
     if (rows <= 0) return;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int w = threadIdx.x >> 6;
     auto stage = [&](const T* p, int64_t step, f16* m, f16* out, float* back) {
         typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
         constexpr int PIECES = O::PIECES, BY = kPrepThreads / PIECES, JOBS = kC / BY;
@@ -477,10 +482,6 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
     Keys<NX, DK>* const key = keys + ((int64_t)b * chunks + c) * d.key_heads + kh;
     stage((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, kq.K, key->K, k_back);
     stage((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, kq.Q, key->Q, q_back);
-    for (int e = threadIdx.x; e < 512; e += kPrepThreads) {  // the tiles over the diagonal that pairs take along
-        const int i = (e >> 4 & 15) + (e >> 8) * 32, j = (e & 15) + (e >> 8) * 32 + 16;
-        M[i * kPitch + j] = P[i * kPitch + j] = 0.0f;
-    }
     __syncthreads();
     const f32x4 zero = {0, 0, 0, 0};
     f32x4 kk[4], qk[4];  // of row tile w
@@ -498,7 +499,14 @@ __global__ __launch_bounds__(kPrepThreads) void k_delta_prepare(DeltaArgs a, int
                 qk[j] = t[1];
             }
     }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 512; e += kPrepThreads) {  // the tiles over the diagonal that pairs take along
+        const int i = (e >> 4 & 15) + (e >> 8) * 32, j = (e & 15) + (e >> 8) * 32 + 16;
+        M[i * kPitch + j] = P[i * kPitch + j] = 0.0f;
+    }
     for (int hh = 0; hh < group; ++hh) {
+        const Lane l = Lane::here();
+        const int n = l.n, g = l.g, lane = 16 * g + n;
         const int h = kh * group + hh;
         Record* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
         if (hh) __syncthreads();
@@ -2060,32 +2068,45 @@ size_t segment_bytes(const gs_delta_rule& r) {
     return s.count == 1 ? 0 : (size_t)r.batch * r.heads * s.count * r.key_dim * (r.value_dim + r.key_dim) * sizeof(float);
 }
 
-template <typename T, int DK, int WAVES>
-hipError_t chain(const DeltaArgs& a, void* scratch, hipStream_t stream) {
+// Waves (of 16 columns) of a chain's workgroup: 8, which read the operands from
+// memory once for 128 columns, or 4 where their workgroups all run at once,
+// each on a compute unit of its own (8 x 2048 steps of 16 heads of 128: 145 us
+// with 4, 176 with 8; 32 heads in 8 segments: 136 and 95).
+bool narrow(int64_t groups, int columns) { return columns <= 64 || groups * ((columns + 63) / 64) <= kUnits; }
+
+template <typename T, int DK, int WAVES, bool OUT>
+void chain(const DeltaArgs& a, int chunks, const void* scratch, const Segments& seg, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
-    const int chunks = chunks_of(r), wide = 16 * WAVES, heads = r.batch * r.heads;
     const auto* const keys = (const Keys<kPlanes<T>, DK>*)scratch;
-    const auto* const records = (const ForwardOf<T>*)((char*)scratch + key_bytes(r));
-    const int blocks = (r.value_dim + wide - 1) / wide;
-    Segments seg = segments_of(r);
-    if (seg.count > 1) {
-        seg.front = (float*)((char*)records + record_bytes(r));
-        seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
-        k_delta_chain<T, DK, WAVES, false><<<dim3(heads, blocks + (r.key_dim + wide - 1) / wide, seg.count), 64 * WAVES, 0, stream>>>(
-            a, chunks, keys, records, seg);
-        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg);
-    }
-    k_delta_chain<T, DK, WAVES, true><<<dim3(heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(a, chunks, keys, records, seg);
-    return hipGetLastError();
+    const auto* const records = (const ForwardOf<T>*)((const char*)scratch + key_bytes(r));
+    constexpr int WIDE = 16 * WAVES;
+    const int blocks = (r.value_dim + WIDE - 1) / WIDE + (OUT ? 0 : (r.key_dim + WIDE - 1) / WIDE);
+    k_delta_chain<T, DK, WAVES, OUT><<<dim3(r.batch * r.heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(
+        a, chunks, keys, records, seg);
 }
 
 template <typename T, int DK>
 hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
-    const int chunks = chunks_of(r);
+    const int chunks = chunks_of(r), heads = r.batch * r.heads;
     k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(
         a, chunks, (Keys<kPlanes<T>, DK>*)scratch, (ForwardOf<T>*)((char*)scratch + key_bytes(r)));
-    return r.value_dim > 64 ? chain<T, DK, 8>(a, scratch, stream) : chain<T, DK, 4>(a, scratch, stream);
+    Segments seg = segments_of(r);
+    const int64_t groups = (int64_t)heads * seg.count;
+    if (seg.count > 1) {
+        seg.front = (float*)((char*)scratch + key_bytes(r) + record_bytes(r));
+        seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
+        if (narrow(groups * 2, std::max(r.value_dim, r.key_dim)))
+            chain<T, DK, 4, false>(a, chunks, scratch, seg, stream);
+        else
+            chain<T, DK, 8, false>(a, chunks, scratch, seg, stream);
+        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg);
+    }
+    if (narrow(groups, r.value_dim))
+        chain<T, DK, 4, true>(a, chunks, scratch, seg, stream);
+    else
+        chain<T, DK, 8, true>(a, chunks, scratch, seg, stream);
+    return hipGetLastError();
 }
 
 template <typename T, int DK>
@@ -2097,10 +2118,10 @@ hipError_t backward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     float* const behind = (float*)((char*)records + back_record_bytes(r));
     if (chunks)
         k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, keys, records);
-    if (r.value_dim > 64)
-        k_delta_back<T, DK, 8><<<r.batch * r.heads, 512, 0, stream>>>(a, chunks, keys, records, behind);
+    if (narrow((int64_t)r.batch * r.heads, r.value_dim))
+        k_delta_back<T, DK, 4><<<dim3(r.batch * r.heads, (r.value_dim + 63) / 64), 256, 0, stream>>>(a, chunks, keys, records, behind);
     else
-        k_delta_back<T, DK, 4><<<r.batch * r.heads, 256, 0, stream>>>(a, chunks, keys, records, behind);
+        k_delta_back<T, DK, 8><<<r.batch * r.heads, 512, 0, stream>>>(a, chunks, keys, records, behind);
     if (chunks) {
         const int grid = r.batch * chunks * r.key_heads;
         if constexpr (sizeof(T) == 2) {
