@@ -1501,7 +1501,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
     __shared__ Backward rec;
     __shared__ float o_back[kC], betas[kGradWaves][kC], front[kGradWaves][kC], after[kGradWaves][kC], dots[kGradWaves];
     __shared__ float most[4][kGradWaves];
-    __shared__ float inside[kTiles][16], across[kTiles][16], tile_beta[kTiles][16];
+    __shared__ float inside[kTiles][16], across[kTiles][16], tile_beta[kTiles][16], total[kTiles];
     __shared__ Chunk gates;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
@@ -1582,6 +1582,15 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         }
         if (w == 0) load_gates(a, b, h, t0, len, gates);
         __syncthreads();
+        // Row `col` of S and of dS, terms 32 s + 8 g .., for the keys' columns below; what is read past a row's end
+        // meets columns of U, dR and dO that are 0.
+        f32x4 srow[8], zrow[8];
+        auto take = [&](const float* p, f32x4 (&x)[8]) {
+            const Buffer from(p, p ? (int)size * 4 : 0);
+            const uint32_t off = col < d.key_dim ? (uint32_t)(col * d.value_dim + 8 * g) * 4u : kNowhere;
+#pragma unroll
+            for (int s = 0; s < 8; ++s) x[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from.r, off + 128 * (s / 2) + 16 * (s & 1), 0, 0));
+        };
         // 16 columns of the values: U and dR
         f32x4 U[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
         {
@@ -1603,6 +1612,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                 products(A, sp, x);
                 products(A, zp, y);
             }
+            take(S0, srow);
+            take(dS, zrow);
             f32x4 R[4], dO[4], dU[4] = {zero, zero, zero, zero};
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
@@ -1675,23 +1686,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         f32x4 aq[4] = {zero, zero, zero, zero}, ar[4] = {zero, zero, zero, zero}, au[4] = {zero, zero, zero, zero};
         float s_back = 0.0f, z_back = 0.0f;
         if (w < KT) {
-            auto take = [&](const float* p, f32x4 (&x)[8]) {  // row `col` of a state, terms 32 s + 8 g ..
-                const Buffer from(p, p ? (int)size * 4 : 0);
-                const uint32_t off = col < d.key_dim ? (uint32_t)(col * d.value_dim + 8 * g) * 4u : kNowhere;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[2 * s + i / 4][i % 4] = from.load<float>(32 * s + 8 * g + i < d.value_dim ? off + (32 * s + i) * 4 : kNowhere);
-            };
-            f32x4 x[8];
-            take(S0, x);
-            Scale scale(over_column(largest(x)));
+            Scale scale(over_column(largest(srow)));
             s_back = scale.back;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 if (s < vs) {
-                    const Planes<2> B = split<2>(x[2 * s], x[2 * s + 1], scale.by);
+                    const Planes<2> B = split<2>(srow[2 * s], srow[2 * s + 1], scale.by);
                     Planes<1> A[4];
                     Planes<2> C[4];
 #pragma unroll
@@ -1702,13 +1702,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                     products(A, B, aq);
                     products(C, B, ar);
                     }
-            take(dS, x);
-            scale = Scale(over_column(largest(x)));
+            scale = Scale(over_column(largest(zrow)));
             z_back = scale.back;
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 if (s < vs) {
-                    const Planes<2> B = split<2>(x[2 * s], x[2 * s + 1], scale.by);
+                    const Planes<2> B = split<2>(zrow[2 * s], zrow[2 * s + 1], scale.by);
                     Planes<2> C[4];
 #pragma unroll
                     for (int ti = 0; ti < 4; ++ti) C[ti] = TV::turned(m.ue[0], ti, s, l);
@@ -1742,7 +1741,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             }
             const int j = 16 * tj + n;
             const float kj = rec.k_back[j];
-            float column = 0.0f;
+            float column = 0.0f, whole = 0.0f;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * ti + 4 * g + r;
@@ -1758,11 +1757,14 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                 const float x = fmaf(p, qk[r] * qi * kj, beta * tb), up = scan_lanes(x);
                 if (ti > tj || i >= j) column += up - x;
                 if (n == 15) across[q][4 * g + r] = up;
+                whole += up;
                 const float sum = sum_lanes(tb);
                 if (n == 0) tile_beta[q][4 * g + r] = sum;
             }
             column = sum_column(column);
+            whole = sum_column(whole);
             if (g == 0) inside[q][n] = column;
+            if (lane == 15) total[q] = whole;
         }
         pm = over_column(over_lanes<16>(pm));
         am = over_column(over_lanes<16>(am));
@@ -1839,39 +1841,52 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
             }
         }
         __syncthreads();
-        if (w == 0) {
-            const int tt = lane >> 4;
-            float f = 0.0f, af = 0.0f, be = 0.0f, dot = 0.0f, t = 0.0f;
-            for (int x = 0; x < kGradWaves; ++x) {
-                be += betas[x][lane];
-                dot += dots[x];
-            }
+        const int64_t at = ((int64_t)b * d.steps + t0 + lane) * d.heads + h;
+        const int tt = lane >> 4;
+        if (w == 0 && lane < all) {
+            float be = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kGradWaves; ++x) be += betas[x][lane];
+#pragma unroll
+            for (int tj = 0; tj < 4; ++tj)
+                if (tj <= tt) be += tile_beta[tri(tt, tj)][n];
+            a.grad_beta[at] = lane < rows ? be : 0.0f;
+        }
+        if (w == 1) {
+            float f = 0.0f, af = 0.0f, dot = 0.0f, t = 0.0f, row = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kGradWaves; ++x) dot += dots[x];
+#pragma unroll
             for (int x = 0; x < KT; ++x) {
                 f += front[x][lane];
                 af += after[x][lane];
             }
-            for (int tj = 0; tj <= tt; ++tj) be += tile_beta[tri(tt, tj)][n];
-            // between every j < t <= i: in this step's column of tiles, and of whole rows of the columns in front
-            for (int ti = tt; ti < 4; ++ti) t += inside[tri(ti, tt)][n];
-            for (int tj = 0; tj < tt; ++tj)
-                for (int ti = tt; ti < 4; ++ti)
-                    for (int r = ti == tt ? n : 0; r < 16; ++r) t += across[tri(ti, tj)][r];
+            // between every j < t <= i: of the tiles of this step's columns, then of whole rows of the columns in front
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+                if (ti >= tt) t += inside[tri(ti, tt)][n];
+#pragma unroll
+            for (int tj = 0; tj < 3; ++tj)
+                if (tj < tt) row += across[tri(tt, tj)][n];
+#pragma unroll
+            for (int ti = 2; ti < 4; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < 3; ++tj)
+                    if (ti > tt && tj < tt) t += total[tri(ti, tj)];
             float all_f = f, all_a = af;
 #pragma unroll
             for (int x = 1; x < 64; x <<= 1) {
-                const float p = __shfl_down(all_f, x), o = __shfl_up(all_a, x);
+                const float p = __shfl_down(all_f, x), o = __shfl_up(all_a, x), q = __shfl_down(row, x);
                 if (lane + x < 64) all_f += p;
                 if (lane >= x) all_a += o;
+                if (x < 16 && n + x < 16) row += q;  // rows from this one to the tile's last
             }
             all_a = __shfl_up(all_a, 1);
-            t += all_f + (lane ? all_a : 0.0f) + gates.whole * dot;
+            t += row + all_f + (lane ? all_a : 0.0f) + gates.whole * dot;
             if (lane < all) {
-                const int64_t at = ((int64_t)b * d.steps + t0 + lane) * d.heads + h;
-                const bool live = lane < rows;
                 // the decay of a restart is not applied
                 const bool cut = lane ? gates.seg[lane] != gates.seg[lane - 1] : gates.seg[0] != 0;
-                a.grad_log_decay[at] = live && !cut ? t : 0.0f;
-                a.grad_beta[at] = live ? be : 0.0f;
+                a.grad_log_decay[at] = lane < rows && !cut ? t : 0.0f;
             }
         }
     }
