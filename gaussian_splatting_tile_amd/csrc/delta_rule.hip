@@ -1113,7 +1113,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
     __shared__ Chunk s;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int w = threadIdx.x >> 6;
     const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
     const int64_t first = (((int64_t)b * d.steps + t0) * d.key_heads + kh) * d.key_dim;
     T* const gq = (T*)a.grad_q + first;
@@ -1133,16 +1133,17 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
     }
     const T* const q = (const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head;
     const T* const k = (const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head;
-    auto q4 = [&](int row, int at) {
-        f32x4 x;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = row < rows && at + r < d.key_dim ? (float)q[row * d.q_step + at + r] : 0.0f;
-        return x;
+    const int qs = (int)d.q_step * (int)sizeof(T);
+    const Buffer queries(q, (min(rows, kC) - 1) * qs + d.key_dim * (int)sizeof(T));
+    auto four = [](const Buffer& m, uint32_t off, int left) {  // elements from `left` on are 0
+        const f32x4 x = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(m.r, off, 0, 0));
+        return f32x4{left > 0 ? x[0] : 0.0f, left > 1 ? x[1] : 0.0f, left > 2 ? x[2] : 0.0f, left > 3 ? x[3] : 0.0f};
     };
+    auto q4 = [&](int row, int at) { return four(queries, row < rows ? row * qs + at * 4 : kNowhere, d.key_dim - at); };
     auto qcol = [&](int row, int at) {
         f32x4 x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) x[r] = row + r < rows && at < d.key_dim ? (float)q[(row + r) * d.q_step + at] : 0.0f;
+        for (int r = 0; r < 4; ++r) x[r] = queries.load<float>(row + r < rows && at < d.key_dim ? (row + r) * qs + at * 4 : kNowhere);
         return x;
     };
     load_rows<DK>(k, d.k_step, rows, d.key_dim, K, kThreads);
@@ -1151,6 +1152,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
 #pragma unroll
     for (int ti = 0; ti < 4; ++ti) dq[ti] = dk[ti] = zero;
     for (int hh = 0; hh < group; ++hh) {
+        const Lane l = Lane::here();
+        const int n = l.n, g = l.g, lane = 16 * g + n;
         const int h = kh * group + hh;
         const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
         const float* const S0 = c == 0 ? (a.h0 ? a.h0 + head * size : nullptr)
@@ -1159,6 +1162,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
         const float* const M = inverse + ((int64_t)(b * chunks + c) * d.heads + h) * kLower;
         const T* const v = (const T*)a.v + b * d.v_batch + t0 * d.v_step + h * d.v_head;
         const T* const go = (const T*)a.grad_o + (((int64_t)b * d.steps + t0) * d.heads + h) * d.value_dim;
+        const Buffer front_state(S0, S0 ? (int)size * 4 : 0), behind_state(dS, (int)size * 4);
+        const int os = (int)o_step * (int)sizeof(T);
+        const Buffer upstream(go, (min(rows, kC) - 1) * os + d.value_dim * (int)sizeof(T));
         __syncthreads();
         if (w == 0) load_gates(a, b, h, t0, len, s);
         __syncthreads();
@@ -1180,14 +1186,16 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             const bool on = col < d.value_dim;
             f32x4 S[KT], Z[KT];
             float dot = 0.0f;
+            Values<T> vals, ups;
+            vals.load(v, d.v_step, rows, on, col, d.value_dim, l);
+            ups.load(go, o_step, rows, on, col, d.value_dim, l);
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * kt + 4 * g + r;
-                    const bool in = on && row < d.key_dim;
-                    S[kt][r] = in && S0 ? S0[(int64_t)row * d.value_dim + col] : 0.0f;
-                    Z[kt][r] = in ? dS[(int64_t)row * d.value_dim + col] : 0.0f;
+                    const uint32_t off = on ? ((16 * kt + 4 * g + r) * d.value_dim + col) * 4 : kNowhere;
+                    S[kt][r] = front_state.load<float>(off);
+                    Z[kt][r] = behind_state.load<float>(off);
                     dot = fmaf(S[kt][r], Z[kt][r], dot);
                 }
 #pragma unroll
@@ -1206,10 +1214,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = 16 * ti + 4 * g + r;
-                    const bool in = on && i < rows;
-                    e[ti][r] = (in ? (float)v[i * d.v_step + col] : 0.0f) - s.gamma[i] * x[r];
+                    e[ti][r] = vals[4 * ti + r] - s.gamma[i] * x[r];
                     R[ti][r] = s.beta[i] * e[ti][r];
-                    dO[ti][r] = in ? (float)go[i * o_step + col] : 0.0f;
+                    dO[ti][r] = ups[4 * ti + r];
                     dU[ti][r] = s.end[i] * y[r];
                 }
             }
@@ -1242,12 +1249,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
                 }
         }
         __syncthreads();
-        auto o4 = [&](int row, int at) {
-            f32x4 x;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = row < rows && at + r < d.value_dim ? (float)go[row * o_step + at + r] : 0.0f;
-            return x;
-        };
+        auto o4 = [&](int row, int at) { return four(upstream, row < rows ? row * os + at * 4 : kNowhere, d.value_dim - at); };
         const int vt = (d.value_dim + 15) / 16;
         float part[2][4] = {};  // of the gradient of beta, from the tiles of this wave
         for (int p = w, turn = 0; p < kTiles; p += kGradWaves, ++turn) {
@@ -1284,14 +1286,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
         const int row = 16 * w + n;  // of the keys
         if (w < KT) {
             for (int ct = 0; ct < vt; ++ct) {
-                f32x4 x, y;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = 16 * ct + 4 * g + r;
-                    const bool in = row < d.key_dim && at < d.value_dim;
-                    x[r] = in && S0 ? S0[(int64_t)row * d.value_dim + at] : 0.0f;
-                    y[r] = in ? dS[(int64_t)row * d.value_dim + at] : 0.0f;
-                }
+                const int at = 16 * ct + 4 * g;
+                const uint32_t off = row < d.key_dim ? (row * d.value_dim + at) * 4 : kNowhere;
+                const f32x4 x = four(front_state, off, d.value_dim - at), y = four(behind_state, off, d.value_dim - at);
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) {
                     aq[ti] = mma(o4(16 * ti + n, 16 * ct + 4 * g), x, aq[ti]);
@@ -1391,7 +1388,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             }
         }
     }
-    const int row = 16 * w + n;
+    const int n = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, row = 16 * w + n;
     if (w < KT && row < d.key_dim)
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti)
