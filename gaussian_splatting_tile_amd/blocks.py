@@ -12,8 +12,8 @@ import torch
 
 from . import _lib
 from ._lib import (GS_BLOCK_GATE_NONE, GS_BLOCK_GATE_SIGMOID, GS_BLOCK_GATE_SILU, GS_BLOCK_NORM_LAYER,
-                   GS_BLOCK_NORM_NONE, GS_BLOCK_NORM_RMS, GS_DELTA_CHUNK)
-from .training import _dtype, _elsewhere, _launch, _on, _ptr, _stream
+                   GS_BLOCK_NORM_NONE, GS_BLOCK_NORM_RMS, GS_DELTA_CHUNK, GS_DELTA_FEW)
+from .training import _TYPES, _dtype, _elsewhere, _launch, _on, _ptr, _stream
 
 BLOCK_NORM_NONE, BLOCK_NORM_RMS, BLOCK_NORM_LAYER = GS_BLOCK_NORM_NONE, GS_BLOCK_NORM_RMS, GS_BLOCK_NORM_LAYER
 BLOCK_GATE_NONE, BLOCK_GATE_SIGMOID, BLOCK_GATE_SILU = GS_BLOCK_GATE_NONE, GS_BLOCK_GATE_SIGMOID, GS_BLOCK_GATE_SILU
@@ -29,28 +29,28 @@ def _strided(t, shape, dtype, name, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[-1] > 1 and t.stride(-1) != 1:
+    if not t.is_contiguous() and shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have a contiguous last dimension")
     return t.data_ptr()
 
 
 def _delta(q, k, v, log_decay, beta, scale, lengths, restart):
     """The C description of a call, the addresses of its inputs, and its sizes."""
-    if q.dim() != 4 or v.dim() != 4:
+    shape, vshape, n, t = q.shape, v.shape, q.get_device(), q.dtype
+    if len(shape) != 4 or len(vshape) != 4:
         raise ValueError("q, k and v must be [B, T, heads, dim]")
-    if not q.is_cuda:
+    if n < 0:
         raise TypeError("q, k and v must be device tensors")
-    B, T, Hk, dk = q.shape
-    H, dv = v.shape[2:]
-    n, t, f32 = q.get_device(), q.dtype, torch.float32
+    B, T, Hk, dk = shape
+    H, dv = vshape[2:]
+    gates, f32 = (B, T, H), torch.float32
     code = _dtype(q, "q, k and v")
-    p = (_strided(q, (B, T, Hk, dk), t, "q", n), _strided(k, (B, T, Hk, dk), t, "k", n),
-         _strided(v, (B, T, H, dv), t, "v", n), _strided(log_decay, (B, T, H), f32, "log_decay", n),
-         _strided(beta, (B, T, H), f32, "beta", n))
-    r = _lib.GsDeltaRule(code, B, T, Hk, H, dk, dv, dk ** -0.5 if scale is None else float(scale), *q.stride()[:3],
+    p = (_strided(q, shape, t, "q", n), _strided(k, shape, t, "k", n), _strided(v, (B, T, H, dv), t, "v", n),
+         _strided(log_decay, gates, f32, "log_decay", n), _strided(beta, gates, f32, "beta", n))
+    r = _lib.GsDeltaRule(code, B, T, Hk, H, dk, dv, dk ** -0.5 if scale is None else scale, *q.stride()[:3],
                          *k.stride()[:3], *v.stride()[:3], *log_decay.stride()[:2], *beta.stride()[:2],
-                         _ptr(lengths, (B,), torch.int32, "lengths", n),
-                         _ptr(restart, (B, T), torch.uint8, "restart", n))
+                         None if lengths is None else _ptr(lengths, (B,), torch.int32, "lengths", n),
+                         None if restart is None else _ptr(restart, (B, T), torch.uint8, "restart", n))
     return r, p, (B, T, Hk, H, dk, dv)
 
 
@@ -64,10 +64,12 @@ def _scratch(need, scratch, device):
 
 
 def delta_rule_scratch_bytes(batch: int, steps: int, heads: int, key_dim: int, value_dim: int, backward=False,
-                             dtype=torch.float32) -> int:
-    """Bytes of the workspace delta_rule_fwd (or delta_rule_bwd) takes for this shape."""
+                             dtype=torch.float32, key_heads=None) -> int:
+    """Bytes of the workspace delta_rule_fwd (or delta_rule_bwd) takes for this shape; without `key_heads`, bytes that
+    are enough for any number of them."""
     r = _lib.GsDeltaRule()
-    r.batch, r.steps, r.key_heads, r.heads = int(batch), int(steps), 1, int(heads)
+    r.batch, r.steps, r.heads = int(batch), int(steps), int(heads)
+    r.key_heads = r.heads if key_heads is None else int(key_heads)
     r.key_dim, r.value_dim, r.dtype = int(key_dim), int(value_dim), _dtype(torch.empty(0, dtype=dtype), "dtype")
     return int(_lib.load().gs_delta_rule_scratch_bytes(ctypes.byref(r), int(bool(backward))))
 
@@ -89,27 +91,35 @@ def delta_rule_fwd(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, 
     output may overlap an input. With `stream` (not the current one) the call allocates and runs on it: order it
     behind whatever wrote the inputs, and the use of what it returns behind it. Calls that share a `scratch` must
     not overlap."""
-    if _elsewhere(stream, q.device):
+    if stream is not None and _elsewhere(stream, q.device):
         return _on(stream, lambda: delta_rule_fwd(q, k, v, log_decay, beta, h0, scale, lengths, restart, checkpoints,
                                                   out, scratch), out)
     lib = _lib.load()
     r, p, (B, T, Hk, H, dk, dv) = _delta(q, k, v, log_decay, beta, scale, lengths, restart)
     dev, f32, state = q.device, torch.float32, (B, H, dk, dv)
     n = dev.index
-    o = h_last = ckpt = None
+    o = h_last = ckpt = pc = None
     if out is not None:
         o, h_last, ckpt = out.get("o"), out.get("h_last"), out.get("ckpt")
     if o is None:
         o = q.new_empty((B, T, H, dv))
+        po = o.data_ptr()
+    else:
+        po = _ptr(o, (B, T, H, dv), q.dtype, "o", n)
     if h_last is None:
         h_last = q.new_empty(state, dtype=f32)
-    rows = (B, delta_rule_ckpt_rows(T), H, dk, dv)
-    if ckpt is None and checkpoints:
-        ckpt = q.new_empty(rows, dtype=f32)
-    p += (_ptr(h0, state, f32, "h0", n), _ptr(o, (B, T, H, dv), q.dtype, "o", n),
-          _ptr(h_last, state, f32, "h_last", n), _ptr(ckpt, rows, f32, "ckpt", n))
-    scratch, ps, nbytes = _scratch(int(lib.gs_delta_rule_scratch_bytes(ctypes.byref(r), 0)), scratch, dev)
-    _launch(dev, lib.gs_delta_rule_fwd, ctypes.byref(r), *p, ps, nbytes, _stream(stream, dev))
+        pl = h_last.data_ptr()
+    else:
+        pl = _ptr(h_last, state, f32, "h_last", n)
+    if checkpoints or ckpt is not None:
+        rows = (B, delta_rule_ckpt_rows(T), H, dk, dv)
+        if ckpt is None:
+            ckpt = q.new_empty(rows, dtype=f32)
+        pc = _ptr(ckpt, rows, f32, "ckpt", n)
+    ph, ps, nbytes = _ptr(h0, state, f32, "h0", n), None, 0
+    if T > GS_DELTA_FEW:
+        scratch, ps, nbytes = _scratch(int(lib.gs_delta_rule_scratch_bytes(ctypes.byref(r), 0)), scratch, dev)
+    _launch(dev, lib.gs_delta_rule_fwd, ctypes.byref(r), *p, ph, po, pl, pc, ps, nbytes, _stream(stream, dev))
     return dict(o=o, h_last=h_last, ckpt=ckpt)
 
 
@@ -119,7 +129,7 @@ def delta_rule_bwd(q, k, v, log_decay, beta, grad_o, h0=None, ckpt=None, grad_la
     v's type; grad_last float32 [B, H, dk, dv] or None. Returns dict grad_q, grad_k [B, T, Hk, dk] (summed over the
     heads of a key head), grad_v [B, T, H, dv], grad_log_decay, grad_beta float32 [B, T, H], grad_h0 float32
     [B, H, dk, dv]. `stream` and `scratch` as for delta_rule_fwd."""
-    if _elsewhere(stream, q.device):
+    if stream is not None and _elsewhere(stream, q.device):
         return _on(stream, lambda: delta_rule_bwd(q, k, v, log_decay, beta, grad_o, h0, ckpt, grad_last, scale,
                                                   lengths, restart, out, scratch), out)
     lib = _lib.load()
@@ -158,41 +168,43 @@ def _row_strides(t, at):
 
 def _norm_call(y, gate, residual, gating, scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps):
     """The C description of a call and the addresses of its inputs."""
-    if y.dim() < 2:
-        raise ValueError("y must be [..., width]")
-    if not y.is_cuda:
-        raise TypeError("y must be a device tensor")
     shape, t, n = y.shape, y.dtype, y.get_device()
-    code, D = _dtype(y, "y"), shape[-1]
-    if y.numel() == 0 and D == 0:
+    if len(shape) < 2:
+        raise ValueError("y must be [..., width]")
+    if n < 0:
+        raise TypeError("y must be a device tensor")
+    D = shape[-1]
+    if D == 0:
         raise ValueError("y must have at least one element in a row")
-    p = [_strided(y, shape, t, "y", n)]
-    for x, name in ((gate, "gate"), (residual, "residual")):
-        p.append(None if x is None else _strided(x, shape, t, name, n))
-    rows = [x for x in (y, gate, residual) if x is not None]
+    p = [_strided(y, shape, t, "y", n), None if gate is None else _strided(gate, shape, t, "gate", n),
+         None if residual is None else _strided(residual, shape, t, "residual", n)]
     outer, inner = y.numel() // D, 1
-    if all(x.is_contiguous() for x in rows):
-        strides = (D, 0) * 3
+    if y.is_contiguous() and (gate is None or gate.is_contiguous()) and (residual is None or residual.is_contiguous()):
+        strides = (D, 0, D, 0, D, 0)
     else:
+        rows = [x for x in (y, gate, residual) if x is not None]
         cuts = set().union(*(_breaks(x) for x in rows))
         if len(cuts) > 1:
             raise ValueError("the rows of y, gate and residual must follow at one stride, or at two that break at the "
                              "same dimension")
         at = cuts.pop() if cuts else len(shape) - 1
-        inner = 1
         for m in shape[at:-1]:
             inner *= m
         outer = outer // inner if inner else 0
         strides = []
         for x in (y, gate, residual):
             strides += (0, 0) if x is None else _row_strides(x, at)
-    weights = [w for w in (post_weight, post_bias, scale, pre_weight, pre_bias) if w is not None]
-    wt = weights[0].dtype if weights else torch.float32
-    d = _lib.GsBlockNorm(code, _dtype(weights[0], "weights") if weights else _lib.GS_F32, int(post), int(gating),
-                         int(pre), max(inner, 1), D, float(eps), outer, *strides)
-    p += [_ptr(w, (D,), wt, name, n) for w, name in
-          ((post_weight, "post_weight"), (post_bias, "post_bias"), (scale, "scale"), (pre_weight, "pre_weight"),
-           (pre_bias, "pre_bias"))]
+    wt, wide = None, (D,)
+    for w, name in ((post_weight, "post_weight"), (post_bias, "post_bias"), (scale, "scale"),
+                    (pre_weight, "pre_weight"), (pre_bias, "pre_bias")):
+        if w is None:
+            p.append(None)
+        else:
+            if wt is None:
+                wt = w.dtype
+            p.append(_ptr(w, wide, wt, name, n))
+    d = _lib.GsBlockNorm(_dtype(y, "y"), _lib.GS_F32 if wt is None else _TYPES.get(wt, -1), post, gating, pre,
+                         inner or 1, D, eps, outer, *strides)
     return d, p
 
 
@@ -206,23 +218,28 @@ def block_norm_fwd(y, residual=None, gate=None, gating=BLOCK_GATE_NONE, scale=No
     float16), rows at any one stride, or two (tokens and heads of a part of a projection); weights, biases and scale
     [width], all float32 or all of y's type. Returns dict out (None unless want_out) and norm (None without pre). `out` may give them;
     out["out"] may be y, gate or residual itself. `stream` as for delta_rule_fwd."""
-    if _elsewhere(stream, y.device):
+    if stream is not None and _elsewhere(stream, y.device):
         return _on(stream, lambda: block_norm_fwd(y, residual, gate, gating, scale, post, post_weight, post_bias, pre,
                                                   pre_weight, pre_bias, eps, want_out, out), out)
     lib = _lib.load()
     d, p = _norm_call(y, gate, residual, gating, scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps)
-    dev, shape = y.device, y.shape
-    x = norm = None
+    dev = y.device
+    x = norm = px = pn = None
     if out is not None:
         x, norm = out.get("out"), out.get("norm")
-    if x is None and want_out:
-        x = y.new_empty(shape)
+    if x is not None:
+        px = _ptr(x, y.shape, y.dtype, "out", dev.index)
+    elif want_out:
+        x = y.new_empty(y.shape)
+        px = x.data_ptr()
     if pre == BLOCK_NORM_NONE:
         norm = None
-    elif norm is None:
-        norm = y.new_empty(shape)
-    _launch(dev, lib.gs_block_norm_fwd, ctypes.byref(d), *p, _ptr(x, shape, y.dtype, "out", dev.index),
-            _ptr(norm, shape, y.dtype, "norm", dev.index), _stream(stream, dev))
+    elif norm is not None:
+        pn = _ptr(norm, y.shape, y.dtype, "norm", dev.index)
+    else:
+        norm = y.new_empty(y.shape)
+        pn = norm.data_ptr()
+    _launch(dev, lib.gs_block_norm_fwd, ctypes.byref(d), *p, px, pn, _stream(stream, dev))
     return dict(out=x, norm=norm)
 
 
@@ -235,7 +252,7 @@ def block_norm_bwd(y, grad_out, grad_norm=None, residual=None, gate=None, gating
     `out` may give them (those it lacks of gate, residual and the sums are not computed); grad_y, grad_gate and
     grad_residual may each be grad_out or grad_norm itself. `stream` as for delta_rule_fwd; calls that share a
     `scratch` must not overlap."""
-    if _elsewhere(stream, y.device):
+    if stream is not None and _elsewhere(stream, y.device):
         return _on(stream, lambda: block_norm_bwd(y, grad_out, grad_norm, residual, gate, gating, scale, post,
                                                   post_weight, post_bias, pre, pre_weight, pre_bias, eps, out,
                                                   scratch), out)
@@ -243,16 +260,22 @@ def block_norm_bwd(y, grad_out, grad_norm=None, residual=None, gate=None, gating
     d, p = _norm_call(y, gate, residual, gating, scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps)
     dev, shape, t, f32 = y.device, y.shape, y.dtype, torch.float32
     n, wide = dev.index, shape[-1:]
-    rows = dict(grad_y=y, grad_gate=gate if gating != BLOCK_GATE_NONE else None, grad_residual=residual)
-    sums = dict(grad_post_weight=post_weight, grad_post_bias=post_bias, grad_scale=scale, grad_pre_weight=pre_weight,
-                grad_pre_bias=pre_bias)
+    rows = (("grad_y", y), ("grad_gate", None if gating == BLOCK_GATE_NONE else gate), ("grad_residual", residual))
+    sums = (("grad_post_weight", post_weight), ("grad_post_bias", post_bias), ("grad_scale", scale),
+            ("grad_pre_weight", pre_weight), ("grad_pre_bias", pre_bias))
+    p += [_ptr(grad_out, shape, t, "grad_out", n), _ptr(grad_norm, shape, t, "grad_norm", n)]
     if out is None:
-        out = {k: None if x is None else y.new_empty(shape) for k, x in rows.items()}
-        out.update({k: None if w is None else y.new_empty(wide, dtype=f32) for k, w in sums.items()})
-    p += [_ptr(grad_out, shape, t, "grad_out", n), _ptr(grad_norm, shape, t, "grad_norm", n),
-          _ptr(out["grad_y"], shape, t, "grad_y", n), _ptr(out.get("grad_gate"), shape, t, "grad_gate", n),
-          _ptr(out.get("grad_residual"), shape, t, "grad_residual", n)]
-    ps = [_ptr(out.get(k), wide, f32, k, n) for k in sums]
+        out, ps = {}, []
+        for k, x in rows:
+            out[k] = None if x is None else y.new_empty(shape)
+            p.append(None if x is None else out[k].data_ptr())
+        for k, w in sums:
+            out[k] = None if w is None else y.new_empty(wide, dtype=f32)
+            ps.append(None if w is None else out[k].data_ptr())
+    else:
+        p += [_ptr(out["grad_y"], shape, t, "grad_y", n), _ptr(out.get("grad_gate"), shape, t, "grad_gate", n),
+              _ptr(out.get("grad_residual"), shape, t, "grad_residual", n)]
+        ps = [_ptr(out.get(k), wide, f32, k, n) for k, _ in sums]
     need = int(lib.gs_block_norm_scratch_bytes(ctypes.byref(d))) if any(ps) else 0
     scratch, pw, nbytes = _scratch(need, scratch, dev)
     _launch(dev, lib.gs_block_norm_bwd, ctypes.byref(d), *p, *ps, pw, nbytes, _stream(stream, dev))

@@ -1908,7 +1908,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 // S^T q, are formed of the state in front of it (o = a S^T q + (q.k) u), so a
 // step has one exchange through LDS. Everything the steps read is fetched
 // before the first one.
-constexpr int kFewSteps = 16;
+constexpr int kFewSteps = GS_DELTA_FEW;
 
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_delta_steps(DeltaArgs a, int slice, int lanes) {

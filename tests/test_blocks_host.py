@@ -67,7 +67,9 @@ def test_delta_rule_sizes(gs):
     assert size(0, key_dim=0) == 0 and size(1, dtype=7) == 0 and gs.gs_delta_rule_scratch_bytes(None, 0) == 0
     assert size(0, steps=0) == 0
     assert size(1) > size(0) > 0 and size(1, steps=200) == 2 * size(1)
-    assert delta_rule_scratch_bytes(2, 100, 4, 64, 32, True) == size(1)
+    assert delta_rule_scratch_bytes(2, 100, 4, 64, 32, True, key_heads=2) == size(1)
+    for back in (False, True):  # without the key heads: enough for any number of them
+        assert delta_rule_scratch_bytes(2, 100, 4, 64, 32, back) >= max(size(back, key_heads=n) for n in (1, 2, 4))
     assert [delta_rule_ckpt_rows(t) for t in (0, 1, 64, 65, 128, 129)] == [0, 0, 0, 1, 1, 2]
 
 
