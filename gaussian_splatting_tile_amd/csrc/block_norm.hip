@@ -13,11 +13,17 @@
 // of it in the registers of the threads that share it, so the backward
 // recomputes the forward's values (a few operations each) instead of reading
 // them. A row belongs to `lanes` threads (a power of two, chosen so that a
-// thread holds at most NE elements), a workgroup walks rows in strides of the
-// grid and keeps the weights in registers. The sums over the rows are formed
-// per workgroup in registers and added over the workgroups by a second launch,
-// in a fixed order.
+// thread holds at most NE elements) and a workgroup walks rows in strides of
+// the grid. The sums over the rows are formed per workgroup and added over the
+// workgroups by a second launch, in a fixed order.
+//
+// Measured (a copy of as many bytes moves 5.06 TB/s): forward with residual,
+// sigmoid gate and both norms, 16384 x 2048 bf16, 335 MB: 64 us; its backward,
+// 537 MB: 117 us, 4.6 TB/s; 8192 x 8192 f16 forward, 671 MB: 136 us, 4.9 TB/s;
+// 262144 x 128 bf16 with a silu gate, both directions, 537 MB: 103 us. One of
+// 64 x 2048 takes 4.5 us, a launch's latency.
 #include <algorithm>
+#include <type_traits>
 
 #include "gs_internal.h"
 
@@ -34,6 +40,7 @@ struct Geometry {
 
 typedef __bf16 bf16;
 typedef _Float16 f16;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // Aligned to an element only: the hardware takes 16-byte accesses at any address.
 template <typename T, int N>
@@ -162,73 +169,114 @@ struct Rows {
     }
 };
 
-// Sums of two values over the threads of a row, the same in all of them. One
-// barrier where a row is more than a wave; the two halves of `lds` alternate.
+// x and that of another lane: the neighbour at a power of two, or its mirror
+// image where all lanes up to that power hold the same sum already.
+template <int CTRL>
+__device__ __forceinline__ float with_lane(float x) {
+    return x + __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+// The sum over `n` neighbouring lanes (a power of two, 1 to 64), in all of them;
+// register moves only: shuffles through LDS waited for each other (8192 x 8192
+// forward 167 us with them, 143 without).
+__device__ __forceinline__ float over_lanes(float x, int n) {
+    if (n > 1) x = with_lane<0xB1>(x);   // lane ^ 1
+    if (n > 2) x = with_lane<0x4E>(x);   // lane ^ 2
+    if (n > 4) x = with_lane<0x141>(x);  // 7 - lane of 8
+    if (n > 8) x = with_lane<0x140>(x);  // 15 - lane of 16
+    if (n > 16) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    if (n > 32) {
+        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+        x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    }
+    return x;
+}
+
+// Sums of one or two values over the threads of a row, the same in all of them.
+// One barrier where a row is more than a wave; the two halves of `lds` alternate.
 struct RowSum {
     float (*lds)[16][2];
     int lanes, turn;
     __device__ __forceinline__ void operator()(float& a, float& b) {
+        sum<true>(a, b);
+    }
+    __device__ __forceinline__ void operator()(float& a) {
+        float none = 0.0f;
+        sum<false>(a, none);
+    }
+    template <bool BOTH>
+    __device__ __forceinline__ void sum(float& a, float& b) {
         const int in_wave = min(lanes, 64);
-        for (int m = 1; m < in_wave; m <<= 1) {
-            a += __shfl_xor(a, m);
-            b += __shfl_xor(b, m);
-        }
+        a = over_lanes(a, in_wave);
+        if (BOTH) b = over_lanes(b, in_wave);
         if (lanes > 64) {
             const int wave = threadIdx.x >> 6, waves = lanes >> 6, first = wave & ~(waves - 1);
+            float (*const to)[2] = lds[turn];
             if ((threadIdx.x & 63) == 0) {
-                lds[turn][wave][0] = a;
-                lds[turn][wave][1] = b;
+                to[wave][0] = a;
+                if (BOTH) to[wave][1] = b;
             }
             __syncthreads();
-            a = b = 0.0f;
-            for (int w = 0; w < waves; ++w) {
-                a += lds[turn][first + w][0];
-                b += lds[turn][first + w][1];
-            }
+            const int from = first + (threadIdx.x & (waves - 1));
+            a = over_lanes(to[from][0], waves);
+            if (BOTH) b = over_lanes(to[from][1], waves);
             turn ^= 1;
         }
     }
 };
 
-// x -> (x - m) r in place (0 past the width); returns r.
+// 1 / sqrt(v) within an ulp; the hardware's takes normal numbers only.
+__device__ __forceinline__ float inverse_root(float v) {
+    const bool small = v < 0x1p-96f;
+    return __builtin_amdgcn_rsqf(small ? v * 0x1p64f : v) * (small ? 0x1p32f : 1.0f);
+}
+
+// x -> (x - m) r in place; returns r. Elements past the width are 0 and stay it. `inv`: 1 / width.
 template <typename R>
-__device__ __forceinline__ float normalise(const R& rows, RowSum& sum, int kind, float eps, float (&x)[R::NE]) {
-    const float inv = 1.0f / (float)rows.width;
-    float s = 0.0f, none = 0.0f;
+__device__ __forceinline__ float normalise(const R& rows, RowSum& sum, int kind, float inv, float eps, float (&x)[R::NE]) {
+    float s = 0.0f;
     if (kind == GS_BLOCK_NORM_LAYER) {
         float m = 0.0f;
 #pragma unroll
         for (int i = 0; i < R::NE; ++i) m += x[i];
-        sum(m, none);
+        sum(m);
         m *= inv;
 #pragma unroll
         for (int i = 0; i < R::NE; ++i) x[i] = rows.in(i) ? x[i] - m : 0.0f;
     }
 #pragma unroll
     for (int i = 0; i < R::NE; ++i) s = fmaf(x[i], x[i], s);
-    sum(s, none);
-    const float r = 1.0f / sqrtf(fmaf(s, inv, eps));
+    sum(s);
+    const float r = inverse_root(fmaf(s, inv, eps));
 #pragma unroll
     for (int i = 0; i < R::NE; ++i) x[i] *= r;
     return r;
 }
 
-// g -> r (g - [layer] <g> - xhat <g xhat>).
+// g -> r (g - [layer] <g> - xhat <g xhat>); 0 past the width where g and xhat are.
 template <typename R>
-__device__ __forceinline__ void normalise_back(const R& rows, RowSum& sum, int kind, float r,
+__device__ __forceinline__ void normalise_back(const R& rows, RowSum& sum, int kind, float inv, float r,
                                                const float (&xhat)[R::NE], float (&g)[R::NE]) {
-    const float inv = 1.0f / (float)rows.width;
-    float a = 0.0f, b = 0.0f;
+    float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < R::NE; ++i) {
-        a = fmaf(g[i], xhat[i], a);
-        b += g[i];
+    for (int i = 0; i < R::NE; ++i) a = fmaf(g[i], xhat[i], a);
+    if (kind == GS_BLOCK_NORM_LAYER) {
+        float b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R::NE; ++i) b += g[i];
+        sum(a, b);
+        a *= -inv;
+        b *= inv;
+#pragma unroll
+        for (int i = 0; i < R::NE; ++i) g[i] = rows.in(i) ? r * fmaf(xhat[i], a, g[i] - b) : 0.0f;
+    } else {
+        sum(a);
+        a *= -inv;
+#pragma unroll
+        for (int i = 0; i < R::NE; ++i) g[i] = r * fmaf(xhat[i], a, g[i]);
     }
-    sum(a, b);
-    a *= inv;
-    b = kind == GS_BLOCK_NORM_LAYER ? b * inv : 0.0f;
-#pragma unroll
-    for (int i = 0; i < R::NE; ++i) g[i] = r * (g[i] - b - xhat[i] * a);
 }
 
 // 1 / (1 + exp(-z)); the hardware's exponential and reciprocal are within an ulp, the product z log2(e) adds |z| 2^-24.
@@ -236,15 +284,39 @@ __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * z));
 }
 
-__device__ __forceinline__ int64_t row_at(int64_t row, int inner, int64_t so, int64_t si) {
-    const int64_t o = row / inner;
-    return o * so + (row - o * inner) * si;
-}
+// What differs between the gates act(z) = sigmoid(z) e, e being z (silu) or 1,
+// chosen by bits: a select on a value that all threads share becomes a branch
+// for every element (8192 x 8192 forward 143 us with, 139 without). act'(z) = sigmoid(z) [silu] + e sigmoid(z) (1 - sigmoid(z)).
+struct Gate {
+    uint32_t silu;
+    __device__ __forceinline__ explicit Gate(int gating) : silu(gating == GS_BLOCK_GATE_SILU ? ~0u : 0u) {
+        asm volatile("" : "+v"(silu));
+    }
+    __device__ __forceinline__ float factor(float z) const {
+        return __uint_as_float((__float_as_uint(z) & silu) | (__float_as_uint(1.0f) & ~silu));
+    }
+    __device__ __forceinline__ float slope(float e, float sg) const {
+        return fmaf(e, sg - sg * sg, __uint_as_float(__float_as_uint(sg) & silu));
+    }
+};
+
+// Where a row lies: rows are fewer than 2^31, so their place is found in 32 bits, and without a division where they
+// follow at one stride.
+struct Place {
+    uint32_t outer, inner;
+    __device__ __forceinline__ Place(int64_t row, int n) : outer((uint32_t)row), inner(0) {
+        if (n > 1) {
+            outer = (uint32_t)row / (uint32_t)n;
+            inner = (uint32_t)row - outer * (uint32_t)n;
+        }
+    }
+    __device__ __forceinline__ int64_t at(int64_t so, int64_t si) const { return outer * so + inner * si; }
+};
 
 // Rows of up to 2048 elements: 256 threads that keep the weights in registers.
 // Longer ones: 512 or 1024 threads, whose registers do not hold them; they are
 // read again for every row, from the caches.
-template <typename T, int V, int NV, int BLOCK>
+template <typename T, int V, int NV, int BLOCK, bool GATED>
 __global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geometry g) {
     typedef Rows<T, V, NV> R;
     constexpr int NE = R::NE;
@@ -271,28 +343,43 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geome
         }
     };
     if constexpr (KEEP) weights(true, true);
+    const float inv = 1.0f / (float)d.width;
+    const Gate gate(d.gating);
     for (int64_t base = (int64_t)blockIdx.x * sets; base < g.rows; base += (int64_t)gridDim.x * sets) {
         const int64_t row = KEEP ? base + threadIdx.x / lanes : base;
         const bool here = row < g.rows;
         rows.width = here ? d.width : 0;
         typename R::Raw y{}, z{}, res{};
         float x[NE];
-        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), y);
-        if (d.gating != GS_BLOCK_GATE_NONE) rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), z);
-        if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), res);
+        const Place place(row, d.inner);
+        rows.load(a.y, place.at(d.y_outer, d.y_inner), y);
+        if (GATED) rows.load(a.gate, place.at(d.gate_outer, d.gate_inner), z);
+        if (a.residual) rows.load(a.residual, place.at(d.residual_outer, d.residual_inner), res);
         rows.width = d.width;
         rows.settle(y);
         rows.settle(z);
         rows.settle(res);
 #pragma unroll
         for (int i = 0; i < NE; ++i) x[i] = y[i];
-        if (d.post != GS_BLOCK_NORM_NONE) normalise(rows, sum, d.post, d.eps, x);
+        // rows behind the last one hold zeros, which no eps may turn into others
+        const float eps = here ? d.eps : 1.0f;
+        if (d.post != GS_BLOCK_NORM_NONE) normalise(rows, sum, d.post, inv, eps, x);
         if constexpr (!KEEP) weights(true, false);
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            x[i] = fmaf(x[i], w[i], b[i]);
-            if (d.gating != GS_BLOCK_GATE_NONE) x[i] *= sigmoid(z[i]) * (d.gating == GS_BLOCK_GATE_SILU ? z[i] : 1.0f);
-            x[i] = a.residual ? fmaf(s[i], x[i], res[i]) : s[i] * x[i];
+        for (int i = 0; i < NE; ++i) x[i] = fmaf(x[i], w[i], b[i]);
+        if constexpr (GATED) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                x[i] *= sigmoid(z[i]) * gate.factor(z[i]);
+                if (NE > 8 && i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // 16 at once would not fit the registers
+            }
+        }
+        if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) x[i] = fmaf(s[i], x[i], res[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) x[i] *= s[i];
         }
         const int64_t at = row * d.width;
         if (!here) rows.width = 0;
@@ -300,10 +387,7 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geome
         if (d.pre != GS_BLOCK_NORM_NONE) {
             rows.width = d.width;
             if constexpr (!KEEP) weights(false, true);
-            // what lies past the width holds the biases
-#pragma unroll
-            for (int i = 0; i < NE; ++i) x[i] = rows.in(i) ? x[i] : 0.0f;
-            normalise(rows, sum, d.pre, d.eps, x);
+            normalise(rows, sum, d.pre, inv, eps, x);
 #pragma unroll
             for (int i = 0; i < NE; ++i) x[i] = fmaf(x[i], w2[i], b2[i]);
             if (here) rows.store(a.norm, at, x);
@@ -311,13 +395,20 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geome
     }
 }
 
-// The sums of a workgroup go to partial[workgroup][5][width]. BIAS: with a bias
-// of the post norm, or the gradient of one asked for.
-template <typename T, int V, int NV, int BLOCK, bool BIAS>
+// What a backward kernel is compiled for: a pre norm, a gate, and norms by RMS
+// without biases or any. Branches that all threads take alike cost no time by
+// themselves, but every value that lives across them costs registers: one
+// kernel for all takes 208 where that for a pre norm and a gate takes 194, that
+// for a gate alone 137 and that for neither 110 (both directions of 16384 x 2048
+// 222 -> 183 us, of 262144 x 128 125 -> 107).
+enum { kWithPre = 1, kWithGate = 2, kAnyNorm = 4 };
+
+// The sums of a workgroup go to partial[workgroup][5][width].
+template <typename T, int V, int NV, int BLOCK, int KIND>
 __global__ __launch_bounds__(BLOCK) void k_block_norm_bwd(BlockNormArgs a, Geometry g, float* partial) {
     typedef Rows<T, V, NV> R;
     constexpr int NE = R::NE;
-    constexpr bool KEEP = BLOCK == 256;
+    constexpr bool KEEP = BLOCK == 256, BIAS = (KIND & kAnyNorm) != 0;
     __shared__ float lds[2][16][2];
     const gs_block_norm& d = a.d;
     R rows;
@@ -337,28 +428,82 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_bwd(BlockNormArgs a, Geome
         weights();
         rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
     }
+    // The next rows are fetched in front of the work on these, where their registers allow it: two workgroups a CU that
+    // do so (16384 x 2048: 183 us) are as good as three that do not (186), and leave half the partial sums.
+    constexpr bool AHEAD = BLOCK < 1024;
     constexpr int NS = BIAS ? 5 : 3;
-    float acc[NS][NE];  // post_weight, scale, pre_weight, post_bias, pre_bias
+    // Sums over the rows: post_weight, scale, pre_weight, post_bias, pre_bias. 1024 threads have 128 registers each and
+    // keep the first of them in LDS, where a thread's 4 neighbours of one sum lie together (4096 x 8192 bf16: 182 us, from
+    // 248 with all in registers and 242 with 512 threads of 16 elements). Rows of more than 8192 spill all the same.
+    constexpr int NL = BLOCK < 1024 ? 0 : NE == 8 ? std::min(NS, 4) : 2;
+    __shared__ f32x4 held[NL ? NL * NE / 4 * BLOCK : 1];
+    float acc[NS][NE];
+    auto slot = [&](int k, int i) -> f32x4& { return held[(k * (NE / 4) + i / 4) * BLOCK + threadIdx.x]; };
 #pragma unroll
     for (int k = 0; k < NS; ++k)
 #pragma unroll
-        for (int i = 0; i < NE; ++i) acc[k][i] = 0.0f;
-    const bool gated = d.gating != GS_BLOCK_GATE_NONE, silu = d.gating == GS_BLOCK_GATE_SILU;
-    const bool pre = d.pre != GS_BLOCK_NORM_NONE;
-    for (int64_t base = (int64_t)blockIdx.x * sets; base < g.rows; base += (int64_t)gridDim.x * sets) {
+        for (int i = 0; i < NE; ++i) {
+            if (k >= NL)
+                acc[k][i] = 0.0f;
+            else if (i % 4 == 0)
+                slot(k, i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    auto add = [&](int k, const float (&x)[NE], const float (&y)[NE]) {
+        if (k >= NL) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) acc[k][i] = fmaf(x[i], y[i], acc[k][i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4) {
+                f32x4 t = slot(k, i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) t[j] = fmaf(x[i + j], y[i + j], t[j]);
+                slot(k, i) = t;
+            }
+        }
+    };
+    auto add_one = [&](int k, const float (&x)[NE]) {
+        if (k >= NL) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) acc[k][i] += x[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; i += 4) slot(k, i) += f32x4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+        }
+    };
+    constexpr bool gated = (KIND & kWithGate) != 0, pre = (KIND & kWithPre) != 0;
+    const Gate gate(d.gating);
+    const int post_kind = BIAS ? d.post : GS_BLOCK_NORM_RMS, pre_kind = BIAS ? d.pre : GS_BLOCK_NORM_RMS;
+    const float inv = 1.0f / (float)d.width;
+    struct In {
+        typename R::Raw y, z, res, gn, go;
+    };
+    auto fetch = [&](int64_t base, In& in) {
+        const int64_t row = KEEP ? base + threadIdx.x / lanes : base;
+        R from = rows;
+        from.width = row < g.rows ? d.width : 0;
+        const Place place(row, d.inner);
+        from.load(a.y, place.at(d.y_outer, d.y_inner), in.y);
+        if (gated) from.load(a.gate, place.at(d.gate_outer, d.gate_inner), in.z);
+        if (pre) {
+            if (a.residual) from.load(a.residual, place.at(d.residual_outer, d.residual_inner), in.res);
+            from.load(a.grad_norm, row * d.width, in.gn);
+        }
+        if (a.grad_out) from.load(a.grad_out, row * d.width, in.go);
+    };
+    In next{};
+    const int64_t stride = (int64_t)gridDim.x * sets;
+    if constexpr (AHEAD) fetch((int64_t)blockIdx.x * sets, next);
+    for (int64_t base = (int64_t)blockIdx.x * sets; base < g.rows; base += stride) {
         const int64_t row = KEEP ? base + threadIdx.x / lanes : base;
         const bool here = row < g.rows;
         const int64_t at = row * d.width;
-        rows.width = here ? d.width : 0;
-        typename R::Raw y{}, z{}, res{}, gn{}, go{};
         float x[NE], u[NE], dn[NE];
-        rows.load(a.y, row_at(row, d.inner, d.y_outer, d.y_inner), y);
-        if (gated) rows.load(a.gate, row_at(row, d.inner, d.gate_outer, d.gate_inner), z);
-        if (pre) {
-            if (a.residual) rows.load(a.residual, row_at(row, d.inner, d.residual_outer, d.residual_inner), res);
-            rows.load(a.grad_norm, at, gn);
-        }
-        if (a.grad_out) rows.load(a.grad_out, at, go);
+        if constexpr (!AHEAD) fetch(base, next);
+        In in = next;
+        typename R::Raw &y = in.y, &z = in.z, &res = in.res, &gn = in.gn, &go = in.go;
+        if constexpr (AHEAD)
+            if (base + stride < g.rows) fetch(base + stride, next);
         rows.width = d.width;
         rows.settle(y);
         rows.settle(z);
@@ -367,79 +512,89 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_bwd(BlockNormArgs a, Geome
         rows.settle(go);
 #pragma unroll
         for (int i = 0; i < NE; ++i) x[i] = y[i];
+        // rows behind the last one hold zeros, which no eps may turn into others
+        const float eps = here ? d.eps : 1.0f;
         float r = 1.0f;
-        if (d.post != GS_BLOCK_NORM_NONE) r = normalise(rows, sum, d.post, d.eps, x);
+        if (d.post != GS_BLOCK_NORM_NONE) r = normalise(rows, sum, post_kind, inv, eps, x);
         if constexpr (!KEEP) weights();
-        // the post norm's output, and that with the gate's factor
+        // the post norm's output
         auto normed = [&](int i) {
-            float t = x[i] * w[i];
-            if constexpr (BIAS) t += b[i];
-            return t;
+            if constexpr (BIAS) return fmaf(x[i], w[i], b[i]);
+            return x[i] * w[i];
         };
-        auto factor = [&](int i, float sg) { return silu ? z[i] * sg : sg; };
+        float sg[NE];
+        if (gated) {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) sg[i] = sigmoid(z[i]);
+        }
         if (pre) {
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                float v = normed(i);
-                if (gated) v *= factor(i, sigmoid(z[i]));
-                v = a.residual ? fmaf(s[i], v, res[i]) : s[i] * v;
-                u[i] = here && rows.in(i) ? v : 0.0f;
+            for (int i = 0; i < NE; ++i) u[i] = normed(i);
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < NE; ++i) u[i] *= sg[i] * gate.factor(z[i]);
             }
-            const float r2 = normalise(rows, sum, d.pre, d.eps, u);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) u[i] = fmaf(s[i], u[i], res[i]);  // no residual: zeros
+            const float r2 = normalise(rows, sum, pre_kind, inv, eps, u);
             if constexpr (!KEEP) rows.weights(a.pre_weight, d.weight_dtype, 1.0f, w2);
 #pragma unroll
-            for (int i = 0; i < NE; ++i) {
-                acc[2][i] = fmaf(gn[i], u[i], acc[2][i]);
-                if constexpr (BIAS) acc[4][i] += gn[i];
-                dn[i] = gn[i] * w2[i];
-            }
-            normalise_back(rows, sum, d.pre, r2, u, dn);
+            for (int i = 0; i < NE; ++i) dn[i] = gn[i];
+            add(2, dn, u);
+            if constexpr (BIAS) add_one(4, dn);
 #pragma unroll
-            for (int i = 0; i < NE; ++i) dn[i] = a.grad_out ? dn[i] + go[i] : dn[i];
+            for (int i = 0; i < NE; ++i) dn[i] *= w2[i];
+            normalise_back(rows, sum, pre_kind, inv, r2, u, dn);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) dn[i] += go[i];  // no grad_out: zeros
         } else {
 #pragma unroll
             for (int i = 0; i < NE; ++i) dn[i] = go[i];
         }
-        // past the width (and past the rows) everything upstream is 0, but for a layer norm's mean
-#pragma unroll
-        for (int i = 0; i < NE; ++i) dn[i] = here && rows.in(i) ? dn[i] : 0.0f;
         if (!here) rows.width = 0;
         if (a.grad_residual) rows.store(a.grad_residual, at, dn);
+        // dn: from the gradient of the sum to that of the post norm's output; u: the gate's
+        if (gated) {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) {
-            float t = normed(i), f = 1.0f;
-            const float ds = dn[i] * s[i];
-            if (gated) {
-                const float sg = sigmoid(z[i]);
-                f = factor(i, sg);
-                u[i] = ds * t * (silu ? sg * fmaf(z[i], 1.0f - sg, 1.0f) : sg * (1.0f - sg));
+            for (int i = 0; i < NE; ++i) u[i] = sg[i] * gate.factor(z[i]) * normed(i);
+            add(1, dn, u);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) {
+                const float ds = dn[i] * s[i], e = gate.factor(z[i]);
+                u[i] = ds * normed(i) * gate.slope(e, sg[i]);
+                dn[i] = ds * (sg[i] * e);
             }
-            acc[1][i] = fmaf(dn[i], f * t, acc[1][i]);
-            dn[i] = ds * f;
-            acc[0][i] = fmaf(dn[i], x[i], acc[0][i]);
-            if constexpr (BIAS) acc[3][i] += dn[i];
-            dn[i] *= w[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < NE; ++i) u[i] = normed(i);
+            add(1, dn, u);
+#pragma unroll
+            for (int i = 0; i < NE; ++i) dn[i] *= s[i];
         }
+        add(0, dn, x);
+        if constexpr (BIAS) add_one(3, dn);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) dn[i] *= w[i];
         if (gated && a.grad_gate) rows.store(a.grad_gate, at, u);
         if (d.post != GS_BLOCK_NORM_NONE) {
             rows.width = d.width;
-            normalise_back(rows, sum, d.post, r, x, dn);
+            normalise_back(rows, sum, post_kind, inv, r, x, dn);
             if (!here) rows.width = 0;
         }
         rows.store(a.grad_y, at, dn);
     }
     rows.width = d.width;
-    __shared__ float join[256 * 8];
+    __shared__ float join[KEEP ? 256 * 8 : 1];
     constexpr int kTo[5] = {0, 2, 3, 1, 4};
 #pragma unroll
     for (int k = 0; k < NS; ++k) {
         if (!a.sums[kTo[k]]) continue;
         float* const to = partial + ((int64_t)blockIdx.x * 5 + kTo[k]) * d.width;
-        if (sets == 1) {
+        if (!KEEP || sets == 1) {
 #pragma unroll
             for (int i = 0; i < NE; ++i)
-                if (rows.in(i)) to[rows.at(i / V) + i % V] = acc[k][i];
-        } else {  // the rows a workgroup holds at once, through LDS in their order
+                if (rows.in(i)) to[rows.at(i / V) + i % V] = k < NL ? slot(k, i)[i % 4] : acc[k][i];
+        } else if constexpr (KEEP) {  // the rows a workgroup holds at once, through LDS in their order
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < NE; ++i) join[i * BLOCK + threadIdx.x] = acc[k][i];
@@ -489,20 +644,43 @@ Geometry geometry(const gs_block_norm& d, bool backward) {
     g.lanes = lanes;
     g.block = std::max(lanes, 256);
     const int64_t sets = (g.rows + g.block / lanes - 1) / (g.block / lanes);
-    // Workgroups: what the chip holds at once forward; backward every one writes a row of sums.
-    const int64_t most = (backward ? (d.width > 1024 ? 512 : 1024) : 2048) * 256 / g.block;
+    // Workgroups: what the chip holds at once; more would wait for the first (and backward write more rows of sums).
+    const bool heavy = d.post == GS_BLOCK_NORM_LAYER || d.pre == GS_BLOCK_NORM_LAYER ||
+                       (d.pre != GS_BLOCK_NORM_NONE && d.gating != GS_BLOCK_GATE_NONE);
+    const int64_t most = backward ? std::max((heavy ? 512 : 768) * 256 / g.block, 256) : 2048 * 256 / g.block;
     g.grid = (int)std::min(sets, most);
     return g;
 }
 
 template <typename T, int V, int NV, int BLOCK>
 hipError_t go(const BlockNormArgs& a, const Geometry& g, float* scratch, bool back, hipStream_t stream) {
-    if (!back)
-        k_block_norm_fwd<T, V, NV, BLOCK><<<g.grid, BLOCK, 0, stream>>>(a, g);
-    else if (a.post_bias || a.sums[1] || a.sums[4])
-        k_block_norm_bwd<T, V, NV, BLOCK, true><<<g.grid, BLOCK, 0, stream>>>(a, g, scratch);
-    else
-        k_block_norm_bwd<T, V, NV, BLOCK, false><<<g.grid, BLOCK, 0, stream>>>(a, g, scratch);
+    const bool pre = a.d.pre != GS_BLOCK_NORM_NONE, gated = a.d.gating != GS_BLOCK_GATE_NONE;
+    if (!back) {
+        if (gated)
+            k_block_norm_fwd<T, V, NV, BLOCK, true><<<g.grid, BLOCK, 0, stream>>>(a, g);
+        else
+            k_block_norm_fwd<T, V, NV, BLOCK, false><<<g.grid, BLOCK, 0, stream>>>(a, g);
+        return hipGetLastError();
+    }
+    auto run = [&](auto kind) {
+        k_block_norm_bwd<T, V, NV, BLOCK, decltype(kind)::value><<<g.grid, BLOCK, 0, stream>>>(a, g, scratch);
+    };
+    auto kinds = [&](auto any) {
+        constexpr int K = decltype(any)::value;
+        if (pre && gated)
+            run(std::integral_constant<int, K | kWithPre | kWithGate>{});
+        else if (pre)
+            run(std::integral_constant<int, K | kWithPre>{});
+        else if (gated)
+            run(std::integral_constant<int, K | kWithGate>{});
+        else
+            run(std::integral_constant<int, K>{});
+    };
+    const bool any = a.post_bias || a.sums[1] || a.sums[4] || a.d.post == GS_BLOCK_NORM_LAYER || a.d.pre == GS_BLOCK_NORM_LAYER;
+    if (V == 1 || any)
+        kinds(std::integral_constant<int, kAnyNorm>{});
+    else if constexpr (V > 1)
+        kinds(std::integral_constant<int, 0>{});
     return hipGetLastError();
 }
 

@@ -226,3 +226,25 @@ def test_no_rows():
     assert gs.block_norm_fwd(y, post_weight=w, pre_weight=w, **k)["norm"].shape == (0, 16)
     back = gs.block_norm_bwd(y, y, grad_norm=y, post_weight=w, pre_weight=w, **k)
     assert (back["grad_post_weight"] == 0).all() and (back["grad_pre_weight"] == 0).all()
+
+
+@pytest.mark.parametrize("post,gating,pre", [("rms", "none", "none"), ("layer", "silu", "layer"), ("rms", "silu", "rms")])
+def test_rows_behind_the_last_with_no_eps(post, gating, pre):
+    """A workgroup's threads that have no row add nothing to the sums, also where eps is 0 and a row of zeros has no norm."""
+    for rows in (3, 33):
+        d, up = make((rows, 64), "f32", 41, post, gating, pre)
+        out = run(d, up, post, gating, pre, 0.0)
+        want = blocks.block_norm(**host(d), **host(up), post=post, gating=gating, pre=pre, eps=0.0)
+        check(out, want, "f32", rows)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("post,gating,pre", [("rms", "silu", "rms"), ("rms", "none", "rms"), ("rms", "sigmoid", "none"),
+                                             ("none", "none", "rms"), ("layer", "sigmoid", "layer")])
+@pytest.mark.parametrize("shape", [(1700, 500), (1100, 2048), (530, 2050), (520, 4100), (300, 9000)])
+def test_more_rows_than_workgroups(shape, post, gating, pre, bias, dtype):
+    """Every kind of backward kernel at every width, with rows that a workgroup takes one after another."""
+    d, up = make(shape, dtype, 43, post, gating, pre, bias=bias)
+    out = run(d, up, post, gating, pre, 1e-5)
+    check(out, blocks.block_norm(**host(d), **host(up), post=post, gating=gating, pre=pre, eps=1e-5), dtype, shape[0])
