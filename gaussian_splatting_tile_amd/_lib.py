@@ -16,7 +16,7 @@ GS_GATE_LINEAR, GS_GATE_SIGMOID = range(2)
 GS_RECURRENCE_CHUNK = 128
 GS_NORM_L2, GS_NORM_MAX = range(2)
 GS_ADAM_SKIP_NONFINITE = 1
-GS_DELTA_CHUNK, GS_DELTA_FEW, GS_DELTA_MAX_DIM = 64, 16, 128
+GS_DELTA_CHUNK, GS_DELTA_FEW, GS_DELTA_MAX_DIM = 64, 8, 128
 GS_BLOCK_NORM_NONE, GS_BLOCK_NORM_RMS, GS_BLOCK_NORM_LAYER = range(3)
 GS_BLOCK_GATE_NONE, GS_BLOCK_GATE_SIGMOID, GS_BLOCK_GATE_SILU = range(3)
 STATUS_NAMES = {0: "GS_OK", 1: "GS_ERR_INVALID", 2: "GS_ERR_CAPACITY", 3: "GS_ERR_OVERFLOW",

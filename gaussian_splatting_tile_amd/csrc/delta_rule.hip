@@ -104,9 +104,10 @@ __device__ __forceinline__ f32x4 col4(const float* m, int pitch, int row, int co
     return f32x4{p[0], p[pitch], p[2 * pitch], p[3 * pitch]};
 }
 
-// M = (I + A)^-1 of every chunk and head: its lower 16 x 16 tiles, row-major, in
-// to[b][chunk][h][10][16][16]. The diagonal tiles by forward substitution, the
-// others from them, M21 = -M22 A21 M11 for pairs of tiles and of pairs.
+// For the gradients of float32 inputs: M = (I + A)^-1 of every chunk and head,
+// its lower 16 x 16 tiles, row-major, in to[b][chunk][h][10][16][16]. The diagonal tiles by forward substitution, the
+// others from them, M21 = -M22 A21 M11 for pairs of tiles and of pairs. 18 us for
+// 195 of them (3 x 777 steps of 5 heads).
 template <typename T, int DK>
 __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs a, int chunks, float* to) {
     __shared__ float K[kC * (DK + 4)];
@@ -182,24 +183,6 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs a, int chunks, 
     for (int e = threadIdx.x; e < kLower; e += 256) {
         const int q = e >> 8, i = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, j = q - tri(i, 0);
         out[e] = M[(16 * i + (e >> 4 & 15)) * kPitch + 16 * j + (e & 15)];
-    }
-}
-
-// P of a chunk into LDS, its tiles spread over the waves of the workgroup.
-template <int DK>
-__device__ __forceinline__ void chunk_p(const float* Q, const float* K, const Chunk& s, float scale, float* P, int waves) {
-    const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-    for (int q = threadIdx.x >> 6; q < kTiles; q += waves) {
-        const int ti = q >= 6 ? 3 : q >= 3 ? 2 : q >= 1 ? 1 : 0, tj = q - tri(ti, 0);
-        f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-        for (int kt = 0; kt < DK / 16; ++kt)
-            acc = mma(row4<DK>(Q, 16 * ti + n, 16 * kt + 4 * g), row4<DK>(K, 16 * tj + n, 16 * kt + 4 * g), acc);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * ti + 4 * g + r, j = 16 * tj + n;
-            P[i * kPitch + j] = i >= j ? scale * decay(s, i, j) * acc[r] : 0.0f;
-        }
     }
 }
 
@@ -423,7 +406,11 @@ constexpr int kPrepThreads = 256;
 // Records of a chunk for all heads of a key head: the rows of keys and queries
 // (0 at padding), K K^T and Q K^T, then per head the decays, and M by forward
 // substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
-// and of pairs, in float32.
+// and of pairs, in float32. Bound by the work of one chunk after another in a
+// workgroup, most of it the substitution and the conversions; three workgroups a
+// compute unit (two with float32 inputs) run side by side in what LDS the rows
+// leave. 8192 steps of 16 key heads and 32 heads of 128, bf16: 99 us for 217 MB,
+// 2.2 TB/s.
 template <typename T, int DK, typename Record>
 __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
                                                                 Record* to) {
@@ -759,6 +746,10 @@ struct Segments {
 // what follows from it (R, U) never leave its registers, each product's result
 // is the next one's right operand. What the waves share is fetched a chunk
 // ahead. The columns of S are held scaled to at most about 1, S = unit * S.t.
+// Bound by the splitting of states into planes and by LDS, from which every wave
+// reads all operands of a chunk for its 16 columns (32 columns a wave would read
+// half as much and spill): 4.4 us a chunk where a compute unit holds 128
+// columns, of which the matrix instructions are 1.
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
                                                                const ForwardOf<T>* records, Segments seg) {
@@ -917,8 +908,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 
 // The state in front of every segment, in place of its B: S <- Phi S + B from
 // segment to segment, 16 columns a workgroup and 16 rows a wave, on the float32
-// matrix instructions. Bound by the latency of a step: Phi is fetched three
-// steps ahead.
+// matrix instructions. Bound by the latency of a step (2.3 us; its products are
+// 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 73 us.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg) {
     constexpr int KT = DK / 16, PITCH = DK + 4, AHEAD = 4;
@@ -970,7 +961,8 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
 
 // The gradients of the states, from the last chunk to the first, 16 columns a
 // wave, held and scaled as the states of k_delta_chain; behind[b][chunk][h]
-// receives the one behind each chunk.
+// receives the one behind each chunk. Bound as k_delta_chain: 5.2 us a chunk
+// (8 x 2048 steps of 16 heads of 128: 167 us).
 template <typename T, int DK, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
                                                                const Backward* records, float* behind) {
@@ -1099,7 +1091,9 @@ constexpr int kV = GS_DELTA_MAX_DIM;
 // The gradients of a chunk's queries, keys and gates from the states in front
 // and the gradients behind, for all heads of a key head, one after another.
 // First a wave takes 16 columns of the values (U and dR, to LDS), then 16 of
-// the keys.
+// the keys. Of float32 inputs, on the float32 matrix instructions: their two
+// planes with those of U, dR and the states would not fit LDS. 3 x 777 steps of
+// 5 heads of 96 x 80: 70 us.
 template <typename T, int DK>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int chunks, const float* inverse, const float* behind) {
     constexpr int KT = DK / 16, kThreads = 64 * kGradWaves;
@@ -1479,7 +1473,10 @@ __device__ __forceinline__ float sum_column(float m) {
 
 // k_delta_grad for 16-bit inputs, on float16 planes. A wave takes 16 columns of
 // the values and leaves U and dR in LDS, then tiles of the 64 x 64 matrices and
-// 16 columns of the keys, from rows of S and dS that it reads again.
+// 16 columns of the keys, from rows of S and dS that it reads again. One
+// workgroup fills a compute unit's LDS, so its waits show: 8 x 2048 steps of 8
+// key heads and 16 heads of 128: 265 us for 390 MB, 1.5 TB/s (with the float32
+// instructions 683 us).
 template <typename T, int DK>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, int chunks, const Keys<1, DK>* keys,
                                                                 const Backward* records, const float* behind) {
@@ -1908,6 +1905,12 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 // S^T q, are formed of the state in front of it (o = a S^T q + (q.k) u), so a
 // step has one exchange through LDS. Everything the steps read is fetched
 // before the first one.
+//
+// Measured: one step of 64 sequences of 16 heads of 128 x 128, whose states are
+// 134 MB: 29 us, 4.6 TB/s; of 1 sequence of 8 heads of 64: 5 us, a launch's
+// latency. A call of 8 steps takes as long as the chunks' kernels take for 9 to
+// 64 (64 sequences of 16 heads 75 us both, 4 sequences 20 and 28 us), one of 16
+// steps more (125 and 36 us).
 constexpr int kFewSteps = GS_DELTA_FEW;
 
 template <typename T, int V>
@@ -2030,7 +2033,9 @@ template <typename T>
 hipError_t steps(const DeltaArgs& a, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const bool wide = r.value_dim % 4 == 0 && !(((uintptr_t)a.h0 | (uintptr_t)a.h_last) & 15);
-    // columns of a workgroup: all, but fewer where that leaves compute units without work
+    // Columns of a workgroup: all, but fewer where that makes fewer than 512 of them. 16 heads of 128, one step: 8
+    // sequences 7.4 us with 32 columns (512 workgroups), 7.8 with 64, 9.0 with 128, 11.3 with 16; 32 sequences 16 us
+    // with 128 columns and 20 with 64; 1 sequence 5.4 us with 16 columns and 7.6 with 128.
     int slice = r.value_dim;
     const int most = wide ? 128 : 64;
     if (slice > most) slice = most;
@@ -2064,12 +2069,15 @@ size_t record_bytes(const gs_delta_rule& r) {
 
 // Segments of a sequence: enough workgroups for the chip, each of them long
 // enough for the walk over them and the first pass (more than the work of the
-// second) to pay.
+// second) to pay. Heads of 128 x 128, bf16, with segments and without: 4 heads
+// of 65536 steps 459 and 3912 us; 32 heads of 2048 steps 120 and 150 us, of 8192
+// 373 and 619; 64 heads of 2048 steps 208 and 181, of 8192 691 and 740; 85 heads
+// of 8192 steps 1049 and 827.
 constexpr int kUnits = 256;  // compute units
 Segments segments_of(const gs_delta_rule& r) {
     Segments s{1, chunks_of(r), nullptr, nullptr};
     const int64_t heads = (int64_t)r.batch * r.heads;
-    if (heads > kUnits / 3 || s.chunks < 32) return s;
+    if (heads > (s.chunks >= 128 ? kUnits / 4 : kUnits / 8) || s.chunks < 32) return s;
     const int most = (int)std::min<int64_t>((kUnits + heads - 1) / heads, 32);
     s.chunks = std::max((s.chunks + most - 1) / most, 8);
     s.count = (chunks_of(r) + s.chunks - 1) / s.chunks;

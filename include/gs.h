@@ -796,7 +796,7 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
  * formed over at most 64 steps and may leave float32's range there.
  * ------------------------------------------------------------------- */
 #define GS_DELTA_CHUNK 64
-#define GS_DELTA_FEW 16 /* steps up to which the forward needs no workspace */
+#define GS_DELTA_FEW 8 /* steps up to which the forward needs no workspace */
 #define GS_DELTA_MAX_DIM 128
 typedef struct {
     int32_t dtype;

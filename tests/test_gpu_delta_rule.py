@@ -5,6 +5,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+from gaussian_splatting_tile_amd._lib import GS_DELTA_FEW
 from oracle import blocks
 
 pytestmark = pytest.mark.gpu
@@ -66,7 +67,9 @@ def check(out, want, dtype, sums=1.0):
         if name == "terms":
             continue
         kind = "f32" if name in ("h_last", "grad_h0", "grad_log_decay", "grad_beta") else dtype
-        lost = blocks.LOST * want["terms"] if name == "o" and dtype == "bf16" and w.shape[1] > 16 else 0.0
+        # LOST is derived for the kernels that work in chunks, which take what is more than a few steps
+        chunked = w.shape[1] > GS_DELTA_FEW
+        lost = blocks.LOST * want["terms"] if name == "o" and dtype == "bf16" and chunked else 0.0
         far = blocks.off(out[name].double().cpu().numpy(), w, kind, sums, lost=lost)
         assert far <= 1, (name, far)
 
@@ -74,6 +77,7 @@ def check(out, want, dtype, sums=1.0):
 # B, T, Hk, H, dk, dv, flags
 CASES = [
     (1, 1, 1, 1, 16, 16, ""), (2, 1, 2, 4, 128, 128, "p"), (3, 2, 1, 3, 17, 33, ""), (2, 5, 2, 2, 64, 64, "r"),
+    (3, 8, 2, 4, 128, 100, "lr"), (3, 9, 2, 4, 128, 100, "lr"), (2, 100, 2, 6, 128, 128, "p"),
     (1, 15, 1, 1, 1, 1, ""), (2, 16, 1, 2, 8, 128, "p"), (1, 17, 2, 2, 128, 8, ""), (2, 63, 1, 1, 40, 24, "r"),
     (1, 64, 2, 4, 64, 64, "p"), (1, 65, 1, 2, 64, 128, "r"), (4, 130, 2, 2, 128, 64, "lr"), (3, 200, 2, 6, 24, 40, "lrp"),
     (1, 257, 1, 1, 100, 128, "p"), (2, 192, 2, 4, 128, 128, "lr"), (5, 129, 1, 2, 72, 56, "l"),
