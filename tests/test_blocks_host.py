@@ -182,3 +182,22 @@ def test_block_norm_refuses_tensors():
         gs.block_norm_fwd(on(0, 3, 4, 5, 8).transpose(0, 2), residual=on(0, 5, 4, 3, 16)[..., :8])
     with pytest.raises(ValueError, match="stream belongs to cuda:1"):
         gs.block_norm_fwd(y, stream=STREAM)
+
+
+def test_delta_rule_addresses(gs):
+    """A chunk's rows are addressed in 32 bits: wider strides are refused, as is a workspace that is not aligned."""
+    from gaussian_splatting_tile_amd import _lib
+    wide = (1 << 22) + 1
+    for kw in (dict(q_step=wide), dict(k_step=wide), dict(v_step=wide)):
+        r = _delta(**kw)
+        assert gs.gs_delta_rule_fwd(ctypes.byref(r), D, D, D, D, D, None, P(512), None, None, D, 1 << 40, None) == _lib.GS_ERR_INVALID
+        assert b"stride" in gs.gs_last_error()
+        assert gs.gs_delta_rule_scratch_bytes(ctypes.byref(r), 0) == 0
+
+
+def test_block_norm_weights_type(gs):
+    """Weights are float32 or of the rows' type."""
+    from gaussian_splatting_tile_amd import _lib
+    d = _norm(dtype=_lib.GS_BF16, weight_dtype=_lib.GS_F16)
+    assert gs.gs_block_norm_fwd(ctypes.byref(d), D, D, None, None, None, None, None, None, P(512), P(768), None) == _lib.GS_ERR_INVALID
+    assert b"weight_dtype" in gs.gs_last_error()
