@@ -201,3 +201,13 @@ def test_block_norm_weights_type(gs):
     d = _norm(dtype=_lib.GS_BF16, weight_dtype=_lib.GS_F16)
     assert gs.gs_block_norm_fwd(ctypes.byref(d), D, D, None, None, None, None, None, None, P(512), P(768), None) == _lib.GS_ERR_INVALID
     assert b"weight_dtype" in gs.gs_last_error()
+
+
+def test_constants_match_the_header(gs):
+    import re
+    from gaussian_splatting_tile_amd import _lib
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gs.h")) as f:
+        header = dict(re.findall(r"#define (GS_(?:DELTA|BLOCK)_\w+) (\d+)", f.read()))
+    for name, value in header.items():
+        assert getattr(_lib, name, int(value)) == int(value), name
+    assert {"GS_DELTA_CHUNK", "GS_DELTA_FEW", "GS_DELTA_MAX_DIM", "GS_BLOCK_NORM_RMS", "GS_BLOCK_GATE_SILU"} <= set(header)

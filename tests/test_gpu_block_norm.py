@@ -248,3 +248,18 @@ def test_more_rows_than_workgroups(shape, post, gating, pre, bias, dtype):
     d, up = make(shape, dtype, 43, post, gating, pre, bias=bias)
     out = run(d, up, post, gating, pre, 1e-5)
     check(out, blocks.block_norm(**host(d), **host(up), post=post, gating=gating, pre=pre, eps=1e-5), dtype, shape[0])
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie more than 2^31 elements apart in one buffer."""
+    import torch
+    d, up = make((3, 64), "bf16", 47, "rms", "silu", "rms")
+    far = 1 << 31
+    buffer = torch.empty(2 * far + 4096, dtype=torch.bfloat16, device="cuda")
+    e = dict(d)
+    for i, k in enumerate(("y", "gate", "residual")):
+        e[k] = buffer.as_strided((3, 64), (far, 1), i * 1024 + i)
+        e[k].copy_(d[k])
+    got, want = run(e, up, "rms", "silu", "rms", 1e-6), run(d, up, "rms", "silu", "rms", 1e-6)
+    for k in want:
+        assert want[k] is None or torch.equal(got[k], want[k]), k

@@ -263,3 +263,22 @@ def test_empty():
                              grad_last=h)
     assert torch.equal(back["grad_h0"], h)
     assert gs.delta_rule_fwd(e(0, 3, 1, 8), e(0, 3, 1, 8), e(0, 3, 2, 8), e(0, 3, 2), e(0, 3, 2))["o"].shape == (0, 3, 2, 8)
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_offsets_past_32_bits(T):
+    """Sequences and heads that lie more than 2^31 elements apart in one buffer."""
+    import torch
+    d, up = make(2, T, 1, 2, 32, 48, "bf16", 47)
+    far = 1 << 31
+    buffer = torch.empty(2 * far + (1 << 16), dtype=torch.bfloat16, device="cuda")
+    e = dict(d)
+    for i, (k, by) in enumerate((("q", "batch"), ("k", "batch"), ("v", "head"))):
+        B, _, H, dim = d[k].shape
+        strides = (far, H * dim, dim, 1) if by == "batch" else (T * dim, dim, far, 1)
+        e[k] = buffer.as_strided(d[k].shape, strides, i << 14)
+        e[k].copy_(d[k])
+    got, want = run(e, up), run(d, up)
+    for k in want:
+        if k != "ckpt":
+            assert torch.equal(got[k], want[k]), k
