@@ -907,11 +907,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 }
 
 // The state in front of every segment, in place of its B: S <- Phi S + B from
-// segment to segment, 16 columns a workgroup and 16 rows a wave, on the float32
+// segment to segment (`back`: from the last to the first, the gradient behind), 16 columns a workgroup and 16 rows a wave, on the float32
 // matrix instructions. Bound by the latency of a step (2.3 us; its products are
 // 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 73 us.
 template <int DK>
-__global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg) {
+__global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg, const float* start, bool back) {
     constexpr int KT = DK / 16, PITCH = DK + 4, AHEAD = 4;
     __shared__ float L[2][16 * PITCH];  // S by columns
     const gs_delta_rule& d = a.r;
@@ -925,8 +925,9 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
     const uint32_t from = (uint32_t)(left * d.key_dim + 4 * g) * 4u;
     f32x4 A[AHEAD][KT], B[AHEAD], S;
     // What is read past a row's end meets rows of S that are 0.
+    auto place = [&](int z) { return (int64_t)(back ? seg.count - 1 - z : z); };
     auto fetch = [&](int z, f32x4 (&x)[KT], f32x4& y) {
-        const Buffer p(phi + (int64_t)z * square, square * 4), f(front + (int64_t)z * size, size * 4);
+        const Buffer p(phi + place(z) * square, square * 4), f(front + place(z) * size, size * 4);
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt)
             x[kt] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(p.r, from + 64 * kt, 0, 0));
@@ -934,7 +935,7 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
         for (int r = 0; r < 4; ++r) y[r] = f.load<float>(at + r * d.value_dim * 4);
     };
     {
-        const Buffer h(a.h0 + head * size, a.h0 ? size * 4 : 0);
+        const Buffer h(start + head * size, start ? size * 4 : 0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) S[r] = h.load<float>(at + r * d.value_dim * 4);
     }
@@ -949,7 +950,7 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
             float* const s = L[x & 1];
             *(f32x4*)(s + n * PITCH + row) = S;
             __syncthreads();
-            const Buffer f(front + (int64_t)(z + x) * size, size * 4);
+            const Buffer f(front + place(z + x) * size, size * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) f.store(at + r * d.value_dim * 4, S[r]);
             f32x4 acc[2] = {B[x], {0, 0, 0, 0}};
@@ -962,10 +963,11 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
 // The gradients of the states, from the last chunk to the first, 16 columns a
 // wave, held and scaled as the states of k_delta_chain; behind[b][chunk][h]
 // receives the one behind each chunk. Bound as k_delta_chain: 5.2 us a chunk
-// (8 x 2048 steps of 16 heads of 128: 167 us).
-template <typename T, int DK, int WAVES>
+// (8 x 2048 steps of 16 heads of 128: 167 us). In segments as it is: the
+// gradient in front of a segment is Phi^T of that behind it and a B of its own.
+template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
-                                                               const Backward* records, float* behind) {
+                                                               const Backward* records, float* behind, Segments seg) {
     constexpr int NX = kPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
     typedef Operand<NX, DK> O;
     __shared__ Keys<NX, DK> kq;
@@ -976,9 +978,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
     const gs_delta_rule& d = a.r;
     const int b = blockIdx.x / d.heads, h = blockIdx.x % d.heads, kh = h / (d.heads / d.key_heads);
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-    const int col0 = (blockIdx.y * WAVES + w) * 16, col = col0 + n;
-    const bool on = col < d.value_dim;
-    const int len = length_of(d, b), mine = (len + kC - 1) / kC;
+    // behind the values' columns, in workgroups of their own, those of Phi^T
+    const int blocks = (d.value_dim + 16 * WAVES - 1) / (16 * WAVES);
+    const bool values = OUT || (int)blockIdx.y < blocks;
+    const int col0 = ((values ? blockIdx.y : blockIdx.y - blocks) * WAVES + w) * 16, col = col0 + n;
+    const bool on = col < (values ? d.value_dim : d.key_dim);
+    const int len = length_of(d, b), z = blockIdx.z;
+    const int c0 = z * seg.chunks, c1 = min((len + kC - 1) / kC, c0 + seg.chunks);
     const int64_t size = (int64_t)d.key_dim * d.value_dim, head = (int64_t)b * d.heads + h;
     const int64_t o_step = (int64_t)d.heads * d.value_dim, first_o = ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
     const T* const go = (const T*)a.grad_o + first_o;
@@ -987,9 +993,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
     const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
     Column<KT> S;
     float unit = 1.0f;
-    S.load(a.grad_last ? a.grad_last + head * size : nullptr, on, col, d.key_dim, d.value_dim);
-    if (on)
-        for (int t = mine * kC + g; t < d.steps; t += 4) gv[t * o_step + col] = (T)0.0f;
+    if constexpr (OUT) {
+        const float* const from = seg.count > 1 ? seg.front + (head * seg.count + z) * size
+                                  : a.grad_last ? a.grad_last + head * size : nullptr;
+        S.load(from, on, col, d.key_dim, d.value_dim);
+        // the steps of the segment that are padding behind its last chunk
+        const int end = z + 1 < seg.count ? min((c0 + seg.chunks) * kC, d.steps) : d.steps;
+        if (on)
+            for (int t = max(c0, c1) * kC + g; t < end; t += 4) gv[t * o_step + col] = (T)0.0f;
+    } else {
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S.t[t][r] = !values && key_row(t, g, r) == col ? 1.0f : 0.0f;
+    }
     Copy<sizeof(Keys<NX, DK>), kThreads> fk;
     Copy<sizeof(Backward) - SKIP, kThreads> fr;
     Values<T> fo;
@@ -998,30 +1015,31 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         fr.load((const char*)(first + (int64_t)c * d.heads) + SKIP);
         fk.load(first_keys + (int64_t)c * d.key_heads);
         __builtin_amdgcn_sched_barrier(0);  // the values last: when they are there, so is the rest
-        fo.load(go + t0 * o_step, o_step, len - t0, on, col, d.value_dim);
+        if (values) fo.load(go + t0 * o_step, o_step, len - t0, on, col, d.value_dim);
     };
     // taken over before a chunk's stores, with which they would be waited for
     f32x4 next[4];
     auto take = [&] {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) next[e / 4][e % 4] = fo[e];
+        for (int e = 0; e < 16; ++e) next[e / 4][e % 4] = values ? fo[e] : 0.0f;
     };
-    if (mine > 0) {
-        fetch(mine - 1);
+    if (c0 < c1) {
+        fetch(c1 - 1);
         take();
     }
     const f32x4 zero = {0, 0, 0, 0};
-    for (int c = mine - 1; c >= 0; --c) {
+    for (int c = c1 - 1; c >= c0; --c) {
         const Lane l = Lane::here();
         const int g = l.g, col = col0 + l.n;
         const int t0 = c * kC;
-        S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit, l);
+        if constexpr (OUT)
+            S.store(behind + (((int64_t)b * chunks + c) * d.heads + h) * size, on, col, d.key_dim, d.value_dim, unit, l);
         __syncthreads();
         fr.store(part);
         fk.store(&kq);
         f32x4 dO[4] = {next[0], next[1], next[2], next[3]};
         __syncthreads();
-        if (c > 0) fetch(c - 1);
+        if (c > c0) fetch(c - 1);
         const Scale big(over_column(largest(S.t)));
         f32x4 dU[4] = {zero, zero, zero, zero}, x[4] = {zero, zero, zero, zero};
 #pragma unroll
@@ -1063,7 +1081,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             }
         }
         take();
-        Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
+        if constexpr (OUT)
+            Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
         const float whole = rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
         const float keep = whole * es.by;
@@ -1082,7 +1101,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             }
         }
     }
-    if (a.grad_h0) S.store(a.grad_h0 + head * size, on, col, d.key_dim, d.value_dim, unit);
+    if constexpr (OUT) {
+        if (a.grad_h0 && z == 0) S.store(a.grad_h0 + head * size, on, col, d.key_dim, d.value_dim, unit);
+    } else {
+        const int64_t at = head * seg.count + z;
+        S.store(values ? seg.front + at * size : seg.phi + at * d.key_dim * d.key_dim, on, col, d.key_dim,
+                values ? d.value_dim : d.key_dim, unit);
+    }
 }
 
 constexpr int kGradWaves = 8;
@@ -2072,7 +2097,8 @@ size_t record_bytes(const gs_delta_rule& r) {
 // second) to pay. Heads of 128 x 128, bf16, with segments and without: 4 heads
 // of 65536 steps 459 and 3912 us; 32 heads of 2048 steps 120 and 150 us, of 8192
 // 373 and 619; 64 heads of 2048 steps 208 and 181, of 8192 691 and 740; 85 heads
-// of 8192 steps 1049 and 827.
+// of 8192 steps 1049 and 827. The backward of 4 heads of 8192 steps 216 and 634
+// us, of 32 heads 999 and 1247, of 64 heads 1905 and 1890.
 constexpr int kUnits = 256;  // compute units
 Segments segments_of(const gs_delta_rule& r) {
     Segments s{1, chunks_of(r), nullptr, nullptr};
@@ -2120,7 +2146,7 @@ hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
             chain<T, DK, 4, false>(a, chunks, scratch, seg, stream);
         else
             chain<T, DK, 8, false>(a, chunks, scratch, seg, stream);
-        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg);
+        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg, a.h0, false);
     }
     if (narrow(groups, r.value_dim))
         chain<T, DK, 4, true>(a, chunks, scratch, seg, stream);
@@ -2129,25 +2155,45 @@ hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     return hipGetLastError();
 }
 
+template <typename T, int DK, int WAVES, bool OUT>
+void chain_back(const DeltaArgs& a, int chunks, const void* scratch, float* behind, const Segments& seg, hipStream_t stream) {
+    const gs_delta_rule& r = a.r;
+    constexpr int WIDE = 16 * WAVES;
+    const int blocks = (r.value_dim + WIDE - 1) / WIDE + (OUT ? 0 : (r.key_dim + WIDE - 1) / WIDE);
+    k_delta_back<T, DK, WAVES, OUT><<<dim3(r.batch * r.heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(
+        a, chunks, (const Keys<kPlanes<T>, DK>*)scratch, (const Backward*)((const char*)scratch + key_bytes(r)), behind, seg);
+}
+
 template <typename T, int DK>
 hipError_t backward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
-    const int chunks = chunks_of(r);
+    const int chunks = chunks_of(r), heads = r.batch * r.heads;
     auto* const keys = (Keys<kPlanes<T>, DK>*)scratch;
     auto* const records = (Backward*)((char*)scratch + key_bytes(r));
     float* const behind = (float*)((char*)records + back_record_bytes(r));
     if (chunks)
         k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(a, chunks, keys, records);
-    if (narrow((int64_t)r.batch * r.heads, r.value_dim))
-        k_delta_back<T, DK, 4><<<dim3(r.batch * r.heads, (r.value_dim + 63) / 64), 256, 0, stream>>>(a, chunks, keys, records, behind);
+    Segments seg = segments_of(r);
+    const int64_t groups = (int64_t)heads * seg.count;
+    float* const inverse = behind + behind_floats(r);
+    if (seg.count > 1) {
+        seg.front = inverse + (r.dtype == GS_F32 ? inverse_floats(r) : 0);
+        seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
+        if (narrow(groups * 2, std::max(r.value_dim, r.key_dim)))
+            chain_back<T, DK, 4, false>(a, chunks, scratch, behind, seg, stream);
+        else
+            chain_back<T, DK, 8, false>(a, chunks, scratch, behind, seg, stream);
+        k_delta_join<DK><<<dim3(heads, (r.value_dim + 15) / 16), DK * 4, 0, stream>>>(a, seg, a.grad_last, true);
+    }
+    if (narrow(groups, r.value_dim))
+        chain_back<T, DK, 4, true>(a, chunks, scratch, behind, seg, stream);
     else
-        k_delta_back<T, DK, 8><<<r.batch * r.heads, 512, 0, stream>>>(a, chunks, keys, records, behind);
+        chain_back<T, DK, 8, true>(a, chunks, scratch, behind, seg, stream);
     if (chunks) {
         const int grid = r.batch * chunks * r.key_heads;
         if constexpr (sizeof(T) == 2) {
             k_delta_grads<T, DK><<<grid, 64 * kGradWaves, 0, stream>>>(a, chunks, keys, records, behind);
         } else {
-            float* const inverse = behind + behind_floats(r);
             k_delta_inverse<T, DK><<<r.batch * chunks * r.heads, 256, 0, stream>>>(a, chunks, inverse);
             k_delta_grad<T, DK><<<grid, 64 * kGradWaves, 0, stream>>>(a, chunks, inverse, behind);
         }
@@ -2176,7 +2222,7 @@ size_t delta_rule_scratch_bytes(const gs_delta_rule& r, bool backward) {
     if (!backward && r.steps <= kFewSteps) return 0;
     if (!backward) return key_bytes(r) + record_bytes(r) + segment_bytes(r);
     return key_bytes(r) + back_record_bytes(r) + behind_floats(r) * sizeof(float) +
-           (r.dtype == GS_F32 ? inverse_floats(r) * sizeof(float) : 0);
+           (r.dtype == GS_F32 ? inverse_floats(r) * sizeof(float) : 0) + segment_bytes(r);
 }
 
 hipError_t launch_delta_rule_fwd(const DeltaArgs& a, void* scratch, hipStream_t stream) {
