@@ -406,11 +406,11 @@ constexpr int kPrepThreads = 256;
 // Records of a chunk for all heads of a key head: the rows of keys and queries
 // (0 at padding), K K^T and Q K^T, then per head the decays, and M by forward
 // substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
-// and of pairs, in float32. Bound by the work of one chunk after another in a
-// workgroup, most of it the substitution and the conversions; three workgroups a
-// compute unit (two with float32 inputs) run side by side in what LDS the rows
-// leave. 8192 steps of 16 key heads and 32 heads of 128, bf16: 99 us for 217 MB,
-// 2.2 TB/s.
+// and of pairs, in float32. Bound by the waits between its steps (three in four
+// of its cycles), which three workgroups a compute unit (two with float32 inputs)
+// share. All rows are fetched before the first is used, and as many heads' gates
+// as there are waves are formed meanwhile (one head after another: 100 us). 8192
+// steps of 16 key heads and 32 heads of 128, bf16: 90 us for 217 MB, 2.4 TB/s.
 template <typename T, int DK, typename Record>
 __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
                                                                 Record* to) {
@@ -426,17 +426,17 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
     float* const M = sh.mp[0];
     float* const P = sh.mp[1];
     __shared__ float k_back[kC], q_back[kC], most[2][4];
-    __shared__ Chunk s;
+    constexpr int WAVES = kPrepThreads / 64;
+    __shared__ Chunk gates[WAVES];  // of as many heads, a wave each
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
     const int len = length_of(d, b), t0 = c * kC, rows = len - t0, group = d.heads / d.key_heads;
     if (rows <= 0) return;
     const int w = threadIdx.x >> 6;
-    auto stage = [&](const T* p, int64_t step, f16* m, f16* out, float* back) {
-        typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
-        constexpr int PIECES = O::PIECES, BY = kPrepThreads / PIECES, JOBS = kC / BY;
-        const int at = threadIdx.x % PIECES, dim = at * 8;
-        T8 x[JOBS];
+    typedef T T8 __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+    constexpr int PIECES = O::PIECES, BY = kPrepThreads / PIECES, JOBS = kC / BY;
+    const int at = threadIdx.x % PIECES, dim = at * 8;
+    auto fetch = [&](const T* p, int64_t step, T8 (&x)[JOBS]) {
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
             const int t = threadIdx.x / PIECES + j * BY;
@@ -450,6 +450,8 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
                     if (dim + i < d.key_dim) x[j][i] = from[i];
             }
         }
+    };
+    auto stage = [&](const T8 (&x)[JOBS], f16* m, f16* out, float* back) {
 #pragma unroll
         for (int j = 0; j < JOBS; ++j) {
             const int t = threadIdx.x / PIECES + j * BY;
@@ -467,8 +469,14 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
         }
     };
     Keys<NX, DK>* const key = keys + ((int64_t)b * chunks + c) * d.key_heads + kh;
-    stage((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, kq.K, key->K, k_back);
-    stage((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, kq.Q, key->Q, q_back);
+    {
+        T8 k[JOBS], q[JOBS];
+        fetch((const T*)a.k + b * d.k_batch + t0 * d.k_step + kh * d.k_head, d.k_step, k);
+        fetch((const T*)a.q + b * d.q_batch + t0 * d.q_step + kh * d.q_head, d.q_step, q);
+        if (w < group) load_gates(a, b, kh * group + w, t0, len, gates[w]);
+        stage(k, kq.K, key->K, k_back);
+        stage(q, kq.Q, key->Q, q_back);
+    }
     __syncthreads();
     const f32x4 zero = {0, 0, 0, 0};
     f32x4 kk[4], qk[4];  // of row tile w
@@ -497,8 +505,11 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
         const int h = kh * group + hh;
         Record* const out = to + ((int64_t)b * chunks + c) * d.heads + h;
         if (hh) __syncthreads();
-        if (w == 0) load_gates(a, b, h, t0, len, s);
-        __syncthreads();
+        if (hh && hh % WAVES == 0) {
+            if (hh + w < group) load_gates(a, b, h + w, t0, len, gates[w]);
+            __syncthreads();
+        }
+        const Chunk& s = gates[hh % WAVES];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (j <= w)

@@ -78,6 +78,7 @@ def check(out, want, dtype, sums=1.0):
 CASES = [
     (1, 1, 1, 1, 16, 16, ""), (2, 1, 2, 4, 128, 128, "p"), (3, 2, 1, 3, 17, 33, ""), (2, 5, 2, 2, 64, 64, "r"),
     (3, 8, 2, 4, 128, 100, "lr"), (3, 9, 2, 4, 128, 100, "lr"), (2, 100, 2, 6, 128, 128, "p"),
+    (2, 150, 1, 5, 48, 40, "lr"), (1, 70, 1, 9, 128, 32, ""),
     (1, 15, 1, 1, 1, 1, ""), (2, 16, 1, 2, 8, 128, "p"), (1, 17, 2, 2, 128, 8, ""), (2, 63, 1, 1, 40, 24, "r"),
     (1, 64, 2, 4, 64, 64, "p"), (1, 65, 1, 2, 64, 128, "r"), (4, 130, 2, 2, 128, 64, "lr"), (3, 200, 2, 6, 24, 40, "lrp"),
     (1, 257, 1, 1, 100, 128, "p"), (2, 192, 2, 4, 128, 128, "lr"), (5, 129, 1, 2, 72, 56, "l"),
@@ -282,3 +283,18 @@ def test_offsets_past_32_bits(T):
     for k in want:
         if k != "ckpt":
             assert torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_state_in_place_in_segments(dtype):
+    """h_last in h0's place where a sequence is cut into segments, forward; and the backward from that state."""
+    import torch
+    import gaussian_splatting_tile_amd as gs
+    d, up = make(1, 2300, 1, 2, 64, 48, dtype, 53)
+    want = run(d, up)
+    h = d["h0"].clone()
+    out = gs.delta_rule_fwd(**dict(d, h0=h), out=dict(h_last=h), checkpoints=True)
+    assert torch.equal(h, want["h_last"]) and torch.equal(out["o"], want["o"])
+    back = gs.delta_rule_bwd(**d, ckpt=out["ckpt"], **up)
+    for k in back:
+        assert torch.equal(back[k], want[k]), k
