@@ -406,7 +406,7 @@ constexpr int kPrepThreads = 256;
 // Records of a chunk for all heads of a key head: the rows of keys and queries
 // (0 at padding), K K^T and Q K^T, then per head the decays, and M by forward
 // substitution in the diagonal tiles and M21 = -M22 A21 M11 for pairs of tiles
-// and of pairs, in float32. Bound by the waits between its steps (three in four
+// and of pairs, in float32. Bound by the waits between its steps (two in three
 // of its cycles), which three workgroups a compute unit (two with float32 inputs)
 // share. All rows are fetched before the first is used, and as many heads' gates
 // as there are waves are formed meanwhile (one head after another: 100 us). 8192
