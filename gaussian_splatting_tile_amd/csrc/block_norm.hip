@@ -18,10 +18,10 @@
 // workgroups by a second launch, in a fixed order.
 //
 // Measured (a copy of as many bytes moves 5.06 TB/s): forward with residual,
-// sigmoid gate and both norms, 16384 x 2048 bf16, 335 MB: 64 us; its backward,
-// 537 MB: 117 us, 4.6 TB/s; 8192 x 8192 f16 forward, 671 MB: 136 us, 4.9 TB/s;
-// 262144 x 128 bf16 with a silu gate, both directions, 537 MB: 103 us. One of
-// 64 x 2048 takes 4.5 us, a launch's latency.
+// sigmoid gate and both norms, 16384 x 2048 bf16, 335 MB: 64 us, 5.2 TB/s; its
+// backward, 537 MB: 122 us, 4.4 TB/s; 8192 x 8192 f16 forward, 671 MB: 136 us,
+// 4.9 TB/s; 262144 x 128 bf16 with a silu gate, both directions, 537 MB: 103 us.
+// One of 64 x 2048 takes 4.2 us, a launch's latency.
 #include <algorithm>
 #include <type_traits>
 

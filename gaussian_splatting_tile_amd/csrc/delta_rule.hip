@@ -409,8 +409,9 @@ constexpr int kPrepThreads = 256;
 // and of pairs, in float32. Bound by the waits between its steps (two in three
 // of its cycles), which three workgroups a compute unit (two with float32 inputs)
 // share. All rows are fetched before the first is used, and as many heads' gates
-// as there are waves are formed meanwhile (one head after another: 100 us). 8192
-// steps of 16 key heads and 32 heads of 128, bf16: 90 us for 217 MB, 2.4 TB/s.
+// as there are waves are formed meanwhile (a call of 8192 steps of 16 key heads
+// and 32 heads of 128, bf16: 329 us, 344 with one after another). Of that call
+// 96 us for 217 MB, 2.3 TB/s.
 template <typename T, int DK, typename Record>
 __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
                                                                 Record* to) {
@@ -920,7 +921,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 // The state in front of every segment, in place of its B: S <- Phi S + B from
 // segment to segment (`back`: from the last to the first, the gradient behind), 16 columns a workgroup and 16 rows a wave, on the float32
 // matrix instructions. Bound by the latency of a step (2.3 us; its products are
-// 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 73 us.
+// 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 75 us.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg, const float* start, bool back) {
     constexpr int KT = DK / 16, PITCH = DK + 4, AHEAD = 4;
@@ -974,7 +975,7 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
 // The gradients of the states, from the last chunk to the first, 16 columns a
 // wave, held and scaled as the states of k_delta_chain; behind[b][chunk][h]
 // receives the one behind each chunk. Bound as k_delta_chain: 5.2 us a chunk
-// (8 x 2048 steps of 16 heads of 128: 167 us). In segments as it is: the
+// (8 x 2048 steps of 16 heads of 128: 169 us). In segments as it is: the
 // gradient in front of a segment is Phi^T of that behind it and a B of its own.
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
