@@ -760,8 +760,10 @@ struct Segments {
 // ahead. The columns of S are held scaled to at most about 1, S = unit * S.t.
 // Bound by the splitting of states into planes and by LDS, from which every wave
 // reads all operands of a chunk for its 16 columns (32 columns a wave would read
-// half as much and spill): 4.4 us a chunk where a compute unit holds 128
-// columns, of which the matrix instructions are 1.
+// half as much and spill): 4.4 us a chunk where a compute unit holds 64 columns
+// (8 x 2048 steps of 16 heads: 144 us) and 6.5 where it holds 128 (8192 steps of
+// 32 heads in 8 segments: 104 us), of which the matrix instructions are 0.7 and
+// 1.4.
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
                                                                const ForwardOf<T>* records, Segments seg) {
@@ -1512,8 +1514,8 @@ __device__ __forceinline__ float sum_column(float m) {
 // the values and leaves U and dR in LDS, then tiles of the 64 x 64 matrices and
 // 16 columns of the keys, from rows of S and dS that it reads again. One
 // workgroup fills a compute unit's LDS, so its waits show: 8 x 2048 steps of 8
-// key heads and 16 heads of 128: 265 us for 390 MB, 1.5 TB/s (with the float32
-// instructions 683 us).
+// key heads and 16 heads of 128: 265 us, the chunk of a head reading 128 KB of
+// states. (With addresses held in registers through the loop it spilled: 683 us.)
 template <typename T, int DK>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, int chunks, const Keys<1, DK>* keys,
                                                                 const Backward* records, const float* behind) {
