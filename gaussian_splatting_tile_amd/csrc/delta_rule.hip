@@ -833,7 +833,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         __syncthreads();
         if (c + 1 < c1) fetch(c + 1);
         f32x4 R[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};  // K S, then R; Q S, then O
-        const Scale big(over_column(largest(S.t)));
+        const float top = over_column(largest(S.t));
+        const Scale big(top);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const Planes<2> sp = split<2>(S.t[2 * s], S.t[2 * s + 1], big.by);
@@ -888,8 +889,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 #pragma unroll
         for (int ti = 0; ti < 4; ++ti) U[ti] *= *(const f32x4*)(rec.end + 16 * ti + 4 * g);
         if constexpr (!OUT) take();
-        // one scale for what is kept of S and what is added
-        const float whole = rec.misc[0] * unit;
+        // one scale for what is kept of S and what is added; a column of zeros, which keeps nothing, has no part in it
+        const float whole = top == 0.0f ? 0.0f : rec.misc[0] * unit;
         const Scale es(fmaxf(over_column(largest(U)), whole * big.back));
         const float keep = whole * es.by;
 #pragma unroll
@@ -1054,7 +1055,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         f32x4 dO[4] = {next[0], next[1], next[2], next[3]};
         __syncthreads();
         if (c > c0) fetch(c - 1);
-        const Scale big(over_column(largest(S.t)));
+        const float top = over_column(largest(S.t));
+        const Scale big(top);
         f32x4 dU[4] = {zero, zero, zero, zero}, x[4] = {zero, zero, zero, zero};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -1097,7 +1099,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         take();
         if constexpr (OUT)
             Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
-        const float whole = rec.misc[0] * unit;
+        const float whole = top == 0.0f ? 0.0f : rec.misc[0] * unit;  // as in k_delta_chain
         const Scale es(fmaxf(over_column(fmaxf(largest(dO), largest(dR))), whole * big.back));
         const float keep = whole * es.by;
 #pragma unroll

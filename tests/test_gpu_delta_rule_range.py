@@ -1,0 +1,87 @@
+"""The gated delta rule on the GPU where values are far from 1: it is linear in the values and the first state, and in
+the upstream gradients, so a power of two on them is one on the outputs, to the last bit."""
+from __future__ import annotations
+
+import pytest
+
+from oracle import blocks
+from test_gpu_delta_rule import host, make, run
+
+pytestmark = pytest.mark.gpu
+
+# chunks of one workgroup, one boundary between chunks, several with lengths that differ, and segments
+CASES = [(2, 65, 1, 2, 64, 48, ""), (3, 200, 2, 4, 128, 128, "lr"), (1, 2100, 1, 2, 64, 80, ""), (2, 2100, 1, 1, 128, 64, "r")]
+
+
+def moderate(d):
+    """Decays of which no product over a chunk is near float32's smallest, so that powers of two stay exact; those of
+    the last head close to 1."""
+    d["log_decay"].clamp_(min=-0.3)
+    d["log_decay"][:, :, -1] *= 1e-3
+
+
+def scaled(d, up, by, up_by):
+    """The inputs with values, states and upstream gradients times powers of two (numbers, or one a value channel)."""
+    d, up = dict(d), dict(up)
+    for x, names, f in ((d, ("v", "h0"), by), (up, ("grad_o", "grad_last"), up_by)):
+        for n in names:
+            if n in x:
+                x[n] = (x[n] * f).to(x[n].dtype)
+    return d, up
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("B,T,Hk,H,dk,dv,flags", CASES)
+def test_powers_of_two(B, T, Hk, H, dk, dv, flags, state, dtype):
+    import torch
+    d, up = make(B, T, Hk, H, dk, dv, dtype, 3 * T + dk, "l" in flags, "r" in flags, state=state)
+    moderate(d)
+    if not state:
+        del up["grad_last"]
+    want = run(d, up)
+    for a, b in ((20, 0), (0, 20), (10, 30), (-12, 24)):
+        got = run(*scaled(d, up, 2.0 ** -a, 2.0 ** -b))
+        for names, by in ((("o", "h_last"), a), (("grad_v", "grad_h0"), b),
+                          (("grad_q", "grad_k", "grad_log_decay", "grad_beta"), a + b)):
+            for n in names:
+                assert torch.equal(got[n].double() * 2.0 ** by, want[n].double()), (n, a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("B,T,Hk,H,dk,dv,flags", CASES)
+def test_channels_of_other_sizes(B, T, Hk, H, dk, dv, flags, state, dtype):
+    """A value channel's outputs follow from that channel alone, so one that is small beside its neighbours, or has a
+    first state of zeros beside others that have none, loses nothing."""
+    import torch
+    d, up = make(B, T, Hk, H, dk, dv, dtype, 5 * T + dk, "l" in flags, "r" in flags, state=state)
+    moderate(d)
+    if state:
+        d["h0"][..., 2::7] = 0.0
+        up["grad_last"][..., 4::7] = 0.0
+    else:
+        del up["grad_last"]
+    f = torch.exp2(torch.arange(dv, device="cuda") % 7 * -5.0)
+    want, got = run(d, up), run(*scaled(d, up, f, f))
+    for n in ("o", "h_last", "grad_v", "grad_h0"):
+        assert torch.equal(got[n].double() / f.double(), want[n].double()), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [130, 2100])
+def test_small_values_against_oracle(T, dtype):
+    """A step of training as it begins: no first state, no gradient of the last, small values and gradients of a mean,
+    heads that forget slowly. Each head by itself."""
+    import torch
+    d, up = make(1, T, 1, 3, 64, 64, dtype, T, state=False)
+    del up["grad_last"]
+    d["log_decay"] *= torch.tensor([1.0, 1e-2, 1e-4], device="cuda")
+    d, up = scaled(d, up, 2.0 ** -14, 2.0 ** -22)
+    out, want = run(d, up), blocks.delta_rule(**host(d), **host(up), terms=True)
+    for n in ("o", "h_last", "grad_v", "grad_h0", "grad_log_decay", "grad_beta"):
+        kind = dtype if n in ("o", "grad_v") else "f32"
+        for h in range(3):
+            at = (slice(None), h) if n in ("h_last", "grad_h0") else (slice(None), slice(None), h)
+            lost = blocks.LOST * want["terms"][at] if n == "o" and dtype == "bf16" else 0.0
+            assert blocks.off(out[n].double().cpu().numpy()[at], want[n][at], kind, lost=lost) <= 1, (n, h)
