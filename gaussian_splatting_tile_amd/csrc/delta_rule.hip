@@ -296,11 +296,9 @@ __device__ __forceinline__ void products(const Planes<NA> (&A)[COUNT], const Pla
                     c[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(A[t].p[i], B.p[sum - i], c[t], 0, 0, 0);
 }
 
-// Planes of an input, and of P and what it multiplies where that is rounded to bfloat16's 8 bits, float16's 11 or not.
+// Planes of an input. What the kernels form themselves has two, whatever it is rounded to at the end.
 template <typename T>
 constexpr int kPlanes = sizeof(T) == 4 ? 2 : 1;
-template <typename T>
-constexpr int kOutPlanes = std::is_same_v<T, bf16> ? 1 : 2;
 
 // 64 rows of an input, plane after plane, in 16-byte pieces; piece c of row t
 // lies at c ^ t (within the row), so that the same piece of 16 rows covers all
@@ -378,16 +376,11 @@ struct Keys {
 // and beta.
 constexpr int kPairs = 6;
 constexpr int kPair = 512;  // elements of a pair's plane
-template <int NP>
 struct Forward {
-    static constexpr int N = NP;
-    f16 M[kPairs * 2 * kPair];
-    f16 P[kPairs * NP * kPair];
+    f16 M[kPairs * 2 * kPair], P[kPairs * 2 * kPair];
     float gamma[kC], query[kC], end[kC], beta[kC];
     float misc[kC];  // 0: gamma of the chunk, 1 and 2: the inverse scales of M and P
 };
-template <typename T>
-using ForwardOf = Forward<kOutPlanes<T>>;
 // Of the backward's: M, and M and P transposed, and per step gamma, e, beta and
 // the inverse scales of the keys' and queries' rows.
 struct Backward {
@@ -592,20 +585,20 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
         for (int f = 0; f < 2; ++f)
             if (f == 0 || w < 2) {
                 const int pair = 4 * f + w;
-                auto put_planes = [&](f16* to, const auto& x, int planes) {
+                auto put_planes = [&](f16* to, const Planes<2>& x) {
 #pragma unroll
-                    for (int k = 0; k < planes; ++k) *(f16x8*)(to + (pair * planes + k) * kPair + lane * 8) = x.p[k];
+                    for (int k = 0; k < 2; ++k) *(f16x8*)(to + (pair * 2 + k) * kPair + lane * 8) = x.p[k];
                 };
-                put_planes(out->M, split<2>(m[2 * f], m[2 * f + 1], ms.by), 2);
+                put_planes(out->M, split<2>(m[2 * f], m[2 * f + 1], ms.by));
                 if constexpr (BACK) {
                     auto transposed = [&](const float* from, float scale) {
                         const int row = 32 * upper_col(pair) + 4 * g, col = 16 * upper_row(pair) + n;
                         return split<2>(col4(from, kPitch, row, col), col4(from, kPitch, row + 16, col), scale);
                     };
-                    put_planes(out->MT, transposed(M, ms.by), 2);
-                    put_planes(out->PT, transposed(P, ps.by), 2);
+                    put_planes(out->MT, transposed(M, ms.by));
+                    put_planes(out->PT, transposed(P, ps.by));
                 } else {
-                    put_planes(out->P, split<Record::N>(p[2 * f], p[2 * f + 1], ps.by), Record::N);
+                    put_planes(out->P, split<2>(p[2 * f], p[2 * f + 1], ps.by));
                 }
             }
         if (w == 2) {
@@ -766,13 +759,12 @@ struct Segments {
 // 1.4.
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
-                                                               const ForwardOf<T>* records, Segments seg) {
-    typedef ForwardOf<T> Record;
-    constexpr int NX = kPlanes<T>, NP = kOutPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
+                                                               const Forward* records, Segments seg) {
+    constexpr int NX = kPlanes<T>, KT = DK / 16, KS = DK / 32, kThreads = 64 * WAVES;
     typedef Operand<NX, DK> O;
     constexpr int KEYS = OUT ? sizeof(Keys<NX, DK>) : sizeof(Keys<NX, DK>) / 2;  // without outputs no queries
     __shared__ alignas(16) char kq[KEYS];
-    __shared__ Record rec;
+    __shared__ Forward rec;
     const f16* const K = (const f16*)kq;
     const f16* const Q = K + O::SIZE;
     const gs_delta_rule& d = a.r;
@@ -789,7 +781,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
     const T* const v = (const T*)a.v + b * d.v_batch + h * d.v_head;
     const int64_t o_step = (int64_t)d.heads * d.value_dim;
     T* const o = (T*)a.o + ((int64_t)b * d.steps * d.heads + h) * d.value_dim;
-    const Record* const first = records + (int64_t)b * chunks * d.heads + h;
+    const Forward* const first = records + (int64_t)b * chunks * d.heads + h;
     const Keys<NX, DK>* const first_keys = keys + (int64_t)b * chunks * d.key_heads + kh;
     Column<KT> S;
     float unit = 1.0f;
@@ -803,7 +795,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             for (int r = 0; r < 4; ++r) S.t[t][r] = !values && key_row(t, g, r) == col ? 1.0f : 0.0f;
     }
     Copy<KEYS, kThreads> fk;
-    Copy<sizeof(Record), kThreads> fr;
+    Copy<sizeof(Forward), kThreads> fr;
     Values<T> fv;
     auto fetch = [&](int c) {
         const int t0 = c * kC;
@@ -845,10 +837,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
             if constexpr (OUT) {
 #pragma unroll
                 for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(Q, ti, s, l);
-                Planes<NP> high;
-#pragma unroll
-                for (int k = 0; k < NP; ++k) high.p[k] = sp.p[k];
-                products(A, high, y);
+                products(A, sp, y);
             }
         }
         const float from = unit * big.back;
@@ -875,9 +864,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         }
         if constexpr (OUT) {
             const Scale us(over_column(largest(U)));
-            const Planes<NP> B[2] = {split<NP>(U[0], U[1], us.by), split<NP>(U[2], U[3], us.by)};
+            const Planes<2> B[2] = {split<2>(U[0], U[1], us.by), split<2>(U[2], U[3], us.by)};
             f32x4 x[4] = {zero, zero, zero, zero};
-            lower<NP>(rec.P, B, x, l);
+            lower<2>(rec.P, B, x, l);
             const float back = us.back * rec.misc[2];
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti)
@@ -2105,7 +2094,7 @@ size_t behind_floats(const gs_delta_rule& r) {
 }
 size_t back_record_bytes(const gs_delta_rule& r) { return (size_t)r.batch * chunks_of(r) * r.heads * sizeof(Backward); }
 size_t record_bytes(const gs_delta_rule& r) {
-    return (size_t)r.batch * chunks_of(r) * r.heads * (r.dtype == GS_BF16 ? sizeof(Forward<1>) : sizeof(Forward<2>));
+    return (size_t)r.batch * chunks_of(r) * r.heads * sizeof(Forward);
 }
 
 // Segments of a sequence: enough workgroups for the chip, each of them long
@@ -2140,7 +2129,7 @@ template <typename T, int DK, int WAVES, bool OUT>
 void chain(const DeltaArgs& a, int chunks, const void* scratch, const Segments& seg, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const auto* const keys = (const Keys<kPlanes<T>, DK>*)scratch;
-    const auto* const records = (const ForwardOf<T>*)((const char*)scratch + key_bytes(r));
+    const auto* const records = (const Forward*)((const char*)scratch + key_bytes(r));
     constexpr int WIDE = 16 * WAVES;
     const int blocks = (r.value_dim + WIDE - 1) / WIDE + (OUT ? 0 : (r.key_dim + WIDE - 1) / WIDE);
     k_delta_chain<T, DK, WAVES, OUT><<<dim3(r.batch * r.heads, blocks, seg.count), 64 * WAVES, 0, stream>>>(
@@ -2152,7 +2141,7 @@ hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     const gs_delta_rule& r = a.r;
     const int chunks = chunks_of(r), heads = r.batch * r.heads;
     k_delta_prepare<T, DK><<<r.batch * chunks * r.key_heads, kPrepThreads, 0, stream>>>(
-        a, chunks, (Keys<kPlanes<T>, DK>*)scratch, (ForwardOf<T>*)((char*)scratch + key_bytes(r)));
+        a, chunks, (Keys<kPlanes<T>, DK>*)scratch, (Forward*)((char*)scratch + key_bytes(r)));
     Segments seg = segments_of(r);
     const int64_t groups = (int64_t)heads * seg.count;
     if (seg.count > 1) {

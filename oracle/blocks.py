@@ -15,20 +15,16 @@ unit in its last place, at least half its smallest subnormal. A norm's sums are
 longer (16384 terms), but each thread adds at most 16 of them one by one and
 the rest as a tree, so the same bound holds for them.
 
-The bfloat16 outputs of the delta rule are sums of products whose factors are
-rounded to float16's 11 bits: the state in front of a chunk of 64 steps, the
-chunk's u, and the factors of u. A rounding is off by at most float16's unit
-roundoff 2^-11 of the factor, 2^-11 / sqrt(3) in the root mean square; two
-factors of a term make 2^-11 sqrt(2 / 3) of it, and a sum of such terms is off
-by as much of the root of the sum of their squares. LOST is 6 times that;
-delta_rule gives those roots ("terms") when asked.
+LOST is what a bfloat16 output of the delta rule may lack beside that, as a
+part of the root of the sum of its terms' squares ("terms" of delta_rule):
+nothing, as the bound above holds before the rounding to any type.
 """
 from __future__ import annotations
 
 import numpy as np
 
 TOL = 2.0 ** -18
-LOST = 6 * 2.0 ** -11 * (2 / 3) ** 0.5
+LOST = 0.0
 # unit roundoff and half of the smallest subnormal
 TYPES = {"f32": (2.0 ** -24, 2.0 ** -150), "bf16": (2.0 ** -8, 2.0 ** -134), "f16": (2.0 ** -11, 2.0 ** -25)}
 

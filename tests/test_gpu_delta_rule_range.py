@@ -85,3 +85,12 @@ def test_small_values_against_oracle(T, dtype):
             at = (slice(None), h) if n in ("h_last", "grad_h0") else (slice(None), slice(None), h)
             lost = blocks.LOST * want["terms"][at] if n == "o" and dtype == "bf16" else 0.0
             assert blocks.off(out[n].double().cpu().numpy()[at], want[n][at], kind, lost=lost) <= 1, (n, h)
+
+
+@pytest.mark.parametrize("T", [9, 200, 2100])
+def test_sixteen_bits_round_once(T):
+    """A 16-bit output is a float32 one rounded at the end: no product is formed from fewer bits for it."""
+    for dtype in ("bf16", "f16"):
+        d, _ = make(1, T, 2, 4, 128, 128, dtype, 7 + T, train=False)
+        o = run(d, {})["o"].double().cpu().numpy()
+        assert blocks.off(o, blocks.delta_rule(**host(d))["o"], dtype) <= 1, dtype
