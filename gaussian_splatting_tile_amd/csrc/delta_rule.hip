@@ -52,6 +52,7 @@ struct Chunk {
     float beta[kC];
     int seg[kC];        // restarts up to each step
     float whole;        // product of all decays, 0 with a restart
+    float ends[2];      // steps in front of the first restart (64 without one), the last restart (or 0)
 };
 
 __device__ __forceinline__ int length_of(const gs_delta_rule& r, int b) {
@@ -79,8 +80,14 @@ __device__ __forceinline__ void load_gates(const DeltaArgs& a, int b, int h, int
     s.beta[lane] = beta;
     s.gamma[lane] = seg == 0 ? __builtin_amdgcn_exp2f((float)G) : 0.0f;
     s.end[lane] = seg == segs ? __builtin_amdgcn_exp2f((float)(last - G)) : 0.0f;
-    if (lane == 63) s.whole = segs == 0 ? __builtin_amdgcn_exp2f((float)G) : 0.0f;
+    if (lane == 63) {
+        s.whole = segs == 0 ? __builtin_amdgcn_exp2f((float)G) : 0.0f;
+        s.ends[0] = cuts ? __ffsll((unsigned long long)cuts) - 1 : kC;
+        s.ends[1] = cuts ? 63 - __clzll(cuts) : 0;
+    }
 }
+
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < __builtin_inff(); }
 
 __device__ __forceinline__ float decay(const Chunk& s, int i, int j) {
     return s.seg[i] == s.seg[j] ? __builtin_amdgcn_exp2f((float)(s.G[i] - s.G[j])) : 0.0f;
@@ -379,7 +386,7 @@ constexpr int kPair = 512;  // elements of a pair's plane
 struct Forward {
     f16 M[kPairs * 2 * kPair], P[kPairs * 2 * kPair];
     float gamma[kC], query[kC], end[kC], beta[kC];
-    float misc[kC];  // 0: gamma of the chunk, 1 and 2: the inverse scales of M and P
+    float misc[kC];  // 0: gamma of the chunk, 1 and 2: the inverse scales of M and P, 3 and 4: Chunk's ends
 };
 // Of the backward's: M, and M and P transposed, and per step gamma, e, beta and
 // the inverse scales of the keys' and queries' rows.
@@ -613,7 +620,7 @@ __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_
                 out->end[lane] = s.end[lane] * k_back[lane];
             }
             out->beta[lane] = s.beta[lane];
-            out->misc[lane] = lane == 0 ? s.whole : lane == 1 ? ms.back : ps.back;
+            out->misc[lane] = lane == 0 ? s.whole : lane == 1 ? ms.back : lane == 2 ? ps.back : s.ends[lane == 4];
         }
     }
 }
@@ -693,6 +700,26 @@ struct Column {
     }
 };
 
+// A restart drops a state (its gradient) whatever it holds, and a product with a factor of 0 would not. Zeros the columns
+// that are not finite, which are the bits (by lanes) of what it returns.
+template <int KT>
+__device__ __forceinline__ uint64_t drop(Column<KT>& S) {
+    float x = 0.0f;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x = fmaf(S.t[t][r], 0.0f, x);  // 0 or NaN
+    uint64_t lost = __ballot(x != x);
+    lost |= lost >> 32;
+    lost = (lost | lost >> 16) & 0xffff;
+    lost |= lost << 16;
+    lost |= lost << 32;
+    if (lost >> (threadIdx.x & 63) & 1)
+#pragma unroll
+        for (int t = 0; t < KT; ++t) S.t[t] = f32x4{0, 0, 0, 0};
+    return lost;
+}
+
 // The values of a chunk in a column, as results lie: rows 16 t + 4g + r; p at the chunk's first row, rows from `rows`
 // on are 0. (Where rows overlap, step < dim, the rows behind the last one may hold something of it instead, which
 // their beta of 0 keeps out.)
@@ -742,9 +769,10 @@ struct Values {
 // the segments (k_delta_join) the state in front of each, and the pass with
 // outputs starts from those.
 struct Segments {
-    int count, chunks;  // of a sequence; of a segment
+    int count, chunks;  // of a sequence (at most 32); of a segment
     float* front;       // [b][h][segment][key_dim][value_dim] B, then the state in front
     float* phi;         // [b][h][segment][key_dim][key_dim]
+    uint32_t* cut;      // [b][h][segment] whether it holds a restart, so that Phi is 0
 };
 
 // The states, chunk after chunk, 16 columns of the values a wave: S and
@@ -815,6 +843,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         take();
     }
     const f32x4 zero = {0, 0, 0, 0};
+    [[maybe_unused]] bool cut = false;
     for (int c = c0; c < c1; ++c) {
         const Lane l = Lane::here();
         const int g = l.g, col = col0 + l.n;
@@ -825,6 +854,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         __syncthreads();
         if (c + 1 < c1) fetch(c + 1);
         f32x4 R[4] = {zero, zero, zero, zero}, y[4] = {zero, zero, zero, zero};  // K S, then R; Q S, then O
+        uint64_t lost = 0;  // columns that are not finite, in a chunk with a restart
+        if (rec.misc[3] < (float)kC) {
+            lost = drop(S);
+            cut = true;
+        }
         const float top = over_column(largest(S.t));
         const Scale big(top);
 #pragma unroll
@@ -873,6 +907,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 #pragma unroll
                 for (int r = 0; r < 4; ++r) y[ti][r] = fmaf(x[ti][r], back, y[ti][r]);
             take();
+            if (lost >> lane & 1)  // they end with the step in front of the restart
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if ((float)(16 * (e / 4) + 4 * g + e % 4) < rec.misc[3]) y[e / 4][e % 4] = __builtin_nanf("");
             Values<T>::store(o + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, y, l);
         }
 #pragma unroll
@@ -907,6 +945,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
         const int64_t at = head * seg.count + z;
         S.store(values ? seg.front + at * size : seg.phi + at * d.key_dim * d.key_dim, on, col, d.key_dim,
                 values ? d.value_dim : d.key_dim, unit);
+        if (blockIdx.y == 0 && threadIdx.x == 0) seg.cut[at] = cut;
     }
 }
 
@@ -938,6 +977,8 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
 #pragma unroll
         for (int r = 0; r < 4; ++r) y[r] = f.load<float>(at + r * d.value_dim * 4);
     };
+    // bit z: a restart in segment place(z) drops what S holds
+    const uint64_t cuts = __ballot(lane < seg.count && seg.cut[head * seg.count + place(min(lane, seg.count - 1))]);
     {
         const Buffer h(start + head * size, start ? size * 4 : 0);
 #pragma unroll
@@ -957,6 +998,10 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
             const Buffer f(front + place(z + x) * size, size * 4);
 #pragma unroll
             for (int r = 0; r < 4; ++r) f.store(at + r * d.value_dim * 4, S[r]);
+            if (cuts >> (z + x) & 1) {
+                S = B[x];
+                continue;
+            }
             f32x4 acc[2] = {B[x], {0, 0, 0, 0}};
 #pragma unroll
             for (int kt = 0; kt < KT; ++kt) acc[kt & 1] = mma(A[x][kt], *(const f32x4*)(s + n * PITCH + 16 * kt + 4 * g), acc[kt & 1]);
@@ -1032,6 +1077,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         take();
     }
     const f32x4 zero = {0, 0, 0, 0};
+    [[maybe_unused]] bool cut = false;
     for (int c = c1 - 1; c >= c0; --c) {
         const Lane l = Lane::here();
         const int g = l.g, col = col0 + l.n;
@@ -1054,6 +1100,19 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) A[ti] = O::row(kq.K, ti, s, l);
             products(A, sp, dU);
+        }
+        // as in k_delta_chain; where an element is not finite, so are all sums of its column (one of its planes is NaN)
+        const bool restart = rec.misc[3] < (float)kC;
+        const uint64_t lost = __ballot(restart && !finite(dU[0][0]));
+        cut |= restart;
+        if (lost) {
+            const bool mine = lost >> lane & 1;
+#pragma unroll
+            for (int ti = 0; ti < 4; ++ti)
+                if (mine) dU[ti] = zero;
+#pragma unroll
+            for (int t = 0; t < KT; ++t)
+                if (mine) S.t[t] = zero;
         }
         {
             const Scale os(over_column(largest(dO)));
@@ -1086,6 +1145,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
             }
         }
         take();
+        if (OUT && (lost >> lane & 1))
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if ((float)(16 * (e / 4) + 4 * g + e % 4) >= rec.misc[4]) x[e / 4][e % 4] = __builtin_nanf("");
         if constexpr (OUT)
             Values<T>::store(gv + t0 * o_step, o_step, len - t0, d.steps - t0, on, col, d.value_dim, x, l);
         const float whole = top == 0.0f ? 0.0f : rec.misc[0] * unit;  // as in k_delta_chain
@@ -1112,6 +1175,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chun
         const int64_t at = head * seg.count + z;
         S.store(values ? seg.front + at * size : seg.phi + at * d.key_dim * d.key_dim, on, col, d.key_dim,
                 values ? d.value_dim : d.key_dim, unit);
+        if (blockIdx.y == 0 && threadIdx.x == 0) seg.cut[at] = cut;
     }
 }
 
@@ -1134,6 +1198,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
     __shared__ float A[kC * kPitch];     // Ad
     __shared__ float X[kC * (kC + 1)];
     __shared__ float betas[kGradWaves][kC], front[kGradWaves][kC], after[kGradWaves][kC], dots[kGradWaves];
+    __shared__ float spoilt[2][kGradWaves];  // not finite where a restart drops such a state, or gradient, of a wave
     __shared__ Chunk s;
     const gs_delta_rule& d = a.r;
     const int kh = blockIdx.x % d.key_heads, c = blockIdx.x / d.key_heads % chunks, b = blockIdx.x / d.key_heads / chunks;
@@ -1235,13 +1300,19 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
                     x = mma(kk, S[kt], x);
                     y = mma(kk, Z[kt], y);
                 }
+                // as in the chains
+                const bool cut = s.seg[kC - 1] != 0, s_lost = cut && !finite(x[0]), z_lost = cut && !finite(y[0]);
+                if (ti == 0) {
+                    spoilt[0][w] = __ballot(s_lost) ? __builtin_nanf("") : 0.0f;
+                    spoilt[1][w] = __ballot(z_lost) ? __builtin_nanf("") : 0.0f;
+                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = 16 * ti + 4 * g + r;
-                    e[ti][r] = vals[4 * ti + r] - s.gamma[i] * x[r];
+                    e[ti][r] = vals[4 * ti + r] - (s_lost ? 0.0f : s.gamma[i] * x[r]);
                     R[ti][r] = s.beta[i] * e[ti][r];
                     dO[ti][r] = ups[4 * ti + r];
-                    dU[ti][r] = s.end[i] * y[r];
+                    dU[ti][r] = z_lost ? 0.0f : s.end[i] * y[r];
                 }
             }
 #pragma unroll
@@ -1332,6 +1403,22 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             __syncthreads();
         }
         if (w < KT) {
+            if (s.seg[kC - 1]) {  // a restart drops the state and the gradient whatever they hold
+                float s_spoilt = 0.0f, z_spoilt = 0.0f;
+                for (int i = 0; i < kGradWaves; ++i) {
+                    s_spoilt += spoilt[0][i];
+                    z_spoilt += spoilt[1][i];
+                }
+#pragma unroll
+                for (int ti = 0; ti < 4; ++ti)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int seg = s.seg[16 * ti + 4 * g + r];
+                        aq[ti][r] = seg == 0 ? aq[ti][r] + s_spoilt : 0.0f;
+                        ar[ti][r] = seg == 0 ? ar[ti][r] + s_spoilt : 0.0f;
+                        au[ti][r] = seg == s.seg[kC - 1] ? au[ti][r] + z_spoilt : 0.0f;
+                    }
+            }
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
                 f32x4 x, y, fr, af;
@@ -1391,6 +1478,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
                 f += front[x][lane];
                 af += after[x][lane];
             }
+            be += 0.0f * f + 0.0f * af;  // as in k_delta_grads
             float all_f = f, all_a = af;
 #pragma unroll
             for (int m = 1; m < 64; m <<= 1) {
@@ -1401,7 +1489,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             all_a = __shfl_up(all_a, 1);
             float t = 0.0f;
             for (int i = lane; i < kC; ++i) t += X[i * (kC + 1) + lane];
-            t += all_f + (lane ? all_a : 0.0f) + s.whole * dot;
+            t += all_f + (lane ? all_a : 0.0f) + (s.seg[kC - 1] ? 0.0f : s.whole * dot);
             if (lane < all) {
                 const int64_t at = ((int64_t)b * d.steps + t0 + lane) * d.heads + h;
                 const bool live = lane < rows;
@@ -1524,7 +1612,7 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
     } m;
     __shared__ Backward rec;
     __shared__ float o_back[kC], betas[kGradWaves][kC], front[kGradWaves][kC], after[kGradWaves][kC], dots[kGradWaves];
-    __shared__ float most[4][kGradWaves];
+    __shared__ float most[4][kGradWaves], spoilt[2][kGradWaves];
     __shared__ float inside[kTiles][16], across[kTiles][16], tile_beta[kTiles][16], total[kTiles];
     __shared__ Chunk gates;
     const gs_delta_rule& d = a.r;
@@ -1618,6 +1706,10 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         // 16 columns of the values: U and dR
         f32x4 U[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
         {
+            if (gates.seg[kC - 1]) {  // as in the chains
+                spoilt[0][w] = drop(S) ? __builtin_nanf("") : 0.0f;
+                spoilt[1][w] = drop(Z) ? __builtin_nanf("") : 0.0f;
+            }
             float dot = 0.0f;
 #pragma unroll
             for (int t = 0; t < KT; ++t)
@@ -1737,6 +1829,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                     for (int ti = 0; ti < 4; ++ti) C[ti] = TV::turned(m.ue[0], ti, s, l);
                     products(C, B, au);
                     }
+            if (gates.seg[kC - 1])  // no gradient of a step that a dropped column belongs to is finite
+                for (int i = 0; i < kGradWaves; ++i) {
+                    s_back += spoilt[0][i];
+                    z_back += spoilt[1][i];
+                }
         }
         // tiles of Pd and Ad, and of what the gates' gradients need of them
         f32x4 pd[2] = {zero, zero}, ad[2] = {zero, zero};
@@ -1843,17 +1940,21 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                     }
                 }
             }
+            const int segs = __builtin_amdgcn_readfirstlane(gates.seg[kC - 1]);
 #pragma unroll
             for (int ti = 0; ti < 4; ++ti) {
                 const int i0 = 16 * ti + 4 * g;
                 const f32x4 gamma = *(const f32x4*)(rec.gamma + i0), beta = *(const f32x4*)(rec.beta + i0), end = *(const f32x4*)(rec.end + i0);
                 const f32x4 kb = *(const f32x4*)(rec.k_back + i0), qb = *(const f32x4*)(rec.q_back + i0), ob = *(const f32x4*)(o_back + i0);
+                const int* const seg = gates.seg + i0;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int i = i0 + r, at = O::at(i, 2 * w + n / 8) + (n & 7);
                     const float kv = (float)kq.K[at] * kb[r], qv = (float)kq.Q[at] * qb[r];
-                    const float x = d.scale * gamma[r] * ob[r] * s_back * aq[ti][r];
-                    const float y = beta[r] * gamma[r] * es.back * s_back * ar[ti][r], z = end[r] * us.back * z_back * au[ti][r];
+                    // what a restart has dropped is 0 whatever it was
+                    const float x = seg[r] == 0 ? d.scale * gamma[r] * ob[r] * s_back * aq[ti][r] : 0.0f;
+                    const float y = seg[r] == 0 ? beta[r] * gamma[r] * es.back * s_back * ar[ti][r] : 0.0f;
+                    const float z = seg[r] == segs ? end[r] * us.back * z_back * au[ti][r] : 0.0f;
                     const float f = sum_lanes(qv * x - kv * y), af = sum_lanes(kv * z);
                     if (n == 0) {
                         front[w][i] = f;
@@ -1874,6 +1975,9 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 #pragma unroll
             for (int tj = 0; tj < 4; ++tj)
                 if (tj <= tt) be += tile_beta[tri(tt, tj)][n];
+            // not finite where the state in front (the gradient behind) is not and no restart lies between
+#pragma unroll
+            for (int x = 0; x < KT; ++x) be += 0.0f * front[x][lane] + 0.0f * after[x][lane];
             a.grad_beta[at] = lane < rows ? be : 0.0f;
         }
         if (w == 1) {
@@ -2106,7 +2210,7 @@ size_t record_bytes(const gs_delta_rule& r) {
 // us, of 32 heads 999 and 1247, of 64 heads 1905 and 1890.
 constexpr int kUnits = 256;  // compute units
 Segments segments_of(const gs_delta_rule& r) {
-    Segments s{1, chunks_of(r), nullptr, nullptr};
+    Segments s{1, chunks_of(r), nullptr, nullptr, nullptr};
     const int64_t heads = (int64_t)r.batch * r.heads;
     if (heads > (s.chunks >= 128 ? kUnits / 4 : kUnits / 8) || s.chunks < 32) return s;
     const int most = (int)std::min<int64_t>((kUnits + heads - 1) / heads, 32);
@@ -2116,7 +2220,8 @@ Segments segments_of(const gs_delta_rule& r) {
 }
 size_t segment_bytes(const gs_delta_rule& r) {
     const Segments s = segments_of(r);
-    return s.count == 1 ? 0 : (size_t)r.batch * r.heads * s.count * r.key_dim * (r.value_dim + r.key_dim) * sizeof(float);
+    if (s.count == 1) return 0;
+    return (size_t)r.batch * r.heads * s.count * ((size_t)r.key_dim * (r.value_dim + r.key_dim) * sizeof(float) + sizeof(uint32_t));
 }
 
 // Waves (of 16 columns) of a chain's workgroup: 8, which read the operands from
@@ -2147,6 +2252,7 @@ hipError_t forward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     if (seg.count > 1) {
         seg.front = (float*)((char*)scratch + key_bytes(r) + record_bytes(r));
         seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
+        seg.cut = (uint32_t*)(seg.phi + (size_t)heads * seg.count * r.key_dim * r.key_dim);
         if (narrow(groups * 2, std::max(r.value_dim, r.key_dim)))
             chain<T, DK, 4, false>(a, chunks, scratch, seg, stream);
         else
@@ -2184,6 +2290,7 @@ hipError_t backward(const DeltaArgs& a, void* scratch, hipStream_t stream) {
     if (seg.count > 1) {
         seg.front = inverse + (r.dtype == GS_F32 ? inverse_floats(r) : 0);
         seg.phi = seg.front + (size_t)heads * seg.count * r.key_dim * r.value_dim;
+        seg.cut = (uint32_t*)(seg.phi + (size_t)heads * seg.count * r.key_dim * r.key_dim);
         if (narrow(groups * 2, std::max(r.value_dim, r.key_dim)))
             chain_back<T, DK, 4, false>(a, chunks, scratch, behind, seg, stream);
         else

@@ -790,9 +790,10 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
  *   restart     [B][T] uint8, or NULL
  * All other arrays are contiguous. Sums and states are float32, sums of
  * log_decay float64; with more than GS_DELTA_FEW steps factors of products keep
- * 22 bits (of the largest value in their row, column or chunk), and inputs or
- * states that are not finite make every result of their chunk of 64 steps and of
- * those behind it not finite, across a restart too. Products of decays above 1 (log_decay above 0) are formed over
+ * 22 bits (of the largest value in their row, column or chunk), and an input
+ * that is not finite may make every result of its chunk of 64 steps not finite.
+ * Outside its chunk, and from h0 and grad_last on, what is not finite ends at a
+ * restart. Products of decays above 1 (log_decay above 0) are formed over
  * 64 steps, and where up to 64 heads (of all sequences) have 2048 steps or more
  * over segments of at least 512, and may leave float32's range there.
  * ------------------------------------------------------------------- */

@@ -101,8 +101,8 @@ def delta_rule(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, rest
         dv_[:, t] = b * du
         db[:, t] = (du * errs[t]).sum(-1)
         dS = dS - k[:, t, :, :, None] * (b * du)[:, :, None, :]
-        dg[:, t] = (dS * D).sum((-1, -2))
-        dS = a * dS
+        dg[:, t] = np.where(a == 0.0, 0.0, dS * D).sum((-1, -2))
+        dS = np.where(a == 0.0, 0.0, a * dS)
     m, m1 = live[:, :, None], live[:, :, None, None]
     shared = lambda x: np.where(m1, x, 0.0).reshape(B, T, Hk, r, dk).sum(3)  # noqa: E731
     out.update(grad_q=shared(dq), grad_k=shared(dk_), grad_v=np.where(m1, dv_, 0.0), grad_log_decay=np.where(m, dg, 0.0),
