@@ -1694,14 +1694,22 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         }
         if (w == 0) load_gates(a, b, h, t0, len, gates);
         __syncthreads();
-        // Row `col` of S and of dS, terms 32 s + 8 g .., for the keys' columns below; what is read past a row's end
-        // meets columns of U, dR and dO that are 0.
+        // Row `col` of S and of dS, terms 32 s + 8 g .., for the keys' columns below; what is read past a row's end is
+        // the next rows' and has no part in a row's scale.
         f32x4 srow[8], zrow[8];
         auto take = [&](const float* p, f32x4 (&x)[8]) {
             const Buffer from(p, p ? (int)size * 4 : 0);
             const uint32_t off = col < d.key_dim ? (uint32_t)(col * d.value_dim + 8 * g) * 4u : kNowhere;
 #pragma unroll
             for (int s = 0; s < 8; ++s) x[s] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from.r, off + 128 * (s / 2) + 16 * (s & 1), 0, 0));
+        };
+        auto within = [&](f32x4 (&x)[8]) {
+            if (d.value_dim < kV)
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (32 * (s / 2) + 8 * g + 4 * (s & 1) + r >= d.value_dim) x[s][r] = 0.0f;
         };
         // 16 columns of the values: U and dR
         f32x4 U[4] = {zero, zero, zero, zero}, E[4] = {zero, zero, zero, zero};
@@ -1802,6 +1810,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
         f32x4 aq[4] = {zero, zero, zero, zero}, ar[4] = {zero, zero, zero, zero}, au[4] = {zero, zero, zero, zero};
         float s_back = 0.0f, z_back = 0.0f;
         if (w < KT) {
+            within(srow);
+            within(zrow);
             Scale scale(over_column(largest(srow)));
             s_back = scale.back;
 #pragma unroll
