@@ -95,7 +95,7 @@ gs::RecurrenceArgs recurrence_args(const gs_recurrence& r) {
     return a;
 }
 
-gs_status check_delta_rule(const gs_delta_rule* r, const char* who) {
+gs_status check_delta_rule(const gs_delta_rule* r, bool backward, const char* who) {
     if (!r) return fail(GS_ERR_INVALID, "%s: the description is NULL", who);
     if (!type_bytes(r->dtype)) return fail(GS_ERR_INVALID, "%s: unknown dtype %d", who, r->dtype);
     if (r->batch < 0 || r->steps < 0 || (int64_t)r->batch * r->steps > (1 << 30) || r->steps > (1 << 30))
@@ -116,9 +116,10 @@ gs_status check_delta_rule(const gs_delta_rule* r, const char* who) {
     for (int64_t s : {r->q_batch, r->q_step, r->q_head, r->k_batch, r->k_step, r->k_head, r->v_batch, r->v_step,
                       r->v_head, r->decay_batch, r->decay_step, r->beta_batch, r->beta_step})
         if (s < 0) return fail(GS_ERR_INVALID, "%s: a stride is negative", who);
-    // a chunk's rows are addressed by 32-bit offsets in bytes
-    for (int64_t s : {r->q_step, r->k_step, r->v_step, (int64_t)r->heads * r->value_dim})
-        if (s > (1 << 22)) return fail(GS_ERR_INVALID, "%s: a step stride of %lld is over 2^22", who, (long long)s);
+    // a chunk's rows are addressed by 32-bit offsets in bytes; calls of a few steps know no chunks, and one step no stride
+    if (r->steps > (backward ? 1 : GS_DELTA_FEW))
+        for (int64_t s : {r->q_step, r->k_step, r->v_step})
+            if (s > (1 << 22)) return fail(GS_ERR_INVALID, "%s: a step stride of %lld is over 2^22", who, (long long)s);
     if ((uintptr_t)r->lengths & 3) return fail(GS_ERR_INVALID, "%s: lengths is not 4-byte aligned", who);
     return GS_OK;
 }
@@ -851,7 +852,7 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
 
 size_t gs_delta_rule_scratch_bytes(const gs_delta_rule* r, int32_t backward) {
     g_last_error.clear();
-    if (check_delta_rule(r, "gs_delta_rule_scratch_bytes")) return 0;
+    if (check_delta_rule(r, backward != 0, "gs_delta_rule_scratch_bytes")) return 0;
     return gs::delta_rule_scratch_bytes(*r, backward != 0);
 }
 
@@ -860,7 +861,7 @@ gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k
                             float* ckpt, void* scratch, size_t scratch_bytes, void* stream) {
     const char* const who = "gs_delta_rule_fwd";
     g_last_error.clear();
-    if (gs_status s = check_delta_rule(r, who)) return s;
+    if (gs_status s = check_delta_rule(r, false, who)) return s;
     if (r->batch == 0) return GS_OK;
     if (r->steps > 0 && (!q || !k || !v || !log_decay || !beta || !o))
         return fail(GS_ERR_INVALID, "%s: a required pointer is NULL", who);
@@ -890,7 +891,7 @@ gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k
                             size_t scratch_bytes, void* stream) {
     const char* const who = "gs_delta_rule_bwd";
     g_last_error.clear();
-    if (gs_status s = check_delta_rule(r, who)) return s;
+    if (gs_status s = check_delta_rule(r, true, who)) return s;
     if (r->batch == 0) return GS_OK;
     if (r->steps > 0 && (!q || !k || !v || !log_decay || !beta || !grad_o || !grad_q || !grad_k || !grad_v ||
                          !grad_log_decay || !grad_beta))
@@ -914,6 +915,7 @@ gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k
     a.beta = beta;
     a.h0 = h0;
     a.ckpt_in = ckpt;
+    if (r->steps == 1) a.r.q_step = a.r.k_step = a.r.v_step = 0;
     a.grad_o = grad_o;
     a.grad_last = grad_last;
     a.grad_q = grad_q;

@@ -782,9 +782,10 @@ gs_status gs_adam_step(const gs_adam* cfg, const gs_adam_tensor* tensors, int32_
  *   scale       of the queries, finite
  *   *_batch, *_step, *_head  strides of q [B][T][Hk][key_dim], k (the same)
  *               and v [B][T][H][value_dim] in elements, >= 0, a head's
- *               elements contiguous, the step strides at most 2^22; decay and
- *               beta strides of log_decay and
- *               beta, float32 [B][T][H], heads contiguous
+ *               elements contiguous; the step strides at most 2^22, forward
+ *               where T > GS_DELTA_FEW and backward where T > 1; decay and beta
+ *               strides of log_decay and beta, float32 [B][T][H], heads
+ *               contiguous
  *   lengths     [B] int32, or NULL (every length is T); values outside
  *               [0, T] are clamped to it
  *   restart     [B][T] uint8, or NULL

@@ -1,0 +1,44 @@
+"""Which sizes and strides calls of the recurrent block refuse, and which they must not. Needs no GPU."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from test_blocks_host import D, P, _delta, on
+
+
+@pytest.fixture(scope="module")
+def gs():
+    from gaussian_splatting_tile_amd import _lib
+    if not os.path.exists(_lib.LIB_PATH):
+        pytest.fail("libgs.so is not built: run __graft_entry__.build()")
+    return _lib.load()
+
+
+@pytest.mark.parametrize("stride", ["q_step", "k_step", "v_step"])
+def test_wide_steps(gs, stride):
+    """Refused where a chunk's rows are addressed by them, only there. (The calls that pass are refused for an address
+    that is not aligned, the last check.)"""
+    from gaussian_splatting_tile_amd import _lib
+    wide = {stride: (1 << 22) + 1}
+
+    def fwd(**kw):
+        assert gs.gs_delta_rule_fwd(ctypes.byref(_delta(**kw)), D, D, D, P(257), D, None, P(512), None, None, D, 1 << 40,
+                                    None) == _lib.GS_ERR_INVALID
+        return gs.gs_last_error()
+
+    def bwd(**kw):
+        assert gs.gs_delta_rule_bwd(ctypes.byref(_delta(**kw)), D, D, D, P(257), D, None, D, D, None, P(512), P(768),
+                                    P(1024), P(1280), P(1536), None, D, 1 << 40, None) == _lib.GS_ERR_INVALID
+        return gs.gs_last_error()
+
+    few = _lib.GS_DELTA_FEW
+    for steps in (0, 1, few):
+        assert b"aligned" in fwd(steps=steps, **wide)
+    assert b"stride" in fwd(steps=few + 1, **wide)
+    for steps in (0, 1):
+        assert b"aligned" in bwd(steps=steps, **wide)
+    assert b"stride" in bwd(steps=2, **wide)
+    size = lambda steps: gs.gs_delta_rule_scratch_bytes(ctypes.byref(_delta(steps=steps, **wide)), 1)  # noqa: E731
+    assert size(1) > 0 and size(2) == 0

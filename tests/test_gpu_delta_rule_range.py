@@ -113,3 +113,21 @@ def test_key_dimensions_of_other_sizes(T, dv, dtype):
     for n in ("grad_q", "grad_k"):
         for at in (slice(0, None, 2), slice(1, None, 2)):
             assert blocks.off(out[n].double().cpu().numpy()[..., at], want[n][..., at], dtype) <= 1, (n, at)
+
+
+@pytest.mark.parametrize("T,train", [(1, True), (8, False)])
+def test_wide_steps_of_short_calls(T, train):
+    """Steps of more than 2^22 elements, as of the tokens of many sequences, in calls that address no chunk by them."""
+    import torch
+    d, up = make(2, T, 1, 2, 32, 48, "bf16", 41, train=train)
+    wide = (1 << 22) + 64
+    buffer = torch.empty(T * wide, dtype=torch.bfloat16, device="cuda")
+    e, at = dict(d), 0
+    for n in ("q", "k", "v"):
+        B, _, H, dim = d[n].shape
+        e[n] = buffer.as_strided(d[n].shape, (H * dim, wide, dim, 1), at)
+        e[n].copy_(d[n])
+        at += B * H * dim
+    got, want = run(e, up), run(d, up)
+    for n in want:
+        assert got[n] is None or torch.equal(got[n], want[n]), n
