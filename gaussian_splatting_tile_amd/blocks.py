@@ -19,6 +19,9 @@ BLOCK_NORM_NONE, BLOCK_NORM_RMS, BLOCK_NORM_LAYER = GS_BLOCK_NORM_NONE, GS_BLOCK
 BLOCK_GATE_NONE, BLOCK_GATE_SIGMOID, BLOCK_GATE_SILU = GS_BLOCK_GATE_NONE, GS_BLOCK_GATE_SIGMOID, GS_BLOCK_GATE_SILU
 
 
+_MOST = 1 << 30  # what the library takes along a dimension; more would not fit the fields of a description
+
+
 # ---------------------------------------------------------------- the delta rule
 
 def _strided(t, shape, dtype, name, device):
@@ -41,6 +44,8 @@ def _delta(q, k, v, log_decay, beta, scale, lengths, restart):
         raise ValueError("q, k and v must be [B, T, heads, dim]")
     if n < 0:
         raise TypeError("q, k and v must be device tensors")
+    if max(shape) > _MOST or max(vshape) > _MOST:
+        raise ValueError(f"q, k and v may have at most {_MOST} elements along a dimension")
     B, T, Hk, dk = shape
     H, dv = vshape[2:]
     gates, f32 = (B, T, H), torch.float32
@@ -174,8 +179,8 @@ def _norm_call(y, gate, residual, gating, scale, post, post_weight, post_bias, p
     if n < 0:
         raise TypeError("y must be a device tensor")
     D = shape[-1]
-    if D == 0:
-        raise ValueError("y must have at least one element in a row")
+    if not 0 < D <= _MOST:
+        raise ValueError(f"a row of y must have 1 to {_MOST} elements")
     p = [_strided(y, shape, t, "y", n), None if gate is None else _strided(gate, shape, t, "gate", n),
          None if residual is None else _strided(residual, shape, t, "residual", n)]
     outer, inner = y.numel() // D, 1
@@ -191,6 +196,8 @@ def _norm_call(y, gate, residual, gating, scale, post, post_weight, post_bias, p
         for m in shape[at:-1]:
             inner *= m
         outer = outer // inner if inner else 0
+        if inner > _MOST:
+            raise ValueError(f"y, gate and residual may have at most {_MOST} rows")
         strides = []
         for x in (y, gate, residual):
             strides += (0, 0) if x is None else _row_strides(x, at)

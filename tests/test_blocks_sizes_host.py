@@ -42,3 +42,25 @@ def test_wide_steps(gs, stride):
     assert b"stride" in bwd(steps=2, **wide)
     size = lambda steps: gs.gs_delta_rule_scratch_bytes(ctypes.byref(_delta(steps=steps, **wide)), 1)  # noqa: E731
     assert size(1) > 0 and size(2) == 0
+
+
+def test_sizes_past_32_bits(gs):
+    """A dimension that a description's 32-bit fields cannot hold is refused, not cut to its low bits (1 and 3 here)."""
+    import gaussian_splatting_tile_amd as g
+    much = (1 << 32) + 1
+    q, v, gates = on(0, 1, 1, 1, 1), on(0, 1, 1, 1, 1), on(0, 1, 1, 1)
+    for shape in ((1, much, 1, 1), (much, 1, 1, 1), (1, 1, much, 1), (1, 1, 1, much)):
+        with pytest.raises(ValueError, match="at most"):
+            g.delta_rule_fwd(q.expand(shape), q.expand(shape), v.expand(shape), gates.expand(shape[:3]), gates.expand(shape[:3]))
+        with pytest.raises(ValueError, match="at most"):
+            g.delta_rule_bwd(q, q, v.expand(shape), gates, gates, v.expand(shape))
+    y = on(0, 2, 1, 1).expand(2, much + 2, 1)
+    for kw in (dict(), dict(residual=y)):
+        with pytest.raises(ValueError, match="rows"):
+            g.block_norm_fwd(y, **kw)
+        with pytest.raises(ValueError, match="rows"):
+            g.block_norm_bwd(y, y, **kw)
+    with pytest.raises(ValueError, match="elements"):
+        g.block_norm_fwd(on(0, 1, 1).expand(1, much))
+    with pytest.raises(ValueError, match="elements"):
+        g.block_norm_fwd(on(0, 1, 0))
