@@ -2122,7 +2122,6 @@ __global__ __launch_bounds__(256) void k_delta_steps(DeltaArgs a, int slice, int
                 x[i] += __shfl_xor(x[i], m);
                 y[i] += __shfl_xor(y[i], m);
             }
-        // a wave's sums: where a row takes several waves, of its own columns
         const int turn = t & 1;
         if ((int)(threadIdx.x & 63) < lanes && on) {
 #pragma unroll
@@ -2133,13 +2132,13 @@ __global__ __launch_bounds__(256) void k_delta_steps(DeltaArgs a, int slice, int
         }
         __syncthreads();
         const float decay = gates[t][0], beta = gates[t][1], dot = qk[t];
-        const int first = lanes > 64 ? wave & (lanes / 64 - 1) : 0, by = lanes > 64 ? lanes / 64 : 1;
         Vec u{};
         if (on) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 float sx = 0.0f, sy = 0.0f;
-                for (int w = first; w < 4; w += by) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
                     sx += part[turn][w][0][col + i];
                     sy += part[turn][w][1][col + i];
                 }
