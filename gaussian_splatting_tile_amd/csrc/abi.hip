@@ -868,8 +868,13 @@ gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k
     if (!aligned(type_bytes(r->dtype), q, k, v, o) || !aligned(4, log_decay, beta, h0, h_last, ckpt))
         return fail(GS_ERR_INVALID, "%s: a buffer is not aligned to its type", who);
     if (gs_status s = check_scratch(scratch, scratch_bytes, gs::delta_rule_scratch_bytes(*r, false), 16, who)) return s;
-    for (const void* in : {q, k, v})
-        if (o && o == in) return fail(GS_ERR_INVALID, "%s: o overlaps an input", who);
+    if (r->steps > 0) {
+        for (const void* in : {q, k, v, (const void*)log_decay, (const void*)beta, (const void*)h0})
+            for (const void* out : {(const void*)o, (const void*)ckpt, (const void*)(h_last == h0 ? nullptr : h_last)})
+                if (in && in == out) return fail(GS_ERR_INVALID, "%s: o, ckpt or h_last overlaps an input", who);
+        if (o == (void*)h_last || o == (void*)ckpt || (ckpt && ckpt == h_last))
+            return fail(GS_ERR_INVALID, "%s: two outputs are one buffer", who);
+    }
     gs::DeltaArgs a{};
     a.r = *r;
     a.q = q;
@@ -906,6 +911,10 @@ gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k
         for (const void* out : {(const void*)grad_q, (const void*)grad_k, (const void*)grad_v,
                                 (const void*)grad_log_decay, (const void*)grad_beta, (const void*)grad_h0})
             if (in && in == out) return fail(GS_ERR_INVALID, "%s: a gradient overlaps an input", who);
+    const void* const outs[] = {grad_q, grad_k, grad_v, grad_log_decay, grad_beta, grad_h0};
+    for (int i = 0; r->steps > 0 && i < 6; ++i)
+        for (int j = 0; j < i; ++j)
+            if (outs[i] && outs[i] == outs[j]) return fail(GS_ERR_INVALID, "%s: two gradients are one buffer", who);
     gs::DeltaArgs a{};
     a.r = *r;
     a.q = q;

@@ -827,8 +827,8 @@ size_t gs_delta_rule_scratch_bytes(const gs_delta_rule* r, int32_t backward);
  *               NULL: row c is the state in front of step 64 (c + 1), for
  *               gs_delta_rule_bwd; rows at or behind the length are not
  *               written. Not needed when T <= 64.
- * o must not overlap an input. Two calls on the same inputs give the same
- * bits. */
+ * Otherwise outputs must not overlap inputs or each other. Two calls on the
+ * same inputs give the same bits. */
 gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
                             const float* log_decay, const float* beta, const float* h0, void* o, float* h_last,
                             float* ckpt, void* scratch, size_t scratch_bytes, void* stream);
@@ -845,7 +845,7 @@ gs_status gs_delta_rule_fwd(const gs_delta_rule* r, const void* q, const void* k
  *   grad_q, grad_k  out [B][T][Hk][key_dim];  grad_v  out like grad_o
  *   grad_log_decay, grad_beta  out [B][T][H] float32
  *   grad_h0     out like h0, or NULL
- * Outputs must not overlap inputs. */
+ * Outputs must not overlap inputs or each other. */
 gs_status gs_delta_rule_bwd(const gs_delta_rule* r, const void* q, const void* k, const void* v,
                             const float* log_decay, const float* beta, const float* h0, const float* ckpt,
                             const void* grad_o, const float* grad_last, void* grad_q, void* grad_k, void* grad_v,

@@ -64,3 +64,28 @@ def test_sizes_past_32_bits(gs):
         g.block_norm_fwd(on(0, 1, 1).expand(1, much))
     with pytest.raises(ValueError, match="elements"):
         g.block_norm_fwd(on(0, 1, 0))
+
+
+def test_outputs_of_one_buffer(gs):
+    """Refused, but for h_last in the place of h0."""
+    from gaussian_splatting_tile_amd import _lib
+    bad, big = _lib.GS_ERR_INVALID, 1 << 40
+    a = [P(4096 * i) for i in range(1, 20)]
+
+    def fwd(h0=a[5], o=a[6], last=a[7], ck=a[8], steps=100):
+        return gs.gs_delta_rule_fwd(ctypes.byref(_delta(steps=steps)), *a[:5], h0, o, last, ck, a[9], big, None)
+
+    def bwd(outs):
+        return gs.gs_delta_rule_bwd(ctypes.byref(_delta()), *a[:9], *outs, a[18], big, None)
+
+    for kw in (dict(o=a[3]), dict(o=a[5]), dict(ck=a[0]), dict(ck=a[5]), dict(last=a[4])):
+        for steps in (3, 100):
+            assert fwd(steps=steps, **kw) == bad and b"overlaps an input" in gs.gs_last_error(), kw
+    for kw in (dict(o=a[7]), dict(o=a[8]), dict(ck=a[7])):
+        assert fwd(**kw) == bad and b"one buffer" in gs.gs_last_error(), kw
+    outs = a[9:15]
+    for i in range(6):
+        for j in range(i):
+            same = list(outs)
+            same[i] = same[j]
+            assert bwd(same) == bad and b"one buffer" in gs.gs_last_error(), (i, j)
