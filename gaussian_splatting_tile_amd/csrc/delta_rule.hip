@@ -1508,8 +1508,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int
             for (int r = 0; r < 4; ++r) {
                 const int i = 16 * ti + 4 * g + r;
                 if (i < all) {
-                    gq[i * k_step + row] = (T)dq[ti][r];
-                    gk[i * k_step + row] = (T)dk[ti][r];
+                    gq[i * k_step + row] = (T)(i < rows ? dq[ti][r] : 0.0f);
+                    gk[i * k_step + row] = (T)(i < rows ? dk[ti][r] : 0.0f);
                 }
             }
 }

@@ -88,3 +88,18 @@ def test_inputs_end_at_a_restart_of_another_chunk(shift, dtype):
         assert blocks.off(got[:, doc], w[:, doc], kind) <= 1, n
     assert blocks.off(out["o"].double().cpu().numpy()[:, shift + 70:], want["o"][:, shift + 70:], dtype) <= 1
     assert blocks.off(out["h_last"].cpu().numpy(), want["h_last"]) <= 1
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T", [8, 100, 2100])
+def test_padding_stays_zero(T, dtype):
+    """Outputs and gradients of padding are 0 whatever the states hold."""
+    d, up = make(3, T, 1, 2, 64, 48, dtype, 23 + T, ragged=True)
+    d["lengths"][:] = d["lengths"].new_tensor([T, max(T - 5, 1), 3])
+    d["h0"][:, 1], up["grad_last"][:, 0] = float("nan"), float("inf")
+    out = run(d, up)
+    for b in range(3):
+        n = int(d["lengths"][b])
+        assert not out["o"][b, :n, 1].isfinite().any() and out["o"][b, :n, 0].isfinite().all()
+        for k in ("o", "grad_q", "grad_k", "grad_v", "grad_log_decay", "grad_beta"):
+            assert (out[k][b, n:] == 0).all(), (k, b)
