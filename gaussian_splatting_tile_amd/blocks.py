@@ -93,7 +93,7 @@ def delta_rule_fwd(q, k, v, log_decay, beta, h0=None, scale=None, lengths=None, 
     h0 float32 [B, H, dk, dv]; lengths int32 [B]; restart uint8 [B, T]. Returns dict o [B, T, H, dv], h_last float32
     [B, H, dk, dv] and ckpt (float32 [B, delta_rule_ckpt_rows(T), H, dk, dv] with checkpoints, for delta_rule_bwd;
     else None). `out` may give any of them; out["h_last"] may be h0 itself (one state buffer for serving), no other
-    output may overlap an input. With `stream` (not the current one) the call allocates and runs on it: order it
+    output may overlap an input or another output. Past 8 steps a step's stride in q, k and v is at most 2 ** 22. With `stream` (not the current one) the call allocates and runs on it: order it
     behind whatever wrote the inputs, and the use of what it returns behind it. Calls that share a `scratch` must
     not overlap."""
     if stream is not None and _elsewhere(stream, q.device):
@@ -133,7 +133,7 @@ def delta_rule_bwd(q, k, v, log_decay, beta, grad_o, h0=None, ckpt=None, grad_la
     """gs_delta_rule_bwd: gradients of delta_rule_fwd, which gave `ckpt` (needed when T > 64). grad_o [B, T, H, dv] of
     v's type; grad_last float32 [B, H, dk, dv] or None. Returns dict grad_q, grad_k [B, T, Hk, dk] (summed over the
     heads of a key head), grad_v [B, T, H, dv], grad_log_decay, grad_beta float32 [B, T, H], grad_h0 float32
-    [B, H, dk, dv]. `stream` and `scratch` as for delta_rule_fwd."""
+    [B, H, dk, dv]. `out` may give all of them (grad_h0 or not). `stream` and `scratch` as for delta_rule_fwd."""
     if stream is not None and _elsewhere(stream, q.device):
         return _on(stream, lambda: delta_rule_bwd(q, k, v, log_decay, beta, grad_o, h0, ckpt, grad_last, scale,
                                                   lengths, restart, out, scratch), out)

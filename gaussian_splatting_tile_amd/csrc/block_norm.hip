@@ -19,7 +19,7 @@
 //
 // Measured (a copy of as many bytes moves 5.06 TB/s): forward with residual,
 // sigmoid gate and both norms, 16384 x 2048 bf16, 335 MB: 64 us, 5.2 TB/s; its
-// backward, 537 MB: 122 us, 4.4 TB/s; 8192 x 8192 f16 forward, 671 MB: 136 us,
+// backward, 537 MB: 120 us, 4.5 TB/s; 8192 x 8192 f16 forward, 671 MB: 136 us,
 // 4.9 TB/s; 262144 x 128 bf16 with a silu gate, both directions, 537 MB: 103 us.
 // One of 64 x 2048 takes 4.2 us, a launch's latency.
 #include <algorithm>
@@ -417,10 +417,11 @@ __global__ __launch_bounds__(BLOCK) void k_block_norm_fwd(BlockNormArgs a, Geome
 
 // What a backward kernel is compiled for: a pre norm, a gate, and norms by RMS
 // without biases or any. Branches that all threads take alike cost no time by
-// themselves, but every value that lives across them costs registers: one
-// kernel for all takes 208 where that for a pre norm and a gate takes 194, that
-// for a gate alone 137 and that for neither 110 (both directions of 16384 x 2048
-// 222 -> 183 us, of 262144 x 128 125 -> 107).
+// themselves, but every value that lives across them costs registers: of bf16
+// the kernel for any norm, a pre norm and a gate takes 251, that for a pre norm
+// and a gate 202, for a gate alone 142 and for neither 110 (both directions of
+// 16384 x 2048 222 -> 183 us, of 262144 x 128 125 -> 107 at that step). Two waves
+// a SIMD at least, which the first of float32 would miss by two registers.
 enum { kWithPre = 1, kWithGate = 2, kAnyNorm = 4 };
 
 // The sums of a workgroup go to partial[workgroup][5][width].
@@ -453,8 +454,8 @@ __global__ __launch_bounds__(BLOCK, 2) void k_block_norm_bwd(BlockNormArgs a, Ge
     constexpr bool AHEAD = BLOCK < 1024;
     constexpr int NS = BIAS ? 5 : 3;
     // Sums over the rows: post_weight, scale, pre_weight, post_bias, pre_bias. 1024 threads have 128 registers each and
-    // keep the first of them in LDS, where a thread's 4 neighbours of one sum lie together (4096 x 8192 bf16: 182 us, from
-    // 248 with all in registers and 242 with 512 threads of 16 elements). Rows of more than 8192 spill all the same.
+    // keep the first of them in LDS, where a thread's 4 neighbours of one sum lie together (4096 x 8192 bf16: 181 us; at
+    // that step 182, from 248 with all in registers and 242 with 512 threads of 16 elements). Rows of more than 8192 spill all the same.
     constexpr int NL = BLOCK < 1024 ? 0 : NE == 8 ? std::min(NS, 4) : 2;
     __shared__ f32x4 held[NL ? NL * NE / 4 * BLOCK : 1];
     float acc[NS][NE];

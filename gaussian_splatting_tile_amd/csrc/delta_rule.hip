@@ -410,8 +410,8 @@ constexpr int kPrepThreads = 256;
 // of its cycles), which three workgroups a compute unit (two with float32 inputs)
 // share. All rows are fetched before the first is used, and as many heads' gates
 // as there are waves are formed meanwhile (a call of 8192 steps of 16 key heads
-// and 32 heads of 128, bf16: 329 us, 344 with one after another). Of that call
-// 96 us for 217 MB, 2.3 TB/s.
+// and 32 heads of 128, bf16: 329 us at that step, 344 with one after another).
+// Of that call, now 340 us, 94 us for 242 MB, 2.6 TB/s.
 template <typename T, int DK, typename Record>
 __global__ __launch_bounds__(kPrepThreads, sizeof(T) == 4 ? 2 : 3) void k_delta_prepare(DeltaArgs a, int chunks, Keys<kPlanes<T>, DK>* keys,
                                                                 Record* to) {
@@ -781,10 +781,10 @@ struct Segments {
 // ahead. The columns of S are held scaled to at most about 1, S = unit * S.t.
 // Bound by the splitting of states into planes and by LDS, from which every wave
 // reads all operands of a chunk for its 16 columns (32 columns a wave would read
-// half as much and spill): 4.4 us a chunk where a compute unit holds 64 columns
-// (8 x 2048 steps of 16 heads: 144 us) and 6.5 where it holds 128 (8192 steps of
-// 32 heads in 8 segments: 104 us), of which the matrix instructions are 0.7 and
-// 1.4.
+// half as much and spill): 4.9 us a chunk where a compute unit holds 64 columns
+// (8 x 2048 steps of 16 heads: 159 us) and 7.4 where it holds 128 (8192 steps of
+// 32 heads in 8 segments: 118 us), of which the matrix instructions are 0.9 and
+// 1.8. (One plane of S, U and P for a bfloat16 o, 11 bits, took 144 and 104 us.)
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
                                                                const Forward* records, Segments seg) {
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_delta_chain(DeltaArgs a, int chu
 // The state in front of every segment, in place of its B: S <- Phi S + B from
 // segment to segment (`back`: from the last to the first, the gradient behind), 16 columns a workgroup and 16 rows a wave, on the float32
 // matrix instructions. Bound by the latency of a step (2.3 us; its products are
-// 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 75 us.
+// 0.9): Phi is fetched three steps ahead. 4 heads of 32 segments: 72 us.
 template <int DK>
 __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg, const float* start, bool back) {
     constexpr int KT = DK / 16, PITCH = DK + 4, AHEAD = 4;
@@ -1012,7 +1012,7 @@ __global__ __launch_bounds__(DK * 4) void k_delta_join(DeltaArgs a, Segments seg
 // The gradients of the states, from the last chunk to the first, 16 columns a
 // wave, held and scaled as the states of k_delta_chain; behind[b][chunk][h]
 // receives the one behind each chunk. Bound as k_delta_chain: 5.2 us a chunk
-// (8 x 2048 steps of 16 heads of 128: 169 us). In segments as it is: the
+// (8 x 2048 steps of 16 heads of 128: 167 us). In segments as it is: the
 // gradient in front of a segment is Phi^T of that behind it and a B of its own.
 template <typename T, int DK, int WAVES, bool OUT>
 __global__ __launch_bounds__(64 * WAVES) void k_delta_back(DeltaArgs a, int chunks, const Keys<kPlanes<T>, DK>* keys,
@@ -1187,7 +1187,7 @@ constexpr int kV = GS_DELTA_MAX_DIM;
 // First a wave takes 16 columns of the values (U and dR, to LDS), then 16 of
 // the keys. Of float32 inputs, on the float32 matrix instructions: their two
 // planes with those of U, dR and the states would not fit LDS. 3 x 777 steps of
-// 5 heads of 96 x 80: 70 us.
+// 5 heads of 96 x 80: 71 us.
 template <typename T, int DK>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grad(DeltaArgs a, int chunks, const float* inverse, const float* behind) {
     constexpr int KT = DK / 16, kThreads = 64 * kGradWaves;
@@ -1593,7 +1593,7 @@ __device__ __forceinline__ float sum_column(float m) {
 // the values and leaves U and dR in LDS, then tiles of the 64 x 64 matrices and
 // 16 columns of the keys, from rows of S and dS that it reads again. One
 // workgroup fills a compute unit's LDS, so its waits show: 8 x 2048 steps of 8
-// key heads and 16 heads of 128: 265 us, the chunk of a head reading 128 KB of
+// key heads and 16 heads of 128: 266 us, the chunk of a head reading 128 KB of
 // states. (With addresses held in registers through the loop it spilled: 683 us.)
 template <typename T, int DK>
 __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, int chunks, const Keys<1, DK>* keys,
@@ -2052,9 +2052,8 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
 //
 // Measured: one step of 64 sequences of 16 heads of 128 x 128, whose states are
 // 134 MB: 29 us, 4.6 TB/s; of 1 sequence of 8 heads of 64: 5 us, a launch's
-// latency. A call of 8 steps takes as long as the chunks' kernels take for 9 to
-// 64 (64 sequences of 16 heads 75 us both, 4 sequences 20 and 28 us), one of 16
-// steps more (125 and 36 us).
+// latency. A call of 8 steps takes 61 us where the chunks' kernels take 81 to 89
+// for 9 to 64 (64 sequences of 16 heads), or 19 and 20 (4 sequences).
 constexpr int kFewSteps = GS_DELTA_FEW;
 
 template <typename T, int V>
@@ -2213,10 +2212,10 @@ size_t record_bytes(const gs_delta_rule& r) {
 // Segments of a sequence: enough workgroups for the chip, each of them long
 // enough for the walk over them and the first pass (more than the work of the
 // second) to pay. Heads of 128 x 128, bf16, with segments and without: 4 heads
-// of 65536 steps 459 and 3912 us; 32 heads of 2048 steps 120 and 150 us, of 8192
-// 373 and 619; 64 heads of 2048 steps 208 and 181, of 8192 691 and 740; 85 heads
-// of 8192 steps 1049 and 827. The backward of 4 heads of 8192 steps 216 and 634
-// us, of 32 heads 999 and 1247, of 64 heads 1905 and 1890.
+// of 65536 steps 460 and 4387 us; 32 heads of 2048 steps 121 and 162 us, of 8192
+// 379 and 668; 64 heads of 2048 steps 214 and 187, of 8192 712 and 776; 85 heads
+// of 8192 steps 1081 and 845. The backward of 4 heads of 8192 steps 206 and 639
+// us, of 32 heads 1001 and 1269, of 64 heads 1918 and 1915.
 constexpr int kUnits = 256;  // compute units
 Segments segments_of(const gs_delta_rule& r) {
     Segments s{1, chunks_of(r), nullptr, nullptr, nullptr};
@@ -2235,8 +2234,9 @@ size_t segment_bytes(const gs_delta_rule& r) {
 
 // Waves (of 16 columns) of a chain's workgroup: 8, which read the operands from
 // memory once for 128 columns, or 4 where their workgroups all run at once,
-// each on a compute unit of its own (8 x 2048 steps of 16 heads of 128: 145 us
-// with 4, 176 with 8; 32 heads in 8 segments: 136 and 95).
+// each on a compute unit of its own (a call of 8 x 2048 steps of 16 heads of
+// 128: 274 us with 4, 308 with 8; of 8192 steps of 32 heads in 8 segments, with
+// 4 in both passes 427 and with 8 379).
 bool narrow(int64_t groups, int columns) { return columns <= 64 || groups * ((columns + 63) / 64) <= kUnits; }
 
 template <typename T, int DK, int WAVES, bool OUT>
