@@ -1561,7 +1561,7 @@ struct Turned {
     }
 };
 
-// Sums over 16 neighbouring lanes, and over the lanes up to each.
+// Sums over 16 neighbouring lanes, and over the lanes in front of each.
 __device__ __forceinline__ float sum_lanes(float x) {
     auto with = [&](auto ctrl) {
         x += __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
@@ -1572,11 +1572,13 @@ __device__ __forceinline__ float sum_lanes(float x) {
     with(std::integral_constant<int, 0x140>{});
     return x;
 }
-__device__ __forceinline__ float scan_lanes(float x) {
-    auto with = [&](auto ctrl) {
-        x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
+__device__ __forceinline__ float sum_before(float x) {
+    auto from = [&](auto ctrl) {
+        return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), decltype(ctrl)::value, 0xf, 0xf, true));
     };
-    with(std::integral_constant<int, 0x111>{});  // row_shr
+    auto with = [&](auto ctrl) { x += from(ctrl); };
+    x = from(std::integral_constant<int, 0x111>{});  // row_shr
+    with(std::integral_constant<int, 0x111>{});
     with(std::integral_constant<int, 0x112>{});
     with(std::integral_constant<int, 0x114>{});
     with(std::integral_constant<int, 0x118>{});
@@ -1884,11 +1886,11 @@ __global__ __launch_bounds__(64 * kGradWaves) void k_delta_grads(DeltaArgs a, in
                 ad[turn][r] = beta * t;
                 pm = fmaxf(pm, fabsf(p) * fmaxf(kj, qi));
                 am = fmaxf(am, fabsf(beta * t) * fmaxf(kj, ki));
-                // sums over the columns up to this one; the decay of step j lies behind them
-                const float x = fmaf(p, qk[r] * qi * kj, beta * tb), up = scan_lanes(x);
-                if (ti > tj || i >= j) column += up - x;
-                if (n == 15) across[q][4 * g + r] = up;
-                whole += up;
+                // sums over the columns in front of this one, behind which the decay of step j lies
+                const float x = fmaf(p, qk[r] * qi * kj, beta * tb), before = sum_before(x);
+                if (ti > tj || i >= j) column += before;
+                if (n == 15) across[q][4 * g + r] = before + x;
+                whole += before + x;
                 const float sum = sum_lanes(tb);
                 if (n == 0) tile_beta[q][4 * g + r] = sum;
             }

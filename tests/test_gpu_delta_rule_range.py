@@ -131,3 +131,18 @@ def test_wide_steps_of_short_calls(T, train):
     got, want = run(e, up), run(d, up)
     for n in want:
         assert got[n] is None or torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,decay", [(2, -18.0), (2, -1.0), (64, -12.0), (130, -9.0)])
+def test_gradients_of_strong_decays(T, decay, dtype):
+    """The gradient of a decay is a sum of what it reaches over: where it lets little through it is small beside the
+    sums of the steps themselves, which are no part of it. (A restart at the first step leaves no state to the others.)"""
+    d, up = make(4, T, 16, 16, 64, 64, dtype, T, restarts=True, state=False)
+    del up["grad_last"]
+    d["restart"].zero_()
+    d["restart"][:, 0] = 1
+    d["log_decay"].fill_(decay)
+    got, want = run(d, up)["grad_log_decay"].double().cpu().numpy(), blocks.delta_rule(**host(d), **host(up))["grad_log_decay"]
+    for t in range(1, T):
+        assert blocks.off(got[:, t], want[:, t]) <= 1, t
